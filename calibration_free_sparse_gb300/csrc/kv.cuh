@@ -1,0 +1,65 @@
+// Declarations shared by the paged cache's translation units.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "moe_reader.h"
+
+struct moe_reader_kv {
+  moe_reader_kv_config cfg;
+  int device;
+  int sms;                    // CTAs of attend: one per SM
+  int page_shift;             // log2(page_size)
+  int group;                  // query heads per KV head
+  void* k;                    // caller-owned [num_pages][Hkv][page_size][D]
+  void* v;
+  int8_t* codes;              // caller-owned [num_pages][Hkv][2][D] or null
+  float* steps;               // caller-owned [num_pages][Hkv] or null
+  const float* k_scale;       // caller-owned [Hkv] or null
+  const float* v_scale;
+  // workspace
+  void* base;
+  float* part_o;              // [sms][2][16][D]  unnormalised outputs of split rows
+  float* part_ml;             // [sms][2][2][16]  their running maximum and sum
+  uint32_t* arrived;          // [items]          pieces written; zero between launches
+  uint32_t* err;              // [1]              device error word
+  cudaStream_t last_stream;
+  int used;
+};
+
+namespace mr {
+
+constexpr int kMaxGroup = 64;
+constexpr int kMaxRequests = 1024;
+constexpr int kMaxSelectPages = 49152;
+
+constexpr uint32_t kErrLength = MOE_READER_ERR_LENGTH;
+constexpr uint32_t kErrPage = MOE_READER_ERR_PAGE;
+constexpr uint32_t kErrPool = MOE_READER_ERR_POOL;
+
+cudaError_t launch_kv_plan(const moe_reader_kv& kv, const moe_reader_kv_plan_args& a,
+                           cudaStream_t s);
+cudaError_t launch_kv_append(const moe_reader_kv& kv, const moe_reader_kv_append_args& a,
+                             cudaStream_t s);
+cudaError_t launch_kv_attend(const moe_reader_kv& kv, const moe_reader_kv_attend_args& a,
+                             cudaStream_t s);
+cudaError_t configure_kv_attend(const moe_reader_kv& kv);
+// Items of attend: (request, KV head, tile of the group's query heads).
+int attend_row_tiles(const moe_reader_kv_config& c);
+cudaError_t launch_kv_select(const moe_reader_kv& kv, const moe_reader_kv_select_args& a,
+                             cudaStream_t s);
+cudaError_t configure_kv_select(const moe_reader_kv& kv);
+
+// 2^e, -126 <= e <= 127
+__device__ __forceinline__ float two_to(int e) { return __int_as_float((e + 127) << 23); }
+// floor(log2 a) of a finite a >= 0, held to -100 .. 100
+__device__ __forceinline__ int floor_log2_held(float a) {
+  a = fminf(fmaxf(a, 7.8886090522101181e-31f), 1.2676506002282294e30f);   // 2^-100, 2^100
+  return (__float_as_int(a) >> 23) - 127;
+}
+
+}  // namespace mr

@@ -1,0 +1,893 @@
+// Attention of one new token per request over a paged cache, split over the
+// cache's length and joined in the same launch.
+//
+// Per (request, KV head) the group's query heads share every key and value
+// read, so the arithmetic intensity is about 2 * group operations per cached
+// element: the kernel is bound by HBM, and the tensor cores only have to keep
+// the group's products off the FP32 pipes.  The products are formed
+// transposed, S^T = K Q^T (16 keys x 8 heads per instruction) and
+// O^T = V^T P^T (16 coordinates x 8 heads): a group of up to 8 heads fills the
+// short side of the instruction, K and V come from shared memory as the long
+// side, and the accumulators cost D / 4 registers per 8 heads.
+//
+// Work is a list of (request, KV head, tile of keys), dealt to one CTA per SM
+// in equal contiguous shares computed on the device from the lengths.  Inside
+// a CTA every warp takes every kWarps-th tile of the share with a private
+// cp.async pipeline, softmax state and output: no barrier until the share or
+// the row ends.  A row that several CTAs hold is joined by the CTA that
+// finishes last, in piece order, so the result does not depend on timing.
+#include <algorithm>
+#include <type_traits>
+
+#include "kv.cuh"
+
+namespace mr {
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+constexpr int kBf16 = MOE_READER_TYPE_BF16;
+constexpr int kF16 = MOE_READER_TYPE_F16;
+constexpr int kE4m3 = MOE_READER_TYPE_E4M3;
+
+// Shapes of one instantiation: D coordinates, NT tiles of 8 query heads, cache type CT.
+template <int D_, int NT_, int CT_>
+struct Shape {
+  static constexpr int D = D_, NT = NT_, CT = CT_;
+  static constexpr int kBytes = CT == kE4m3 ? 1 : 2;
+  static constexpr int kRow = D * kBytes;                    // bytes of a key
+  static constexpr int kMt = kRow >= 256 ? 1 : 2;            // 16-key subtiles per tile
+  static constexpr int kKeys = 16 * kMt;                     // keys per tile
+  static constexpr int kTile = 2 * kKeys * kRow;             // bytes of a tile, K then V
+  static constexpr int kWarps = kRow >= 512 ? 4 : 8;
+  static constexpr int kThreads = 32 * kWarps;
+  static constexpr int kStages = kTile <= 4096 ? 6 : 3;
+  static constexpr int kRows = 8 * NT;                       // query heads of an item
+  // the cross-warp sum runs over chunks of the coordinates that fit 16 KB
+  static constexpr int kChunk = 4096 / (kWarps * kRows) < D ? 4096 / (kWarps * kRows) : D;
+  static constexpr int kPitch = kChunk + 4;
+  static constexpr int kPipe = kWarps * kStages * kTile;
+  static constexpr int kSum = kWarps * kRows * kPitch * 4;
+  static constexpr int kMl = kWarps * kRows * 2 * 4;
+  static constexpr int kPos = kWarps * kStages * kMt * 4;
+  static constexpr int kSmem = kPipe + kSum + kMl + kPos + (kMaxRequests + 1) * 4;
+  static_assert(kRows * 256 * 4 <= kSum, "join weights of at most 256 pieces");
+  static_assert(kSmem <= 227 * 1024, "shared memory");
+};
+
+struct Params {
+  const void* q;
+  const int32_t* table;
+  const int32_t* lens;
+  const int32_t* pages;
+  const float* sinks;
+  void* out;
+  float* lse;
+  long long q_request, q_head;
+  int q_type, requests, width, keep, window;
+  float scale;
+  const char* k;
+  const char* v;
+  const float* k_scale;
+  const float* v_scale;
+  int heads, kv_heads, group, row_tiles, shift, num_pages;
+  float* part_o;
+  float* part_ml;
+  uint32_t* arrived;
+  uint32_t* err;
+};
+
+// ---- instructions ---------------------------------------------------------
+__device__ __forceinline__ uint32_t smem_addr(const void* p) {
+  return (uint32_t)__cvta_generic_to_shared(p);
+}
+// 16 bytes, or zeros where `bytes` is 0
+__device__ __forceinline__ void cp_async(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void ldsm(uint32_t (&r)[4], uint32_t a) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
+}
+__device__ __forceinline__ void ldsm_t(uint32_t (&r)[4], uint32_t a) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
+}
+__device__ __forceinline__ uint32_t transpose8(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+template <bool BF>
+__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                    uint32_t b1) {
+  if constexpr (BF) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
+                 "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  } else {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+                 "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  }
+}
+__device__ __forceinline__ float exp2_fast(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+template <bool BF>
+__device__ __forceinline__ uint32_t pack(float lo, float hi) {
+  uint32_t r;
+  if constexpr (BF) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  else asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two) {
+  uint32_t r;
+  asm("{ .reg .b16 h, u; mov.b32 {h, u}, %1; cvt.rn.f16x2.e4m3x2 %0, h; }" : "=r"(r) : "r"(two));
+  return r;
+}
+__device__ __forceinline__ float load_q(const uint16_t* p, int type) {
+  const uint16_t u = __ldg(p);
+  return type == kBf16 ? __uint_as_float((uint32_t)u << 16) : __half2float(__ushort_as_half(u));
+}
+
+// 16-byte chunk `c` of row `r`, placed so that the eight rows of a matrix load
+// (and of its transpose) fall on different banks.
+template <int kRow>
+__device__ __forceinline__ uint32_t place(int r, int c) {
+  constexpr int kChunks = kRow / 16;
+  if constexpr (kChunks >= 8) return (uint32_t)(r * kRow + ((c ^ (r & 7)) << 4));
+  else return (uint32_t)(r * kRow + ((c ^ ((r >> 1) & 3)) << 4));
+}
+
+// What is attended to of a request: keys [lo, len), as `span` virtual keys
+// from `base` on (a multiple of 16).  With a page list the virtual keys are
+// the listed pages' rows.
+struct Row {
+  int len, lo, base, span;
+};
+
+__device__ __forceinline__ Row row_of(const Params& P, int r, uint32_t& bad) {
+  Row w;
+  const int room = P.width << P.shift;
+  w.len = __ldg(P.lens + r);
+  if (w.len < 0) w.len = 0, bad |= kErrLength;
+  if (w.len > room) w.len = room, bad |= kErrLength;
+  w.lo = P.window ? max(0, w.len - P.window) : 0;
+  if (P.pages) {
+    w.base = 0;
+    w.span = w.len > 0 ? P.keep << P.shift : 0;
+  } else {
+    w.base = w.lo & ~15;
+    w.span = w.len - w.base;
+  }
+  return w;
+}
+
+template <class S>
+__device__ __forceinline__ int tiles_of(const Row& w) {
+  return (w.span + S::kKeys - 1) / S::kKeys;
+}
+
+// Finds the items that a warp's tiles belong to and where their keys lie.
+template <class S>
+struct Cursor {
+  int r, sub;            // request; KV head * row_tiles + row tile
+  int begin, end, tiles; // the item's indices in the (padded) list, its real tiles
+  Row row;
+
+  // Moves to the item of index t (t never decreases).
+  __device__ __forceinline__ void seek(const Params& P, const int* prefix, int t, uint32_t& bad) {
+    if (t < end) return;
+    const int per = P.kv_heads * P.row_tiles;
+    bool moved = false;
+    while (t >= prefix[r + 1] * per) ++r, moved = true;
+    if (moved) {
+      row = row_of(P, r, bad);
+      tiles = tiles_of<S>(row);
+    }
+    const int padded = prefix[r + 1] - prefix[r];
+    sub = (t - prefix[r] * per) / padded;
+    begin = prefix[r] * per + sub * padded;
+    end = begin + padded;
+  }
+};
+
+// One 16-key subtile's source: the byte offset of its first row (both caches),
+// and the first key's position (or a position past the end where nothing is read).
+struct Source {
+  long long at;
+  int pos;
+};
+
+template <class S>
+__device__ __forceinline__ Source source_of(const Params& P, const Cursor<S>& c, int tile, int s,
+                                            uint32_t& bad) {
+  Source o;
+  o.at = 0;
+  o.pos = INT32_MAX - 64;
+  const int j = c.row.base + tile * S::kKeys + s * 16;
+  const int head = c.sub / P.row_tiles;
+  int lp = j >> P.shift;
+  if (P.pages) {
+    if (j >= c.row.span) return o;
+    const int listed = __ldg(P.pages + ((size_t)c.r * P.kv_heads + head) * P.keep + lp);
+    if (listed < 0 || listed >= (c.row.len + (1 << P.shift) - 1) >> P.shift) {
+      if (listed != -1) bad |= kErrPage;
+      return o;
+    }
+    lp = listed;
+  } else if (j >= c.row.len) {
+    return o;
+  }
+  const int id = __ldg(P.table + (size_t)c.r * P.width + lp);
+  if (id < 0 || id >= P.num_pages) {
+    bad |= kErrPage;
+    return o;
+  }
+  const int in = j & ((1 << P.shift) - 1);
+  o.pos = (lp << P.shift) + in;
+  o.at = ((((long long)id * P.kv_heads + head) << P.shift) + in) * S::kRow;
+  return o;
+}
+
+// Copies one subtile's K and V rows; rows outside [lo, len) become zeros, so
+// that whatever an unwritten row holds meets no weight.
+template <class S>
+__device__ __forceinline__ void copy_subtile(const Params& P, const Source& o, const Row& row,
+                                             uint32_t k_dst, uint32_t v_dst) {
+  constexpr int kChunks = S::kRow / 16;
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int i = 0; i < 16 * kChunks / 32; ++i) {
+    const int n = i * 32 + lane, rr = n / kChunks, cc = n % kChunks;
+    const int pos = o.pos + rr;
+    const int bytes = pos >= row.lo && pos < row.len ? 16 : 0;
+    const long long off = o.at + (bytes ? rr * S::kRow + cc * 16 : 0);
+    cp_async(k_dst + place<S::kRow>(rr, cc), P.k + off, bytes);
+    cp_async(v_dst + place<S::kRow>(rr, cc), P.v + off, bytes);
+  }
+}
+
+// ---- the kernel -----------------------------------------------------------
+template <class S>
+__global__ void __launch_bounds__(S::kThreads, 1) attend_kernel(const Params P) {
+  constexpr int D = S::D, NT = S::NT, kMt = S::kMt, kWarps = S::kWarps;
+  constexpr bool kBf = S::CT == kBf16, k8 = S::CT == kE4m3;
+  extern __shared__ __align__(1024) unsigned char smem[];
+  float* s_sum = reinterpret_cast<float*>(smem + S::kPipe);
+  float* s_ml = reinterpret_cast<float*>(smem + S::kPipe + S::kSum);
+  int* s_pos = reinterpret_cast<int*>(smem + S::kPipe + S::kSum + S::kMl);
+  int* s_prefix = s_pos + S::kPos / 4;
+  __shared__ int s_scan[kWarps + 1];
+  __shared__ int s_flag;
+  const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+  const int g = lane >> 2, t4 = lane & 3;
+  const int per = P.kv_heads * P.row_tiles;
+  uint32_t bad = 0;
+
+  // ---- shares: U tiles per CTA ----
+  // Few rows: each row is padded to whole shares, so that a CTA holds one
+  // piece of one row.  Many rows: one list cut into equal shares, whatever the
+  // lengths are.
+  constexpr int kPer = kMaxRequests / S::kThreads;
+  int mine[kPer], sum = 0, rows = 0;
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    const int r = tid * kPer + j;
+    mine[j] = 0;
+    if (r < P.requests) mine[j] = tiles_of<S>(row_of(P, r, bad));
+    sum += mine[j];
+    rows += mine[j] > 0;
+  }
+  if (blockIdx.x == 0 && bad) atomicOr(P.err, bad);
+  bad = 0;
+  auto block_sum = [&](int v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    __syncthreads();
+    if (lane == 0) s_scan[wid] = v;
+    __syncthreads();
+    int all = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) all += s_scan[w];
+    return all;
+  };
+  const int grid = (int)gridDim.x;
+  const long long total = (long long)block_sum(sum) * per;
+  const int items = block_sum(rows) * per;
+  constexpr int kLeast = kWarps;            // tiles: one per warp
+  const bool whole = items * 2 <= grid;
+  int U = (int)((total + grid - 1) / grid);
+  if (whole) U = (int)((total + (grid - items) - 1) / (grid - items));
+  U = max(U, kLeast);
+  // prefix of the (padded) tiles of a request's one item
+  {
+    int run = 0;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      if (whole) mine[j] = (mine[j] + U - 1) / U * U;
+      run += mine[j];
+    }
+    int in = run;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, in, o);
+      if (lane >= o) in += u;
+    }
+    __syncthreads();
+    if (lane == 31) s_scan[wid] = in;
+    __syncthreads();
+    int at = in - run;
+    for (int w = 0; w < wid; ++w) at += s_scan[w];
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const int r = tid * kPer + j;
+      if (r <= P.requests) s_prefix[r] = at;
+      at += mine[j];
+    }
+    if (tid == S::kThreads - 1 && P.requests == kMaxRequests) s_prefix[kMaxRequests] = at;
+  }
+  __syncthreads();
+  const long long all = (long long)s_prefix[P.requests] * per;
+
+  // rows with nothing to read
+  for (int r = blockIdx.x; r < P.requests; r += grid) {
+    if (s_prefix[r + 1] != s_prefix[r]) continue;
+    uint4* o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(P.out) + (size_t)r * P.heads * D);
+    for (int i = tid; i < P.heads * D / 8; i += S::kThreads) o[i] = make_uint4(0, 0, 0, 0);
+    if (P.lse)
+      for (int i = tid; i < P.heads; i += S::kThreads)
+        P.lse[(size_t)r * P.heads + i] = P.sinks ? P.sinks[i] : -INFINITY;
+  }
+
+  const long long c0 = (long long)blockIdx.x * U, c1 = min(c0 + U, all);
+  if (c0 >= all) return;
+
+  // ---- this warp's pipeline ----
+  const uint32_t pipe = smem_addr(smem) + wid * S::kStages * S::kTile;
+  Cursor<S> pc;            // where the copies are
+  {
+    int lo = 0, hi = P.requests - 1;
+    while (lo < hi) {       // the request of c0
+      const int mid = (lo + hi + 1) >> 1;
+      if ((long long)s_prefix[mid] * per <= c0) lo = mid; else hi = mid - 1;
+    }
+    while (s_prefix[lo + 1] == s_prefix[lo]) ++lo;
+    pc.r = lo;
+    pc.row = row_of(P, lo, bad);
+    pc.tiles = tiles_of<S>(pc.row);
+    pc.end = 0;
+  }
+  Cursor<S> cc = pc;       // where the products are
+  int pt = (int)c0 + wid;  // next tile to copy
+  Source src[kMt];
+  bool have = false;       // the next tile exists and is not padding
+  auto look = [&]() {      // finds the next tile to copy and asks for its page ids
+    have = pt < c1;
+    if (have) {
+      pc.seek(P, s_prefix, pt, bad);
+      have = pt - pc.begin < pc.tiles;
+    }
+    if (have) {
+#pragma unroll
+      for (int s = 0; s < kMt; ++s) src[s] = source_of<S>(P, pc, pt - pc.begin, s, bad);
+    }
+  };
+  int in_stage = 0, out_stage = 0;
+  auto issue = [&]() {
+    if (have) {
+      const uint32_t base = pipe + in_stage * S::kTile;
+#pragma unroll
+      for (int s = 0; s < kMt; ++s)
+        copy_subtile<S>(P, src[s], pc.row, base + s * 16 * S::kRow,
+                        base + (S::kKeys + s * 16) * S::kRow);
+      // the positions of the stage's keys, for the mask
+      if (lane < kMt)
+        s_pos[(wid * S::kStages + in_stage) * kMt + lane] = lane ? src[kMt - 1].pos : src[0].pos;
+    }
+    cp_commit();
+    in_stage = in_stage + 1 == S::kStages ? 0 : in_stage + 1;
+    pt += kWarps;
+    look();
+  };
+  look();
+#pragma unroll 1
+  for (int i = 0; i < S::kStages - 1; ++i) issue();
+
+  // ---- pieces: the rows (or parts of rows) of this share ----
+  int t = (int)c0 + wid;
+  for (int p0 = (int)c0; p0 < c1;) {
+    cc.seek(P, s_prefix, p0, bad);
+    const int p1 = min((int)c1, cc.end);
+    const int real = min(p1, cc.begin + cc.tiles);     // tiles beyond are padding
+    const int kvh = cc.sub / P.row_tiles, row0 = (cc.sub % P.row_tiles) * S::kRows;
+    const int rows_here = min(S::kRows, P.group - row0);
+    const int head0 = kvh * P.group + row0;
+
+    // the query's fragments: head g of each tile of eight, two coordinates a register
+    uint32_t qf[NT][D / 16][2];
+    float fac[NT][2];
+    {
+      const float ks = k8 ? __ldg(P.k_scale + kvh) : 1.f;
+      const float base = P.scale * ks * kLog2e;
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const int h = n * 8 + g;
+        const uint16_t* q = static_cast<const uint16_t*>(P.q) + cc.r * P.q_request +
+                            (long long)(head0 + (h < rows_here ? h : 0)) * P.q_head;
+        if constexpr (!k8) {
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const uint16_t* at = q + k * 16 + i * 8 + 2 * t4;
+              qf[n][k][i] = (uint32_t)__ldg(at) | (uint32_t)__ldg(at + 1) << 16;
+            }
+          fac[n][0] = fac[n][1] = base;
+        } else {
+          // q as fp16: a power of two brings the head's largest value to [1, 2),
+          // which keeps every bit of it (what underflows is 2^-24 of the largest)
+          float top = 0.f;
+          float f[D / 16][4];
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              f[k][i] = load_q(q + k * 16 + 4 * t4 + i, P.q_type);
+              top = fmaxf(top, fabsf(f[k][i]));
+            }
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+          const int e = floor_log2_held(top);
+          const float down = two_to(-e);
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            qf[n][k][0] = pack<false>(f[k][0] * down, f[k][1] * down);
+            qf[n][k][1] = pack<false>(f[k][2] * down, f[k][3] * down);
+          }
+          const float up = two_to(e);
+          fac[n][0] = base * __shfl_sync(0xffffffffu, up, 8 * t4);
+          fac[n][1] = base * __shfl_sync(0xffffffffu, up, 8 * t4 + 4);
+        }
+      }
+    }
+
+    float o[D / 16][NT][4], m[NT][2], l[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      m[n][0] = m[n][1] = -INFINITY;
+      l[n][0] = l[n][1] = 0.f;
+#pragma unroll
+      for (int d = 0; d < D / 16; ++d)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[d][n][i] = 0.f;
+    }
+
+#pragma unroll 1
+    for (; t < p1; t += kWarps) {
+      cp_wait<S::kStages - 2>();
+      __syncwarp();
+      issue();          // into the stage that the previous tile left
+      const uint32_t ks = pipe + out_stage * S::kTile, vs = ks + S::kKeys * S::kRow;
+      const int* pos = s_pos + (wid * S::kStages + out_stage) * kMt;
+      out_stage = out_stage + 1 == S::kStages ? 0 : out_stage + 1;
+      if (t >= real) continue;
+      if (pos[0] >= cc.row.len && pos[kMt - 1] >= cc.row.len) continue;   // no page there
+
+      // S^T = K Q^T
+      float sc[kMt][NT][4];
+#pragma unroll
+      for (int s = 0; s < kMt; ++s)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) sc[s][n][i] = 0.f;
+#pragma unroll
+      for (int s = 0; s < kMt; ++s) {
+        const uint32_t kb = ks + s * 16 * S::kRow;
+        if constexpr (!k8) {
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) {
+            uint32_t a[4];
+            ldsm(a, kb + place<S::kRow>(lane & 15, 2 * k + (lane >> 4)));
+#pragma unroll
+            for (int n = 0; n < NT; ++n) mma<kBf>(sc[s][n], a, qf[n][k][0], qf[n][k][1]);
+          }
+        } else {
+#pragma unroll
+          for (int k = 0; k < D / 32; ++k) {
+            uint32_t b[4];      // rows 0-7 and 8-15 of 16 coordinates, then of the next 16
+            ldsm(b, kb + place<S::kRow>(lane & 15, 2 * k + (lane >> 4)));
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const uint32_t a[4] = {e4m3x2_to_f16x2(b[2 * j]), e4m3x2_to_f16x2(b[2 * j + 1]),
+                                     e4m3x2_to_f16x2(b[2 * j] >> 16),
+                                     e4m3x2_to_f16x2(b[2 * j + 1] >> 16)};
+#pragma unroll
+              for (int n = 0; n < NT; ++n)
+                mma<false>(sc[s][n], a, qf[n][2 * k + j][0], qf[n][2 * k + j][1]);
+            }
+          }
+        }
+      }
+
+      // logits in units of log2, masked
+      bool seen[kMt][2];
+#pragma unroll
+      for (int s = 0; s < kMt; ++s) {
+        const int at = pos[s] + g;
+        seen[s][0] = at >= cc.row.lo && at < cc.row.len;
+        seen[s][1] = at + 8 >= cc.row.lo && at + 8 < cc.row.len;
+      }
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        float top[2] = {m[n][0], m[n][1]};
+#pragma unroll
+        for (int s = 0; s < kMt; ++s)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            sc[s][n][i] = seen[s][i >> 1] ? sc[s][n][i] * fac[n][i & 1] : -INFINITY;
+            top[i & 1] = fmaxf(top[i & 1], sc[s][n][i]);
+          }
+#pragma unroll
+        for (int x = 4; x < 32; x <<= 1) {
+          top[0] = fmaxf(top[0], __shfl_xor_sync(0xffffffffu, top[0], x));
+          top[1] = fmaxf(top[1], __shfl_xor_sync(0xffffffffu, top[1], x));
+        }
+        // the running maximum moves seldom: rescale only then
+        if (__any_sync(0xffffffffu, top[0] > m[n][0] || top[1] > m[n][1])) {
+          const float a0 = exp2_fast(m[n][0] - (top[0] == -INFINITY ? 0.f : top[0]));
+          const float a1 = exp2_fast(m[n][1] - (top[1] == -INFINITY ? 0.f : top[1]));
+          l[n][0] *= a0;
+          l[n][1] *= a1;
+#pragma unroll
+          for (int d = 0; d < D / 16; ++d) {
+            o[d][n][0] *= a0;
+            o[d][n][1] *= a1;
+            o[d][n][2] *= a0;
+            o[d][n][3] *= a1;
+          }
+          m[n][0] = top[0];
+          m[n][1] = top[1];
+        }
+        const float r0 = m[n][0] == -INFINITY ? 0.f : m[n][0];
+        const float r1 = m[n][1] == -INFINITY ? 0.f : m[n][1];
+#pragma unroll
+        for (int s = 0; s < kMt; ++s) {
+          sc[s][n][0] = exp2_fast(sc[s][n][0] - r0);
+          sc[s][n][1] = exp2_fast(sc[s][n][1] - r1);
+          sc[s][n][2] = exp2_fast(sc[s][n][2] - r0);
+          sc[s][n][3] = exp2_fast(sc[s][n][3] - r1);
+          l[n][0] += sc[s][n][0] + sc[s][n][2];
+          l[n][1] += sc[s][n][1] + sc[s][n][3];
+        }
+      }
+
+      // O^T += V^T P^T, the weights rounded to the products' type
+#pragma unroll
+      for (int s = 0; s < kMt; ++s) {
+        uint32_t pf[NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          pf[n][0] = transpose8(pack<kBf>(sc[s][n][0], sc[s][n][1]));
+          pf[n][1] = transpose8(pack<kBf>(sc[s][n][2], sc[s][n][3]));
+        }
+        const uint32_t vb = vs + s * 16 * S::kRow;
+        if constexpr (!k8) {
+#pragma unroll
+          for (int d = 0; d < D / 16; ++d) {
+            uint32_t a[4];
+            ldsm_t(a, vb + place<S::kRow>((lane & 7) + ((lane >> 4) << 3),
+                                          2 * d + ((lane >> 3) & 1)));
+#pragma unroll
+            for (int n = 0; n < NT; ++n) mma<kBf>(o[d][n], a, pf[n][0], pf[n][1]);
+          }
+        } else {
+          // a transposed pair of bytes is coordinates 2g and 2g + 1 of two keys:
+          // row g of the tile takes the even ones, row g + 8 the odd ones
+#pragma unroll
+          for (int d = 0; d < D / 32; ++d) {
+            uint32_t b[4];
+            ldsm_t(b, vb + place<S::kRow>(lane & 15, 2 * d + (lane >> 4)));
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const uint32_t x = __byte_perm(b[2 * j], 0, 0x3120);
+              const uint32_t y = __byte_perm(b[2 * j + 1], 0, 0x3120);
+              const uint32_t a[4] = {e4m3x2_to_f16x2(x), e4m3x2_to_f16x2(x >> 16),
+                                     e4m3x2_to_f16x2(y), e4m3x2_to_f16x2(y >> 16)};
+#pragma unroll
+              for (int n = 0; n < NT; ++n) mma<false>(o[2 * d + j][n], a, pf[n][0], pf[n][1]);
+            }
+          }
+        }
+      }
+    }
+
+    // ---- the warps' states into one ----
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int x = 4; x < 32; x <<= 1) l[n][i] += __shfl_xor_sync(0xffffffffu, l[n][i], x);
+    if (g == 0) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int h = n * 8 + 2 * t4 + i;
+          s_ml[wid * S::kRows + h] = m[n][i];
+          s_ml[(kWarps + wid) * S::kRows + h] = l[n][i];
+        }
+    }
+    __syncthreads();
+    float mine_f[NT][2];      // this warp's factor per column
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int h = n * 8 + 2 * t4 + i;
+        float top = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_ml[w * S::kRows + h]);
+        mine_f[n][i] = m[n][i] == -INFINITY ? 0.f : exp2_fast(m[n][i] - top);
+      }
+    const int first_cta = cc.begin / U;
+    const int pieces = (cc.begin + cc.tiles - 1) / U - first_cta + 1;
+    const bool alone = pieces == 1;
+    const size_t slot = (size_t)blockIdx.x * 2 + (p0 == c0 ? 0 : 1);
+    float* po = P.part_o + slot * 16 * D;
+    float* pml = P.part_ml + slot * 32;
+    // a row's maximum and sum over the warps
+    auto row_state = [&](int h, float& top, float& den) {
+      top = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_ml[w * S::kRows + h]);
+      den = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float mw = s_ml[w * S::kRows + h];
+        if (mw != -INFINITY) den += s_ml[(kWarps + w) * S::kRows + h] * exp2_fast(mw - top);
+      }
+    };
+    // out = sum * final_scale(h): the sink joins the denominator here
+    auto finish = [&](int h, float top, float den, float& mul, float& lse) {
+      const float vs = k8 ? __ldg(P.v_scale + kvh) : 1.f;
+      float ref = top;
+      if (P.sinks) {
+        const float sink = __ldg(P.sinks + head0 + h) * kLog2e;
+        ref = fmaxf(top, sink);
+        const float down = top == -INFINITY ? 0.f : exp2_fast(top - ref);
+        den = den * down + (sink == -INFINITY ? 0.f : exp2_fast(sink - ref));
+        mul = den == 0.f ? 0.f : vs * down / den;
+      } else {
+        mul = den == 0.f ? 0.f : vs / den;
+      }
+      lse = ref == -INFINITY ? -INFINITY : (ref + log2f(den)) * kLn2;
+    };
+    auto store_out = [&](int h, int d, float a, float b) {
+      uint32_t* at = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(P.out) +
+                                                 ((size_t)cc.r * P.heads + head0 + h) * D + d);
+      *at = P.q_type == kBf16 ? pack<true>(a, b) : pack<false>(a, b);
+    };
+    if (tid < S::kRows) {
+      float top, den;
+      row_state(tid, top, den);
+      if (!alone) {
+        pml[tid] = top;
+        pml[16 + tid] = den;
+      } else if (tid < rows_here && P.lse) {
+        float mul, lse;
+        finish(tid, top, den, mul, lse);
+        P.lse[(size_t)cc.r * P.heads + head0 + tid] = lse;
+      }
+    }
+#pragma unroll
+    for (int c = 0; c < D / S::kChunk; ++c) {
+      constexpr int kDt = S::kChunk / 16;
+#pragma unroll
+      for (int dd = 0; dd < kDt; ++dd)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int h = n * 8 + 2 * t4 + (i & 1);
+            const int d = dd * 16 + (k8 ? 2 * g + (i >> 1) : g + 8 * (i >> 1));
+            s_sum[(wid * S::kRows + h) * S::kPitch + d] =
+                o[c * kDt + dd][n][i] * mine_f[n][i & 1];
+          }
+      __syncthreads();
+      for (int e = tid; e < S::kRows * S::kChunk / 2; e += S::kThreads) {
+        const int h = e / (S::kChunk / 2), d = e % (S::kChunk / 2) * 2;
+        float a = 0.f, b = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          const float2 v =
+              *reinterpret_cast<const float2*>(s_sum + (w * S::kRows + h) * S::kPitch + d);
+          a += v.x;
+          b += v.y;
+        }
+        if (!alone) {
+          *reinterpret_cast<float2*>(po + h * D + c * S::kChunk + d) = make_float2(a, b);
+        } else if (h < rows_here) {
+          float top, den, mul, lse;
+          row_state(h, top, den);
+          finish(h, top, den, mul, lse);
+          store_out(h, c * S::kChunk + d, a * mul, b * mul);
+        }
+      }
+      __syncthreads();
+    }
+    if (!alone) {
+      // ---- join: the last piece to arrive sums all of them, in order ----
+      if (tid == 0) {
+        __threadfence();
+        const int item = cc.r * per + cc.sub;
+        const uint32_t before = atomicAdd(P.arrived + item, 1u);
+        s_flag = before + 1 == (uint32_t)pieces;
+        if (s_flag) P.arrived[item] = 0;      // for the next launch
+        __threadfence();
+      }
+      __syncthreads();
+      if (s_flag) {
+        // the slot of a piece: a CTA's first piece unless the row began inside it
+        auto slot_of = [&](int p) {
+          const int cta = first_cta + p;
+          return (size_t)cta * 2 + ((long long)cta * U >= cc.begin ? 0 : 1);
+        };
+        float* wgt = s_sum;                    // [pieces][kRows]
+        if (wid < kWarps) {
+          for (int h = wid; h < rows_here; h += kWarps) {
+            float top = -INFINITY;
+            for (int p = lane; p < pieces; p += 32)
+              top = fmaxf(top, __ldcg(P.part_ml + slot_of(p) * 32 + h));
+#pragma unroll
+            for (int x = 16; x > 0; x >>= 1)
+              top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+            float den = 0.f;
+            for (int p = lane; p < pieces; p += 32) {
+              const float mp = __ldcg(P.part_ml + slot_of(p) * 32 + h);
+              const float w = mp == -INFINITY ? 0.f : exp2_fast(mp - top);
+              wgt[p * S::kRows + h] = w;
+              den += w * __ldcg(P.part_ml + slot_of(p) * 32 + 16 + h);
+            }
+#pragma unroll
+            for (int x = 16; x > 0; x >>= 1) den += __shfl_xor_sync(0xffffffffu, den, x);
+            float mul, lse;
+            finish(h, top, den, mul, lse);
+            if (lane == 0) {
+              s_ml[h] = mul;
+              if (P.lse) P.lse[(size_t)cc.r * P.heads + head0 + h] = lse;
+            }
+          }
+        }
+        __syncthreads();
+        for (int e = tid; e < rows_here * D / 4; e += S::kThreads) {
+          const int h = e / (D / 4), d = e % (D / 4) * 4;
+          float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+          for (int p = 0; p < pieces; ++p) {
+            const float4 v =
+                __ldcg(reinterpret_cast<const float4*>(P.part_o + slot_of(p) * 16 * D + h * D + d));
+            const float w = wgt[p * S::kRows + h];
+            acc.x += w * v.x;
+            acc.y += w * v.y;
+            acc.z += w * v.z;
+            acc.w += w * v.w;
+          }
+          const float mul = s_ml[h];
+          store_out(h, d, acc.x * mul, acc.y * mul);
+          store_out(h, d + 2, acc.z * mul, acc.w * mul);
+        }
+      }
+      __syncthreads();
+    }
+    p0 = p1;
+  }
+  if (bad) atomicOr(P.err, bad);
+}
+
+template <class S>
+cudaError_t configure() {
+  return cudaFuncSetAttribute(attend_kernel<S>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              S::kSmem);
+}
+template <class S>
+void launch(const Params& P, const moe_reader_kv& kv, const moe_reader_kv_attend_args& a,
+            cudaStream_t s) {
+  // one CTA per SM, fewer where even full tables cannot fill them
+  const long long keys = (long long)(a.pages ? a.keep : a.width) << P.shift;
+  const long long tiles = (keys + S::kKeys - 1) / S::kKeys * a.requests * P.kv_heads * P.row_tiles;
+  const int grid = (int)std::min<long long>(kv.sms, (tiles + S::kWarps - 1) / S::kWarps);
+  attend_kernel<S><<<grid, S::kThreads, S::kSmem, s>>>(P);
+}
+
+// Tiles of eight query heads per item: both where the group has more than eight
+// heads and the accumulators of 16 fit the registers (D <= 128).
+int head_tiles(const moe_reader_kv_config& c) {
+  const int group = c.num_q_heads / c.num_kv_heads;
+  return group > 8 && c.head_dim <= 128 ? 2 : 1;
+}
+
+// Calls f with the Shape of a handle.
+template <class F>
+auto with_shape(const moe_reader_kv_config& c, F f) {
+  const int nt = head_tiles(c);
+  auto typed = [&](auto d, auto n) {
+    constexpr int D = decltype(d)::value, N = decltype(n)::value;
+    switch (c.cache_type) {
+      case kBf16: return f(Shape<D, N, kBf16>{});
+      case kF16: return f(Shape<D, N, kF16>{});
+      default: return f(Shape<D, N, kE4m3>{});
+    }
+  };
+  using I64 = std::integral_constant<int, 64>;
+  using I128 = std::integral_constant<int, 128>;
+  using I256 = std::integral_constant<int, 256>;
+  using One = std::integral_constant<int, 1>;
+  using Two = std::integral_constant<int, 2>;
+  if (c.head_dim == 64) return nt == 1 ? typed(I64{}, One{}) : typed(I64{}, Two{});
+  if (c.head_dim == 128) return nt == 1 ? typed(I128{}, One{}) : typed(I128{}, Two{});
+  return typed(I256{}, One{});
+}
+
+}  // namespace
+
+int attend_row_tiles(const moe_reader_kv_config& c) {
+  const int rows = 8 * head_tiles(c);
+  return (c.num_q_heads / c.num_kv_heads + rows - 1) / rows;
+}
+
+cudaError_t configure_kv_attend(const moe_reader_kv& kv) {
+  return with_shape(kv.cfg, [](auto s) { return configure<decltype(s)>(); });
+}
+
+cudaError_t launch_kv_attend(const moe_reader_kv& kv, const moe_reader_kv_attend_args& a,
+                             cudaStream_t s) {
+  Params P;
+  P.q = a.q;
+  P.table = a.table;
+  P.lens = a.lens;
+  P.pages = a.pages;
+  P.sinks = a.sinks;
+  P.out = a.out;
+  P.lse = a.lse;
+  P.q_request = a.q_request_stride;
+  P.q_head = a.q_head_stride;
+  P.q_type = a.q_type;
+  P.requests = a.requests;
+  P.width = a.width;
+  P.keep = a.keep;
+  P.window = a.window;
+  P.scale = a.scale;
+  P.k = static_cast<const char*>(kv.k);
+  P.v = static_cast<const char*>(kv.v);
+  P.k_scale = kv.k_scale;
+  P.v_scale = kv.v_scale;
+  P.heads = kv.cfg.num_q_heads;
+  P.kv_heads = kv.cfg.num_kv_heads;
+  P.group = kv.group;
+  P.row_tiles = attend_row_tiles(kv.cfg);
+  P.shift = kv.page_shift;
+  P.num_pages = kv.cfg.num_pages;
+  P.part_o = kv.part_o;
+  P.part_ml = kv.part_ml;
+  P.arrived = kv.arrived;
+  P.err = kv.err;
+  with_shape(kv.cfg, [&](auto sh) { launch<decltype(sh)>(P, kv, a, s); return 0; });
+  return cudaGetLastError();
+}
+
+}  // namespace mr

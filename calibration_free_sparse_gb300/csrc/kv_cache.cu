@@ -1,0 +1,608 @@
+// The paged key/value cache: its handle and argument checks, the page plan of
+// a step, and the append of new rows with the summaries of their pages.
+#include <stdlib.h>
+#include <string.h>
+
+#include <algorithm>
+
+#include "device_util.cuh"
+#include "internal.cuh"
+#include "kv.cuh"
+
+namespace mr {
+namespace {
+
+// ---------------------------------------------------------------------------
+// plan
+// ---------------------------------------------------------------------------
+constexpr int kPlanThreads = 256;
+constexpr int kPlanPer = kMaxRequests / kPlanThreads;   // requests per thread of the scan
+
+__device__ __forceinline__ long long warp_scan(long long v) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long u = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += u;
+  }
+  return v;
+}
+
+// Largest r with at[r] <= i, at ascending with at[0] = 0 (entries may repeat:
+// the last of equals holds i).
+__device__ __forceinline__ int find_request(const int* at, int n, int i) {
+  int lo = 0, hi = n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (at[mid] <= i) lo = mid; else hi = mid - 1;
+  }
+  return lo;
+}
+
+// Every CTA scans the lengths itself (two prefix sums over at most 1024
+// requests: new tokens and missing pages), then takes its share of the tokens
+// and of the fresh table entries: one launch and no hand-off between CTAs.  A
+// token whose page is fresh takes its id from free_pages, not from the table
+// that another CTA is writing.
+__global__ void __launch_bounds__(kPlanThreads)
+plan_kernel(moe_reader_kv_plan_args a, int shift, int num_pages, uint32_t* err) {
+  __shared__ int s_start[kMaxRequests], s_page[kMaxRequests];
+  __shared__ int s_prev[kMaxRequests], s_have[kMaxRequests];
+  __shared__ long long w_tok[kPlanThreads / 32], w_page[kPlanThreads / 32];
+  const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+  const int ps = 1 << shift;
+  const long long room = (long long)a.width << shift;     // tokens a table row can hold
+  uint32_t bad = 0;
+
+  int prev[kPlanPer], add[kPlanPer], have[kPlanPer], need[kPlanPer];
+  long long tok = 0, pages = 0;
+#pragma unroll
+  for (int j = 0; j < kPlanPer; ++j) {
+    const int r = tid * kPlanPer + j;
+    prev[j] = add[j] = have[j] = need[j] = 0;
+    if (r >= a.requests) continue;
+    int p = __ldg(a.prev_lens + r), n = __ldg(a.new_lens + r);
+    if (p < 0 || n < 0) bad |= kErrLength;
+    p = max(p, 0);
+    n = max(n, 0);
+    if (p > room) p = (int)room, bad |= kErrLength;
+    if ((long long)p + n > room) n = (int)(room - p), bad |= kErrLength;
+    prev[j] = p;
+    add[j] = n;
+    have[j] = (int)(((long long)p + ps - 1) >> shift);
+    need[j] = (int)(((long long)p + n + ps - 1) >> shift) - have[j];
+    tok += n;
+    pages += need[j];
+  }
+  const long long tok_in = warp_scan(tok), page_in = warp_scan(pages);
+  if (lane == 31) {
+    w_tok[wid] = tok_in;
+    w_page[wid] = page_in;
+  }
+  __syncthreads();
+  long long t0 = tok_in - tok, p0 = page_in - pages, t_all = 0, p_all = 0;
+#pragma unroll
+  for (int w = 0; w < kPlanThreads / 32; ++w) {
+    if (w < wid) t0 += w_tok[w], p0 += w_page[w];
+    t_all += w_tok[w];
+    p_all += w_page[w];
+  }
+  if (t_all > a.max_tokens) bad |= kErrLength;
+  if (p_all > a.num_free) bad |= kErrPool;
+  const int total = (int)min(t_all, (long long)a.max_tokens);
+  const bool first = blockIdx.x == 0;
+#pragma unroll
+  for (int j = 0; j < kPlanPer; ++j) {
+    const int r = tid * kPlanPer + j;
+    if (r < a.requests) {
+      // sums are held to what an int can index: nothing is looked up beyond
+      s_start[r] = (int)min(t0, (long long)a.max_tokens);
+      s_page[r] = (int)min(p0, (long long)INT32_MAX);
+      s_prev[r] = prev[j];
+      s_have[r] = have[j];
+      if (first) {
+        a.lens[r] = prev[j] + add[j];
+        a.starts[r] = s_start[r];
+      }
+    }
+    t0 += add[j];
+    p0 += need[j];
+  }
+  if (first && tid == 0) {
+    a.starts[a.requests] = total;
+    a.taken[0] = (int)min(p_all, (long long)max(a.num_free, 0));
+    if (bad) atomicOr(err, bad);
+  }
+  __syncthreads();
+
+  const long long stride = (long long)gridDim.x * kPlanThreads;
+  const long long at = (long long)blockIdx.x * kPlanThreads + tid;
+  for (long long i = at; i < min(p_all, (long long)INT32_MAX); i += stride) {
+    const int r = find_request(s_page, a.requests, (int)i);
+    const int id = i < a.num_free ? __ldg(a.free_pages + i) : -1;
+    a.table[(size_t)r * a.width + s_have[r] + ((int)i - s_page[r])] = id;
+  }
+  bad = 0;
+  for (long long i = at; i < a.max_tokens; i += stride) {
+    int slot = -1, pos = -1, r = -1;
+    if (i < total) {
+      r = find_request(s_start, a.requests, (int)i);
+      pos = s_prev[r] + ((int)i - s_start[r]);
+      const int lp = pos >> shift, fresh = lp - s_have[r];
+      int id = -1;
+      if (fresh < 0) {
+        id = __ldg(a.table + (size_t)r * a.width + lp);
+      } else {
+        const long long f = (long long)s_page[r] + fresh;
+        if (f < a.num_free) id = __ldg(a.free_pages + f);
+      }
+      if (id >= 0 && id < num_pages) slot = (id << shift) + (pos & (ps - 1));
+      else if (fresh < 0 || id != -1) bad |= kErrPage;
+    }
+    a.slots[i] = slot;
+    a.positions[i] = pos;
+    a.token_requests[i] = r;
+  }
+  if (bad) atomicOr(err, bad);
+}
+
+// ---------------------------------------------------------------------------
+// append
+// ---------------------------------------------------------------------------
+constexpr int kAppendThreads = 128;
+
+template <int CT> struct Cell { using type = uint16_t; };
+template <> struct Cell<MOE_READER_TYPE_E4M3> { using type = uint8_t; };
+
+__device__ __forceinline__ float widen(uint16_t u, int type) {
+  return type == MOE_READER_TYPE_BF16 ? __uint_as_float((uint32_t)u << 16)
+                                      : __half2float(__ushort_as_half(u));
+}
+__device__ __forceinline__ float widen(uint8_t u, int) {
+  __nv_fp8_e4m3 v;
+  v.__x = u;
+  return (float)v;
+}
+
+// Eight values of a row as the cache stores them.
+template <int CT>
+__device__ __forceinline__ void load_new(const uint16_t* p, bool wide, int type, float scale,
+                                         typename Cell<CT>::type (&out)[8]) {
+  __align__(16) uint16_t in[8];
+  if (wide) {
+    *reinterpret_cast<uint4*>(in) = *reinterpret_cast<const uint4*>(p);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) in[i] = p[i];
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if constexpr (CT == MOE_READER_TYPE_E4M3) {
+      // the conversion saturates at +-448 and keeps NaN
+      out[i] = __nv_cvt_float_to_fp8(__fdiv_rn(widen(in[i], type), scale), __NV_SATFINITE,
+                                     __NV_E4M3);
+    } else {
+      out[i] = in[i];
+    }
+  }
+}
+
+template <typename C>
+__device__ __forceinline__ void store8(C* p, const C (&v)[8]) {
+  if constexpr (sizeof(C) == 2) *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(v);
+  else *reinterpret_cast<uint2*>(p) = *reinterpret_cast<const uint2*>(v);
+}
+template <typename C>
+__device__ __forceinline__ void load8(const C* p, C (&v)[8]) {
+  if constexpr (sizeof(C) == 2) *reinterpret_cast<uint4*>(v) = *reinterpret_cast<const uint4*>(p);
+  else *reinterpret_cast<uint2*>(v) = *reinterpret_cast<const uint2*>(p);
+}
+
+// One CTA takes `window` consecutive tokens of one KV head.  The work is done
+// once per page: by the token that is the last new one of its page, for the
+// run of new tokens that ends with it (their slots are consecutive).  It
+// copies the run's rows and, over the page's rows up to that token -- the
+// older ones read from the cache, the new ones from the input -- forms the
+// largest and smallest key per coordinate, so the summary needs no second
+// pass and no other CTA's writes.  D / 8 lanes share a row, 8 values each.
+template <int D, int CT>
+__global__ void __launch_bounds__(kAppendThreads)
+append_kernel(moe_reader_kv_append_args a, typename Cell<CT>::type* __restrict__ kc,
+              typename Cell<CT>::type* __restrict__ vc, int8_t* __restrict__ codes,
+              float* __restrict__ steps, const float* __restrict__ k_scale,
+              const float* __restrict__ v_scale, int heads, int shift, int num_pages, int window,
+              bool wide_k, bool wide_v, uint32_t* err) {
+  using C = typename Cell<CT>::type;
+  constexpr int kLanes = D / 8;                          // lanes of a row
+  constexpr int kRows = kAppendThreads / kLanes;         // rows at a time
+  constexpr int kWarps = kAppendThreads / 32;
+  __shared__ float s_hi[kWarps][D], s_lo[kWarps][D];
+  __shared__ float s_max[kWarps];
+  const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+  const int head = blockIdx.y, ps = 1 << shift;
+  const int col = (tid % kLanes) * 8, row0 = tid / kLanes;
+  const long long slots_all = (long long)num_pages << shift;
+  float ks = 1.f, vs = 1.f;
+  if constexpr (CT == MOE_READER_TYPE_E4M3) {
+    ks = k_scale[head];
+    vs = v_scale[head];
+  }
+  const uint16_t* kin = static_cast<const uint16_t*>(a.k) + head * a.k_head_stride + col;
+  const uint16_t* vin = static_cast<const uint16_t*>(a.v) + head * a.v_head_stride + col;
+
+  const long long first = (long long)blockIdx.x * window;
+  const int last = (int)min(first + window, (long long)a.tokens);
+  for (int t = (int)first; t < last; ++t) {
+    const int slot = __ldg(a.slots + t);
+    if (slot < 0 || slot >= slots_all) {
+      if (slot != -1 && tid == 0) atomicOr(err, kErrPage);
+      continue;
+    }
+    const int off = slot & (ps - 1);
+    if (off != ps - 1 && t + 1 < a.tokens && __ldg(a.slots + t + 1) == slot + 1) continue;
+    // the run of new tokens that ends here: its first offset in the page
+    int run0 = 0;
+    for (int b = 1; b <= off; b += 32) {
+      const int back = b + lane;
+      const bool in = back <= off && t >= back && __ldg(a.slots + t - back) == slot - back;
+      const uint32_t out = __ballot_sync(0xffffffffu, !in);
+      if (out) {
+        run0 = off - (b + __ffs(out) - 1) + 1;
+        break;
+      }
+    }
+    const size_t page = ((size_t)(slot >> shift) * heads + head) << shift;   // first row
+    float hi[8], lo[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) hi[i] = -INFINITY, lo[i] = INFINITY;
+    const int from = codes ? 0 : run0;
+#pragma unroll 2
+    for (int o = from + row0; o <= off; o += kRows) {
+      __align__(16) C kr[8];
+      C* at = kc + (page + o) * D + col;
+      if (o >= run0) {
+        const long long tt = t - (off - o);
+        __align__(16) C vr[8];
+        load_new<CT>(kin + tt * a.k_token_stride, wide_k, a.type, ks, kr);
+        load_new<CT>(vin + tt * a.v_token_stride, wide_v, a.type, vs, vr);
+        store8(at, kr);
+        store8(vc + (page + o) * D + col, vr);
+      } else {
+        load8(at, kr);
+      }
+      if (codes) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float f = widen(kr[i], CT);
+          hi[i] = fmaxf(hi[i], f);
+          lo[i] = fminf(lo[i], f);
+        }
+      }
+    }
+    if (!codes) continue;
+    // rows of a warp, then the warps
+#pragma unroll
+    for (int o = kLanes; o < 32; o <<= 1)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        hi[i] = fmaxf(hi[i], __shfl_xor_sync(0xffffffffu, hi[i], o));
+        lo[i] = fminf(lo[i], __shfl_xor_sync(0xffffffffu, lo[i], o));
+      }
+    if (lane < kLanes) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        s_hi[wid][lane * 8 + i] = hi[i];
+        s_lo[wid][lane * 8 + i] = lo[i];
+      }
+    }
+    __syncthreads();
+    constexpr int kPer = (D + kAppendThreads - 1) / kAppendThreads;
+    float h[kPer], l[kPer], top = 0.f;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const int d = tid + j * kAppendThreads;
+      h[j] = -INFINITY;
+      l[j] = INFINITY;
+      if (d < D) {
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          h[j] = fmaxf(h[j], s_hi[w][d]);
+          l[j] = fminf(l[j], s_lo[w][d]);
+        }
+        top = fmaxf(top, fmaxf(fabsf(h[j]), fabsf(l[j])));
+      }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if (lane == 0) s_max[wid] = top;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_max[w]);
+    top = fminf(fmaxf(top, two_to(-100)), two_to(100));
+    int e = floor_log2_held(top) - 6;
+    if (top > 127.f * two_to(e)) ++e;
+    const float inv = two_to(-e);
+    const size_t at = (size_t)(slot >> shift) * heads + head;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const int d = tid + j * kAppendThreads;
+      if (d < D) {
+        // a power-of-two step: the quotients are exact, but for those that
+        // underflow, which still round away from zero
+        float up = fminf(fmaxf(ceilf(h[j] * inv), -127.f), 127.f);
+        float down = fminf(fmaxf(floorf(l[j] * inv), -127.f), 127.f);
+        if (h[j] > 0.f) up = fmaxf(up, 1.f);
+        if (l[j] < 0.f) down = fminf(down, -1.f);
+        codes[at * 2 * D + d] = (int8_t)up;
+        codes[at * 2 * D + D + d] = (int8_t)down;
+      }
+    }
+    if (tid == 0) steps[at] = two_to(e);
+    __syncthreads();   // s_hi, s_lo and s_max are free again
+  }
+}
+
+template <int D, int CT>
+void append_as(const moe_reader_kv& kv, const moe_reader_kv_append_args& a, cudaStream_t s) {
+  using C = typename Cell<CT>::type;
+  // A window of one token where that fills the GPU a few times over at most
+  // (a decode step: every token closes its page's run); longer windows keep a
+  // prompt's grid from being mostly CTAs whose token closes nothing.
+  const int heads = kv.cfg.num_kv_heads;
+  const int window = std::min(64, std::max(1, (int)((long long)a.tokens * heads / 4096)));
+  auto wide = [](const void* p, int64_t ts, int64_t hs) {
+    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ts % 8 == 0 && hs % 8 == 0;
+  };
+  const dim3 grid((unsigned)((a.tokens + window - 1) / window), (unsigned)heads);
+  append_kernel<D, CT><<<grid, kAppendThreads, 0, s>>>(
+      a, static_cast<C*>(kv.k), static_cast<C*>(kv.v), kv.codes, kv.steps, kv.k_scale, kv.v_scale,
+      heads, kv.page_shift, kv.cfg.num_pages, window, wide(a.k, a.k_token_stride, a.k_head_stride),
+      wide(a.v, a.v_token_stride, a.v_head_stride), kv.err);
+}
+
+template <int D>
+void append_dim(const moe_reader_kv& kv, const moe_reader_kv_append_args& a, cudaStream_t s) {
+  switch (kv.cfg.cache_type) {
+    case MOE_READER_TYPE_BF16: append_as<D, MOE_READER_TYPE_BF16>(kv, a, s); break;
+    case MOE_READER_TYPE_F16: append_as<D, MOE_READER_TYPE_F16>(kv, a, s); break;
+    default: append_as<D, MOE_READER_TYPE_E4M3>(kv, a, s); break;
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_kv_plan(const moe_reader_kv& kv, const moe_reader_kv_plan_args& a,
+                           cudaStream_t s) {
+  // at least one CTA; enough that a prompt's tokens take a few each
+  const long long tokens = std::max(a.max_tokens, 1);
+  const int grid = (int)std::min<long long>(2LL * kv.sms, (tokens + kPlanThreads - 1) / kPlanThreads);
+  plan_kernel<<<grid, kPlanThreads, 0, s>>>(a, kv.page_shift, kv.cfg.num_pages, kv.err);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_kv_append(const moe_reader_kv& kv, const moe_reader_kv_append_args& a,
+                             cudaStream_t s) {
+  switch (kv.cfg.head_dim) {
+    case 64: append_dim<64>(kv, a, s); break;
+    case 128: append_dim<128>(kv, a, s); break;
+    default: append_dim<256>(kv, a, s); break;
+  }
+  return cudaGetLastError();
+}
+
+}  // namespace mr
+
+// ---------------------------------------------------------------------------
+// C ABI
+// ---------------------------------------------------------------------------
+namespace {
+
+bool at_multiple(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+
+int status_of(cudaError_t e) {
+  if (e == cudaSuccess) return MOE_READER_OK;
+  return e == cudaErrorMemoryAllocation ? MOE_READER_ENOMEM : MOE_READER_ECUDA;
+}
+
+int check_kv_config(const moe_reader_kv_config* c) {
+  if (!c || c->flags != 0) return MOE_READER_EINVAL;
+  if (c->num_kv_heads < 1 || c->num_kv_heads > 1024 || c->num_q_heads < 1)
+    return MOE_READER_EINVAL;
+  if (c->num_q_heads % c->num_kv_heads || c->num_q_heads / c->num_kv_heads > mr::kMaxGroup)
+    return MOE_READER_EINVAL;
+  if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256) return MOE_READER_EINVAL;
+  const int ps = c->page_size;
+  if (ps < 16 || ps > 256 || (ps & (ps - 1))) return MOE_READER_EINVAL;
+  if (c->num_pages < 1 || (long long)c->num_pages * ps >= (1LL << 31)) return MOE_READER_EINVAL;
+  if (c->max_requests < 1 || c->max_requests > mr::kMaxRequests) return MOE_READER_EINVAL;
+  if (c->cache_type != MOE_READER_TYPE_BF16 && c->cache_type != MOE_READER_TYPE_F16 &&
+      c->cache_type != MOE_READER_TYPE_E4M3)
+    return MOE_READER_EINVAL;
+  return MOE_READER_OK;
+}
+
+// Rows and queries have the cache's type; an 8-bit cache takes either 16-bit one.
+bool type_fits(int cache, int type) {
+  if (cache == MOE_READER_TYPE_E4M3)
+    return type == MOE_READER_TYPE_BF16 || type == MOE_READER_TYPE_F16;
+  return type == cache;
+}
+
+// Launches go to the calling thread's device: it has to be the handle's.
+bool on_device(const moe_reader_kv* kv) {
+  int dev = -1;
+  return cudaGetDevice(&dev) == cudaSuccess && dev == kv->device;
+}
+
+int done(moe_reader_kv* kv, cudaError_t e, cudaStream_t s) {
+  if (e != cudaSuccess) return status_of(e);
+  kv->last_stream = s;
+  kv->used = 1;
+  return MOE_READER_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int moe_reader_kv_create(const moe_reader_kv_config* cfg, void* k, void* v, int8_t* codes,
+                         float* steps, const float* k_scale, const float* v_scale, void* stream,
+                         moe_reader_kv_t** out) {
+  if (!out) return MOE_READER_EINVAL;
+  *out = nullptr;
+  const int st = check_kv_config(cfg);
+  if (st != MOE_READER_OK) return st;
+  if (!k || !v || k == v || !at_multiple(k, 256) || !at_multiple(v, 256)) return MOE_READER_EINVAL;
+  if (!codes != !steps || !at_multiple(codes, 16) || !at_multiple(steps, 4))
+    return MOE_READER_EINVAL;
+  const bool e4m3 = cfg->cache_type == MOE_READER_TYPE_E4M3;
+  if (e4m3 != (k_scale != nullptr) || e4m3 != (v_scale != nullptr)) return MOE_READER_EINVAL;
+  if (!at_multiple(k_scale, 4) || !at_multiple(v_scale, 4)) return MOE_READER_EINVAL;
+  moe_reader_kv* kv = static_cast<moe_reader_kv*>(calloc(1, sizeof(moe_reader_kv)));
+  if (!kv) return MOE_READER_ENOMEM;
+  kv->cfg = *cfg;
+  kv->k = k;
+  kv->v = v;
+  kv->codes = codes;
+  kv->steps = steps;
+  kv->k_scale = k_scale;
+  kv->v_scale = v_scale;
+  kv->group = cfg->num_q_heads / cfg->num_kv_heads;
+  while ((1 << kv->page_shift) < cfg->page_size) kv->page_shift++;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaGetDevice(&kv->device);
+  const size_t sms_most = 256;
+  const size_t o_bytes = sms_most * 2 * 16 * cfg->head_dim * sizeof(float);
+  const size_t ml_bytes = sms_most * 2 * 2 * 16 * sizeof(float);
+  const size_t items = (size_t)cfg->max_requests * cfg->num_kv_heads * mr::attend_row_tiles(*cfg);
+  const size_t c_bytes = (items * 4 + 255) & ~(size_t)255;
+  const size_t bytes = o_bytes + ml_bytes + c_bytes + 256;
+  cudaError_t ce = mr::device_alloc(&kv->base, bytes);
+  if (ce != cudaSuccess) {
+    free(kv);
+    return status_of(ce);
+  }
+  char* b = static_cast<char*>(kv->base);
+  kv->part_o = reinterpret_cast<float*>(b);
+  kv->part_ml = reinterpret_cast<float*>(b + o_bytes);
+  kv->arrived = reinterpret_cast<uint32_t*>(b + o_bytes + ml_bytes);
+  kv->err = reinterpret_cast<uint32_t*>(b + o_bytes + ml_bytes + c_bytes);
+  do {
+    if ((ce = cudaDeviceGetAttribute(&kv->sms, cudaDevAttrMultiProcessorCount, kv->device)) !=
+        cudaSuccess)
+      break;
+    kv->sms = std::min<int>(kv->sms, (int)sms_most);
+    if ((ce = mr::configure_kv_attend(*kv)) != cudaSuccess) break;
+    if ((ce = mr::configure_kv_select(*kv)) != cudaSuccess) break;
+    if ((ce = cudaMemsetAsync(kv->base, 0, bytes, s)) != cudaSuccess) break;
+    ce = cudaStreamSynchronize(s);
+  } while (0);
+  if (ce != cudaSuccess) {
+    cudaFree(kv->base);
+    free(kv);
+    return status_of(ce);
+  }
+  *out = kv;
+  return MOE_READER_OK;
+}
+
+int moe_reader_kv_plan(moe_reader_kv_t* kv, const moe_reader_kv_plan_args* a, void* stream) {
+  if (!kv || !a) return MOE_READER_EINVAL;
+  if (a->requests < 0 || a->requests > kv->cfg.max_requests) return MOE_READER_EINVAL;
+  if (a->width < 1 || a->num_free < 0 || a->max_tokens < 0) return MOE_READER_EINVAL;
+  if ((long long)a->width << kv->page_shift >= (1LL << 31)) return MOE_READER_EINVAL;
+  if (!a->starts || !a->taken) return MOE_READER_EINVAL;
+  if (a->requests && (!a->prev_lens || !a->new_lens || !a->table || !a->lens))
+    return MOE_READER_EINVAL;
+  if (a->num_free && !a->free_pages) return MOE_READER_EINVAL;
+  if (a->max_tokens && (!a->slots || !a->positions || !a->token_requests))
+    return MOE_READER_EINVAL;
+  const void* words[] = {a->prev_lens, a->new_lens, a->table, a->free_pages, a->lens, a->starts,
+                         a->slots, a->positions, a->token_requests, a->taken};
+  for (const void* p : words)
+    if (!at_multiple(p, 4)) return MOE_READER_EINVAL;
+  // other CTAs still read the lengths while the first one writes its outputs
+  const void* outs[] = {a->lens, a->starts, a->slots, a->positions, a->token_requests, a->taken,
+                        a->table};
+  for (const void* o : outs)
+    if (o && (o == a->prev_lens || o == a->new_lens || o == a->free_pages))
+      return MOE_READER_EINVAL;
+  if (!on_device(kv)) return MOE_READER_EINVAL;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return done(kv, mr::launch_kv_plan(*kv, *a, s), s);
+}
+
+int moe_reader_kv_append(moe_reader_kv_t* kv, const moe_reader_kv_append_args* a, void* stream) {
+  if (!kv || !a || a->tokens < 0) return MOE_READER_EINVAL;
+  if (!type_fits(kv->cfg.cache_type, a->type)) return MOE_READER_EINVAL;
+  if (a->tokens == 0) return MOE_READER_OK;
+  if (!a->k || !a->v || !a->slots) return MOE_READER_EINVAL;
+  if (!at_multiple(a->k, 2) || !at_multiple(a->v, 2) || !at_multiple(a->slots, 4))
+    return MOE_READER_EINVAL;
+  if (!on_device(kv)) return MOE_READER_EINVAL;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return done(kv, mr::launch_kv_append(*kv, *a, s), s);
+}
+
+int moe_reader_kv_attend(moe_reader_kv_t* kv, const moe_reader_kv_attend_args* a, void* stream) {
+  if (!kv || !a) return MOE_READER_EINVAL;
+  if (a->requests < 0 || a->requests > kv->cfg.max_requests) return MOE_READER_EINVAL;
+  if (!type_fits(kv->cfg.cache_type, a->q_type)) return MOE_READER_EINVAL;
+  if (a->width < 1 || a->window < 0 || (a->pages && a->keep < 1)) return MOE_READER_EINVAL;
+  if ((long long)a->width << kv->page_shift >= (1LL << 31)) return MOE_READER_EINVAL;
+  // the work list is indexed with 32 bits
+  const long long pages = a->pages ? a->keep : a->width;
+  const long long items = (long long)a->requests * kv->cfg.num_kv_heads *
+                          mr::attend_row_tiles(kv->cfg);
+  if (items * (pages << kv->page_shift) >= (1LL << 34)) return MOE_READER_EINVAL;
+  if (a->requests == 0) return MOE_READER_OK;
+  if (!a->q || !a->table || !a->lens || !a->out) return MOE_READER_EINVAL;
+  if (!at_multiple(a->q, 2) || !at_multiple(a->out, 16) || a->q == a->out)
+    return MOE_READER_EINVAL;
+  const void* words[] = {a->table, a->lens, a->pages, a->sinks, a->lse};
+  for (const void* p : words)
+    if (!at_multiple(p, 4)) return MOE_READER_EINVAL;
+  if (!on_device(kv)) return MOE_READER_EINVAL;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return done(kv, mr::launch_kv_attend(*kv, *a, s), s);
+}
+
+int moe_reader_kv_select(moe_reader_kv_t* kv, const moe_reader_kv_select_args* a, void* stream) {
+  if (!kv || !a || !kv->codes) return MOE_READER_EINVAL;
+  if (a->requests < 0 || a->requests > kv->cfg.max_requests) return MOE_READER_EINVAL;
+  if (!type_fits(kv->cfg.cache_type, a->q_type)) return MOE_READER_EINVAL;
+  if (a->width < 1 || a->width > mr::kMaxSelectPages) return MOE_READER_EINVAL;
+  if ((long long)a->width << kv->page_shift >= (1LL << 31)) return MOE_READER_EINVAL;
+  if (a->first < 0 || a->last < 0 || a->keep < 1 ||
+      (long long)a->first + a->last > (long long)a->keep)
+    return MOE_READER_EINVAL;
+  if (a->requests == 0) return MOE_READER_OK;
+  if (!a->q || !a->table || !a->lens || !a->pages) return MOE_READER_EINVAL;
+  if (!at_multiple(a->q, 2) || !at_multiple(a->table, 4) || !at_multiple(a->lens, 4) ||
+      !at_multiple(a->pages, 4))
+    return MOE_READER_EINVAL;
+  if (!on_device(kv)) return MOE_READER_EINVAL;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return done(kv, mr::launch_kv_select(*kv, *a, s), s);
+}
+
+int moe_reader_kv_status(moe_reader_kv_t* kv, uint32_t* bits_out) {
+  if (!kv) return MOE_READER_EINVAL;
+  cudaError_t ce = kv->used ? cudaStreamSynchronize(kv->last_stream) : cudaDeviceSynchronize();
+  if (ce != cudaSuccess) return status_of(ce);
+  uint32_t bits = 0;
+  if ((ce = cudaMemcpy(&bits, kv->err, 4, cudaMemcpyDeviceToHost)) != cudaSuccess)
+    return status_of(ce);
+  if ((ce = cudaMemset(kv->err, 0, 4)) != cudaSuccess) return status_of(ce);
+  if (bits_out) *bits_out = bits;
+  return bits ? MOE_READER_EDEVICE : MOE_READER_OK;
+}
+
+void moe_reader_kv_destroy(moe_reader_kv_t* kv) {
+  if (!kv) return;
+  cudaDeviceSynchronize();
+  cudaFree(kv->base);
+  free(kv);
+}
+
+}  // extern "C"

@@ -1,0 +1,301 @@
+// The norm after a block, its gate, the scaled residual and the norm before
+// the next block in one pass over the rows:
+//   z = y rsqrt(mean y^2 + eps) w_post,  h' = h + scale gate z,
+//   x = h' rsqrt(mean h'^2 + eps) w_pre.
+//
+// Bound by HBM for many rows and by latency for few: a row is read once, held
+// in registers in fp32 through both sums, and written once.  A thread holds
+// V vectors of eight neighbouring elements; a row's threads form one CTA.
+// Rows above 16384 elements do not fit the registers that way: their kernel
+// reads the row again (from L2) for each of its passes.
+#include <algorithm>
+
+#include "kv.cuh"
+
+namespace mr {
+namespace {
+
+using Args = moe_reader_residual_norm_args;
+
+// Eight neighbouring elements at element offset `at` (a multiple of 8 from a
+// 16-byte aligned start).  Plain loads: h may be written in place.
+__device__ __forceinline__ void load8(const void* p, long long at, int type, float (&f)[8]) {
+  if (type == MOE_READER_TYPE_F32) {
+    const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(p) + at);
+    const float4 a = q[0], b = q[1];
+    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+    f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+    return;
+  }
+  const uint4 v = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + at);
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (type == MOE_READER_TYPE_BF16) {
+      f[2 * i] = __uint_as_float(w[i] << 16);
+      f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    } else {
+      const float2 u = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+      f[2 * i] = u.x;
+      f[2 * i + 1] = u.y;
+    }
+  }
+}
+
+__device__ __forceinline__ float load1(const void* p, long long at, int type) {
+  if (type == MOE_READER_TYPE_F32) return __ldg(static_cast<const float*>(p) + at);
+  const uint16_t u = __ldg(static_cast<const uint16_t*>(p) + at);
+  return type == MOE_READER_TYPE_BF16 ? __uint_as_float((uint32_t)u << 16)
+                                      : __half2float(__ushort_as_half(u));
+}
+
+__device__ __forceinline__ void store8(void* p, long long at, int type, const float (&f)[8]) {
+  if (type == MOE_READER_TYPE_F32) {
+    float4* q = reinterpret_cast<float4*>(static_cast<float*>(p) + at);
+    q[0] = make_float4(f[0], f[1], f[2], f[3]);
+    q[1] = make_float4(f[4], f[5], f[6], f[7]);
+    return;
+  }
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (type == MOE_READER_TYPE_BF16) {
+      const __nv_bfloat162 b = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t*>(&b);
+    } else {
+      const __half2 b = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t*>(&b);
+    }
+  }
+  *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + at) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Sum over the CTA; `slot` alternates so that one barrier is enough.
+__device__ __forceinline__ float block_sum(float v, float (*s)[32], int slot) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  const int warps = blockDim.x >> 5;
+  if (warps == 1) return v;
+  if ((threadIdx.x & 31) == 0) s[slot][threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = 0.f;
+  for (int w = 0; w < warps; ++w) v += s[slot][w];
+  return v;
+}
+
+constexpr int kThreads = 512;        // at most, of the register kernel
+constexpr int kLongThreads = 1024;
+
+template <int V>
+__global__ void __launch_bounds__(kThreads)
+residual_norm_kernel(const Args a) {
+  __shared__ float s_sum[2][32];
+  const long long row = blockIdx.x;
+  const int vecs = a.hidden / 8;
+  float h[V][8], z[V][8];
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    const int v = threadIdx.x + j * blockDim.x;
+    if (v < vecs) load8(a.h, row * a.h_stride + 8 * v, a.h_type, h[j]);
+    if (a.y && v < vecs) load8(a.y, row * a.y_stride + 8 * v, a.y_type, z[j]);
+  }
+  if (a.y) {
+    float inv = 1.f;
+    if (a.post_weight) {
+      float ss = 0.f;
+#pragma unroll
+      for (int j = 0; j < V; ++j)
+        if ((int)threadIdx.x + j * (int)blockDim.x < vecs)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) ss += z[j][i] * z[j][i];
+      inv = rsqrtf(block_sum(ss, s_sum, 0) / (float)a.hidden + a.eps);
+    }
+    float one = a.scale;
+    if (a.gate && a.gate_col_stride == 0)
+      one *= load1(a.gate, row * a.gate_row_stride, a.gate_type);
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const int v = threadIdx.x + j * blockDim.x;
+      if (v >= vecs) continue;
+      float w[8];
+      if (a.post_weight) {
+        load8(a.post_weight, 8 * v, a.weight_type, w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) z[j][i] *= inv * w[i];
+      }
+      if (a.gate && a.gate_col_stride) {
+        load8(a.gate, row * a.gate_row_stride + 8 * v, a.gate_type, w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) z[j][i] *= w[i];
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) h[j][i] += one * z[j][i];
+    }
+  }
+  if (a.h_out) {
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const int v = threadIdx.x + j * blockDim.x;
+      if (v < vecs) store8(a.h_out, row * a.h_out_stride + 8 * v, a.h_type, h[j]);
+    }
+  }
+  if (!a.x) return;
+  float ss = 0.f;
+#pragma unroll
+  for (int j = 0; j < V; ++j)
+    if ((int)threadIdx.x + j * (int)blockDim.x < vecs)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) ss += h[j][i] * h[j][i];
+  const float inv = rsqrtf(block_sum(ss, s_sum, 1) / (float)a.hidden + a.eps);
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    const int v = threadIdx.x + j * blockDim.x;
+    if (v >= vecs) continue;
+    float w[8];
+    if (a.pre_weight) load8(a.pre_weight, 8 * v, a.weight_type, w);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) h[j][i] *= a.pre_weight ? inv * w[i] : inv;
+    store8(a.x, row * a.x_stride + 8 * v, a.x_type, h[j]);
+  }
+}
+
+__global__ void __launch_bounds__(kLongThreads) residual_norm_long_kernel(const Args a) {
+  __shared__ float s_sum[2][32];
+  const long long row = blockIdx.x;
+  const int vecs = a.hidden / 8;
+  float inv_y = 1.f, one = a.scale;
+  if (a.post_weight) {
+    float ss = 0.f;
+    for (int v = threadIdx.x; v < vecs; v += kLongThreads) {
+      float z[8];
+      load8(a.y, row * a.y_stride + 8 * v, a.y_type, z);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) ss += z[i] * z[i];
+    }
+    inv_y = rsqrtf(block_sum(ss, s_sum, 0) / (float)a.hidden + a.eps);
+  }
+  if (a.gate && a.gate_col_stride == 0) one *= load1(a.gate, row * a.gate_row_stride, a.gate_type);
+  auto joined = [&](int v, float (&h)[8]) {        // h' of one vector
+    load8(a.h, row * a.h_stride + 8 * v, a.h_type, h);
+    if (!a.y) return;
+    float z[8], w[8];
+    load8(a.y, row * a.y_stride + 8 * v, a.y_type, z);
+    if (a.post_weight) {
+      load8(a.post_weight, 8 * v, a.weight_type, w);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) z[i] *= inv_y * w[i];
+    }
+    if (a.gate && a.gate_col_stride) {
+      load8(a.gate, row * a.gate_row_stride + 8 * v, a.gate_type, w);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) z[i] *= w[i];
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) h[i] += one * z[i];
+  };
+  float inv = 1.f;
+  if (a.x) {
+    float ss = 0.f;
+    for (int v = threadIdx.x; v < vecs; v += kLongThreads) {
+      float h[8];
+      joined(v, h);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) ss += h[i] * h[i];
+    }
+    inv = rsqrtf(block_sum(ss, s_sum, 1) / (float)a.hidden + a.eps);
+  }
+  for (int v = threadIdx.x; v < vecs; v += kLongThreads) {
+    float h[8], w[8];
+    joined(v, h);        // before h_out, which may be h, is written
+    if (a.h_out) store8(a.h_out, row * a.h_out_stride + 8 * v, a.h_type, h);
+    if (!a.x) continue;
+    if (a.pre_weight) load8(a.pre_weight, 8 * v, a.weight_type, w);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) h[i] *= a.pre_weight ? inv * w[i] : inv;
+    store8(a.x, row * a.x_stride + 8 * v, a.x_type, h);
+  }
+}
+
+bool float_type(int t) {
+  return t == MOE_READER_TYPE_F32 || t == MOE_READER_TYPE_BF16 || t == MOE_READER_TYPE_F16;
+}
+long long bytes_of(int t) { return t == MOE_READER_TYPE_F32 ? 4 : 2; }
+
+// A matrix that the kernel reads or writes in vectors of eight elements.
+bool rows_fit(const void* p, int type, int64_t stride) {
+  return float_type(type) && reinterpret_cast<uintptr_t>(p) % 16 == 0 && stride % 8 == 0;
+}
+
+// Whether two row-strided matrices share a byte (by their outer extents).
+bool overlap(const void* p, int pt, int64_t ps, const void* q, int qt, int64_t qs, int rows,
+             int hidden) {
+  if (!p || !q) return false;
+  auto extent = [&](const void* m, int t, int64_t s, uintptr_t& lo, uintptr_t& hi) {
+    const long long step = (long long)(rows - 1) * s * bytes_of(t);
+    lo = reinterpret_cast<uintptr_t>(m) + (step < 0 ? step : 0);
+    hi = reinterpret_cast<uintptr_t>(m) + (step > 0 ? step : 0) + hidden * bytes_of(t);
+  };
+  uintptr_t a0, a1, b0, b1;
+  extent(p, pt, ps, a0, a1);
+  extent(q, qt, qs, b0, b1);
+  return a0 < b1 && b0 < a1;
+}
+
+int check(const Args& a) {
+  if (a.rows < 0 || a.hidden < 8 || a.hidden > 65536 || a.hidden % 8) return MOE_READER_EINVAL;
+  if (a.rows == 0) return MOE_READER_OK;
+  if (!a.h || (!a.h_out && !a.x)) return MOE_READER_EINVAL;
+  if (!rows_fit(a.h, a.h_type, a.h_stride)) return MOE_READER_EINVAL;
+  if (a.y && !rows_fit(a.y, a.y_type, a.y_stride)) return MOE_READER_EINVAL;
+  if (a.h_out && !rows_fit(a.h_out, a.h_type, a.h_out_stride)) return MOE_READER_EINVAL;
+  if (a.x && !rows_fit(a.x, a.x_type, a.x_stride)) return MOE_READER_EINVAL;
+  if ((a.post_weight || a.pre_weight) && !float_type(a.weight_type)) return MOE_READER_EINVAL;
+  if (reinterpret_cast<uintptr_t>(a.post_weight) % 16 ||
+      reinterpret_cast<uintptr_t>(a.pre_weight) % 16)
+    return MOE_READER_EINVAL;
+  if (!a.y && (a.post_weight || a.gate)) return MOE_READER_EINVAL;
+  if (a.gate) {
+    if (!float_type(a.gate_type)) return MOE_READER_EINVAL;
+    if (a.gate_col_stride == 1) {
+      if (!rows_fit(a.gate, a.gate_type, a.gate_row_stride)) return MOE_READER_EINVAL;
+    } else if (a.gate_col_stride != 0 ||
+               reinterpret_cast<uintptr_t>(a.gate) % bytes_of(a.gate_type)) {
+      return MOE_READER_EINVAL;
+    }
+  }
+  // h' may replace h in place; any other overlap would be read after a write
+  const bool in_place = a.h_out == a.h && a.h_out_stride == a.h_stride;
+  if (a.h_out && !in_place &&
+      overlap(a.h, a.h_type, a.h_stride, a.h_out, a.h_type, a.h_out_stride, a.rows, a.hidden))
+    return MOE_READER_EINVAL;
+  if (overlap(a.y, a.y_type, a.y_stride, a.h_out, a.h_type, a.h_out_stride, a.rows, a.hidden) ||
+      overlap(a.h, a.h_type, a.h_stride, a.x, a.x_type, a.x_stride, a.rows, a.hidden) ||
+      overlap(a.y, a.y_type, a.y_stride, a.x, a.x_type, a.x_stride, a.rows, a.hidden) ||
+      overlap(a.h_out, a.h_type, a.h_out_stride, a.x, a.x_type, a.x_stride, a.rows, a.hidden))
+    return MOE_READER_EINVAL;
+  return MOE_READER_OK;
+}
+
+template <int V>
+void launch(const Args& a, int threads, cudaStream_t s) {
+  residual_norm_kernel<V><<<(unsigned)a.rows, threads, 0, s>>>(a);
+}
+
+}  // namespace
+}  // namespace mr
+
+extern "C" int moe_reader_residual_norm(const moe_reader_residual_norm_args* a, void* stream) {
+  if (!a) return MOE_READER_EINVAL;
+  const int st = mr::check(*a);
+  if (st != MOE_READER_OK || a->rows == 0) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  // as few vectors a thread as its most threads allow
+  const int vecs = a->hidden / 8;
+  auto threads = [&](int v) { return ((vecs + v - 1) / v + 31) / 32 * 32; };
+  if (vecs <= mr::kThreads) mr::launch<1>(*a, threads(1), s);
+  else if (vecs <= 2 * mr::kThreads) mr::launch<2>(*a, threads(2), s);
+  else if (vecs <= 4 * mr::kThreads) mr::launch<4>(*a, threads(4), s);
+  else
+    mr::residual_norm_long_kernel<<<(unsigned)a->rows, mr::kLongThreads, 0, s>>>(*a);
+  return cudaGetLastError() == cudaSuccess ? MOE_READER_OK : MOE_READER_ECUDA;
+}

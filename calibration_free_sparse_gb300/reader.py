@@ -34,6 +34,9 @@ EXPORTED_SYMBOLS = (
     "moe_reader_set_profiling", "moe_reader_read_profile", "moe_reader_topk_noalloc",
     "moe_reader_decode_stack", "moe_reader_decode_shared", "moe_reader_get_kept_shared",
     "moe_reader_set_wait_limit", "moe_reader_inject_fault",
+    "moe_reader_kv_create", "moe_reader_kv_plan", "moe_reader_kv_append", "moe_reader_kv_attend",
+    "moe_reader_kv_select", "moe_reader_kv_status", "moe_reader_kv_destroy",
+    "moe_reader_residual_norm",
 )
 PHASES = ("decode", "screen", "score_topk", "exact", "out")
 
@@ -116,6 +119,19 @@ def _lib():
         lib.moe_reader_set_wait_limit.restype = ctypes.c_int
         lib.moe_reader_inject_fault.argtypes = [vp, ctypes.c_uint32]
         lib.moe_reader_inject_fault.restype = ctypes.c_int
+        # the decode-step calls take packed argument structs (block.py)
+        lib.moe_reader_kv_create.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, ctypes.POINTER(vp)]
+        lib.moe_reader_kv_create.restype = ctypes.c_int
+        for name in ("plan", "append", "attend", "select"):
+            fn = getattr(lib, "moe_reader_kv_" + name)
+            fn.argtypes = [vp, ctypes.c_char_p, vp]
+            fn.restype = ctypes.c_int
+        lib.moe_reader_kv_status.argtypes = [vp, ctypes.POINTER(ctypes.c_uint32)]
+        lib.moe_reader_kv_status.restype = ctypes.c_int
+        lib.moe_reader_kv_destroy.argtypes = [vp]
+        lib.moe_reader_kv_destroy.restype = None
+        lib.moe_reader_residual_norm.argtypes = [ctypes.c_char_p, vp]
+        lib.moe_reader_residual_norm.restype = ctypes.c_int
         lib.moe_reader_abi_version.argtypes = []
         lib.moe_reader_abi_version.restype = ctypes.c_int
         _LIB = lib

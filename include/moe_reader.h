@@ -404,6 +404,258 @@ int moe_reader_topk_noalloc(const float* scores, const int32_t* ids, int32_t row
  * Synchronizes the handle's device first. */
 void moe_reader_destroy(moe_reader_t* h);
 
+/* ------------------------------------------------------------------------
+ * The rest of a decode step: a paged key/value cache (page plan, append,
+ * attention of one new token per request, page selection) and the norm that
+ * joins it to the reader.  The reader takes x and the routing as inputs; these
+ * calls make x.  The conventions at the top of this file hold here too.
+ * ------------------------------------------------------------------------ */
+
+/* Element types of the calls below. */
+#define MOE_READER_TYPE_F32  0
+#define MOE_READER_TYPE_BF16 1
+#define MOE_READER_TYPE_F16  2
+#define MOE_READER_TYPE_E4M3 3   /* 8-bit float: 4 exponent bits, 3 mantissa bits, largest 448 */
+
+/* Device error bits reported by moe_reader_kv_status(). */
+#define MOE_READER_ERR_LENGTH  0x20u  /* a length negative or above the table, or too many tokens */
+#define MOE_READER_ERR_PAGE    0x40u  /* a page, slot or selected page out of range (skipped) */
+#define MOE_READER_ERR_POOL    0x80u  /* fewer free pages than the plan needs */
+
+typedef struct moe_reader_kv moe_reader_kv_t;   /* opaque handle of one layer's cache */
+
+typedef struct {
+  int32_t num_q_heads;      /* Hq: a multiple of num_kv_heads, Hq / Hkv <= 64 */
+  int32_t num_kv_heads;     /* Hkv >= 1; query head i reads KV head i / (Hq / Hkv) */
+  int32_t head_dim;         /* D: 64, 128 or 256 */
+  int32_t page_size;        /* tokens per page: 16, 32, 64, 128 or 256 */
+  int32_t num_pages;        /* pages of the pool; num_pages * page_size < 2^31 */
+  int32_t max_requests;     /* 1..1024 requests per call */
+  int32_t cache_type;       /* MOE_READER_TYPE_BF16, _F16 or _E4M3 */
+  int32_t flags;            /* 0 */
+} moe_reader_kv_config;
+
+/*
+ * moe_reader_kv_create -- a handle on one layer's paged cache.
+ *
+ *   k, v      dev, [num_pages][Hkv][page_size][D] of cache_type, 256-byte
+ *             aligned.  A page holds page_size consecutive tokens of one
+ *             request; a token's slot is page * page_size + offset.
+ *   codes     dev, int8 [num_pages][Hkv][2][D] (16-byte aligned), and
+ *   steps     dev, fp32 [num_pages][Hkv]: the page summaries that append
+ *             writes and select reads; both NULL for a cache without them.
+ *   k_scale, v_scale  dev, fp32 [Hkv]: what a stored e4m3 value is multiplied
+ *             by (finite, > 0); required for E4M3, NULL otherwise.
+ *
+ * All of them are the caller's and must outlive the handle, which owns only
+ * its workspace (partial results and counters of attend).  Calls on one
+ * handle must not overlap on the GPU, and the calling thread's current device
+ * has to be the handle's (EINVAL).  Errors: EINVAL, ENOMEM, ECUDA.
+ */
+int moe_reader_kv_create(const moe_reader_kv_config* cfg, void* k, void* v, int8_t* codes,
+                         float* steps, const float* k_scale, const float* v_scale, void* stream,
+                         moe_reader_kv_t** out);
+
+/*
+ * moe_reader_kv_plan -- page table and slot map of a step, from the
+ * requests' lengths.  Asynchronous; one launch.
+ *
+ * Request r holds prev_lens[r] tokens in its table row and gets new_lens[r]
+ * more.  Pages that it lacks are taken from free_pages in request order and
+ * written behind the ones it has; entries beyond are left alone.
+ *
+ *   prev_lens, new_lens  dev, int32 [requests], >= 0.
+ *   table       dev, int32 [requests][width]: updated in place.
+ *   free_pages  dev, int32 [num_free].
+ *   lens        dev, int32 [requests]: prev + new (may not alias prev_lens).
+ *   starts      dev, int32 [requests + 1]: a request's first new token.
+ *   slots, positions, token_requests  dev, int32 [max_tokens]: each new
+ *               token's slot, position and request, in request order; -1
+ *               behind the last one.
+ *   taken       dev, int32 [1]: free pages used, from the front.
+ *
+ * Device-side errors (moe_reader_kv_status): a negative length counts as 0;
+ * a request that outgrows `width` pages is cut there; tokens beyond
+ * max_tokens get no entry (all ERR_LENGTH); a page that free_pages does not
+ * have is -1 in the table and its tokens' slots are -1 (ERR_POOL); so are
+ * slots of tokens whose page is not in the pool (ERR_PAGE).
+ */
+typedef struct {
+  const int32_t* prev_lens;
+  const int32_t* new_lens;
+  int32_t* table;
+  const int32_t* free_pages;
+  int32_t* lens;
+  int32_t* starts;
+  int32_t* slots;
+  int32_t* positions;
+  int32_t* token_requests;
+  int32_t* taken;
+  int32_t requests;         /* 0..max_requests */
+  int32_t width;            /* pages per table row, >= 1 */
+  int32_t num_free;
+  int32_t max_tokens;
+} moe_reader_kv_plan_args;
+int moe_reader_kv_plan(moe_reader_kv_t* kv, const moe_reader_kv_plan_args* a, void* stream);
+
+/*
+ * moe_reader_kv_append -- write the new tokens' key and value rows into their
+ * slots and bring the summaries of the touched pages up to date.
+ * Asynchronous; one launch.
+ *
+ *   k, v      dev, [tokens][Hkv][D] rows of `type` (the cache's type; BF16 or
+ *             F16 into an E4M3 cache), D contiguous, strides in elements.
+ *   slots     dev, int32 [tokens]; -1 skips the token, a slot outside the
+ *             pool too (ERR_PAGE).  A request's tokens are consecutive and
+ *             ascending, as moe_reader_kv_plan writes them; no slot twice.
+ *
+ * E4M3 stores rn(clamp(x / scale, -448, 448)), NaN stays NaN.  The summary of
+ * a page and head covers its rows up to the newest written: per coordinate
+ * the largest and the smallest key (a NaN key is passed over), as codes
+ * ceil(hi / step) and floor(lo / step) clamped to +-127, where a = max(|hi|,
+ * |lo|) over the coordinates (clamped to 2^-100 .. 2^100) and step =
+ * 2^(floor(log2 a) - 6), doubled if a > 127 step.
+ */
+typedef struct {
+  const void* k;
+  const void* v;
+  const int32_t* slots;
+  int64_t k_token_stride, k_head_stride;
+  int64_t v_token_stride, v_head_stride;
+  int32_t type;
+  int32_t tokens;
+} moe_reader_kv_append_args;
+int moe_reader_kv_append(moe_reader_kv_t* kv, const moe_reader_kv_append_args* a, void* stream);
+
+/*
+ * moe_reader_kv_attend -- attention of one new token per request over its
+ * cached tokens (the new one included, once appended).  Asynchronous; one
+ * launch, deterministic.
+ *
+ *   s_j = scale * q . k_j,  j in [max(0, len - window), len)  (window 0: all)
+ *   out = sum_j exp(s_j) v_j / (sum_j exp(s_j) + exp(sink))
+ *
+ *   q        dev, [requests][Hq][D] of q_type (the cache's type; BF16 or F16
+ *            for an E4M3 cache), D contiguous, strides in elements.
+ *   table    dev, int32 [requests][width] pages;  lens dev, int32 [requests].
+ *   pages    dev, int32 [requests][Hkv][keep] or NULL: attend only to these
+ *            pages of the request (indices into its table row; -1 is skipped),
+ *            as moe_reader_kv_select writes them.
+ *   sinks    dev, fp32 [Hq] or NULL: a logit per head that takes weight and
+ *            adds nothing.
+ *   out      dev, [requests][Hq][D] of q_type, contiguous, 16-byte aligned.
+ *   lse      dev, fp32 [requests][Hq] or NULL: log of the denominator.
+ *
+ * A row with nothing to attend to is zeros, its lse the sink or -infinity.
+ * Rows outside [max(0, len - window), len) are not read, whatever they hold.
+ * Logits, running maximum and sums are fp32; the weights are rounded to the
+ * cache's type (fp16 for E4M3) for the product with V.
+ * A length below 0 counts as 0, one beyond the table is cut (ERR_LENGTH); a
+ * page that is not in the pool is skipped (ERR_PAGE).  EINVAL where requests *
+ * Hkv * ceil(Hq / Hkv / 8) * width (keep with pages) * page_size >= 2^34.
+ */
+typedef struct {
+  const void* q;
+  const int32_t* table;
+  const int32_t* lens;
+  const int32_t* pages;
+  const float* sinks;
+  void* out;
+  float* lse;
+  int64_t q_request_stride, q_head_stride;
+  int32_t q_type;
+  int32_t requests;
+  int32_t width;
+  int32_t keep;             /* >= 1 when pages is given */
+  int32_t window;           /* >= 0 */
+  float scale;
+} moe_reader_kv_attend_args;
+int moe_reader_kv_attend(moe_reader_kv_t* kv, const moe_reader_kv_attend_args* a, void* stream);
+
+/*
+ * moe_reader_kv_select -- choose `keep` pages per request and KV head for
+ * moe_reader_kv_attend by a score of their summaries (the reader's screen,
+ * applied to attention).  Asynchronous; one launch.
+ *
+ * Over the group's query heads, P_d = sum_g max(q_gd, 0) and N_d = sum_g
+ * max(-q_gd, 0) are brought to 7-bit codes (below); a page's score is
+ *   step * sum_d (hi_d P_d - lo_d N_d),
+ * the sum over the heads of a bound on q . k in the page.  It is an integer
+ * times a power of two: exact, so the choice does not depend on the order of
+ * a sum.  The first `first` and last `last` pages of a request are always
+ * chosen, the others by score, ties to the lower page.
+ * Codes: with e = floor(log2 max |q|) over the group (clamped to +-100),
+ * f = rint(q 2^(13 - e)); P and N sum f; with t = floor(log2 max(P, N, 1)),
+ * code = min(rint(P 2^(6 - t)), 127), likewise N.  A NaN in q counts as 0.
+ *
+ *   pages    dev, int32 [requests][Hkv][keep]: chosen pages (indices into the
+ *            request's table row), ascending, -1 behind the last one.
+ * q, table, lens, errors as for moe_reader_kv_attend.  A page that is not in
+ * the pool ranks last (ERR_PAGE).  EINVAL on a cache without summaries;
+ * width <= 49152.
+ */
+typedef struct {
+  const void* q;
+  const int32_t* table;
+  const int32_t* lens;
+  int32_t* pages;
+  int64_t q_request_stride, q_head_stride;
+  int32_t q_type;
+  int32_t requests;
+  int32_t width;
+  int32_t keep;             /* >= max(1, first + last) */
+  int32_t first, last;      /* >= 0 */
+} moe_reader_kv_select_args;
+int moe_reader_kv_select(moe_reader_kv_t* kv, const moe_reader_kv_select_args* a, void* stream);
+
+/* moe_reader_kv_status -- synchronize the stream of the last call on the
+ * handle, read and clear its device error word.  *bits (host, may be NULL)
+ * receives the MOE_READER_ERR_* bits.  Returns OK, EDEVICE or ECUDA. */
+int moe_reader_kv_status(moe_reader_kv_t* kv, uint32_t* bits);
+
+/* moe_reader_kv_destroy -- free the handle and its workspace (NULL is a
+ * no-op).  Synchronizes the handle's device first. */
+void moe_reader_kv_destroy(moe_reader_kv_t* kv);
+
+/*
+ * moe_reader_residual_norm -- the norm after a block, its gate, the scaled
+ * residual and the norm before the next block, per row and in one pass:
+ *
+ *   z  = y / sqrt(mean(y^2) + eps) * post_weight   (z = y without post_weight)
+ *   h' = h + scale * gate * z                      (h' = h without y)
+ *   x  = h' / sqrt(mean(h'^2) + eps) * pre_weight  (ones without pre_weight)
+ *
+ *   h, y       dev, [rows][hidden] of h_type, y_type (F32, BF16 or F16); y NULL
+ *              for the norm alone.  Row strides in elements.
+ *   gate       dev, of gate_type, or NULL (1): element (row, c) at
+ *              gate[row * gate_row_stride + c * gate_col_stride]; a stride of
+ *              0 broadcasts, gate_col_stride is 0 or 1.
+ *   post_weight, pre_weight  dev, [hidden] of weight_type, or NULL.
+ *   h_out      dev, [rows][hidden] of h_type, or NULL (not written); may be h.
+ *   x          dev, [rows][hidden] of x_type, or NULL (not written); may not
+ *              overlap h, y or h_out.
+ *
+ * hidden is a multiple of 8, 8..65536.  Everything is held in fp32 and rounded
+ * once, on the way out: x is formed from the unrounded h'.  Asynchronous; one
+ * launch, deterministic.  EINVAL for argument errors.
+ */
+typedef struct {
+  const void* h;
+  const void* y;
+  const void* gate;
+  const void* post_weight;
+  const void* pre_weight;
+  void* h_out;
+  void* x;
+  int64_t h_stride, y_stride, h_out_stride, x_stride;
+  int64_t gate_row_stride, gate_col_stride;
+  int32_t rows;
+  int32_t hidden;
+  int32_t h_type, y_type, x_type, gate_type, weight_type;
+  float scale, eps;
+} moe_reader_residual_norm_args;
+int moe_reader_residual_norm(const moe_reader_residual_norm_args* a, void* stream);
+
 /* moe_reader_strerror -- static text of a status code. */
 const char* moe_reader_strerror(int code);
 
