@@ -43,6 +43,7 @@ struct Shape {
   static constexpr int kWarps = kRow >= 512 ? 4 : 8;
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kStages = kTile <= 4096 ? 6 : 3;
+  static constexpr int kSplit = 24;                          // tiles that a join is worth
   static constexpr int kRows = 8 * NT;                       // query heads of an item
   // the cross-warp sum runs over chunks of the coordinates that fit 16 KB
   static constexpr int kChunk = 4096 / (kWarps * kRows) < D ? 4096 / (kWarps * kRows) : D;
@@ -180,83 +181,85 @@ __device__ __forceinline__ int tiles_of(const Row& w) {
   return (w.span + S::kKeys - 1) / S::kKeys;
 }
 
-// Finds the items that a warp's tiles belong to and where their keys lie.
+// The item at an index of the list.
 template <class S>
-struct Cursor {
+struct Item {
   int r, sub;            // request; KV head * row_tiles + row tile
   int begin, end, tiles; // the item's indices in the (padded) list, its real tiles
   Row row;
-
-  // Moves to the item of index t (t never decreases).
-  __device__ __forceinline__ void seek(const Params& P, const int* prefix, int t, uint32_t& bad) {
-    if (t < end) return;
-    const int per = P.kv_heads * P.row_tiles;
-    bool moved = false;
-    while (t >= prefix[r + 1] * per) ++r, moved = true;
-    if (moved) {
-      row = row_of(P, r, bad);
-      tiles = tiles_of<S>(row);
-    }
-    const int padded = prefix[r + 1] - prefix[r];
-    sub = (t - prefix[r] * per) / padded;
-    begin = prefix[r] * per + sub * padded;
-    end = begin + padded;
-  }
-};
-
-// One 16-key subtile's source: the byte offset of its first row (both caches),
-// and the first key's position (or a position past the end where nothing is read).
-struct Source {
-  long long at;
-  int pos;
 };
 
 template <class S>
-__device__ __forceinline__ Source source_of(const Params& P, const Cursor<S>& c, int tile, int s,
-                                            uint32_t& bad) {
+__device__ __forceinline__ Item<S> item_at(const Params& P, const int* prefix, int per, int t,
+                                           uint32_t& bad) {
+  int lo = 0, hi = P.requests - 1;
+  while (lo < hi) {                      // the last request that begins at t or before
+    const int mid = (lo + hi + 1) >> 1;
+    if (prefix[mid] * per <= t) lo = mid; else hi = mid - 1;
+  }
+  Item<S> o;
+  o.r = lo;
+  o.row = row_of(P, lo, bad);
+  o.tiles = tiles_of<S>(o.row);
+  const int first = prefix[lo] * per, padded = prefix[lo + 1] - prefix[lo];
+  o.sub = (t - first) / padded;
+  o.begin = first + o.sub * padded;
+  o.end = o.begin + padded;
+  return o;
+}
+
+// One 16-key subtile's source: its page and the first row in it, the position
+// of that key (past the end where nothing is read) and the keys in use.
+struct Source {
+  int id, head, in, pos, lo, len;
+};
+constexpr int kNowhere = INT32_MAX - 64;
+
+// Source of subtile s of the tile at index t.  The page id is used by the
+// caller only later, so that its load is in flight meanwhile.
+template <class S>
+__device__ __forceinline__ Source source_at(const Params& P, const int* prefix, int per, int t,
+                                            int s, uint32_t& bad) {
   Source o;
-  o.at = 0;
-  o.pos = INT32_MAX - 64;
-  const int j = c.row.base + tile * S::kKeys + s * 16;
-  const int head = c.sub / P.row_tiles;
+  const Item<S> it = item_at<S>(P, prefix, per, t, bad);
+  o.id = 0;
+  o.pos = kNowhere;
+  o.lo = it.row.lo;
+  o.len = it.row.len;
+  o.head = it.sub / P.row_tiles;
+  const int v = (t - it.begin) * S::kKeys + s * 16;      // virtual key of the item
+  const int j = it.row.base + v;
+  o.in = j & ((1 << P.shift) - 1);
+  if (t - it.begin >= it.tiles || v >= it.row.span) return o;
   int lp = j >> P.shift;
   if (P.pages) {
-    if (j >= c.row.span) return o;
-    const int listed = __ldg(P.pages + ((size_t)c.r * P.kv_heads + head) * P.keep + lp);
-    if (listed < 0 || listed >= (c.row.len + (1 << P.shift) - 1) >> P.shift) {
+    const int listed = __ldg(P.pages + ((size_t)it.r * P.kv_heads + o.head) * P.keep + lp);
+    if (listed < 0 || listed >= (it.row.len + (1 << P.shift) - 1) >> P.shift) {
       if (listed != -1) bad |= kErrPage;
       return o;
     }
     lp = listed;
-  } else if (j >= c.row.len) {
-    return o;
   }
-  const int id = __ldg(P.table + (size_t)c.r * P.width + lp);
-  if (id < 0 || id >= P.num_pages) {
-    bad |= kErrPage;
-    return o;
-  }
-  const int in = j & ((1 << P.shift) - 1);
-  o.pos = (lp << P.shift) + in;
-  o.at = ((((long long)id * P.kv_heads + head) << P.shift) + in) * S::kRow;
+  o.id = __ldg(P.table + (size_t)it.r * P.width + lp);
+  o.pos = (lp << P.shift) + o.in;
   return o;
 }
 
 // Copies one subtile's K and V rows; rows outside [lo, len) become zeros, so
 // that whatever an unwritten row holds meets no weight.
 template <class S>
-__device__ __forceinline__ void copy_subtile(const Params& P, const Source& o, const Row& row,
-                                             uint32_t k_dst, uint32_t v_dst) {
+__device__ __forceinline__ void copy_subtile(const Params& P, long long at, int pos, int lo,
+                                             int len, uint32_t k_dst, uint32_t v_dst) {
   constexpr int kChunks = S::kRow / 16;
   const int lane = threadIdx.x & 31;
+  const bool whole = pos >= lo && pos + 16 <= len;
 #pragma unroll
   for (int i = 0; i < 16 * kChunks / 32; ++i) {
     const int n = i * 32 + lane, rr = n / kChunks, cc = n % kChunks;
-    const int pos = o.pos + rr;
-    const int bytes = pos >= row.lo && pos < row.len ? 16 : 0;
-    const long long off = o.at + (bytes ? rr * S::kRow + cc * 16 : 0);
-    cp_async(k_dst + place<S::kRow>(rr, cc), P.k + off, bytes);
-    cp_async(v_dst + place<S::kRow>(rr, cc), P.v + off, bytes);
+    const bool in = whole || (pos + rr >= lo && pos + rr < len);
+    const long long off = in ? at + n * 16 : 0;
+    cp_async(k_dst + place<S::kRow>(rr, cc), P.k + off, in ? 16 : 0);
+    cp_async(v_dst + place<S::kRow>(rr, cc), P.v + off, in ? 16 : 0);
   }
 }
 
@@ -270,7 +273,8 @@ __global__ void __launch_bounds__(S::kThreads, 1) attend_kernel(const Params P) 
   float* s_ml = reinterpret_cast<float*>(smem + S::kPipe + S::kSum);
   int* s_pos = reinterpret_cast<int*>(smem + S::kPipe + S::kSum + S::kMl);
   int* s_prefix = s_pos + S::kPos / 4;
-  __shared__ int s_scan[kWarps + 1];
+  __shared__ int4 s_scan[kWarps];
+  __shared__ int s_before[kWarps];
   __shared__ int s_flag;
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
   const int g = lane >> 2, t4 = lane & 3;
@@ -278,11 +282,8 @@ __global__ void __launch_bounds__(S::kThreads, 1) attend_kernel(const Params P) 
   uint32_t bad = 0;
 
   // ---- shares: U tiles per CTA ----
-  // Few rows: each row is padded to whole shares, so that a CTA holds one
-  // piece of one row.  Many rows: one list cut into equal shares, whatever the
-  // lengths are.
   constexpr int kPer = kMaxRequests / S::kThreads;
-  int mine[kPer], sum = 0, rows = 0;
+  int mine[kPer], sum = 0, rows = 0, most = 0;
 #pragma unroll
   for (int j = 0; j < kPer; ++j) {
     const int r = tid * kPer + j;
@@ -290,28 +291,39 @@ __global__ void __launch_bounds__(S::kThreads, 1) attend_kernel(const Params P) 
     if (r < P.requests) mine[j] = tiles_of<S>(row_of(P, r, bad));
     sum += mine[j];
     rows += mine[j] > 0;
+    most = max(most, mine[j]);
   }
   if (blockIdx.x == 0 && bad) atomicOr(P.err, bad);
   bad = 0;
-  auto block_sum = [&](int v) {
+  sum = __reduce_add_sync(0xffffffffu, sum);
+  rows = __reduce_add_sync(0xffffffffu, rows);
+  most = __reduce_max_sync(0xffffffffu, most);
+  if (lane == 0) s_scan[wid] = make_int4(sum, rows, most, 0);
+  __syncthreads();
+  sum = rows = most = 0;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    __syncthreads();
-    if (lane == 0) s_scan[wid] = v;
-    __syncthreads();
-    int all = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) all += s_scan[w];
-    return all;
-  };
+  for (int w = 0; w < kWarps; ++w) {
+    const int4 v = s_scan[w];
+    sum += v.x;
+    rows += v.y;
+    most = max(most, v.z);
+  }
   const int grid = (int)gridDim.x;
-  const long long total = (long long)block_sum(sum) * per;
-  const int items = block_sum(rows) * per;
-  constexpr int kLeast = kWarps;            // tiles: one per warp
-  const bool whole = items * 2 <= grid;
-  int U = (int)((total + grid - 1) / grid);
-  if (whole) U = (int)((total + (grid - items) - 1) / (grid - items));
-  U = max(U, kLeast);
+  const int total = sum * per, items = rows * per;
+  // Shares of equal size: best where the cache is long.  A row of its own per
+  // CTA (or a whole number of CTAs per row) where that costs no CTA more than
+  // kSplit tiles extra: a row that is split costs its CTAs the join.
+  constexpr int kSplit = S::kSplit;
+  int U = max((total + grid - 1) / grid, kWarps);
+  bool whole = false;
+  if (items <= grid) {
+    int W = most;                                 // no row split
+    if (items < grid) {
+      const int cut = max((total + (grid - items) - 1) / (grid - items), kWarps);
+      if (cut + kSplit < W) W = cut;
+    }
+    if (W <= U + kSplit) whole = true, U = max(W, 1);
+  }
   // prefix of the (padded) tiles of a request's one item
   {
     int run = 0;
@@ -326,11 +338,10 @@ __global__ void __launch_bounds__(S::kThreads, 1) attend_kernel(const Params P) 
       const int u = __shfl_up_sync(0xffffffffu, in, o);
       if (lane >= o) in += u;
     }
-    __syncthreads();
-    if (lane == 31) s_scan[wid] = in;
+    if (lane == 31) s_before[wid] = in;
     __syncthreads();
     int at = in - run;
-    for (int w = 0; w < wid; ++w) at += s_scan[w];
+    for (int w = 0; w < wid; ++w) at += s_before[w];
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
       const int r = tid * kPer + j;
@@ -340,7 +351,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) attend_kernel(const Params P) 
     if (tid == S::kThreads - 1 && P.requests == kMaxRequests) s_prefix[kMaxRequests] = at;
   }
   __syncthreads();
-  const long long all = (long long)s_prefix[P.requests] * per;
+  const int all = s_prefix[P.requests] * per;
 
   // rows with nothing to read
   for (int r = blockIdx.x; r < P.requests; r += grid) {
@@ -352,65 +363,62 @@ __global__ void __launch_bounds__(S::kThreads, 1) attend_kernel(const Params P) 
         P.lse[(size_t)r * P.heads + i] = P.sinks ? P.sinks[i] : -INFINITY;
   }
 
-  const long long c0 = (long long)blockIdx.x * U, c1 = min(c0 + U, all);
-  if (c0 >= all) return;
+  if ((long long)blockIdx.x * U >= all) return;
+  const int c0 = blockIdx.x * U, c1 = min(all - c0, U) + c0;
 
   // ---- this warp's pipeline ----
+  // Lane i looks up the source of subtile i of the warp's next 32 subtiles; a
+  // batch is looked up while the one before it is copied.
+  constexpr int kBatch = 32 / kMt;
   const uint32_t pipe = smem_addr(smem) + wid * S::kStages * S::kTile;
-  Cursor<S> pc;            // where the copies are
-  {
-    int lo = 0, hi = P.requests - 1;
-    while (lo < hi) {       // the request of c0
-      const int mid = (lo + hi + 1) >> 1;
-      if ((long long)s_prefix[mid] * per <= c0) lo = mid; else hi = mid - 1;
-    }
-    while (s_prefix[lo + 1] == s_prefix[lo]) ++lo;
-    pc.r = lo;
-    pc.row = row_of(P, lo, bad);
-    pc.tiles = tiles_of<S>(pc.row);
-    pc.end = 0;
-  }
-  Cursor<S> cc = pc;       // where the products are
-  int pt = (int)c0 + wid;  // next tile to copy
-  Source src[kMt];
-  bool have = false;       // the next tile exists and is not padding
-  auto look = [&]() {      // finds the next tile to copy and asks for its page ids
-    have = pt < c1;
-    if (have) {
-      pc.seek(P, s_prefix, pt, bad);
-      have = pt - pc.begin < pc.tiles;
-    }
-    if (have) {
-#pragma unroll
-      for (int s = 0; s < kMt; ++s) src[s] = source_of<S>(P, pc, pt - pc.begin, s, bad);
-    }
+  int copied = 0;          // tiles copied by this warp
+  Source now, next;
+  long long now_at = 0;    // byte offset of the lane's subtile
+  auto look = [&](int n) { // the batch that begins with the warp's tile n
+    const int t = c0 + wid + (n + lane / kMt) * kWarps;
+    next.pos = kNowhere;
+    next.id = next.head = next.in = next.lo = next.len = 0;
+    if (t < c1) next = source_at<S>(P, s_prefix, per, t, lane % kMt, bad);
   };
   int in_stage = 0, out_stage = 0;
   auto issue = [&]() {
-    if (have) {
+    const int n = copied % kBatch;
+    if (n == 0) {
+      now = next;
+      if (now.pos != kNowhere && (now.id < 0 || now.id >= P.num_pages)) {
+        bad |= kErrPage;
+        now.pos = kNowhere;
+      }
+      now_at = ((((long long)now.id * P.kv_heads + now.head) << P.shift) + now.in) * S::kRow;
+      look(copied + kBatch);
+    }
+    if (c0 + wid + copied * kWarps < c1) {
       const uint32_t base = pipe + in_stage * S::kTile;
 #pragma unroll
-      for (int s = 0; s < kMt; ++s)
-        copy_subtile<S>(P, src[s], pc.row, base + s * 16 * S::kRow,
+      for (int s = 0; s < kMt; ++s) {
+        const int from = n * kMt + s;
+        copy_subtile<S>(P, __shfl_sync(0xffffffffu, now_at, from),
+                        __shfl_sync(0xffffffffu, now.pos, from),
+                        __shfl_sync(0xffffffffu, now.lo, from),
+                        __shfl_sync(0xffffffffu, now.len, from), base + s * 16 * S::kRow,
                         base + (S::kKeys + s * 16) * S::kRow);
+      }
       // the positions of the stage's keys, for the mask
-      if (lane < kMt)
-        s_pos[(wid * S::kStages + in_stage) * kMt + lane] = lane ? src[kMt - 1].pos : src[0].pos;
+      if (lane / kMt == n) s_pos[(wid * S::kStages + in_stage) * kMt + lane % kMt] = now.pos;
     }
     cp_commit();
     in_stage = in_stage + 1 == S::kStages ? 0 : in_stage + 1;
-    pt += kWarps;
-    look();
+    ++copied;
   };
-  look();
+  look(0);
 #pragma unroll 1
   for (int i = 0; i < S::kStages - 1; ++i) issue();
 
   // ---- pieces: the rows (or parts of rows) of this share ----
-  int t = (int)c0 + wid;
-  for (int p0 = (int)c0; p0 < c1;) {
-    cc.seek(P, s_prefix, p0, bad);
-    const int p1 = min((int)c1, cc.end);
+  int t = c0 + wid;
+  for (int p0 = c0; p0 < c1;) {
+    const Item<S> cc = item_at<S>(P, s_prefix, per, p0, bad);
+    const int p1 = min(c1, cc.end);
     const int real = min(p1, cc.begin + cc.tiles);     // tiles beyond are padding
     const int kvh = cc.sub / P.row_tiles, row0 = (cc.sub % P.row_tiles) * S::kRows;
     const int rows_here = min(S::kRows, P.group - row0);
@@ -745,7 +753,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) attend_kernel(const Params P) 
         // the slot of a piece: a CTA's first piece unless the row began inside it
         auto slot_of = [&](int p) {
           const int cta = first_cta + p;
-          return (size_t)cta * 2 + ((long long)cta * U >= cc.begin ? 0 : 1);
+          return (size_t)cta * 2 + (cta * U >= cc.begin ? 0 : 1);
         };
         float* wgt = s_sum;                    // [pieces][kRows]
         if (wid < kWarps) {
