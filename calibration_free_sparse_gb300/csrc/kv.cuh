@@ -24,8 +24,8 @@ struct moe_reader_kv {
   // workspace
   void* base;
   float* part_o;              // [sms][2][16][D]  unnormalised outputs of split rows
-  float* part_ml;             // [sms][2][2][16]  their running maximum and sum
-  uint32_t* arrived;          // [items]          pieces written; zero between launches
+  float* part_ml;             // [sms][2][2][16]  their references and sums of weights
+  uint32_t* arrived;          // [rows]           pieces written; zero between launches
   uint32_t* err;              // [1]              device error word
   cudaStream_t last_stream;
   int used;
@@ -36,6 +36,7 @@ namespace mr {
 constexpr int kMaxGroup = 64;
 constexpr int kMaxRequests = 1024;
 constexpr int kMaxSelectPages = 49152;
+constexpr int kMaxSms = 256;          // CTAs of attend at most
 
 constexpr uint32_t kErrLength = MOE_READER_ERR_LENGTH;
 constexpr uint32_t kErrPage = MOE_READER_ERR_PAGE;

@@ -10,12 +10,17 @@
 // short side of the instruction, K and V come from shared memory as the long
 // side, and the accumulators cost D / 4 registers per 8 heads.
 //
-// Work is a list of (request, KV head, tile of keys), dealt to one CTA per SM
-// in equal contiguous shares computed on the device from the lengths.  Inside
-// a CTA every warp takes every kWarps-th tile of the share with a private
-// cp.async pipeline, softmax state and output: no barrier until the share or
-// the row ends.  A row that several CTAs hold is joined by the CTA that
-// finishes last, in piece order, so the result does not depend on timing.
+// Work is a list of (row, tile of keys), a row being a request, a KV head and
+// up to 16 of its query heads.  The lengths are on the device, so every CTA
+// counts the tiles itself and takes an equal contiguous share of the list (or,
+// with few rows, a whole number of CTAs per row).  Inside a CTA every warp
+// takes every kWarps-th tile with a private cp.async pipeline, softmax state
+// and output, and its copies run on across rows: no barrier until the share
+// ends.  Where a row ends before the share does, the warps add their states to
+// one in shared memory in turns, beginning with another warp each time, and go
+// on; a barrier there left HBM idle for about 3 us a row.  A row that several
+// CTAs hold is joined by the CTA that finishes it, in the order of the shares.
+// All sums have a fixed order: the result does not depend on timing.
 #include <algorithm>
 #include <type_traits>
 
@@ -44,17 +49,21 @@ struct Shape {
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kStages = kTile <= 4096 ? 6 : 3;
   static constexpr int kSplit = 24;                          // tiles that a join is worth
-  static constexpr int kRows = 8 * NT;                       // query heads of an item
-  // the cross-warp sum runs over chunks of the coordinates that fit 16 KB
-  static constexpr int kChunk = 4096 / (kWarps * kRows) < D ? 4096 / (kWarps * kRows) : D;
-  static constexpr int kPitch = kChunk + 4;
+  static constexpr int kRows = 8 * NT;                       // query heads of a row
+  // the sum over the warps at the end runs over slices of the coordinates
+  static constexpr int kSlice = 4096 / (kWarps * kRows) < D ? 4096 / (kWarps * kRows) : D;
+  static constexpr int kPitch = kSlice + 4;
+  // two rows' states in shared memory, for the rows that end inside a share
+  static constexpr int kAccPitch = D + 4;
+  static constexpr int kAcc = kRows * kAccPitch;
+  static constexpr int kSumA = kWarps * kRows * kPitch * 4, kSumB = 2 * kAcc * 4;
   static constexpr int kPipe = kWarps * kStages * kTile;
-  static constexpr int kSum = kWarps * kRows * kPitch * 4;
+  static constexpr int kSum = kSumA > kSumB ? kSumA : kSumB;
   static constexpr int kMl = kWarps * kRows * 2 * 4;
   static constexpr int kPos = kWarps * kStages * kMt * 4;
   static constexpr int kSmem = kPipe + kSum + kMl + kPos + (kMaxRequests + 1) * 4;
-  static_assert(kRows * 256 * 4 <= kSum, "join weights of at most 256 pieces");
-  static_assert(kSmem <= 227 * 1024, "shared memory");
+  static_assert(kRows * kMaxSms * 4 <= kSum, "join weights of a piece per CTA");
+  static_assert(kSmem + 2048 <= 227 * 1024, "shared memory");
 };
 
 struct Params {
@@ -66,7 +75,7 @@ struct Params {
   void* out;
   float* lse;
   long long q_request, q_head;
-  int q_type, requests, width, keep, window;
+  int q_type, q_pairs, requests, width, keep, window;
   float scale;
   const char* k;
   const char* v;
@@ -83,8 +92,12 @@ struct Params {
 __device__ __forceinline__ uint32_t smem_addr(const void* p) {
   return (uint32_t)__cvta_generic_to_shared(p);
 }
-// 16 bytes, or zeros where `bytes` is 0
-__device__ __forceinline__ void cp_async(uint32_t dst, const void* src, int bytes) {
+__device__ __forceinline__ void cp_async(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(dst), "l"(src)
+               : "memory");
+}
+// zeros where `bytes` is 0
+__device__ __forceinline__ void cp_async_or_zero(uint32_t dst, const void* src, int bytes) {
   asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
                "r"(bytes) : "memory");
 }
@@ -103,19 +116,19 @@ __device__ __forceinline__ void ldsm_t(uint32_t (&r)[4], uint32_t a) {
 }
 __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
   uint32_t r;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
   return r;
 }
 template <bool BF>
 __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
                                     uint32_t b1) {
   if constexpr (BF) {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
                  "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
   } else {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
                  "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
@@ -250,17 +263,128 @@ __device__ __forceinline__ Source source_at(const Params& P, const int* prefix, 
 template <class S>
 __device__ __forceinline__ void copy_subtile(const Params& P, long long at, int pos, int lo,
                                              int len, uint32_t k_dst, uint32_t v_dst) {
-  constexpr int kChunks = S::kRow / 16;
+  constexpr int kChunks = S::kRow / 16, kStep = 32 / kChunks;    // rows per 32 lanes
   const int lane = threadIdx.x & 31;
+  const int r0 = lane / kChunks;
+  const uint32_t d0 = place<S::kRow>(r0, lane % kChunks);
+  const char* ks = P.k + at + lane * 16;
+  const char* vs = P.v + at + lane * 16;
   const bool whole = pos >= lo && pos + 16 <= len;
 #pragma unroll
-  for (int i = 0; i < 16 * kChunks / 32; ++i) {
-    const int n = i * 32 + lane, rr = n / kChunks, cc = n % kChunks;
-    const bool in = whole || (pos + rr >= lo && pos + rr < len);
-    const long long off = in ? at + n * 16 : 0;
-    cp_async(k_dst + place<S::kRow>(rr, cc), P.k + off, in ? 16 : 0);
-    cp_async(v_dst + place<S::kRow>(rr, cc), P.v + off, in ? 16 : 0);
+  for (int i = 0; i < 16 / kStep; ++i) {
+    // place(r0 + i kStep, c): r0 < kStep, so the row's swizzle bits split
+    const uint32_t flip = kChunks >= 8 ? ((i * kStep) & 7) << 4 : 0;
+    const uint32_t d = (d0 ^ flip) + i * 512;
+    if (whole) {
+      cp_async(k_dst + d, ks + i * 512);
+      cp_async(v_dst + d, vs + i * 512);
+    } else {
+      const int p = pos + r0 + i * kStep;
+      const bool in = p >= lo && p < len;
+      cp_async_or_zero(k_dst + d, in ? ks + i * 512 : P.k, in ? 16 : 0);
+      cp_async_or_zero(v_dst + d, in ? vs + i * 512 : P.v, in ? 16 : 0);
+    }
   }
+}
+
+// Waits until shared word `turn` reaches `want`; gives up after a fraction of
+// a second (the warps that it waits for only compute, so this cannot happen).
+__device__ __forceinline__ void wait_turn(const uint32_t* turn, uint32_t want, uint32_t& bad) {
+  const uint32_t a = smem_addr(turn);
+  for (int n = 0; n < (1 << 21); ++n) {
+    uint32_t v;
+    asm volatile("ld.acquire.cta.shared.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+    if (v == want) return;
+    __nanosleep(64);
+  }
+  bad |= MOE_READER_ERR_TIMEOUT;
+}
+__device__ __forceinline__ void pass_turn(uint32_t* turn, uint32_t next) {
+  asm volatile("st.release.cta.shared.u32 [%0], %1;" ::"r"(smem_addr(turn)), "r"(next) : "memory");
+}
+
+// What scales a row's weighted sum to its output, and the log of its
+// denominator: here the sink joins.  top and den: the row's reference (in
+// units of log2) and the sum of its weights.
+template <class S>
+__device__ __forceinline__ void finish(const Params& P, int kvh, int head, float top, float den,
+                                       float& mul, float& lse) {
+  const float vs = S::CT == kE4m3 ? __ldg(P.v_scale + kvh) : 1.f;
+  float ref = top;
+  if (P.sinks) {
+    const float sink = __ldg(P.sinks + head) * kLog2e;
+    ref = fmaxf(top, sink);
+    const float down = top == -INFINITY ? 0.f : exp2_fast(top - ref);
+    den = den * down + (sink == -INFINITY ? 0.f : exp2_fast(sink - ref));
+    mul = den == 0.f ? 0.f : vs * down / den;
+  } else {
+    mul = den == 0.f ? 0.f : vs / den;
+  }
+  lse = ref == -INFINITY ? -INFINITY : (ref + log2f(den)) * kLn2;
+}
+
+// Two neighbouring outputs of a query head.
+__device__ __forceinline__ void store_out(const Params& P, int r, int head, int D, int d, float a,
+                                          float b) {
+  uint32_t* at = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(P.out) +
+                                             ((size_t)r * P.heads + head) * D + d);
+  *at = P.q_type == kBf16 ? pack<true>(a, b) : pack<false>(a, b);
+}
+
+// Sums the pieces of a row that several CTAs wrote, in order; all of the CTA.
+template <class S>
+__device__ __forceinline__ void join_row(const Params& P, const Item<S>& it, int U, int pieces,
+                                         float* wgt, float* s_mul) {
+  constexpr int D = S::D;
+  const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+  const int kvh = it.sub / P.row_tiles, row0 = (it.sub % P.row_tiles) * S::kRows;
+  const int rows = min(S::kRows, P.group - row0), head0 = kvh * P.group + row0;
+  const int first = it.begin / U;
+  // a CTA's first piece is in its slot 0, unless the row began inside its share
+  auto slot = [&](int p) {
+    return (size_t)(first + p) * 2 + ((first + p) * U >= it.begin ? 0 : 1);
+  };
+  for (int h = wid; h < rows; h += S::kWarps) {
+    float top = -INFINITY;
+    for (int p = lane; p < pieces; p += 32)
+      top = fmaxf(top, __ldcg(P.part_ml + slot(p) * 32 + h));
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+    float den = 0.f;
+    for (int p = lane; p < pieces; p += 32) {
+      const float mp = __ldcg(P.part_ml + slot(p) * 32 + h);
+      const float w = mp == -INFINITY ? 0.f : exp2_fast(mp - top);
+      wgt[p * S::kRows + h] = w;
+      den += w * __ldcg(P.part_ml + slot(p) * 32 + 16 + h);
+    }
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) den += __shfl_xor_sync(0xffffffffu, den, x);
+    float mul, lse;
+    finish<S>(P, kvh, head0 + h, top, den, mul, lse);
+    if (lane == 0) {
+      s_mul[h] = mul;
+      if (P.lse) P.lse[(size_t)it.r * P.heads + head0 + h] = lse;
+    }
+  }
+  __syncthreads();
+  for (int e = tid; e < rows * D / 4; e += S::kThreads) {
+    const int h = e / (D / 4), d = e % (D / 4) * 4;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+    for (int p = 0; p < pieces; ++p) {
+      const float4 v =
+          __ldcg(reinterpret_cast<const float4*>(P.part_o + (slot(p) * 16 + h) * D + d));
+      const float w = wgt[p * S::kRows + h];
+      acc.x += w * v.x;
+      acc.y += w * v.y;
+      acc.z += w * v.z;
+      acc.w += w * v.w;
+    }
+    const float mul = s_mul[h];
+    store_out(P, it.r, head0 + h, D, d, acc.x * mul, acc.y * mul);
+    store_out(P, it.r, head0 + h, D, d + 2, acc.z * mul, acc.w * mul);
+  }
+  __syncthreads();
 }
 
 // ---- the kernel -----------------------------------------------------------
@@ -275,12 +399,15 @@ __global__ void __launch_bounds__(S::kThreads, 1) attend_kernel(const Params P) 
   int* s_prefix = s_pos + S::kPos / 4;
   __shared__ int4 s_scan[kWarps];
   __shared__ int s_before[kWarps];
-  __shared__ int s_flag;
+  __shared__ uint32_t s_turn[2];
+  __shared__ int s_last[2];
+  __shared__ float s_mul[S::kRows];
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
   const int g = lane >> 2, t4 = lane & 3;
   const int per = P.kv_heads * P.row_tiles;
   uint32_t bad = 0;
 
+  if (tid < 2) s_turn[tid] = 0, s_last[tid] = 0;
   // ---- shares: U tiles per CTA ----
   constexpr int kPer = kMaxRequests / S::kThreads;
   int mine[kPer], sum = 0, rows = 0, most = 0;
@@ -366,6 +493,20 @@ __global__ void __launch_bounds__(S::kThreads, 1) attend_kernel(const Params P) 
   if ((long long)blockIdx.x * U >= all) return;
   const int c0 = blockIdx.x * U, c1 = min(all - c0, U) + c0;
 
+  // CTAs that hold a part of a row; one more part of it is written (the last
+  // to say so gets true, and clears the counter for the next launch)
+  auto pieces_of = [&](const Item<S>& it) {
+    return (it.begin + it.tiles - 1) / U - it.begin / U + 1;
+  };
+  auto arrive = [&](const Item<S>& it) -> int {
+    uint32_t* count = P.arrived + it.r * per + it.sub;
+    __threadfence();
+    const bool last = atomicAdd(count, 1u) + 1 == (uint32_t)pieces_of(it);
+    if (last) *count = 0;
+    __threadfence();
+    return last;
+  };
+
   // ---- this warp's pipeline ----
   // Lane i looks up the source of subtile i of the warp's next 32 subtiles; a
   // batch is looked up while the one before it is copied.
@@ -414,10 +555,18 @@ __global__ void __launch_bounds__(S::kThreads, 1) attend_kernel(const Params P) 
 #pragma unroll 1
   for (int i = 0; i < S::kStages - 1; ++i) issue();
 
-  // ---- pieces: the rows (or parts of rows) of this share ----
-  int t = c0 + wid;
-  for (int p0 = c0; p0 < c1;) {
-    const Item<S> cc = item_at<S>(P, s_prefix, per, p0, bad);
+  // The lane's row and 16-byte chunk in the matrix loads; the loads of the next
+  // 32 bytes of the rows flip bits above (place() is an exclusive or).
+  const uint32_t k_lane = place<S::kRow>(lane & 15, lane >> 4);
+  const uint32_t v_lane =
+      k8 ? k_lane : place<S::kRow>((lane & 7) + ((lane >> 4) << 3), (lane >> 3) & 1);
+
+  // ---- pieces: the rows, or parts of rows, of this share ----
+  float o[D / 16][NT][4], m[NT][2], l[NT][2];
+  Item<S> cc;
+  int p0 = c0, t = c0 + wid;
+  for (int k = 0;; ++k) {
+    cc = item_at<S>(P, s_prefix, per, p0, bad);
     const int p1 = min(c1, cc.end);
     const int real = min(p1, cc.begin + cc.tiles);     // tiles beyond are padding
     const int kvh = cc.sub / P.row_tiles, row0 = (cc.sub % P.row_tiles) * S::kRows;
@@ -441,7 +590,8 @@ __global__ void __launch_bounds__(S::kThreads, 1) attend_kernel(const Params P) 
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
               const uint16_t* at = q + k * 16 + i * 8 + 2 * t4;
-              qf[n][k][i] = (uint32_t)__ldg(at) | (uint32_t)__ldg(at + 1) << 16;
+              qf[n][k][i] = P.q_pairs ? __ldg(reinterpret_cast<const uint32_t*>(at))
+                                      : (uint32_t)__ldg(at) | (uint32_t)__ldg(at + 1) << 16;
             }
           fac[n][0] = fac[n][1] = base;
         } else {
@@ -472,7 +622,6 @@ __global__ void __launch_bounds__(S::kThreads, 1) attend_kernel(const Params P) 
       }
     }
 
-    float o[D / 16][NT][4], m[NT][2], l[NT][2];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       m[n][0] = m[n][1] = -INFINITY;
@@ -494,92 +643,116 @@ __global__ void __launch_bounds__(S::kThreads, 1) attend_kernel(const Params P) 
       if (t >= real) continue;
       if (pos[0] >= cc.row.len && pos[kMt - 1] >= cc.row.len) continue;   // no page there
 
-      // S^T = K Q^T
-      float sc[kMt][NT][4];
+      // S^T = K Q^T, as kSplitK sums where the tile alone gives one chain of products
+      constexpr int kSplitK = NT * kMt == 1 ? 2 : 1;
+      float sc[kMt][NT][4], sx[NT][4];
 #pragma unroll
-      for (int s = 0; s < kMt; ++s)
+      for (int n1 = 0; n1 < NT; ++n1)
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+        for (int i = 0; i < 4; ++i) {
+          sx[n1][i] = 0.f;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) sc[s][n][i] = 0.f;
+          for (int s = 0; s < kMt; ++s) sc[s][n1][i] = 0.f;
+        }
 #pragma unroll
       for (int s = 0; s < kMt; ++s) {
         const uint32_t kb = ks + s * 16 * S::kRow;
         if constexpr (!k8) {
 #pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
+          for (int x = 0; x < D / 16; ++x) {
             uint32_t a[4];
-            ldsm(a, kb + place<S::kRow>(lane & 15, 2 * k + (lane >> 4)));
+            ldsm(a, kb + (k_lane ^ (x << 5)));
 #pragma unroll
-            for (int n = 0; n < NT; ++n) mma<kBf>(sc[s][n], a, qf[n][k][0], qf[n][k][1]);
+            for (int n1 = 0; n1 < NT; ++n1)
+              mma<kBf>(kSplitK == 2 && (x & 1) ? sx[n1] : sc[s][n1], a, qf[n1][x][0], qf[n1][x][1]);
           }
         } else {
 #pragma unroll
-          for (int k = 0; k < D / 32; ++k) {
+          for (int x = 0; x < D / 32; ++x) {
             uint32_t b[4];      // rows 0-7 and 8-15 of 16 coordinates, then of the next 16
-            ldsm(b, kb + place<S::kRow>(lane & 15, 2 * k + (lane >> 4)));
+            ldsm(b, kb + (k_lane ^ (x << 5)));
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
               const uint32_t a[4] = {e4m3x2_to_f16x2(b[2 * j]), e4m3x2_to_f16x2(b[2 * j + 1]),
                                      e4m3x2_to_f16x2(b[2 * j] >> 16),
                                      e4m3x2_to_f16x2(b[2 * j + 1] >> 16)};
 #pragma unroll
-              for (int n = 0; n < NT; ++n)
-                mma<false>(sc[s][n], a, qf[n][2 * k + j][0], qf[n][2 * k + j][1]);
+              for (int n1 = 0; n1 < NT; ++n1)
+                mma<false>(kSplitK == 2 && j ? sx[n1] : sc[s][n1], a, qf[n1][2 * x + j][0],
+                           qf[n1][2 * x + j][1]);
             }
           }
         }
       }
 
       // logits in units of log2, masked
-      bool seen[kMt][2];
 #pragma unroll
       for (int s = 0; s < kMt; ++s) {
-        const int at = pos[s] + g;
-        seen[s][0] = at >= cc.row.lo && at < cc.row.len;
-        seen[s][1] = at + 8 >= cc.row.lo && at + 8 < cc.row.len;
-      }
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        float top[2] = {m[n][0], m[n][1]};
-#pragma unroll
-        for (int s = 0; s < kMt; ++s)
+        for (int n1 = 0; n1 < NT; ++n1)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            sc[s][n][i] = seen[s][i >> 1] ? sc[s][n][i] * fac[n][i & 1] : -INFINITY;
-            top[i & 1] = fmaxf(top[i & 1], sc[s][n][i]);
+            if (kSplitK == 2) sc[s][n1][i] += sx[n1][i];
+            sc[s][n1][i] *= fac[n1][i & 1];
+          }
+        const int at = pos[s];
+        if (at < cc.row.lo || at + 16 > cc.row.len) {
+          const bool in0 = at + g >= cc.row.lo && at + g < cc.row.len;
+          const bool in1 = at + g + 8 >= cc.row.lo && at + g + 8 < cc.row.len;
+#pragma unroll
+          for (int n1 = 0; n1 < NT; ++n1)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (!(i < 2 ? in0 : in1)) sc[s][n1][i] = -INFINITY;
+        }
+      }
+      // The weights are taken relative to a reference that follows the maximum
+      // only when that has grown by more than 2^kSlack: the sums stay exact to
+      // a common factor, and nearly every tile saves the rescaling.  fp16
+      // weights reach 2^kSlack at most, far from their end.
+      constexpr float kSlack = 8.f;
+      float top[NT][2];
+      bool grown = false;
+#pragma unroll
+      for (int n1 = 0; n1 < NT; ++n1) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          float v = fmaxf(sc[0][n1][i], sc[0][n1][i + 2]);
+#pragma unroll
+          for (int s = 1; s < kMt; ++s) v = fmaxf(v, fmaxf(sc[s][n1][i], sc[s][n1][i + 2]));
+          top[n1][i] = v;
+          grown |= v > m[n1][i] + kSlack;
+        }
+      }
+      if (__any_sync(0xffffffffu, grown)) {
+#pragma unroll
+        for (int n1 = 0; n1 < NT; ++n1) {
+          float a[2];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            float v = fmaxf(top[n1][i], m[n1][i]);
+#pragma unroll
+            for (int x = 4; x < 32; x <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, x));
+            a[i] = exp2_fast(m[n1][i] - (v == -INFINITY ? 0.f : v));
+            m[n1][i] = v;
+            l[n1][i] *= a[i];
           }
 #pragma unroll
-        for (int x = 4; x < 32; x <<= 1) {
-          top[0] = fmaxf(top[0], __shfl_xor_sync(0xffffffffu, top[0], x));
-          top[1] = fmaxf(top[1], __shfl_xor_sync(0xffffffffu, top[1], x));
-        }
-        // the running maximum moves seldom: rescale only then
-        if (__any_sync(0xffffffffu, top[0] > m[n][0] || top[1] > m[n][1])) {
-          const float a0 = exp2_fast(m[n][0] - (top[0] == -INFINITY ? 0.f : top[0]));
-          const float a1 = exp2_fast(m[n][1] - (top[1] == -INFINITY ? 0.f : top[1]));
-          l[n][0] *= a0;
-          l[n][1] *= a1;
+          for (int d = 0; d < D / 16; ++d)
 #pragma unroll
-          for (int d = 0; d < D / 16; ++d) {
-            o[d][n][0] *= a0;
-            o[d][n][1] *= a1;
-            o[d][n][2] *= a0;
-            o[d][n][3] *= a1;
-          }
-          m[n][0] = top[0];
-          m[n][1] = top[1];
+            for (int i = 0; i < 4; ++i) o[d][n1][i] *= a[i & 1];
         }
-        const float r0 = m[n][0] == -INFINITY ? 0.f : m[n][0];
-        const float r1 = m[n][1] == -INFINITY ? 0.f : m[n][1];
+      }
+#pragma unroll
+      for (int n1 = 0; n1 < NT; ++n1) {
+        const float r0 = m[n1][0] == -INFINITY ? 0.f : m[n1][0];
+        const float r1 = m[n1][1] == -INFINITY ? 0.f : m[n1][1];
 #pragma unroll
         for (int s = 0; s < kMt; ++s) {
-          sc[s][n][0] = exp2_fast(sc[s][n][0] - r0);
-          sc[s][n][1] = exp2_fast(sc[s][n][1] - r1);
-          sc[s][n][2] = exp2_fast(sc[s][n][2] - r0);
-          sc[s][n][3] = exp2_fast(sc[s][n][3] - r1);
-          l[n][0] += sc[s][n][0] + sc[s][n][2];
-          l[n][1] += sc[s][n][1] + sc[s][n][3];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) sc[s][n1][i] = exp2_fast(sc[s][n1][i] - (i & 1 ? r1 : r0));
+          l[n1][0] += sc[s][n1][0] + sc[s][n1][2];
+          l[n1][1] += sc[s][n1][1] + sc[s][n1][3];
         }
       }
 
@@ -597,8 +770,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) attend_kernel(const Params P) 
 #pragma unroll
           for (int d = 0; d < D / 16; ++d) {
             uint32_t a[4];
-            ldsm_t(a, vb + place<S::kRow>((lane & 7) + ((lane >> 4) << 3),
-                                          2 * d + ((lane >> 3) & 1)));
+            ldsm_t(a, vb + (v_lane ^ (d << 5)));
 #pragma unroll
             for (int n = 0; n < NT; ++n) mma<kBf>(o[d][n], a, pf[n][0], pf[n][1]);
           }
@@ -608,7 +780,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) attend_kernel(const Params P) 
 #pragma unroll
           for (int d = 0; d < D / 32; ++d) {
             uint32_t b[4];
-            ldsm_t(b, vb + place<S::kRow>(lane & 15, 2 * d + (lane >> 4)));
+            ldsm_t(b, vb + (v_lane ^ (d << 5)));
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
               const uint32_t x = __byte_perm(b[2 * j], 0, 0x3120);
@@ -623,187 +795,174 @@ __global__ void __launch_bounds__(S::kThreads, 1) attend_kernel(const Params P) 
       }
     }
 
-    // ---- the warps' states into one ----
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int x = 4; x < 32; x <<= 1) l[n][i] += __shfl_xor_sync(0xffffffffu, l[n][i], x);
-    if (g == 0) {
+    if (p1 == c1) break;
+
+    // ---- the row ends here, the share does not: add to its state in turn ----
+    const int b = k & 1, place_in_turn = (wid - k) & (kWarps - 1);
+    float* acc = s_sum + b * S::kAcc;
+    float* ref = s_ml + b * S::kRows;
+    float* den = s_ml + (2 + b) * S::kRows;
+    const uint32_t turn = (uint32_t)(k >> 1) * kWarps + place_in_turn;
+    wait_turn(&s_turn[b], turn, bad);
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
+    for (int n = 0; n < NT; ++n) {
+      float keep[2] = {0.f, 0.f}, add[2];              // factors of the state and of this warp
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int h = n * 8 + 2 * t4 + i;
-          s_ml[wid * S::kRows + h] = m[n][i];
-          s_ml[(kWarps + wid) * S::kRows + h] = l[n][i];
+      for (int i = 0; i < 2; ++i) {
+        const int h = n * 8 + 2 * t4 + i;
+        const float before = place_in_turn ? ref[h] : -INFINITY;
+        const float now_ref = fmaxf(before, m[n][i]);
+        add[i] = m[n][i] == -INFINITY ? 0.f : exp2_fast(m[n][i] - now_ref);
+        float d = l[n][i] * add[i];
+        if (before != -INFINITY) {
+          keep[i] = exp2_fast(before - now_ref);
+          d += den[h] * keep[i];
+        }
+        __syncwarp();                                  // all lanes of the column have read
+        if (g == 0) ref[h] = now_ref, den[h] = d;
+      }
+#pragma unroll
+      for (int x = 0; x < D / 16; ++x)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int h = n * 8 + 2 * t4 + (i & 1);
+          float* at = acc + h * S::kAccPitch + x * 16 + (k8 ? 2 * g + (i >> 1) : g + 8 * (i >> 1));
+          const float v = o[x][n][i] * add[i & 1];
+          *at = keep[i & 1] != 0.f ? *at * keep[i & 1] + v : v;
         }
     }
-    __syncthreads();
-    float mine_f[NT][2];      // this warp's factor per column
+    __syncwarp();
+    if (place_in_turn == kWarps - 1) {
+      if (cc.begin >= c0) {                            // the whole row
+        if (lane < S::kRows) {
+          float mul, lse;
+          finish<S>(P, kvh, head0 + (lane < rows_here ? lane : 0), ref[lane], den[lane], mul, lse);
+          if (lane < rows_here && P.lse) P.lse[(size_t)cc.r * P.heads + head0 + lane] = lse;
+          den[lane] = mul;
+        }
+        __syncwarp();
+        for (int e = lane; e < rows_here * D / 2; e += 32) {
+          const int h = e / (D / 2), d = e % (D / 2) * 2;
+          const float2 v = *reinterpret_cast<const float2*>(acc + h * S::kAccPitch + d);
+          store_out(P, cc.r, head0 + h, D, d, v.x * den[h], v.y * den[h]);
+        }
+      } else {                                         // the end of a row: slot 0
+        float* po = P.part_o + (size_t)blockIdx.x * 2 * 16 * D;
+        float* pml = P.part_ml + (size_t)blockIdx.x * 2 * 32;
+        for (int e = lane; e < S::kRows * D / 4; e += 32) {
+          const int h = e / (D / 4), d = e % (D / 4) * 4;
+          *reinterpret_cast<float4*>(po + h * D + d) =
+              *reinterpret_cast<const float4*>(acc + h * S::kAccPitch + d);
+        }
+        if (lane < S::kRows) {
+          pml[lane] = ref[lane];
+          pml[16 + lane] = den[lane];
+        }
+        __syncwarp();
+        if (lane == 0) s_last[0] = arrive(cc);
+      }
+      __syncwarp();
+    }
+    if (lane == 0) pass_turn(&s_turn[b], turn + 1);
+    p0 = p1;
+  }
+
+  // ---- the share's last piece: all warps at once ----
+  const int kvh = cc.sub / P.row_tiles, row0 = (cc.sub % P.row_tiles) * S::kRows;
+  const int rows_here = min(S::kRows, P.group - row0);
+  const int head0 = kvh * P.group + row0;
+  __syncthreads();                                     // no turn uses the shared state any more
+  if (g == 0) {
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int h = n * 8 + 2 * t4 + i;
-        float top = -INFINITY;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_ml[w * S::kRows + h]);
-        mine_f[n][i] = m[n][i] == -INFINITY ? 0.f : exp2_fast(m[n][i] - top);
+        s_ml[wid * S::kRows + h] = m[n][i];
+        s_ml[(kWarps + wid) * S::kRows + h] = l[n][i];
       }
-    const int first_cta = cc.begin / U;
-    const int pieces = (cc.begin + cc.tiles - 1) / U - first_cta + 1;
-    const bool alone = pieces == 1;
-    const size_t slot = (size_t)blockIdx.x * 2 + (p0 == c0 ? 0 : 1);
-    float* po = P.part_o + slot * 16 * D;
-    float* pml = P.part_ml + slot * 32;
-    // a row's maximum and sum over the warps
-    auto row_state = [&](int h, float& top, float& den) {
-      top = -INFINITY;
+  }
+  __syncthreads();
+  const bool alone = pieces_of(cc) == 1;
+  const size_t slot = (size_t)blockIdx.x * 2 + (p0 == c0 ? 0 : 1);
+  float* po = P.part_o + slot * 16 * D;
+  float* pml = P.part_ml + slot * 32;
+  if (tid < S::kRows) {
+    float top = -INFINITY, den = 0.f;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_ml[w * S::kRows + h]);
-      den = 0.f;
+    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_ml[w * S::kRows + tid]);
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float mw = s_ml[w * S::kRows + h];
-        if (mw != -INFINITY) den += s_ml[(kWarps + w) * S::kRows + h] * exp2_fast(mw - top);
-      }
-    };
-    // out = sum * final_scale(h): the sink joins the denominator here
-    auto finish = [&](int h, float top, float den, float& mul, float& lse) {
-      const float vs = k8 ? __ldg(P.v_scale + kvh) : 1.f;
-      float ref = top;
-      if (P.sinks) {
-        const float sink = __ldg(P.sinks + head0 + h) * kLog2e;
-        ref = fmaxf(top, sink);
-        const float down = top == -INFINITY ? 0.f : exp2_fast(top - ref);
-        den = den * down + (sink == -INFINITY ? 0.f : exp2_fast(sink - ref));
-        mul = den == 0.f ? 0.f : vs * down / den;
-      } else {
-        mul = den == 0.f ? 0.f : vs / den;
-      }
-      lse = ref == -INFINITY ? -INFINITY : (ref + log2f(den)) * kLn2;
-    };
-    auto store_out = [&](int h, int d, float a, float b) {
-      uint32_t* at = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(P.out) +
-                                                 ((size_t)cc.r * P.heads + head0 + h) * D + d);
-      *at = P.q_type == kBf16 ? pack<true>(a, b) : pack<false>(a, b);
-    };
-    if (tid < S::kRows) {
-      float top, den;
-      row_state(tid, top, den);
-      if (!alone) {
-        pml[tid] = top;
-        pml[16 + tid] = den;
-      } else if (tid < rows_here && P.lse) {
-        float mul, lse;
-        finish(tid, top, den, mul, lse);
-        P.lse[(size_t)cc.r * P.heads + head0 + tid] = lse;
-      }
-    }
-#pragma unroll
-    for (int c = 0; c < D / S::kChunk; ++c) {
-      constexpr int kDt = S::kChunk / 16;
-#pragma unroll
-      for (int dd = 0; dd < kDt; ++dd)
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int h = n * 8 + 2 * t4 + (i & 1);
-            const int d = dd * 16 + (k8 ? 2 * g + (i >> 1) : g + 8 * (i >> 1));
-            s_sum[(wid * S::kRows + h) * S::kPitch + d] =
-                o[c * kDt + dd][n][i] * mine_f[n][i & 1];
-          }
-      __syncthreads();
-      for (int e = tid; e < S::kRows * S::kChunk / 2; e += S::kThreads) {
-        const int h = e / (S::kChunk / 2), d = e % (S::kChunk / 2) * 2;
-        float a = 0.f, b = 0.f;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          const float2 v =
-              *reinterpret_cast<const float2*>(s_sum + (w * S::kRows + h) * S::kPitch + d);
-          a += v.x;
-          b += v.y;
-        }
-        if (!alone) {
-          *reinterpret_cast<float2*>(po + h * D + c * S::kChunk + d) = make_float2(a, b);
-        } else if (h < rows_here) {
-          float top, den, mul, lse;
-          row_state(h, top, den);
-          finish(h, top, den, mul, lse);
-          store_out(h, c * S::kChunk + d, a * mul, b * mul);
-        }
-      }
-      __syncthreads();
+    for (int w = 0; w < kWarps; ++w) {
+      const float mw = s_ml[w * S::kRows + tid];
+      if (mw != -INFINITY) den += s_ml[(kWarps + w) * S::kRows + tid] * exp2_fast(mw - top);
     }
     if (!alone) {
-      // ---- join: the last piece to arrive sums all of them, in order ----
-      if (tid == 0) {
-        __threadfence();
-        const int item = cc.r * per + cc.sub;
-        const uint32_t before = atomicAdd(P.arrived + item, 1u);
-        s_flag = before + 1 == (uint32_t)pieces;
-        if (s_flag) P.arrived[item] = 0;      // for the next launch
-        __threadfence();
-      }
-      __syncthreads();
-      if (s_flag) {
-        // the slot of a piece: a CTA's first piece unless the row began inside it
-        auto slot_of = [&](int p) {
-          const int cta = first_cta + p;
-          return (size_t)cta * 2 + (cta * U >= cc.begin ? 0 : 1);
-        };
-        float* wgt = s_sum;                    // [pieces][kRows]
-        if (wid < kWarps) {
-          for (int h = wid; h < rows_here; h += kWarps) {
-            float top = -INFINITY;
-            for (int p = lane; p < pieces; p += 32)
-              top = fmaxf(top, __ldcg(P.part_ml + slot_of(p) * 32 + h));
-#pragma unroll
-            for (int x = 16; x > 0; x >>= 1)
-              top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-            float den = 0.f;
-            for (int p = lane; p < pieces; p += 32) {
-              const float mp = __ldcg(P.part_ml + slot_of(p) * 32 + h);
-              const float w = mp == -INFINITY ? 0.f : exp2_fast(mp - top);
-              wgt[p * S::kRows + h] = w;
-              den += w * __ldcg(P.part_ml + slot_of(p) * 32 + 16 + h);
-            }
-#pragma unroll
-            for (int x = 16; x > 0; x >>= 1) den += __shfl_xor_sync(0xffffffffu, den, x);
-            float mul, lse;
-            finish(h, top, den, mul, lse);
-            if (lane == 0) {
-              s_ml[h] = mul;
-              if (P.lse) P.lse[(size_t)cc.r * P.heads + head0 + h] = lse;
-            }
-          }
-        }
-        __syncthreads();
-        for (int e = tid; e < rows_here * D / 4; e += S::kThreads) {
-          const int h = e / (D / 4), d = e % (D / 4) * 4;
-          float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-          for (int p = 0; p < pieces; ++p) {
-            const float4 v =
-                __ldcg(reinterpret_cast<const float4*>(P.part_o + slot_of(p) * 16 * D + h * D + d));
-            const float w = wgt[p * S::kRows + h];
-            acc.x += w * v.x;
-            acc.y += w * v.y;
-            acc.z += w * v.z;
-            acc.w += w * v.w;
-          }
-          const float mul = s_ml[h];
-          store_out(h, d, acc.x * mul, acc.y * mul);
-          store_out(h, d + 2, acc.z * mul, acc.w * mul);
-        }
-      }
-      __syncthreads();
+      pml[tid] = top;
+      pml[16 + tid] = den;
+    } else {
+      float mul, lse;
+      finish<S>(P, kvh, head0 + (tid < rows_here ? tid : 0), top, den, mul, lse);
+      s_mul[tid] = mul;                                // read after the slices' barrier
+      if (tid < rows_here && P.lse) P.lse[(size_t)cc.r * P.heads + head0 + tid] = lse;
     }
-    p0 = p1;
   }
+  float mine_f[NT][2];      // this warp's factor per column
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int h = n * 8 + 2 * t4 + i;
+      float top = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_ml[w * S::kRows + h]);
+      mine_f[n][i] = m[n][i] == -INFINITY ? 0.f : exp2_fast(m[n][i] - top);
+    }
+#pragma unroll
+  for (int sl = 0; sl < D / S::kSlice; ++sl) {
+    constexpr int kDt = S::kSlice / 16;
+#pragma unroll
+    for (int dd = 0; dd < kDt; ++dd)
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int h = n * 8 + 2 * t4 + (i & 1);
+          const int d = dd * 16 + (k8 ? 2 * g + (i >> 1) : g + 8 * (i >> 1));
+          s_sum[(wid * S::kRows + h) * S::kPitch + d] =
+              o[sl * kDt + dd][n][i] * mine_f[n][i & 1];
+        }
+    __syncthreads();
+    for (int e = tid; e < S::kRows * S::kSlice / 2; e += S::kThreads) {
+      const int h = e / (S::kSlice / 2), d = e % (S::kSlice / 2) * 2;
+      float x = 0.f, y = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float2 v =
+            *reinterpret_cast<const float2*>(s_sum + (w * S::kRows + h) * S::kPitch + d);
+        x += v.x;
+        y += v.y;
+      }
+      if (!alone)
+        *reinterpret_cast<float2*>(po + h * D + sl * S::kSlice + d) = make_float2(x, y);
+      else if (h < rows_here)
+        store_out(P, cc.r, head0 + h, D, sl * S::kSlice + d, x * s_mul[h], y * s_mul[h]);
+    }
+    __syncthreads();
+  }
+  if (!alone && tid == 0) s_last[p0 == c0 ? 0 : 1] = arrive(cc);
+  __syncthreads();
+  // ---- rows of several shares whose last piece this was ----
+  if (s_last[0]) {
+    const Item<S> it = p0 == c0 ? cc : item_at<S>(P, s_prefix, per, c0, bad);
+    join_row<S>(P, it, U, pieces_of(it), s_sum, s_mul);
+  }
+  if (s_last[1]) join_row<S>(P, cc, U, pieces_of(cc), s_sum, s_mul);
   if (bad) atomicOr(P.err, bad);
 }
 
@@ -875,6 +1034,8 @@ cudaError_t launch_kv_attend(const moe_reader_kv& kv, const moe_reader_kv_attend
   P.q_request = a.q_request_stride;
   P.q_head = a.q_head_stride;
   P.q_type = a.q_type;
+  P.q_pairs = reinterpret_cast<uintptr_t>(a.q) % 4 == 0 && a.q_request_stride % 2 == 0 &&
+              a.q_head_stride % 2 == 0;
   P.requests = a.requests;
   P.width = a.width;
   P.keep = a.keep;

@@ -471,9 +471,8 @@ int moe_reader_kv_create(const moe_reader_kv_config* cfg, void* k, void* v, int8
   while ((1 << kv->page_shift) < cfg->page_size) kv->page_shift++;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaGetDevice(&kv->device);
-  const size_t sms_most = 256;
-  const size_t o_bytes = sms_most * 2 * 16 * cfg->head_dim * sizeof(float);
-  const size_t ml_bytes = sms_most * 2 * 2 * 16 * sizeof(float);
+  const size_t o_bytes = (size_t)mr::kMaxSms * 2 * 16 * cfg->head_dim * sizeof(float);
+  const size_t ml_bytes = (size_t)mr::kMaxSms * 2 * 2 * 16 * sizeof(float);
   const size_t items = (size_t)cfg->max_requests * cfg->num_kv_heads * mr::attend_row_tiles(*cfg);
   const size_t c_bytes = (items * 4 + 255) & ~(size_t)255;
   const size_t bytes = o_bytes + ml_bytes + c_bytes + 256;
@@ -491,7 +490,7 @@ int moe_reader_kv_create(const moe_reader_kv_config* cfg, void* k, void* v, int8
     if ((ce = cudaDeviceGetAttribute(&kv->sms, cudaDevAttrMultiProcessorCount, kv->device)) !=
         cudaSuccess)
       break;
-    kv->sms = std::min<int>(kv->sms, (int)sms_most);
+    kv->sms = std::min(kv->sms, mr::kMaxSms);
     if ((ce = mr::configure_kv_attend(*kv)) != cudaSuccess) break;
     if ((ce = mr::configure_kv_select(*kv)) != cudaSuccess) break;
     if ((ce = cudaMemsetAsync(kv->base, 0, bytes, s)) != cudaSuccess) break;
@@ -595,6 +594,7 @@ int moe_reader_kv_status(moe_reader_kv_t* kv, uint32_t* bits_out) {
     return status_of(ce);
   if ((ce = cudaMemset(kv->err, 0, 4)) != cudaSuccess) return status_of(ce);
   if (bits_out) *bits_out = bits;
+  if (bits & MOE_READER_ERR_TIMEOUT) return MOE_READER_ETIMEOUT;
   return bits ? MOE_READER_EDEVICE : MOE_READER_OK;
 }
 
