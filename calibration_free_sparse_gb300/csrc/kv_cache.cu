@@ -154,57 +154,114 @@ constexpr int kAppendThreads = 128;
 template <int CT> struct Cell { using type = uint16_t; };
 template <> struct Cell<MOE_READER_TYPE_E4M3> { using type = uint8_t; };
 
-__device__ __forceinline__ float widen(uint16_t u, int type) {
-  return type == MOE_READER_TYPE_BF16 ? __uint_as_float((uint32_t)u << 16)
-                                      : __half2float(__ushort_as_half(u));
-}
-__device__ __forceinline__ float widen(uint8_t u, int) {
-  __nv_fp8_e4m3 v;
-  v.__x = u;
-  return (float)v;
-}
+// x / scale for values that are then rounded to e4m3: Markstein's correction
+// of x * (1 / scale) by one fused step gives the rounded quotient where
+// nothing over- or underflows (IBM J. Res. Dev. 34, 1990).  Quotients above
+// 1024 saturate as they are; ones so small that the step underflows round to
+// zero either way.  Scales outside [2^-100, 2^100] take the plain division.
+struct Divider {
+  float scale, inv;
+  bool plain;
+  __device__ __forceinline__ explicit Divider(float s) {
+    scale = s;
+    inv = __frcp_rn(s);
+    plain = !(s >= two_to(-100) && s <= two_to(100));
+  }
+  __device__ __forceinline__ float operator()(float x) const {
+    if (plain) return __fdiv_rn(x, scale);
+    const float q = x * inv;
+    return fabsf(q) < 1024.f ? fmaf(fmaf(-q, scale, x), inv, q) : q;
+  }
+};
 
-// Eight values of a row as the cache stores them.
+// Pairs of values of the cache's type.  The largest and smallest keys are
+// taken in that type (e4m3 in fp16, which holds all its values); a NaN is
+// passed over.
+template <int CT> struct Pair { using type = __half2; };
+template <> struct Pair<MOE_READER_TYPE_BF16> { using type = __nv_bfloat162; };
+
+template <typename P> __device__ __forceinline__ P as_pair(uint32_t v) {
+  return *reinterpret_cast<const P*>(&v);
+}
+template <typename P> __device__ __forceinline__ uint32_t bits_of(P v) {
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ float2 widen2(__half2 v) { return __half22float2(v); }
+__device__ __forceinline__ float2 widen2(__nv_bfloat162 v) { return __bfloat1622float2(v); }
+
+// Eight new values of a row as the cache stores them: 16 bytes, or 8 of e4m3
+// (in words 0 and 1).
 template <int CT>
-__device__ __forceinline__ void load_new(const uint16_t* p, bool wide, int type, float scale,
-                                         typename Cell<CT>::type (&out)[8]) {
-  __align__(16) uint16_t in[8];
+__device__ __forceinline__ uint4 load_new(const uint16_t* p, bool wide, int type,
+                                          const Divider& by) {
+  uint4 in;
   if (wide) {
-    *reinterpret_cast<uint4*>(in) = *reinterpret_cast<const uint4*>(p);
+    in = __ldg(reinterpret_cast<const uint4*>(p));
   } else {
+    uint32_t w[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) in[i] = p[i];
+    for (int i = 0; i < 4; ++i)
+      w[i] = (uint32_t)__ldg(p + 2 * i) | (uint32_t)__ldg(p + 2 * i + 1) << 16;
+    in = make_uint4(w[0], w[1], w[2], w[3]);
   }
+  if constexpr (CT == MOE_READER_TYPE_E4M3) {
+    const uint32_t w[4] = {in.x, in.y, in.z, in.w};
+    uint32_t r[4];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    if constexpr (CT == MOE_READER_TYPE_E4M3) {
+    for (int i = 0; i < 4; ++i) {
+      float2 f;
+      if (type == MOE_READER_TYPE_BF16)
+        f = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+      else
+        f = __half22float2(as_pair<__half2>(w[i]));
       // the conversion saturates at +-448 and keeps NaN
-      out[i] = __nv_cvt_float_to_fp8(__fdiv_rn(widen(in[i], type), scale), __NV_SATFINITE,
-                                     __NV_E4M3);
-    } else {
-      out[i] = in[i];
+      r[i] = __nv_cvt_float2_to_fp8x2(make_float2(by(f.x), by(f.y)), __NV_SATFINITE, __NV_E4M3);
     }
+    return make_uint4(r[0] | r[1] << 16, r[2] | r[3] << 16, 0, 0);
+  } else {
+    return in;
+  }
+}
+template <int CT> __device__ __forceinline__ void put8(void* p, uint4 v) {
+  if constexpr (CT == MOE_READER_TYPE_E4M3) *static_cast<uint2*>(p) = make_uint2(v.x, v.y);
+  else *static_cast<uint4*>(p) = v;
+}
+template <int CT> __device__ __forceinline__ uint4 get8(const void* p) {
+  if constexpr (CT == MOE_READER_TYPE_E4M3) {
+    const uint2 v = *static_cast<const uint2*>(p);
+    return make_uint4(v.x, v.y, 0, 0);
+  } else {
+    return *static_cast<const uint4*>(p);
+  }
+}
+// The four pairs of a row's eight stored values.
+template <int CT>
+__device__ __forceinline__ void pairs_of(uint4 v, typename Pair<CT>::type (&p)[4]) {
+  if constexpr (CT == MOE_READER_TYPE_E4M3) {
+    const uint32_t w[2] = {v.x, v.y};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __half2_raw r = __nv_cvt_fp8x2_to_halfraw2(
+          (__nv_fp8x2_storage_t)(w[i >> 1] >> (16 * (i & 1))), __NV_E4M3);
+      p[i] = __half2(r);
+    }
+  } else {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) p[i] = as_pair<typename Pair<CT>::type>(w[i]);
   }
 }
 
-template <typename C>
-__device__ __forceinline__ void store8(C* p, const C (&v)[8]) {
-  if constexpr (sizeof(C) == 2) *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(v);
-  else *reinterpret_cast<uint2*>(p) = *reinterpret_cast<const uint2*>(v);
-}
-template <typename C>
-__device__ __forceinline__ void load8(const C* p, C (&v)[8]) {
-  if constexpr (sizeof(C) == 2) *reinterpret_cast<uint4*>(v) = *reinterpret_cast<const uint4*>(p);
-  else *reinterpret_cast<uint2*>(v) = *reinterpret_cast<const uint2*>(p);
-}
-
-// One CTA takes `window` consecutive tokens of one KV head.  The work is done
-// once per page: by the token that is the last new one of its page, for the
-// run of new tokens that ends with it (their slots are consecutive).  It
-// copies the run's rows and, over the page's rows up to that token -- the
-// older ones read from the cache, the new ones from the input -- forms the
-// largest and smallest key per coordinate, so the summary needs no second
-// pass and no other CTA's writes.  D / 8 lanes share a row, 8 values each.
+// One CTA looks at `window` (at most 32) consecutive tokens for one KV head,
+// for their keys (blockIdx.z 0) or their values (1), so that a prompt's pages
+// are twice as many independent chains of loads.  Values are copied row by row.
+// Keys are taken once per page: for the token that is the last new one of its
+// page, with the run of new tokens that ends there (their slots are
+// consecutive).  It copies the run's rows and, over the page's rows up to that
+// token -- the older ones read from the cache, the new ones from the input --
+// forms the largest and smallest key per coordinate, so the summary needs no
+// second pass and no other CTA's writes.  D / 8 lanes share a row, 8 values
+// each; a thread has kAhead rows in flight.
 template <int D, int CT>
 __global__ void __launch_bounds__(kAppendThreads)
 append_kernel(moe_reader_kv_append_args a, typename Cell<CT>::type* __restrict__ kc,
@@ -212,70 +269,103 @@ append_kernel(moe_reader_kv_append_args a, typename Cell<CT>::type* __restrict__
               float* __restrict__ steps, const float* __restrict__ k_scale,
               const float* __restrict__ v_scale, int heads, int shift, int num_pages, int window,
               bool wide_k, bool wide_v, uint32_t* err) {
-  using C = typename Cell<CT>::type;
+  using P2 = typename Pair<CT>::type;
   constexpr int kLanes = D / 8;                          // lanes of a row
   constexpr int kRows = kAppendThreads / kLanes;         // rows at a time
   constexpr int kWarps = kAppendThreads / 32;
-  __shared__ float s_hi[kWarps][D], s_lo[kWarps][D];
+  constexpr int kAhead = 4;
+  __shared__ uint32_t s_hi[kWarps][D / 2], s_lo[kWarps][D / 2];
   __shared__ float s_max[kWarps];
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
   const int head = blockIdx.y, ps = 1 << shift;
   const int col = (tid % kLanes) * 8, row0 = tid / kLanes;
   const long long slots_all = (long long)num_pages << shift;
-  float ks = 1.f, vs = 1.f;
-  if constexpr (CT == MOE_READER_TYPE_E4M3) {
-    ks = k_scale[head];
-    vs = v_scale[head];
-  }
-  const uint16_t* kin = static_cast<const uint16_t*>(a.k) + head * a.k_head_stride + col;
-  const uint16_t* vin = static_cast<const uint16_t*>(a.v) + head * a.v_head_stride + col;
 
   const long long first = (long long)blockIdx.x * window;
-  const int last = (int)min(first + window, (long long)a.tokens);
-  for (int t = (int)first; t < last; ++t) {
-    const int slot = __ldg(a.slots + t);
-    if (slot < 0 || slot >= slots_all) {
-      if (slot != -1 && tid == 0) atomicOr(err, kErrPage);
-      continue;
+  if (blockIdx.z) {
+    const Divider vd(CT == MOE_READER_TYPE_E4M3 ? v_scale[head] : 1.f);
+    const uint16_t* vin = static_cast<const uint16_t*>(a.v) + head * a.v_head_stride + col;
+    const int n = (int)min((long long)window, a.tokens - first);
+#pragma unroll 2
+    for (int i = row0; i < n; i += kRows) {
+      const int slot = __ldg(a.slots + first + i);
+      const uint4 v = load_new<CT>(vin + (first + i) * a.v_token_stride, wide_v, a.type, vd);
+      if (slot < 0 || slot >= slots_all) continue;
+      const size_t row = (((size_t)(slot >> shift) * heads + head) << shift) + (slot & (ps - 1));
+      put8<CT>(vc + row * D + col, v);
     }
-    const int off = slot & (ps - 1);
-    if (off != ps - 1 && t + 1 < a.tokens && __ldg(a.slots + t + 1) == slot + 1) continue;
-    // the run of new tokens that ends here: its first offset in the page
+    return;
+  }
+
+  // the tokens of the window that close their page's run (the same in every warp)
+  const long long mine = first + lane;
+  int slot_l = -1;
+  bool closes = false;
+  if (lane < window && mine < a.tokens) {
+    slot_l = __ldg(a.slots + mine);
+    const int after = mine + 1 < a.tokens ? __ldg(a.slots + mine + 1) : -1;
+    if (slot_l >= 0 && slot_l < slots_all)
+      closes = (slot_l & (ps - 1)) == ps - 1 || after != slot_l + 1;
+    else if (slot_l != -1 && wid == 0)
+      atomicOr(err, kErrPage);
+  }
+  uint32_t todo = __ballot_sync(0xffffffffu, closes);
+  if (!todo) return;
+
+  const Divider kd(CT == MOE_READER_TYPE_E4M3 ? k_scale[head] : 1.f);
+  const uint16_t* kin = static_cast<const uint16_t*>(a.k) + head * a.k_head_stride + col;
+  for (; todo; todo &= todo - 1) {
+    const int w = __ffs(todo) - 1;
+    const long long t = first + w;
+    const int slot = __shfl_sync(0xffffffffu, slot_l, w), off = slot & (ps - 1);
+    // the run of new tokens that ends here: its first offset in the page (the
+    // loads of up to 256 slots before it go out together)
     int run0 = 0;
-    for (int b = 1; b <= off; b += 32) {
-      const int back = b + lane;
-      const bool in = back <= off && t >= back && __ldg(a.slots + t - back) == slot - back;
-      const uint32_t out = __ballot_sync(0xffffffffu, !in);
-      if (out) {
-        run0 = off - (b + __ffs(out) - 1) + 1;
-        break;
+    if (off) {
+      int before[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int back = 32 * i + 1 + lane;
+        before[i] = -1;
+        if (back <= off && t >= back) before[i] = __ldg(a.slots + t - back);
+      }
+#pragma unroll
+      for (int i = 7; i >= 0; --i) {
+        const int back = 32 * i + 1 + lane;
+        const uint32_t out = __ballot_sync(0xffffffffu, before[i] != slot - back);
+        if (out) run0 = max(0, off - (32 * i + __ffs(out) - 1));
       }
     }
     const size_t page = ((size_t)(slot >> shift) * heads + head) << shift;   // first row
-    float hi[8], lo[8];
+    P2 hi[4], lo[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) hi[i] = -INFINITY, lo[i] = INFINITY;
-    const int from = codes ? 0 : run0;
-#pragma unroll 2
-    for (int o = from + row0; o <= off; o += kRows) {
-      __align__(16) C kr[8];
-      C* at = kc + (page + o) * D + col;
-      if (o >= run0) {
-        const long long tt = t - (off - o);
-        __align__(16) C vr[8];
-        load_new<CT>(kin + tt * a.k_token_stride, wide_k, a.type, ks, kr);
-        load_new<CT>(vin + tt * a.v_token_stride, wide_v, a.type, vs, vr);
-        store8(at, kr);
-        store8(vc + (page + o) * D + col, vr);
-      } else {
-        load8(at, kr);
+    for (int i = 0; i < 4; ++i) hi[i] = lo[i] = as_pair<P2>(0x7fff7fffu);    // NaN: nothing yet
+    for (int o0 = (codes ? 0 : run0) + row0; o0 <= off; o0 += kRows * kAhead) {
+      uint4 kr[kAhead];
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        const int o = o0 + j * kRows;
+        if (o > off) continue;
+        if (o >= run0) {
+          const long long tt = t - (off - o);
+          kr[j] = load_new<CT>(kin + tt * a.k_token_stride, wide_k, a.type, kd);
+        } else {
+          kr[j] = get8<CT>(kc + (page + o) * D + col);
+        }
       }
-      if (codes) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float f = widen(kr[i], CT);
-          hi[i] = fmaxf(hi[i], f);
-          lo[i] = fminf(lo[i], f);
+      for (int j = 0; j < kAhead; ++j) {
+        const int o = o0 + j * kRows;
+        if (o > off) continue;
+        if (o >= run0) put8<CT>(kc + (page + o) * D + col, kr[j]);
+        if (codes) {
+          P2 p[4];
+          pairs_of<CT>(kr[j], p);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            hi[i] = __hmax2(hi[i], p[i]);
+            lo[i] = __hmin2(lo[i], p[i]);
+          }
         }
       }
     }
@@ -284,58 +374,61 @@ append_kernel(moe_reader_kv_append_args a, typename Cell<CT>::type* __restrict__
 #pragma unroll
     for (int o = kLanes; o < 32; o <<= 1)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        hi[i] = fmaxf(hi[i], __shfl_xor_sync(0xffffffffu, hi[i], o));
-        lo[i] = fminf(lo[i], __shfl_xor_sync(0xffffffffu, lo[i], o));
+      for (int i = 0; i < 4; ++i) {
+        hi[i] = __hmax2(hi[i], as_pair<P2>(__shfl_xor_sync(0xffffffffu, bits_of(hi[i]), o)));
+        lo[i] = __hmin2(lo[i], as_pair<P2>(__shfl_xor_sync(0xffffffffu, bits_of(lo[i]), o)));
       }
     if (lane < kLanes) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        s_hi[wid][lane * 8 + i] = hi[i];
-        s_lo[wid][lane * 8 + i] = lo[i];
+      for (int i = 0; i < 4; ++i) {
+        s_hi[wid][lane * 4 + i] = bits_of(hi[i]);
+        s_lo[wid][lane * 4 + i] = bits_of(lo[i]);
       }
     }
     __syncthreads();
-    constexpr int kPer = (D + kAppendThreads - 1) / kAppendThreads;
-    float h[kPer], l[kPer], top = 0.f;
+    // thread d < D / 2 has two coordinates
+    static_assert(D / 2 <= kAppendThreads, "a thread per pair");
+    float2 h = make_float2(-INFINITY, -INFINITY), l = make_float2(INFINITY, INFINITY);
+    float top = 0.f;
+    if (tid < D / 2) {
+      P2 hp = as_pair<P2>(s_hi[0][tid]), lp = as_pair<P2>(s_lo[0][tid]);
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-      const int d = tid + j * kAppendThreads;
-      h[j] = -INFINITY;
-      l[j] = INFINITY;
-      if (d < D) {
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          h[j] = fmaxf(h[j], s_hi[w][d]);
-          l[j] = fminf(l[j], s_lo[w][d]);
-        }
-        top = fmaxf(top, fmaxf(fabsf(h[j]), fabsf(l[j])));
+      for (int v = 1; v < kWarps; ++v) {
+        hp = __hmax2(hp, as_pair<P2>(s_hi[v][tid]));
+        lp = __hmin2(lp, as_pair<P2>(s_lo[v][tid]));
       }
+      h = widen2(hp);
+      l = widen2(lp);
+      // a coordinate whose keys are all NaN: the empty range
+      if (h.x != h.x) h.x = -INFINITY, l.x = INFINITY;
+      if (h.y != h.y) h.y = -INFINITY, l.y = INFINITY;
+      top = fmaxf(fmaxf(fabsf(h.x), fabsf(l.x)), fmaxf(fabsf(h.y), fabsf(l.y)));
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     if (lane == 0) s_max[wid] = top;
     __syncthreads();
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_max[w]);
+    for (int v = 0; v < kWarps; ++v) top = fmaxf(top, s_max[v]);
     top = fminf(fmaxf(top, two_to(-100)), two_to(100));
     int e = floor_log2_held(top) - 6;
     if (top > 127.f * two_to(e)) ++e;
     const float inv = two_to(-e);
     const size_t at = (size_t)(slot >> shift) * heads + head;
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-      const int d = tid + j * kAppendThreads;
-      if (d < D) {
-        // a power-of-two step: the quotients are exact, but for those that
-        // underflow, which still round away from zero
-        float up = fminf(fmaxf(ceilf(h[j] * inv), -127.f), 127.f);
-        float down = fminf(fmaxf(floorf(l[j] * inv), -127.f), 127.f);
-        if (h[j] > 0.f) up = fmaxf(up, 1.f);
-        if (l[j] < 0.f) down = fminf(down, -1.f);
-        codes[at * 2 * D + d] = (int8_t)up;
-        codes[at * 2 * D + D + d] = (int8_t)down;
-      }
+    if (tid < D / 2) {
+      // a power-of-two step: the quotients are exact, but for those that
+      // underflow, which still round away from zero
+      auto up = [&](float v) {
+        const float c = fminf(fmaxf(ceilf(v * inv), -127.f), 127.f);
+        return (int)(v > 0.f ? fmaxf(c, 1.f) : c);
+      };
+      auto down = [&](float v) {
+        const float c = fminf(fmaxf(floorf(v * inv), -127.f), 127.f);
+        return (int)(v < 0.f ? fminf(c, -1.f) : c);
+      };
+      char2* out = reinterpret_cast<char2*>(codes + at * 2 * D);
+      out[tid] = make_char2((char)up(h.x), (char)up(h.y));
+      out[D / 2 + tid] = make_char2((char)down(l.x), (char)down(l.y));
     }
     if (tid == 0) steps[at] = two_to(e);
     __syncthreads();   // s_hi, s_lo and s_max are free again
@@ -345,15 +438,16 @@ append_kernel(moe_reader_kv_append_args a, typename Cell<CT>::type* __restrict__
 template <int D, int CT>
 void append_as(const moe_reader_kv& kv, const moe_reader_kv_append_args& a, cudaStream_t s) {
   using C = typename Cell<CT>::type;
-  // A window of one token where that fills the GPU a few times over at most
-  // (a decode step: every token closes its page's run); longer windows keep a
-  // prompt's grid from being mostly CTAs whose token closes nothing.
+  // A window of one token while that is a few CTAs per SM (a decode step: every
+  // token closes its page's run); longer windows keep a prompt's grid from
+  // being mostly CTAs whose token closes nothing.
   const int heads = kv.cfg.num_kv_heads;
-  const int window = std::min(64, std::max(1, (int)((long long)a.tokens * heads / 4096)));
+  const int window =
+      (int)std::min(32LL, std::max(1LL, (long long)a.tokens * heads / (16 * kv.sms)));
   auto wide = [](const void* p, int64_t ts, int64_t hs) {
     return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ts % 8 == 0 && hs % 8 == 0;
   };
-  const dim3 grid((unsigned)((a.tokens + window - 1) / window), (unsigned)heads);
+  const dim3 grid((unsigned)((a.tokens + window - 1) / window), (unsigned)heads, 2);
   append_kernel<D, CT><<<grid, kAppendThreads, 0, s>>>(
       a, static_cast<C*>(kv.k), static_cast<C*>(kv.v), kv.codes, kv.steps, kv.k_scale, kv.v_scale,
       heads, kv.page_shift, kv.cfg.num_pages, window, wide(a.k, a.k_token_stride, a.k_head_stride),
