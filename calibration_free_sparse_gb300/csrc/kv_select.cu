@@ -28,6 +28,7 @@ namespace {
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 2048;
+constexpr int kMostCtas = 16;                  // CTAs of a cluster (above 8 on request)
 constexpr uint32_t kForced = 0xffffffffu;      // above every score's key
 
 struct Params {
@@ -65,6 +66,8 @@ template <int D>
 __global__ void __launch_bounds__(kThreads) select_kernel(const Params P) {
   constexpr int kLanes = D / 8;                 // lanes of a page: 16 bytes each of 2D
   constexpr int kGroups = 32 / kLanes;          // pages a warp loads at a time
+  constexpr int kHold = kLanes < 16 ? kLanes : 16;   // loads in flight per lane
+  constexpr int kPages = kHold * kGroups;       // a warp's batch
   extern __shared__ uint32_t s_keys[];          // first CTA: a key per page
   __shared__ __align__(16) int8_t s_q[2 * D];
   __shared__ float s_red[kWarps];
@@ -93,6 +96,38 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const Params P) {
     return;
   }
 
+  // ---- this CTA's pages; the first batch's summaries are on their way while
+  // the query is coded ----
+  const int32_t* table = a.table + (size_t)r * a.width;
+  const int share = ((held + ctas - 1) / ctas + 31) & ~31;
+  const int p_end = min(held, (rank + 1) * share);
+  const int sub = lane / kLanes;
+  // the lane's own page after the sums: load (lane % kHold), group sub
+  const int own = (lane % kHold) * kGroups + sub;
+  const bool owns = lane % kLanes < kHold;
+  int4 c[kHold];
+  int own_id = -1;
+  float step = 0.f;
+  auto fetch = [&](int base) {
+    int id = -1;
+    if (lane < kPages && base + lane < p_end) {
+      id = __ldg(table + base + lane);
+      if (id < 0 || id >= P.num_pages) bad |= kErrPage, id = -1;
+    }
+    own_id = __shfl_sync(0xffffffffu, id, own);
+#pragma unroll
+    for (int i = 0; i < kHold; ++i) {
+      const int at = __shfl_sync(0xffffffffu, id, i * kGroups + sub);
+      c[i] = make_int4(0, 0, 0, 0);
+      if (at >= 0)
+        c[i] = __ldg(reinterpret_cast<const int4*>(
+            P.codes + ((size_t)at * P.kv_heads + head) * 2 * D + 16 * (lane % kLanes)));
+    }
+    step = own_id >= 0 ? __ldg(P.steps + (size_t)own_id * P.kv_heads + head) : 0.f;
+  };
+  int base = rank * share + wid * kPages;
+  fetch(base);
+
   // ---- the group's query as 7-bit codes ----
   const uint16_t* q = static_cast<const uint16_t*>(a.q) + r * a.q_request_stride +
                       (long long)head * P.group * a.q_head_stride;
@@ -102,6 +137,7 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const Params P) {
   const float up = two_to(13 - floor_log2_held(block_max(top, s_red)));
   float pos = 0.f, neg = 0.f;                   // integers below 2^21: exact
   if (tid < D) {
+#pragma unroll 4
     for (int g = 0; g < P.group; ++g) {
       // an infinite q is held to the range the codes can express
       const float f = rintf(fminf(fmaxf(load_q(q + g * a.q_head_stride + tid, a.q_type) * up,
@@ -118,41 +154,29 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const Params P) {
   }
   cluster.sync();                               // s_q is ready; the first CTA has started
 
-  // ---- scores of this CTA's pages ----
+  // ---- scores ----
   uint32_t* keys = cluster.map_shared_rank(s_keys, 0);
   const int4 mine = *reinterpret_cast<const int4*>(s_q + 16 * (lane % kLanes));
-  const int32_t* table = a.table + (size_t)r * a.width;
-  const int share = ((held + ctas - 1) / ctas + 31) & ~31;
-  const int p_end = min(held, (rank + 1) * share);
-  const int sub = lane / kLanes;
-  for (int base = rank * share + wid * 32; base < p_end; base += kWarps * 32) {
-    int id = -1;
-    if (base + lane < p_end) id = __ldg(table + base + lane);
-    if (id < 0 || id >= P.num_pages) {
-      if (base + lane < p_end) bad |= kErrPage;
-      id = -1;
-    }
-    // the lane's own page after the sums: step (lane % kLanes), group sub
-    const int own = (lane % kLanes) * kGroups + sub;
-    const int own_id = __shfl_sync(0xffffffffu, id, own);
-    float step = 0.f;
-    if (own_id >= 0) step = __ldg(P.steps + (size_t)own_id * P.kv_heads + head);
-    int dot[kLanes];
+  while (base < p_end) {
+    int dot[kHold];
 #pragma unroll
-    for (int i = 0; i < kLanes; ++i) {
-      const int at = __shfl_sync(0xffffffffu, id, i * kGroups + sub);
-      int4 c = make_int4(0, 0, 0, 0);
-      if (at >= 0)
-        c = __ldg(reinterpret_cast<const int4*>(
-            P.codes + ((size_t)at * P.kv_heads + head) * 2 * D + 16 * (lane % kLanes)));
-      int v = __dp4a(c.x, mine.x, 0);
-      v = __dp4a(c.y, mine.y, v);
-      v = __dp4a(c.z, mine.z, v);
-      dot[i] = __dp4a(c.w, mine.w, v);
+    for (int i = 0; i < kHold; ++i) {
+      int v = __dp4a(c[i].x, mine.x, 0);
+      v = __dp4a(c[i].y, mine.y, v);
+      v = __dp4a(c[i].z, mine.z, v);
+      dot[i] = __dp4a(c[i].w, mine.w, v);
     }
+    const int page = base + own, id = own_id;
+    const float unit = step;
+    base += kWarps * kPages;
+    if (base < p_end) fetch(base);
     // sums over the lanes of a page, each lane ending with one page's
 #pragma unroll
-    for (int o = kLanes / 2; o > 0; o >>= 1) {
+    for (int o = kLanes / 2; o >= kHold; o >>= 1)
+#pragma unroll
+      for (int i = 0; i < kHold; ++i) dot[i] += __shfl_xor_sync(0xffffffffu, dot[i], o);
+#pragma unroll
+    for (int o = kHold / 2; o > 0; o >>= 1) {
       const bool high = lane & o;
 #pragma unroll
       for (int i = 0; i < o; ++i) {
@@ -161,9 +185,8 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const Params P) {
         dot[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
       }
     }
-    const int page = base + own;
-    if (page < p_end) {
-      uint32_t key = own_id < 0 ? 0u : order_key((float)dot[0] * step);
+    if (owns && page < p_end) {
+      uint32_t key = id < 0 ? 0u : order_key((float)dot[0] * unit);
       if (page < a.first || page >= held - a.last) key = kForced;
       keys[page] = key;
     }
@@ -288,7 +311,7 @@ cudaError_t launch(const Params& P, int sms, cudaStream_t s) {
   // pages per warp at least
   const long long rows = (long long)P.a.requests * P.kv_heads;
   int ctas = 1;
-  while (ctas < 8 && rows * ctas * 2 <= 2LL * sms && P.a.width > ctas * kThreads) ctas *= 2;
+  while (ctas < kMostCtas && rows * ctas <= sms && P.a.width > ctas * kThreads) ctas *= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)ctas, (unsigned)P.kv_heads, (unsigned)P.a.requests);
   cfg.blockDim = dim3(kThreads);
@@ -304,8 +327,10 @@ cudaError_t launch(const Params& P, int sms, cudaStream_t s) {
 
 template <int D>
 cudaError_t configure() {
-  return cudaFuncSetAttribute(select_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              kMaxSelectPages * 4);
+  const cudaError_t e = cudaFuncSetAttribute(
+      select_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSelectPages * 4);
+  if (e != cudaSuccess) return e;
+  return cudaFuncSetAttribute(select_kernel<D>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
 }
 
 }  // namespace
