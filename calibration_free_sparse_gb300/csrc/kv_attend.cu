@@ -48,7 +48,7 @@ struct Shape {
   static constexpr int kWarps = kRow >= 512 ? 4 : 8;
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kStages = kTile <= 4096 ? 6 : 3;
-  static constexpr int kSplit = 24;                          // tiles that a join is worth
+    static constexpr int kSplit = 64;                          // tiles that a join is worth
   static constexpr int kRows = 8 * NT;                       // query heads of a row
   // the sum over the warps at the end runs over slices of the coordinates
   static constexpr int kSlice = 4096 / (kWarps * kRows) < D ? 4096 / (kWarps * kRows) : D;
@@ -61,7 +61,7 @@ struct Shape {
   static constexpr int kSum = kSumA > kSumB ? kSumA : kSumB;
   static constexpr int kMl = kWarps * kRows * 2 * 4;
   static constexpr int kPos = kWarps * kStages * kMt * 4;
-  static constexpr int kSmem = kPipe + kSum + kMl + kPos + (kMaxRequests + 1) * 4;
+  static constexpr int kSmem = kPipe + kSum + kMl + kPos + (2 * kMaxRequests + 1) * 4;
   static_assert(kRows * kMaxSms * 4 <= kSum, "join weights of a piece per CTA");
   static_assert(kSmem + 2048 <= 227 * 1024, "shared memory");
 };
@@ -172,12 +172,9 @@ struct Row {
   int len, lo, base, span;
 };
 
-__device__ __forceinline__ Row row_of(const Params& P, int r, uint32_t& bad) {
+__device__ __forceinline__ Row row_of(const Params& P, int len) {
   Row w;
-  const int room = P.width << P.shift;
-  w.len = __ldg(P.lens + r);
-  if (w.len < 0) w.len = 0, bad |= kErrLength;
-  if (w.len > room) w.len = room, bad |= kErrLength;
+  w.len = len;
   w.lo = P.window ? max(0, w.len - P.window) : 0;
   if (P.pages) {
     w.base = 0;
@@ -203,8 +200,8 @@ struct Item {
 };
 
 template <class S>
-__device__ __forceinline__ Item<S> item_at(const Params& P, const int* prefix, int per, int t,
-                                           uint32_t& bad) {
+__device__ __forceinline__ Item<S> item_at(const Params& P, const int* prefix, const int* lens,
+                                           int per, int t) {
   int lo = 0, hi = P.requests - 1;
   while (lo < hi) {                      // the last request that begins at t or before
     const int mid = (lo + hi + 1) >> 1;
@@ -212,7 +209,7 @@ __device__ __forceinline__ Item<S> item_at(const Params& P, const int* prefix, i
   }
   Item<S> o;
   o.r = lo;
-  o.row = row_of(P, lo, bad);
+  o.row = row_of(P, lens[lo]);
   o.tiles = tiles_of<S>(o.row);
   const int first = prefix[lo] * per, padded = prefix[lo + 1] - prefix[lo];
   o.sub = (t - first) / padded;
@@ -231,10 +228,10 @@ constexpr int kNowhere = INT32_MAX - 64;
 // Source of subtile s of the tile at index t.  The page id is used by the
 // caller only later, so that its load is in flight meanwhile.
 template <class S>
-__device__ __forceinline__ Source source_at(const Params& P, const int* prefix, int per, int t,
-                                            int s, uint32_t& bad) {
+__device__ __forceinline__ Source source_at(const Params& P, const int* prefix, const int* lens,
+                                            int per, int t, int s, uint32_t& bad) {
   Source o;
-  const Item<S> it = item_at<S>(P, prefix, per, t, bad);
+  const Item<S> it = item_at<S>(P, prefix, lens, per, t);
   o.id = 0;
   o.pos = kNowhere;
   o.lo = it.row.lo;
@@ -397,6 +394,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) attend_kernel(const Params P) 
   float* s_ml = reinterpret_cast<float*>(smem + S::kPipe + S::kSum);
   int* s_pos = reinterpret_cast<int*>(smem + S::kPipe + S::kSum + S::kMl);
   int* s_prefix = s_pos + S::kPos / 4;
+  int* s_len = s_prefix + kMaxRequests + 1;
   __shared__ int4 s_scan[kWarps];
   __shared__ int s_before[kWarps];
   __shared__ uint32_t s_turn[2];
@@ -415,7 +413,14 @@ __global__ void __launch_bounds__(S::kThreads, 1) attend_kernel(const Params P) 
   for (int j = 0; j < kPer; ++j) {
     const int r = tid * kPer + j;
     mine[j] = 0;
-    if (r < P.requests) mine[j] = tiles_of<S>(row_of(P, r, bad));
+    if (r < P.requests) {
+      const int room = P.width << P.shift;
+      int len = __ldg(P.lens + r);
+      if (len < 0) len = 0, bad |= kErrLength;
+      if (len > room) len = room, bad |= kErrLength;
+      s_len[r] = len;
+      mine[j] = tiles_of<S>(row_of(P, len));
+    }
     sum += mine[j];
     rows += mine[j] > 0;
     most = max(most, mine[j]);
@@ -519,7 +524,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) attend_kernel(const Params P) 
     const int t = c0 + wid + (n + lane / kMt) * kWarps;
     next.pos = kNowhere;
     next.id = next.head = next.in = next.lo = next.len = 0;
-    if (t < c1) next = source_at<S>(P, s_prefix, per, t, lane % kMt, bad);
+    if (t < c1) next = source_at<S>(P, s_prefix, s_len, per, t, lane % kMt, bad);
   };
   int in_stage = 0, out_stage = 0;
   auto issue = [&]() {
@@ -566,7 +571,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) attend_kernel(const Params P) 
   Item<S> cc;
   int p0 = c0, t = c0 + wid;
   for (int k = 0;; ++k) {
-    cc = item_at<S>(P, s_prefix, per, p0, bad);
+    cc = item_at<S>(P, s_prefix, s_len, per, p0);
     const int p1 = min(c1, cc.end);
     const int real = min(p1, cc.begin + cc.tiles);     // tiles beyond are padding
     const int kvh = cc.sub / P.row_tiles, row0 = (cc.sub % P.row_tiles) * S::kRows;
@@ -890,7 +895,8 @@ __global__ void __launch_bounds__(S::kThreads, 1) attend_kernel(const Params P) 
   }
   __syncthreads();
   const bool alone = pieces_of(cc) == 1;
-  const size_t slot = (size_t)blockIdx.x * 2 + (p0 == c0 ? 0 : 1);
+  const int which = p0 == c0 ? 0 : 1;
+  const size_t slot = (size_t)blockIdx.x * 2 + which;
   float* po = P.part_o + slot * 16 * D;
   float* pml = P.part_ml + slot * 32;
   if (tid < S::kRows) {
@@ -955,14 +961,15 @@ __global__ void __launch_bounds__(S::kThreads, 1) attend_kernel(const Params P) 
     }
     __syncthreads();
   }
-  if (!alone && tid == 0) s_last[p0 == c0 ? 0 : 1] = arrive(cc);
+  if (!alone && tid == 0) s_last[which] = arrive(cc);
   __syncthreads();
-  // ---- rows of several shares whose last piece this was ----
-  if (s_last[0]) {
-    const Item<S> it = p0 == c0 ? cc : item_at<S>(P, s_prefix, per, c0, bad);
+  // ---- rows of several shares whose last piece was written here ----
+#pragma unroll 1
+  for (int e = 0; e < 2; ++e) {
+    if (!s_last[e]) continue;
+    const Item<S> it = item_at<S>(P, s_prefix, s_len, per, e ? c1 - 1 : c0);
     join_row<S>(P, it, U, pieces_of(it), s_sum, s_mul);
   }
-  if (s_last[1]) join_row<S>(P, cc, U, pieces_of(cc), s_sum, s_mul);
   if (bad) atomicOr(P.err, bad);
 }
 
