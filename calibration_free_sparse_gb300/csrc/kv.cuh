@@ -55,6 +55,32 @@ cudaError_t launch_kv_select(const moe_reader_kv& kv, const moe_reader_kv_select
                              cudaStream_t s);
 cudaError_t configure_kv_select(const moe_reader_kv& kv);
 
+// Launch that may start while the stream's previous kernel ends: it has to
+// call wait_for_earlier_launch() before it touches global memory, which returns
+// once that kernel is complete and its writes can be seen.
+template <class... K, class... A>
+inline cudaError_t launch_early(void (*kernel)(K...), dim3 grid, int threads, size_t smem,
+                                cudaStream_t s, const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<K>(args)...);
+}
+__device__ __forceinline__ void wait_for_earlier_launch() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+// Lets such a launch behind this kernel take free SMs already.
+__device__ __forceinline__ void let_next_launch_start() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 // 2^e, -126 <= e <= 127
 __device__ __forceinline__ float two_to(int e) { return __int_as_float((e + 127) << 23); }
 // floor(log2 a) of a finite a >= 0, held to -100 .. 100

@@ -47,11 +47,11 @@ struct Shape {
   static constexpr int kTile = 2 * kKeys * kRow;             // bytes of a tile, K then V
   static constexpr int kWarps = kRow >= 512 ? 4 : 8;
   static constexpr int kThreads = 32 * kWarps;
-  static constexpr int kStages = kTile <= 4096 ? 6 : 3;
+  static constexpr int kStages = 192 * 1024 / (kWarps * kTile);
     static constexpr int kSplit = 64;                          // tiles that a join is worth
   static constexpr int kRows = 8 * NT;                       // query heads of a row
   // the sum over the warps at the end runs over slices of the coordinates
-  static constexpr int kSlice = 4096 / (kWarps * kRows) < D ? 4096 / (kWarps * kRows) : D;
+  static constexpr int kSlice = kWarps * kRows >= 96 ? 32 : 64;
   static constexpr int kPitch = kSlice + 4;
   // two rows' states in shared memory, for the rows that end inside a share
   static constexpr int kAccPitch = D + 4;
@@ -146,9 +146,15 @@ __device__ __forceinline__ uint32_t pack(float lo, float hi) {
   else asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
-__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two) {
+// The lower and the upper two of four e4m3 values.
+__device__ __forceinline__ uint32_t e4m3_low(uint32_t four) {
   uint32_t r;
-  asm("{ .reg .b16 h, u; mov.b32 {h, u}, %1; cvt.rn.f16x2.e4m3x2 %0, h; }" : "=r"(r) : "r"(two));
+  asm("{ .reg .b16 l, h; mov.b32 {l, h}, %1; cvt.rn.f16x2.e4m3x2 %0, l; }" : "=r"(r) : "r"(four));
+  return r;
+}
+__device__ __forceinline__ uint32_t e4m3_high(uint32_t four) {
+  uint32_t r;
+  asm("{ .reg .b16 l, h; mov.b32 {l, h}, %1; cvt.rn.f16x2.e4m3x2 %0, h; }" : "=r"(r) : "r"(four));
   return r;
 }
 __device__ __forceinline__ float load_q(const uint16_t* p, int type) {
@@ -406,8 +412,9 @@ __global__ void __launch_bounds__(S::kThreads, 1) attend_kernel(const Params P) 
   uint32_t bad = 0;
 
   if (tid < 2) s_turn[tid] = 0, s_last[tid] = 0;
+  wait_for_earlier_launch();
   // ---- shares: U tiles per CTA ----
-  constexpr int kPer = kMaxRequests / S::kThreads;
+  constexpr int kPer = (kMaxRequests + S::kThreads - 1) / S::kThreads;
   int mine[kPer], sum = 0, rows = 0, most = 0;
 #pragma unroll
   for (int j = 0; j < kPer; ++j) {
@@ -473,14 +480,15 @@ __global__ void __launch_bounds__(S::kThreads, 1) attend_kernel(const Params P) 
     if (lane == 31) s_before[wid] = in;
     __syncthreads();
     int at = in - run;
-    for (int w = 0; w < wid; ++w) at += s_before[w];
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) at += w < wid ? s_before[w] : 0;
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
       const int r = tid * kPer + j;
-      if (r <= P.requests) s_prefix[r] = at;
+      if (r < P.requests) s_prefix[r] = at;
       at += mine[j];
     }
-    if (tid == S::kThreads - 1 && P.requests == kMaxRequests) s_prefix[kMaxRequests] = at;
+    if (tid == S::kThreads - 1) s_prefix[P.requests] = at;
   }
   __syncthreads();
   const int all = s_prefix[P.requests] * per;
@@ -661,12 +669,12 @@ __global__ void __launch_bounds__(S::kThreads, 1) attend_kernel(const Params P) 
         }
 #pragma unroll
       for (int s = 0; s < kMt; ++s) {
-        const uint32_t kb = ks + s * 16 * S::kRow;
+        const uint32_t kb = ks + s * 16 * S::kRow + k_lane;   // ks: a multiple of the row
         if constexpr (!k8) {
 #pragma unroll
           for (int x = 0; x < D / 16; ++x) {
             uint32_t a[4];
-            ldsm(a, kb + (k_lane ^ (x << 5)));
+            ldsm(a, kb ^ (x << 5));
 #pragma unroll
             for (int n1 = 0; n1 < NT; ++n1)
               mma<kBf>(kSplitK == 2 && (x & 1) ? sx[n1] : sc[s][n1], a, qf[n1][x][0], qf[n1][x][1]);
@@ -675,12 +683,11 @@ __global__ void __launch_bounds__(S::kThreads, 1) attend_kernel(const Params P) 
 #pragma unroll
           for (int x = 0; x < D / 32; ++x) {
             uint32_t b[4];      // rows 0-7 and 8-15 of 16 coordinates, then of the next 16
-            ldsm(b, kb + (k_lane ^ (x << 5)));
+            ldsm(b, kb ^ (x << 5));
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-              const uint32_t a[4] = {e4m3x2_to_f16x2(b[2 * j]), e4m3x2_to_f16x2(b[2 * j + 1]),
-                                     e4m3x2_to_f16x2(b[2 * j] >> 16),
-                                     e4m3x2_to_f16x2(b[2 * j + 1] >> 16)};
+              const uint32_t a[4] = {e4m3_low(b[2 * j]), e4m3_low(b[2 * j + 1]),
+                                     e4m3_high(b[2 * j]), e4m3_high(b[2 * j + 1])};
 #pragma unroll
               for (int n1 = 0; n1 < NT; ++n1)
                 mma<false>(kSplitK == 2 && j ? sx[n1] : sc[s][n1], a, qf[n1][2 * x + j][0],
@@ -770,12 +777,12 @@ __global__ void __launch_bounds__(S::kThreads, 1) attend_kernel(const Params P) 
           pf[n][0] = transpose8(pack<kBf>(sc[s][n][0], sc[s][n][1]));
           pf[n][1] = transpose8(pack<kBf>(sc[s][n][2], sc[s][n][3]));
         }
-        const uint32_t vb = vs + s * 16 * S::kRow;
+        const uint32_t vb = vs + s * 16 * S::kRow + v_lane;
         if constexpr (!k8) {
 #pragma unroll
           for (int d = 0; d < D / 16; ++d) {
             uint32_t a[4];
-            ldsm_t(a, vb + (v_lane ^ (d << 5)));
+            ldsm_t(a, vb ^ (d << 5));
 #pragma unroll
             for (int n = 0; n < NT; ++n) mma<kBf>(o[d][n], a, pf[n][0], pf[n][1]);
           }
@@ -785,13 +792,12 @@ __global__ void __launch_bounds__(S::kThreads, 1) attend_kernel(const Params P) 
 #pragma unroll
           for (int d = 0; d < D / 32; ++d) {
             uint32_t b[4];
-            ldsm_t(b, vb + (v_lane ^ (d << 5)));
+            ldsm_t(b, vb ^ (d << 5));
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
               const uint32_t x = __byte_perm(b[2 * j], 0, 0x3120);
               const uint32_t y = __byte_perm(b[2 * j + 1], 0, 0x3120);
-              const uint32_t a[4] = {e4m3x2_to_f16x2(x), e4m3x2_to_f16x2(x >> 16),
-                                     e4m3x2_to_f16x2(y), e4m3x2_to_f16x2(y >> 16)};
+              const uint32_t a[4] = {e4m3_low(x), e4m3_high(x), e4m3_low(y), e4m3_high(y)};
 #pragma unroll
               for (int n = 0; n < NT; ++n) mma<false>(o[2 * d + j][n], a, pf[n][0], pf[n][1]);
             }
@@ -809,7 +815,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) attend_kernel(const Params P) 
     if (p1 == c1) break;
 
     // ---- the row ends here, the share does not: add to its state in turn ----
-    const int b = k & 1, place_in_turn = (wid - k) & (kWarps - 1);
+    const int b = k & 1, place_in_turn = (wid + kWarps - k % kWarps) % kWarps;
     float* acc = s_sum + b * S::kAcc;
     float* ref = s_ml + b * S::kRows;
     float* den = s_ml + (2 + b) * S::kRows;
@@ -985,7 +991,7 @@ void launch(const Params& P, const moe_reader_kv& kv, const moe_reader_kv_attend
   const long long keys = (long long)(a.pages ? a.keep : a.width) << P.shift;
   const long long tiles = (keys + S::kKeys - 1) / S::kKeys * a.requests * P.kv_heads * P.row_tiles;
   const int grid = (int)std::min<long long>(kv.sms, (tiles + S::kWarps - 1) / S::kWarps);
-  attend_kernel<S><<<grid, S::kThreads, S::kSmem, s>>>(P);
+  launch_early(attend_kernel<S>, dim3(grid), S::kThreads, S::kSmem, s, P);
 }
 
 // Tiles of eight query heads per item: both where the group has more than eight

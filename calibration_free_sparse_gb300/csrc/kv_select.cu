@@ -76,6 +76,7 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const Params P) {
   __shared__ uint32_t s_range[2];
   __shared__ int s_bin, s_need, s_in_bin;
 
+  let_next_launch_start();
   cg::cluster_group cluster = cg::this_cluster();
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
   const int rank = (int)cluster.block_rank(), ctas = (int)cluster.num_blocks();
@@ -95,6 +96,7 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const Params P) {
       for (int i = tid; i < a.keep; i += kThreads) out[i] = i < held ? i : -1;
     return;
   }
+  cluster.barrier_arrive();                     // this CTA has started (waited for below)
 
   // ---- this CTA's pages; the first batch's summaries are on their way while
   // the query is coded ----
@@ -152,9 +154,10 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const Params P) {
     s_q[tid] = (int8_t)fminf(rintf(pos * down), 127.f);
     s_q[D + tid] = (int8_t)-fminf(rintf(neg * down), 127.f);
   }
-  cluster.sync();                               // s_q is ready; the first CTA has started
+  __syncthreads();
 
   // ---- scores ----
+  cluster.barrier_wait();                       // the first CTA's memory can be written
   uint32_t* keys = cluster.map_shared_rank(s_keys, 0);
   const int4 mine = *reinterpret_cast<const int4*>(s_q + 16 * (lane % kLanes));
   while (base < p_end) {
@@ -192,8 +195,9 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const Params P) {
     }
   }
   if (bad) atomicOr(P.err, bad);
-  cluster.sync();
+  cluster.barrier_arrive();                     // the others only hand over their keys
   if (rank != 0) return;
+  cluster.barrier_wait();
 
   // ---- threshold: the need-th largest key that is not forced ----
   int need = a.keep - (a.first + a.last);
@@ -201,6 +205,7 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const Params P) {
   int need_eq = 0;
   if (need > 0) {
     uint32_t lo = kForced, hi = 0;
+#pragma unroll 4
     for (int i = tid; i < held; i += kThreads) {
       const uint32_t k = s_keys[i];
       if (k == kForced) continue;
@@ -221,6 +226,7 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const Params P) {
     for (;;) {
       for (int i = tid; i < kBins; i += kThreads) s_hist[i] = 0;
       __syncthreads();
+#pragma unroll 4
       for (int i = tid; i < held; i += kThreads) {
         const uint32_t k = s_keys[i];
         if (k != kForced && k >= from && k - from <= span) atomicAdd(&s_hist[(k - from) >> shift], 1);
@@ -240,7 +246,8 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const Params P) {
       if (lane == 31) s_warp[0][wid] = in;
       __syncthreads();
       int above = in - sum;
-      for (int w = 0; w < wid; ++w) above += s_warp[0][w];
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) above += w < wid ? s_warp[0][w] : 0;
       if (above < need && need <= above + sum) {
         int j = 0;
 #pragma unroll
@@ -275,6 +282,7 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const Params P) {
   const int seg = ((held + kWarps - 1) / kWarps + 31) & ~31;
   const int b0 = wid * seg, b1 = min(held, b0 + seg);
   int gt = 0, eq = 0;
+#pragma unroll 8
   for (int i = b0 + lane; i < b1; i += 32) {
     gt += s_keys[i] > T;
     eq += s_keys[i] == T;
@@ -288,10 +296,12 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const Params P) {
   }
   __syncthreads();
   gt = eq = 0;
-  for (int w = 0; w < wid; ++w) {
-    gt += s_warp[0][w];
-    eq += s_warp[1][w];
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    gt += w < wid ? s_warp[0][w] : 0;
+    eq += w < wid ? s_warp[1][w] : 0;
   }
+#pragma unroll 8
   for (int i = b0; i < b1; i += 32) {
     const uint32_t k = i + lane < b1 ? s_keys[i + lane] : 0;
     const bool in = i + lane < b1;
