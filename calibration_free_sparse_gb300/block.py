@@ -42,9 +42,12 @@ class Config(ctypes.Structure):
                 ("cache_type", ctypes.c_int32), ("flags", ctypes.c_int32)]
 
 
-def _stream(stream, device):
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(device)
+_current = torch._C._cuda_getCurrentRawStream   # the current stream's handle on a device
+_device = torch._C._cuda_getDevice              # the current device
+
+
+def _handle(stream):
+    """The handle of a stream object, or of an integer that is one."""
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
@@ -114,6 +117,7 @@ class PagePlan:
         self.lens, self.starts = self._lens[:0], self._starts[:1]
         self.slots, self.positions = new(self.max_tokens), new(self.max_tokens)
         self.requests, self.taken = new(self.max_tokens), new(1)
+        self._call = _rd._lib().moe_reader_kv_plan
         self._out = (self._lens.data_ptr(), self._starts.data_ptr(), self.slots.data_ptr(),
                      self.positions.data_ptr(), self.requests.data_ptr(), self.taken.data_ptr())
 
@@ -131,8 +135,9 @@ class PagePlan:
             raise ValueError(f"{R} requests for a table of {self.table.shape[0]} rows")
         args = _PLAN.pack(prev, new, self.table.data_ptr(), free, *self._out, R, self.width, F,
                           self.max_tokens)
-        _check(_rd._lib().moe_reader_kv_plan(self.cache._h, args, _stream(stream, dev)),
-               "moe_reader_kv_plan")
+        code = self._call(self.cache._h, args, _current(dev) if stream is None else _handle(stream))
+        if code:
+            _check(code, "moe_reader_kv_plan")
         if self.lens.shape[0] != R:
             self.lens, self.starts = self._lens[:R], self._starts[:R + 1]
         return self
@@ -154,7 +159,7 @@ class PagedCache:
         if not isinstance(k, torch.Tensor) or k.dtype not in TYPES or k.dtype == torch.float32:
             raise TypeError("k must be a bfloat16, float16 or float8_e4m3fn CUDA tensor")
         self.device = k.get_device()
-        if not k.is_cuda or self.device != torch.cuda.current_device():
+        if not k.is_cuda or self.device != _device():
             raise ValueError("k must be on the current CUDA device")
         if k.dim() != 4:
             raise ValueError("k must be [pages][kv_heads][page_size][head_dim]")
@@ -177,9 +182,12 @@ class PagedCache:
         self._keep = (k, v, codes, steps, k_scale, v_scale)
         cfg = Config(self.q_heads, self.kv_heads, self.head_dim, self.page_size, pages,
                      self.max_requests, TYPES[k.dtype], 0)
+        self._append, self._attend = lib.moe_reader_kv_append, lib.moe_reader_kv_attend
+        self._select = lib.moe_reader_kv_select
         h = ctypes.c_void_p()
-        _check(lib.moe_reader_kv_create(ctypes.byref(cfg), k.data_ptr(), v.data_ptr(), *ptr,
-                                        _stream(stream, self.device), ctypes.byref(h)), "moe_reader_kv_create")
+        at = _current(self.device) if stream is None else _handle(stream)
+        _check(lib.moe_reader_kv_create(ctypes.byref(cfg), k.data_ptr(), v.data_ptr(), *ptr, at,
+                                        ctypes.byref(h)), "moe_reader_kv_create")
         self._h = h
 
     # -- lifetime ---------------------------------------------------------
@@ -217,8 +225,10 @@ class PagedCache:
         if vt != kt:
             raise TypeError("k and v must have one dtype")
         args = _APPEND.pack(kp, vp, at, ks[0], ks[1], vs[0], vs[1], kt, T)
-        _check(_rd._lib().moe_reader_kv_append(self._h, args, _stream(stream, self.device)),
-               "moe_reader_kv_append")
+        code = self._append(self._h, args,
+                            _current(self.device) if stream is None else _handle(stream))
+        if code:
+            _check(code, "moe_reader_kv_append")
 
     def attend(self, q, table, lens, out, scale=None, window=0, sinks=None, lse=None, pages=None,
                stream=None):
@@ -243,8 +253,9 @@ class PagedCache:
             ls = _whole(lse, torch.float32, (R, self.q_heads), "lse", dev)
         args = _ATTEND.pack(qp, tab, ln, pg, sk, o, ls, s[0], s[1], qt, R, width, keep, window,
                             self._scale if scale is None else scale)
-        _check(_rd._lib().moe_reader_kv_attend(self._h, args, _stream(stream, dev)),
-               "moe_reader_kv_attend")
+        code = self._attend(self._h, args, _current(dev) if stream is None else _handle(stream))
+        if code:
+            _check(code, "moe_reader_kv_attend")
 
     def select(self, q, table, lens, pages, first=1, last=1, stream=None):
         """Choose pages.shape[2] pages per request and KV head by the page
@@ -256,8 +267,10 @@ class PagedCache:
         ln = _whole(lens, _I32, (R,), "lens", self.device)
         pg, keep = self._pages(pages, R)
         args = _SELECT.pack(qp, tab, ln, pg, s[0], s[1], qt, R, width, keep, first, last)
-        _check(_rd._lib().moe_reader_kv_select(self._h, args, _stream(stream, self.device)),
-               "moe_reader_kv_select")
+        code = self._select(self._h, args,
+                            _current(self.device) if stream is None else _handle(stream))
+        if code:
+            _check(code, "moe_reader_kv_select")
 
     # -- checks -----------------------------------------------------------
     def _pages(self, pages, R):
@@ -285,7 +298,7 @@ def _matrix(t, what, shape, device):
         if t.dtype in _FLOATS and t.shape == shape and t.get_device() == device:
             s = t.stride()
             if s[1] == 1:
-                return t.data_ptr(), s[0], TYPES[t.dtype]
+                return t.data_ptr(), s[0] if shape[0] > 1 else 0, TYPES[t.dtype]
     except AttributeError:
         pass
     _refuse(t, _FLOATS, shape, what + "'s rows", device)
@@ -302,7 +315,7 @@ def residual_norm(h, x=None, y=None, post_weight=None, gate=None, scale=1.0, pre
     if not isinstance(h, torch.Tensor) or h.dim() != 2 or not h.is_cuda:
         raise TypeError("h must be a CUDA tensor [rows][hidden]")
     dev, shape = h.get_device(), h.shape
-    if dev != torch.cuda.current_device():
+    if dev != _device():
         raise ValueError(f"h is on cuda:{dev}, not the current device")
     rows, hidden = shape
     hp, hs, ht = _matrix(h, "h", shape, dev)
@@ -326,6 +339,7 @@ def residual_norm(h, x=None, y=None, post_weight=None, gate=None, scale=1.0, pre
             gcol = gate.stride(0)
         elif g == shape:
             grow, gcol = gate.stride()
+            grow = grow if rows > 1 else 0
         elif g == (rows, 1):
             grow = gate.stride(0)
         else:
@@ -341,4 +355,7 @@ def residual_norm(h, x=None, y=None, post_weight=None, gate=None, scale=1.0, pre
         raise TypeError("post_weight and pre_weight must have one dtype")
     args = _NORM.pack(hp, yp, gp, wp[0], wp[1], op, xp, hs, ys, os_, xs, grow, gcol, rows, hidden,
                       ht, yt, xt, gt, wt, scale, eps)
-    _check(_rd._lib().moe_reader_residual_norm(args, _stream(stream, dev)), "moe_reader_residual_norm")
+    code = _rd._lib().moe_reader_residual_norm(
+        args, _current(dev) if stream is None else _handle(stream))
+    if code:
+        _check(code, "moe_reader_residual_norm")

@@ -371,13 +371,17 @@ extern "C" int moe_reader_residual_norm(const moe_reader_residual_norm_args* a, 
   const int st = mr::check(*a);
   if (st != MOE_READER_OK || a->rows == 0) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  // as few vectors a thread as its CTA's threads allow (on 8191 rows of 2880,
-  // two to four measured 44.5 us against 42.7 for one)
+  // Many rows: about four warps a row (eight with an fp32 matrix), so that many
+  // rows share an SM and few warps meet at a row's barriers; few rows: one
+  // vector a thread, for latency.  Measured, one vector / this rule: 8191 x 2880
+  // bf16 46.3 / 42.7 us, 2048 x 8192 bf16 36.2 / 26.1, 16384 x 2048 fp32 70.7 /
+  // 70.7 (four warps: 72.8), 16 x 2048 fp32 2.25 (two vectors: 2.43).
   const bool wide = a->h_type == MOE_READER_TYPE_F32 || (a->y && a->y_type == MOE_READER_TYPE_F32) ||
                     (a->gate && a->gate_type == MOE_READER_TYPE_F32);
-  const int vecs = a->hidden / 8, most = wide ? 2 : 4;
+  const bool many = a->rows > 304;                 // two CTAs an SM
+  const int vecs = a->hidden / 8, most = wide ? 2 : 4, aim = wide ? 256 : 128;
   const int least = (vecs + mr::kThreads - 1) / mr::kThreads;
-  const int V = least > most ? 0 : least;
+  const int V = least > most ? 0 : std::max(least, std::min(many ? (vecs + aim - 1) / aim : 1, most));
   if (wide) mr::launch<true>(*a, V, s);
   else mr::launch<false>(*a, V, s);
   return cudaGetLastError() == cudaSuccess ? MOE_READER_OK : MOE_READER_ECUDA;

@@ -626,7 +626,8 @@ void moe_reader_kv_destroy(moe_reader_kv_t* kv);
  *   x  = h' / sqrt(mean(h'^2) + eps) * pre_weight  (ones without pre_weight)
  *
  *   h, y       dev, [rows][hidden] of h_type, y_type (F32, BF16 or F16); y NULL
- *              for the norm alone.  Row strides in elements.
+ *              for the norm alone.  Matrices and weights are 16-byte aligned,
+ *              row strides (in elements) multiples of 8.
  *   gate       dev, of gate_type, or NULL (1): element (row, c) at
  *              gate[row * gate_row_stride + c * gate_col_stride]; a stride of
  *              0 broadcasts, gate_col_stride is 0 or 1.

@@ -769,3 +769,82 @@ def test_a_step_in_a_graph():
         check_attend(c, q, out, pages=want)
     assert c.lens == [120, 57, 20]
     assert c.cache.status() == (0, 0)
+
+
+# --------------------------------------------------------------------------
+# the operators together, as the example runs them
+# --------------------------------------------------------------------------
+def _example():
+    import importlib.util
+    import os
+
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples",
+                        "decode_block.py")
+    spec = importlib.util.spec_from_file_location("decode_block", path)
+    m = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(m)
+    return m
+
+
+def test_decoder_steps_match_a_plain_decoder():
+    """Forty steps of the example's decoder, one request idling now and then,
+    against attention, cache and norms in plain float64 (its matrix products
+    and experts are shared: the bf16 projections are taken from the same x)."""
+    m = _example()
+    dec = m.Decoder(layers=1)
+    layer, w, R = dec.layers[0], dec.w, dec.requests
+    g = torch.Generator(device="cuda").manual_seed(3)
+    keys = [[] for _ in range(R)]
+    values = [[] for _ in range(R)]
+    H, kv, dim, heads = w.H, layer.kv_heads, layer.head_dim, layer.q_heads
+
+    def norm(h, weight):
+        return h / torch.sqrt((h * h).mean(1, keepdim=True) + 1e-6) * weight.double()
+
+    for i in range(40):
+        h = torch.randn((R, H), generator=g, device="cuda")
+        new = torch.ones(R, dtype=torch.int32, device="cuda")
+        if i % 5 == 2:
+            new[1] = 0
+        start = h.double()
+        dec.step(h, new)
+        x = torch.empty_like(h)
+        block.residual_norm(start.float(), x, pre_weight=layer.norm1)
+        assert (x.double() - norm(start, layer.norm1)).abs().max() < 1e-5
+        qkv = (x.bfloat16() @ layer.qkv).view(R, -1, dim)
+        out = torch.zeros((R, heads, dim), dtype=torch.float64, device="cuda")
+        for r in range(R):
+            if new[r]:
+                keys[r].append(qkv[r, heads:heads + kv].double())
+                values[r].append(qkv[r, heads + kv:].double())
+            k, v = torch.stack(keys[r], 1), torch.stack(values[r], 1)      # [kv][n][dim]
+            q = qkv[r, :heads].double().view(kv, heads // kv, dim)
+            p = (q @ k.transpose(1, 2) * dim ** -0.5).softmax(-1)
+            out[r] = (p @ v).view(heads, dim)
+        # bf16 weights and output: two halves of an ulp of values below 8
+        assert (dec.attended.double() - out).abs().max() < 2 * 2.0 ** -8 * out.abs().max()
+        a = dec.attended.view(R, -1) @ layer.out
+        mid = start + dec.scale * a.double()
+        assert (dec.x.double() - norm(mid, layer.norm2)).abs().max() < 1e-4
+        assert (h.double() - (mid + dec.scale * dec.y.double())).abs().max() < 1e-4
+    assert dec.lens.tolist() == [40, 32, 40, 40]
+    dec.status()
+
+
+def test_decoder_with_every_page_kept_attends_like_dense():
+    """One layer on the same inputs, over all pages and over a list of them all:
+    each attention output is within 2^-8 of its weights and 2^-8 of itself."""
+    m = _example()
+    a, b = m.Decoder(layers=1), m.Decoder(layers=1)
+    g = torch.Generator(device="cuda").manual_seed(4)
+    new = torch.ones(a.requests, dtype=torch.int32, device="cuda")
+    for _ in range(50):
+        h = torch.randn((a.requests, a.w.H), generator=g, device="cuda")
+        a.step(h.clone(), new)
+        b.step(h.clone(), new, keep=a.table.shape[1])
+        assert torch.equal(a.layers[0].v, b.layers[0].v)
+        gap = (a.attended.float() - b.attended.float()).abs().max()
+        assert gap <= 4 * 2.0 ** -8 * a.layers[0].v.abs().max()
+    a.status()
+    b.status()
+    m.main(steps=40, keep=2)
