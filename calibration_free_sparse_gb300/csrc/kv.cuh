@@ -26,6 +26,7 @@ struct moe_reader_kv {
   float* part_o;              // [sms][2][16][D]  unnormalised outputs of split rows
   float* part_ml;             // [sms][2][2][16]  their references and sums of weights
   uint32_t* arrived;          // [rows]           pieces written; zero between launches
+  size_t arrived_bytes;
   uint32_t* err;              // [1]              device error word
   cudaStream_t last_stream;
   int used;

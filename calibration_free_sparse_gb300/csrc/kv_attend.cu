@@ -318,7 +318,8 @@ __device__ __forceinline__ void finish(const Params& P, int kvh, int head, float
     const float sink = __ldg(P.sinks + head) * kLog2e;
     ref = fmaxf(top, sink);
     const float down = top == -INFINITY ? 0.f : exp2_fast(top - ref);
-    den = den * down + (sink == -INFINITY ? 0.f : exp2_fast(sink - ref));
+    // the larger of the two by its equality: both may be infinite
+    den = den * down + (sink == -INFINITY ? 0.f : sink == ref ? 1.f : exp2_fast(sink - ref));
     mul = den == 0.f ? 0.f : vs * down / den;
   } else {
     mul = den == 0.f ? 0.f : vs / den;

@@ -579,6 +579,7 @@ int moe_reader_kv_create(const moe_reader_kv_config* cfg, void* k, void* v, int8
   kv->part_o = reinterpret_cast<float*>(b);
   kv->part_ml = reinterpret_cast<float*>(b + o_bytes);
   kv->arrived = reinterpret_cast<uint32_t*>(b + o_bytes + ml_bytes);
+  kv->arrived_bytes = c_bytes;
   kv->err = reinterpret_cast<uint32_t*>(b + o_bytes + ml_bytes + c_bytes);
   do {
     if ((ce = cudaDeviceGetAttribute(&kv->sms, cudaDevAttrMultiProcessorCount, kv->device)) !=
@@ -603,7 +604,7 @@ int moe_reader_kv_plan(moe_reader_kv_t* kv, const moe_reader_kv_plan_args* a, vo
   if (!kv || !a) return MOE_READER_EINVAL;
   if (a->requests < 0 || a->requests > kv->cfg.max_requests) return MOE_READER_EINVAL;
   if (a->width < 1 || a->num_free < 0 || a->max_tokens < 0) return MOE_READER_EINVAL;
-  if ((long long)a->width << kv->page_shift >= (1LL << 31)) return MOE_READER_EINVAL;
+  if ((long long)a->width << kv->page_shift >= (1LL << 30)) return MOE_READER_EINVAL;
   if (!a->starts || !a->taken) return MOE_READER_EINVAL;
   if (a->requests && (!a->prev_lens || !a->new_lens || !a->table || !a->lens))
     return MOE_READER_EINVAL;
@@ -642,7 +643,7 @@ int moe_reader_kv_attend(moe_reader_kv_t* kv, const moe_reader_kv_attend_args* a
   if (a->requests < 0 || a->requests > kv->cfg.max_requests) return MOE_READER_EINVAL;
   if (!type_fits(kv->cfg.cache_type, a->q_type)) return MOE_READER_EINVAL;
   if (a->width < 1 || a->window < 0 || (a->pages && a->keep < 1)) return MOE_READER_EINVAL;
-  if ((long long)a->width << kv->page_shift >= (1LL << 31)) return MOE_READER_EINVAL;
+  if ((long long)a->width << kv->page_shift >= (1LL << 30)) return MOE_READER_EINVAL;
   // the work list is indexed with 32 bits
   const long long pages = a->pages ? a->keep : a->width;
   const long long items = (long long)a->requests * kv->cfg.num_kv_heads *
@@ -650,8 +651,16 @@ int moe_reader_kv_attend(moe_reader_kv_t* kv, const moe_reader_kv_attend_args* a
   if (items * (pages << kv->page_shift) >= (1LL << 34)) return MOE_READER_EINVAL;
   if (a->requests == 0) return MOE_READER_OK;
   if (!a->q || !a->table || !a->lens || !a->out) return MOE_READER_EINVAL;
-  if (!at_multiple(a->q, 2) || !at_multiple(a->out, 16) || a->q == a->out)
-    return MOE_READER_EINVAL;
+  if (!at_multiple(a->q, 2) || !at_multiple(a->out, 16)) return MOE_READER_EINVAL;
+  {
+    // a CTA writes its row's output while others read their rows' queries
+    const long long heads = kv->cfg.num_q_heads, dim = kv->cfg.head_dim;
+    const long long rs = (a->requests - 1) * a->q_request_stride, hs = (heads - 1) * a->q_head_stride;
+    const uintptr_t q = reinterpret_cast<uintptr_t>(a->q), o = reinterpret_cast<uintptr_t>(a->out);
+    const uintptr_t q0 = q + 2 * (std::min(rs, 0LL) + std::min(hs, 0LL));
+    const uintptr_t q1 = q + 2 * (std::max(rs, 0LL) + std::max(hs, 0LL) + dim);
+    if (q0 < o + 2 * a->requests * heads * dim && o < q1) return MOE_READER_EINVAL;
+  }
   const void* words[] = {a->table, a->lens, a->pages, a->sinks, a->lse};
   for (const void* p : words)
     if (!at_multiple(p, 4)) return MOE_READER_EINVAL;
@@ -665,7 +674,7 @@ int moe_reader_kv_select(moe_reader_kv_t* kv, const moe_reader_kv_select_args* a
   if (a->requests < 0 || a->requests > kv->cfg.max_requests) return MOE_READER_EINVAL;
   if (!type_fits(kv->cfg.cache_type, a->q_type)) return MOE_READER_EINVAL;
   if (a->width < 1 || a->width > mr::kMaxSelectPages) return MOE_READER_EINVAL;
-  if ((long long)a->width << kv->page_shift >= (1LL << 31)) return MOE_READER_EINVAL;
+  if ((long long)a->width << kv->page_shift >= (1LL << 30)) return MOE_READER_EINVAL;
   if (a->first < 0 || a->last < 0 || a->keep < 1 ||
       (long long)a->first + a->last > (long long)a->keep)
     return MOE_READER_EINVAL;
@@ -688,7 +697,11 @@ int moe_reader_kv_status(moe_reader_kv_t* kv, uint32_t* bits_out) {
     return status_of(ce);
   if ((ce = cudaMemset(kv->err, 0, 4)) != cudaSuccess) return status_of(ce);
   if (bits_out) *bits_out = bits;
-  if (bits & MOE_READER_ERR_TIMEOUT) return MOE_READER_ETIMEOUT;
+  if (bits & MOE_READER_ERR_TIMEOUT) {
+    // what the launch that gave up has counted does not hold for the next one
+    ce = cudaMemset(kv->arrived, 0, kv->arrived_bytes);
+    return ce == cudaSuccess ? MOE_READER_ETIMEOUT : status_of(ce);
+  }
   return bits ? MOE_READER_EDEVICE : MOE_READER_OK;
 }
 

@@ -543,7 +543,8 @@ int moe_reader_kv_append(moe_reader_kv_t* kv, const moe_reader_kv_append_args* a
  *            as moe_reader_kv_select writes them.
  *   sinks    dev, fp32 [Hq] or NULL: a logit per head that takes weight and
  *            adds nothing.
- *   out      dev, [requests][Hq][D] of q_type, contiguous, 16-byte aligned.
+ *   out      dev, [requests][Hq][D] of q_type, contiguous, 16-byte aligned;
+ *            may not overlap the span of q.
  *   lse      dev, fp32 [requests][Hq] or NULL: log of the denominator.
  *
  * A row with nothing to attend to is zeros, its lse the sink or -infinity.
@@ -551,7 +552,8 @@ int moe_reader_kv_append(moe_reader_kv_t* kv, const moe_reader_kv_append_args* a
  * Logits, running maximum and sums are fp32; the weights are rounded to the
  * cache's type (fp16 for E4M3) for the product with V.
  * A length below 0 counts as 0, one beyond the table is cut (ERR_LENGTH); a
- * page that is not in the pool is skipped (ERR_PAGE).  EINVAL where requests *
+ * page that is not in the pool is skipped (ERR_PAGE).  EINVAL where width *
+ * page_size >= 2^30 (in plan and select too), or where requests *
  * Hkv * ceil(Hq / Hkv / 8) * width (keep with pages) * page_size >= 2^34.
  */
 typedef struct {
@@ -610,7 +612,8 @@ int moe_reader_kv_select(moe_reader_kv_t* kv, const moe_reader_kv_select_args* a
 
 /* moe_reader_kv_status -- synchronize the stream of the last call on the
  * handle, read and clear its device error word.  *bits (host, may be NULL)
- * receives the MOE_READER_ERR_* bits.  Returns OK, EDEVICE or ECUDA. */
+ * receives the MOE_READER_ERR_* bits.  Returns OK, EDEVICE, ETIMEOUT (a bounded
+ * wait inside a kernel ran out) or ECUDA. */
 int moe_reader_kv_status(moe_reader_kv_t* kv, uint32_t* bits);
 
 /* moe_reader_kv_destroy -- free the handle and its workspace (NULL is a

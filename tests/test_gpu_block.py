@@ -214,6 +214,48 @@ def test_attend_window_and_sinks(window, sinks):
     check_attend(c, q, out, lse, window=window, sinks=sk)
 
 
+def test_attend_sink_of_infinity_takes_everything():
+    c = Cache([70, 0], 1, 64, 16, BF, q_heads=2, summaries=False)
+    q, out = queries(2, 2, 64, BF), torch.full((2, 2, 64), 3.0, dtype=BF, device="cuda")
+    lse = torch.empty((2, 2), device="cuda")
+    c.cache.attend(q, c.table, c.lens_t, out, sinks=torch.tensor([math.inf, 0.0], device="cuda"),
+                   lse=lse)
+    assert not out[0, 0].any() and not out[1].any() and out[0, 1].any()
+    assert lse[0, 0] == math.inf and lse[1].tolist() == [math.inf, 0.0]
+
+
+def test_attend_refuses_an_output_over_the_queries():
+    c = Cache([70, 3], 1, 64, 16, BF, q_heads=2, summaries=False)
+    joint = torch.zeros((3, 2, 64), dtype=BF, device="cuda")
+    with pytest.raises(rd.ReaderError) as e:
+        c.cache.attend(joint[:2], c.table, c.lens_t, joint[1:])
+    assert e.value.code == rd.EINVAL
+    c.cache.attend(joint[:1], c.table, c.lens_t[:1], joint[1:2])
+
+
+def test_select_the_widest_table():
+    """As many pages as a CTA's memory holds keys for, in whole clusters."""
+    held = 49152
+    codes = torch.zeros((held, 1, 2, 64), dtype=torch.int8, device="cuda")
+    codes[:, 0, 0, 0] = (torch.arange(held, device="cuda") % 119).to(torch.int8)
+    steps = torch.ones((held, 1), device="cuda")
+    k = torch.zeros((held, 1, 16, 64), dtype=BF, device="cuda")
+    cache = block.PagedCache(k, k.clone(), 1, max_requests=1, codes=codes, steps=steps)
+    q = torch.zeros((1, 1, 64), dtype=BF, device="cuda")
+    q[0, 0, 0] = 1
+    pages = torch.empty((1, 1, 500), dtype=torch.int32, device="cuda")
+    table = torch.arange(held, dtype=torch.int32, device="cuda").reshape(1, -1)
+    cache.select(q, table, to_i32([held * 16]), pages, first=0, last=0)
+    # 413 pages score 118, then the first 87 that score 117
+    top = np.arange(held) % 119
+    want = np.sort(np.concatenate([np.flatnonzero(top == 118), np.flatnonzero(top == 117)[:500 - int((top == 118).sum())]]))
+    assert np.array_equal(pages.cpu().numpy()[0, 0], want)
+    wide = torch.zeros((1, held + 1), dtype=torch.int32, device="cuda")
+    with pytest.raises(rd.ReaderError):
+        cache.select(q, wide, to_i32([16]), pages)
+    assert cache.status() == (0, 0)
+
+
 def test_attend_sinks_of_minus_infinity_change_nothing():
     c = Cache([70, 0], 1, 64, 16, BF, q_heads=2, summaries=False)
     q = queries(2, 2, 64, BF)
