@@ -146,6 +146,11 @@ __device__ __forceinline__ uint32_t pack(float lo, float hi) {
   else asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
+template <bool BF>
+__device__ __forceinline__ float2 unpack(uint32_t v) {
+  if constexpr (BF) return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
+  else return __half22float2(*reinterpret_cast<const __half2*>(&v));
+}
 // The lower and the upper two of four e4m3 values.
 __device__ __forceinline__ uint32_t e4m3_low(uint32_t four) {
   uint32_t r;
@@ -769,15 +774,27 @@ __global__ void __launch_bounds__(S::kThreads, 1) attend_kernel(const Params P) 
         }
       }
 
-      // O^T += V^T P^T, the weights rounded to the products' type
+      // O^T += V^T P^T.  The products' type would round the weights as coarsely
+      // as the output is rounded, which made the result's error 1.42 times that
+      // of one rounding; so what the rounding left goes through a second
+      // product (an e4m3 cache's fp16 weights are finer than bf16 outputs and
+      // need it for fp16 outputs only).
+      const bool two = !k8 || P.q_type == kF16;
 #pragma unroll
       for (int s = 0; s < kMt; ++s) {
-        uint32_t pf[NT][2];
+        uint32_t pf[NT][2], pr[NT][2];
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          pf[n][0] = transpose8(pack<kBf>(sc[s][n][0], sc[s][n][1]));
-          pf[n][1] = transpose8(pack<kBf>(sc[s][n][2], sc[s][n][3]));
-        }
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float a = sc[s][n][2 * i], b = sc[s][n][2 * i + 1];
+            const uint32_t r = pack<kBf>(a, b);
+            pf[n][i] = transpose8(r);
+            if (two) {
+              const float2 f = unpack<kBf>(r);
+              pr[n][i] = transpose8(pack<kBf>(a - f.x, b - f.y));
+            }
+          }
         const uint32_t vb = vs + s * 16 * S::kRow + v_lane;
         if constexpr (!k8) {
 #pragma unroll
@@ -785,7 +802,10 @@ __global__ void __launch_bounds__(S::kThreads, 1) attend_kernel(const Params P) 
             uint32_t a[4];
             ldsm_t(a, vb ^ (d << 5));
 #pragma unroll
-            for (int n = 0; n < NT; ++n) mma<kBf>(o[d][n], a, pf[n][0], pf[n][1]);
+            for (int n = 0; n < NT; ++n) {
+              mma<kBf>(o[d][n], a, pf[n][0], pf[n][1]);
+              mma<kBf>(o[d][n], a, pr[n][0], pr[n][1]);
+            }
           }
         } else {
           // a transposed pair of bytes is coordinates 2g and 2g + 1 of two keys:
@@ -800,7 +820,10 @@ __global__ void __launch_bounds__(S::kThreads, 1) attend_kernel(const Params P) 
               const uint32_t y = __byte_perm(b[2 * j + 1], 0, 0x3120);
               const uint32_t a[4] = {e4m3_low(x), e4m3_high(x), e4m3_low(y), e4m3_high(y)};
 #pragma unroll
-              for (int n = 0; n < NT; ++n) mma<false>(o[2 * d + j][n], a, pf[n][0], pf[n][1]);
+              for (int n = 0; n < NT; ++n) {
+                mma<false>(o[2 * d + j][n], a, pf[n][0], pf[n][1]);
+                if (two) mma<false>(o[2 * d + j][n], a, pr[n][0], pr[n][1]);
+              }
             }
           }
         }

@@ -191,9 +191,8 @@ __device__ __forceinline__ float2 widen2(__nv_bfloat162 v) { return __bfloat1622
 
 // Eight new values of a row as the cache stores them: 16 bytes, or 8 of e4m3
 // (in words 0 and 1).
-template <int CT>
-__device__ __forceinline__ uint4 load_new(const uint16_t* p, bool wide, int type,
-                                          const Divider& by) {
+template <int CT, int IT>
+__device__ __forceinline__ uint4 load_new(const uint16_t* p, bool wide, const Divider& by) {
   uint4 in;
   if (wide) {
     in = __ldg(reinterpret_cast<const uint4*>(p));
@@ -210,7 +209,7 @@ __device__ __forceinline__ uint4 load_new(const uint16_t* p, bool wide, int type
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       float2 f;
-      if (type == MOE_READER_TYPE_BF16)
+      if constexpr (IT == MOE_READER_TYPE_BF16)
         f = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
       else
         f = __half22float2(as_pair<__half2>(w[i]));
@@ -262,7 +261,7 @@ __device__ __forceinline__ void pairs_of(uint4 v, typename Pair<CT>::type (&p)[4
 // forms the largest and smallest key per coordinate, so the summary needs no
 // second pass and no other CTA's writes.  D / 8 lanes share a row, 8 values
 // each; a thread has kAhead rows in flight.
-template <int D, int CT>
+template <int D, int CT, int IT>
 __global__ void __launch_bounds__(kAppendThreads)
 append_kernel(moe_reader_kv_append_args a, typename Cell<CT>::type* __restrict__ kc,
               typename Cell<CT>::type* __restrict__ vc, int8_t* __restrict__ codes,
@@ -289,7 +288,7 @@ append_kernel(moe_reader_kv_append_args a, typename Cell<CT>::type* __restrict__
 #pragma unroll 2
     for (int i = row0; i < n; i += kRows) {
       const int slot = __ldg(a.slots + first + i);
-      const uint4 v = load_new<CT>(vin + (first + i) * a.v_token_stride, wide_v, a.type, vd);
+      const uint4 v = load_new<CT, IT>(vin + (first + i) * a.v_token_stride, wide_v, vd);
       if (slot < 0 || slot >= slots_all) continue;
       const size_t row = (((size_t)(slot >> shift) * heads + head) << shift) + (slot & (ps - 1));
       put8<CT>(vc + row * D + col, v);
@@ -348,7 +347,7 @@ append_kernel(moe_reader_kv_append_args a, typename Cell<CT>::type* __restrict__
         if (o > off) continue;
         if (o >= run0) {
           const long long tt = t - (off - o);
-          kr[j] = load_new<CT>(kin + tt * a.k_token_stride, wide_k, a.type, kd);
+          kr[j] = load_new<CT, IT>(kin + tt * a.k_token_stride, wide_k, kd);
         } else {
           kr[j] = get8<CT>(kc + (page + o) * D + col);
         }
@@ -435,7 +434,7 @@ append_kernel(moe_reader_kv_append_args a, typename Cell<CT>::type* __restrict__
   }
 }
 
-template <int D, int CT>
+template <int D, int CT, int IT>
 void append_as(const moe_reader_kv& kv, const moe_reader_kv_append_args& a, cudaStream_t s) {
   using C = typename Cell<CT>::type;
   // A window of one token while that is a few CTAs per SM (a decode step: every
@@ -448,7 +447,7 @@ void append_as(const moe_reader_kv& kv, const moe_reader_kv_append_args& a, cuda
     return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ts % 8 == 0 && hs % 8 == 0;
   };
   const dim3 grid((unsigned)((a.tokens + window - 1) / window), (unsigned)heads, 2);
-  append_kernel<D, CT><<<grid, kAppendThreads, 0, s>>>(
+  append_kernel<D, CT, IT><<<grid, kAppendThreads, 0, s>>>(
       a, static_cast<C*>(kv.k), static_cast<C*>(kv.v), kv.codes, kv.steps, kv.k_scale, kv.v_scale,
       heads, kv.page_shift, kv.cfg.num_pages, window, wide(a.k, a.k_token_stride, a.k_head_stride),
       wide(a.v, a.v_token_stride, a.v_head_stride), kv.err);
@@ -457,9 +456,13 @@ void append_as(const moe_reader_kv& kv, const moe_reader_kv_append_args& a, cuda
 template <int D>
 void append_dim(const moe_reader_kv& kv, const moe_reader_kv_append_args& a, cudaStream_t s) {
   switch (kv.cfg.cache_type) {
-    case MOE_READER_TYPE_BF16: append_as<D, MOE_READER_TYPE_BF16>(kv, a, s); break;
-    case MOE_READER_TYPE_F16: append_as<D, MOE_READER_TYPE_F16>(kv, a, s); break;
-    default: append_as<D, MOE_READER_TYPE_E4M3>(kv, a, s); break;
+    case MOE_READER_TYPE_BF16: append_as<D, MOE_READER_TYPE_BF16, MOE_READER_TYPE_BF16>(kv, a, s); break;
+    case MOE_READER_TYPE_F16: append_as<D, MOE_READER_TYPE_F16, MOE_READER_TYPE_F16>(kv, a, s); break;
+    default:
+      if (a.type == MOE_READER_TYPE_BF16)
+        append_as<D, MOE_READER_TYPE_E4M3, MOE_READER_TYPE_BF16>(kv, a, s);
+      else
+        append_as<D, MOE_READER_TYPE_E4M3, MOE_READER_TYPE_F16>(kv, a, s);
   }
 }
 

@@ -20,7 +20,14 @@ using Args = moe_reader_residual_norm_args;
 
 // Eight neighbouring elements as they lie in memory: 16 bytes, or (kWide, a
 // call that has an fp32 matrix) 16 or 32.  A row's loads all go out before the
-// first one is converted.  Plain loads: h may be written in place.
+// first one is converted (volatile: the compiler would move some behind the
+// first sum).  Plain loads: h may be written in place.
+__device__ __forceinline__ uint4 load16(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
 template <bool kWide>
 struct Raw {
   uint4 a;
@@ -39,9 +46,9 @@ __device__ __forceinline__ void fetch(const void* p, long long row, int type, in
   for (int j = 0; j < V; ++j) {
     const int v = first + j * step;
     if (v < end) {
-      f[j].a = *reinterpret_cast<const uint4*>(at + (size_t)v * size);
+      f[j].a = load16(at + (size_t)v * size);
       if constexpr (kWide)
-        if (size == 32) f[j].b = *reinterpret_cast<const uint4*>(at + (size_t)v * size + 16);
+        if (size == 32) f[j].b = load16(at + (size_t)v * size + 16);
     }
   }
 }
@@ -170,40 +177,51 @@ __device__ __forceinline__ float block_sum(float v, float (*s)[32], int slot) {
 constexpr int kThreads = 512;        // at most, of the register kernel
 constexpr int kLongThreads = 1024;
 
-template <int V, bool kWide>
+// kType: the one 16-bit type of all matrices, or kMixed.
+constexpr int kMixed = -1;
+
+template <int V, int kType>
 __global__ void __launch_bounds__(kThreads)
 residual_norm_kernel(const Args a, float inv_hidden) {
+  constexpr bool kWide = kType == kMixed;
+  const int h_type = kWide ? a.h_type : kType, y_type = kWide ? a.y_type : kType;
+  const int x_type = kWide ? a.x_type : kType, g_type = kWide ? a.gate_type : kType;
   __shared__ float s_sum[2][32];
   const long long row = blockIdx.x;
   const int vecs = a.hidden / 8, first = threadIdx.x, step = blockDim.x;
   const bool gated = a.gate && a.gate_col_stride;
   Raw<kWide> rh[V], ry[V], rg[V];
-  fetch<V, kWide>(a.h, row * a.h_stride, a.h_type, first, step, vecs, rh);
-  if (a.y) fetch<V, kWide>(a.y, row * a.y_stride, a.y_type, first, step, vecs, ry);
-  if (gated) fetch<V, kWide>(a.gate, row * a.gate_row_stride, a.gate_type, first, step, vecs, rg);
+  fetch<V, kWide>(a.h, row * a.h_stride, h_type, first, step, vecs, rh);
+  if (a.y) fetch<V, kWide>(a.y, row * a.y_stride, y_type, first, step, vecs, ry);
+  if (gated) fetch<V, kWide>(a.gate, row * a.gate_row_stride, g_type, first, step, vecs, rg);
   float one = a.scale;
-  if (a.gate && !gated) one *= load1(a.gate, row * a.gate_row_stride, a.gate_type);
+  if (a.gate && !gated) one *= load1(a.gate, row * a.gate_row_stride, g_type);
+  if (a.post_weight) {
+    float z[V][8], ss = 0.f;
+    widen<V, kWide>(ry, y_type, z);
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+      if (first + j * step < vecs)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) ss += z[j][i] * z[j][i];
+    one *= rsqrtf(block_sum(ss, s_sum, 0) * inv_hidden + a.eps);
+  }
+  // only the raw rows live across the barrier: widening y again is cheaper than
+  // the registers that its floats would hold
   float h[V][8], w[V][8];
-  widen<V, kWide>(rh, a.h_type, h);
+  widen<V, kWide>(rh, h_type, h);
   if (a.y) {
     float z[V][8];
-    widen<V, kWide>(ry, a.y_type, z);
+    widen<V, kWide>(ry, y_type, z);
     if (a.post_weight) {
-      float ss = 0.f;
-#pragma unroll
-      for (int j = 0; j < V; ++j)
-        if (first + j * step < vecs)
-#pragma unroll
-          for (int i = 0; i < 8; ++i) ss += z[j][i] * z[j][i];
       weights<V>(a.post_weight, a.weight_type, first, step, vecs, w);
 #pragma unroll
       for (int j = 0; j < V; ++j)
 #pragma unroll
         for (int i = 0; i < 8; ++i) z[j][i] *= w[j][i];
-      one *= rsqrtf(block_sum(ss, s_sum, 0) * inv_hidden + a.eps);
     }
     if (gated) {
-      widen<V, kWide>(rg, a.gate_type, w);
+      widen<V, kWide>(rg, g_type, w);
 #pragma unroll
       for (int j = 0; j < V; ++j)
 #pragma unroll
@@ -214,7 +232,7 @@ residual_norm_kernel(const Args a, float inv_hidden) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) h[j][i] += one * z[j][i];
   }
-  if (a.h_out) store_row<V>(a.h_out, row * a.h_out_stride, a.h_type, first, step, vecs, h);
+  if (a.h_out) store_row<V>(a.h_out, row * a.h_out_stride, h_type, first, step, vecs, h);
   if (!a.x) return;
   float ss = 0.f;
 #pragma unroll
@@ -228,7 +246,7 @@ residual_norm_kernel(const Args a, float inv_hidden) {
   for (int j = 0; j < V; ++j)
 #pragma unroll
     for (int i = 0; i < 8; ++i) h[j][i] *= a.pre_weight ? inv * w[j][i] : inv;
-  store_row<V>(a.x, row * a.x_stride, a.x_type, first, step, vecs, h);
+  store_row<V>(a.x, row * a.x_stride, x_type, first, step, vecs, h);
 }
 
 __global__ void __launch_bounds__(kLongThreads) residual_norm_long_kernel(const Args a) {
@@ -349,18 +367,18 @@ int check(const Args& a) {
 }
 
 // V vectors a thread; 0: the kernel for long rows.
-template <bool kWide>
+template <int kType>
 void launch(const Args& a, int V, cudaStream_t s) {
   const int threads = V ? ((a.hidden / 8 + V - 1) / V + 31) / 32 * 32 : kLongThreads;
   const unsigned rows = (unsigned)a.rows;
   const float inv = 1.f / (float)a.hidden;
-  switch (V) {
-    case 1: residual_norm_kernel<1, kWide><<<rows, threads, 0, s>>>(a, inv); break;
-    case 2: residual_norm_kernel<2, kWide><<<rows, threads, 0, s>>>(a, inv); break;
-    case 3: if constexpr (!kWide) residual_norm_kernel<3, false><<<rows, threads, 0, s>>>(a, inv); break;
-    case 4: if constexpr (!kWide) residual_norm_kernel<4, false><<<rows, threads, 0, s>>>(a, inv); break;
-    default: residual_norm_long_kernel<<<rows, threads, 0, s>>>(a);
+  if (V == 1) return residual_norm_kernel<1, kType><<<rows, threads, 0, s>>>(a, inv);
+  if (V == 2) return residual_norm_kernel<2, kType><<<rows, threads, 0, s>>>(a, inv);
+  if constexpr (kType != kMixed) {
+    if (V == 3) return residual_norm_kernel<3, kType><<<rows, threads, 0, s>>>(a, inv);
+    if (V == 4) return residual_norm_kernel<4, kType><<<rows, threads, 0, s>>>(a, inv);
   }
+  residual_norm_long_kernel<<<rows, threads, 0, s>>>(a);
 }
 
 }  // namespace
@@ -371,18 +389,22 @@ extern "C" int moe_reader_residual_norm(const moe_reader_residual_norm_args* a, 
   const int st = mr::check(*a);
   if (st != MOE_READER_OK || a->rows == 0) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  // Many rows: about four warps a row (eight with an fp32 matrix), so that many
-  // rows share an SM and few warps meet at a row's barriers; few rows: one
-  // vector a thread, for latency.  Measured, one vector / this rule: 8191 x 2880
-  // bf16 46.3 / 42.7 us, 2048 x 8192 bf16 36.2 / 26.1, 16384 x 2048 fp32 70.7 /
-  // 70.7 (four warps: 72.8), 16 x 2048 fp32 2.25 (two vectors: 2.43).
-  const bool wide = a->h_type == MOE_READER_TYPE_F32 || (a->y && a->y_type == MOE_READER_TYPE_F32) ||
-                    (a->gate && a->gate_type == MOE_READER_TYPE_F32);
-  const bool many = a->rows > 304;                 // two CTAs an SM
-  const int vecs = a->hidden / 8, most = wide ? 2 : 4, aim = wide ? 256 : 128;
+  // Many rows: about four warps a row (eight with matrices of several types or
+  // fp32), so that many rows share an SM and few warps meet at a row's barriers;
+  // few rows: one vector a thread, for latency.  Measured, one vector / this
+  // rule: 8191 x 2880 bf16 46.3 / 41.8 us (5.6 TB/s), 2048 x 8192 bf16 36.2 /
+  // 25.8, 16384 x 2048 fp32 69.3 / 69.3 (6.8 TB/s; four warps: 72.8), 16 x 2048
+  // fp32 2.3 (two vectors: 2.4).
+  int type = a->h_type;
+  if (type == MOE_READER_TYPE_F32 || (a->y && a->y_type != type) || (a->x && a->x_type != type) ||
+      (a->gate && a->gate_type != type))
+    type = mr::kMixed;
+  const bool mixed = type == mr::kMixed, many = a->rows > 304;   // two CTAs an SM
+  const int vecs = a->hidden / 8, most = mixed ? 2 : 4, aim = mixed ? 256 : 128;
   const int least = (vecs + mr::kThreads - 1) / mr::kThreads;
   const int V = least > most ? 0 : std::max(least, std::min(many ? (vecs + aim - 1) / aim : 1, most));
-  if (wide) mr::launch<true>(*a, V, s);
-  else mr::launch<false>(*a, V, s);
+  if (mixed) mr::launch<mr::kMixed>(*a, V, s);
+  else if (type == MOE_READER_TYPE_BF16) mr::launch<MOE_READER_TYPE_BF16>(*a, V, s);
+  else mr::launch<MOE_READER_TYPE_F16>(*a, V, s);
   return cudaGetLastError() == cudaSuccess ? MOE_READER_OK : MOE_READER_ECUDA;
 }
