@@ -42,12 +42,12 @@ struct Shape {
   static constexpr int D = D_, NT = NT_, CT = CT_;
   static constexpr int kBytes = CT == kE4m3 ? 1 : 2;
   static constexpr int kRow = D * kBytes;                    // bytes of a key
-  static constexpr int kMt = kRow >= 256 ? 1 : 2;            // 16-key subtiles per tile
+  static constexpr int kMt = kRow >= 256 ? 1 : kRow == 128 ? 2 : 4;   // 16-key subtiles per tile
   static constexpr int kKeys = 16 * kMt;                     // keys per tile
   static constexpr int kTile = 2 * kKeys * kRow;             // bytes of a tile, K then V
   static constexpr int kWarps = kRow >= 512 ? 4 : 8;
   static constexpr int kThreads = 32 * kWarps;
-  static constexpr int kStages = 192 * 1024 / (kWarps * kTile);
+  static constexpr int kStages = 192 * 1024 / (kWarps * kTile);   // copies in flight: all but one
     static constexpr int kSplit = 64;                          // tiles that a join is worth
   static constexpr int kRows = 8 * NT;                       // query heads of a row
   // the sum over the warps at the end runs over slices of the coordinates
@@ -205,7 +205,7 @@ __device__ __forceinline__ int tiles_of(const Row& w) {
 // The item at an index of the list.
 template <class S>
 struct Item {
-  int r, sub;            // request; KV head * row_tiles + row tile
+  int r, sub;            // request, KV head
   int begin, end, tiles; // the item's indices in the (padded) list, its real tiles
   Row row;
 };
@@ -247,7 +247,7 @@ __device__ __forceinline__ Source source_at(const Params& P, const int* prefix, 
   o.pos = kNowhere;
   o.lo = it.row.lo;
   o.len = it.row.len;
-  o.head = it.sub / P.row_tiles;
+  o.head = it.sub;
   const int v = (t - it.begin) * S::kKeys + s * 16;      // virtual key of the item
   const int j = it.row.base + v;
   o.in = j & ((1 << P.shift) - 1);
@@ -342,16 +342,16 @@ __device__ __forceinline__ void store_out(const Params& P, int r, int head, int 
 
 // Sums the pieces of a row that several CTAs wrote, in order; all of the CTA.
 template <class S>
-__device__ __forceinline__ void join_row(const Params& P, const Item<S>& it, int U, int pieces,
+__device__ __forceinline__ void join_row(const Params& P, const Item<S>& it, int rt, int U, int pieces,
                                          float* wgt, float* s_mul) {
   constexpr int D = S::D;
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
-  const int kvh = it.sub / P.row_tiles, row0 = (it.sub % P.row_tiles) * S::kRows;
+  const int kvh = it.sub, row0 = rt * S::kRows;
   const int rows = min(S::kRows, P.group - row0), head0 = kvh * P.group + row0;
   const int first = it.begin / U;
   // a CTA's first piece is in its slot 0, unless the row began inside its share
   auto slot = [&](int p) {
-    return (size_t)(first + p) * 2 + ((first + p) * U >= it.begin ? 0 : 1);
+    return (size_t)((first + p) * P.row_tiles + rt) * 2 + ((first + p) * U >= it.begin ? 0 : 1);
   };
   for (int h = wid; h < rows; h += S::kWarps) {
     float top = -INFINITY;
@@ -414,7 +414,9 @@ __global__ void __launch_bounds__(S::kThreads, 1) attend_kernel(const Params P) 
   __shared__ float s_mul[S::kRows];
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
   const int g = lane >> 2, t4 = lane & 3;
-  const int per = P.kv_heads * P.row_tiles;
+  // Groups of more query heads than a row holds: their row tiles are dealt to
+  // neighbouring CTAs with one share of keys, which then come from HBM once.
+  const int per = P.kv_heads, rt = blockIdx.x % P.row_tiles, cta = blockIdx.x / P.row_tiles;
   uint32_t bad = 0;
 
   if (tid < 2) s_turn[tid] = 0, s_last[tid] = 0;
@@ -453,7 +455,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) attend_kernel(const Params P) 
     rows += v.y;
     most = max(most, v.z);
   }
-  const int grid = (int)gridDim.x;
+  const int grid = (int)gridDim.x / P.row_tiles;
   const int total = sum * per, items = rows * per;
   // Shares of equal size: best where the cache is long.  A row of its own per
   // CTA (or a whole number of CTAs per row) where that costs no CTA more than
@@ -500,7 +502,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) attend_kernel(const Params P) 
   const int all = s_prefix[P.requests] * per;
 
   // rows with nothing to read
-  for (int r = blockIdx.x; r < P.requests; r += grid) {
+  for (int r = blockIdx.x; r < P.requests; r += gridDim.x) {
     if (s_prefix[r + 1] != s_prefix[r]) continue;
     uint4* o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(P.out) + (size_t)r * P.heads * D);
     for (int i = tid; i < P.heads * D / 8; i += S::kThreads) o[i] = make_uint4(0, 0, 0, 0);
@@ -509,8 +511,8 @@ __global__ void __launch_bounds__(S::kThreads, 1) attend_kernel(const Params P) 
         P.lse[(size_t)r * P.heads + i] = P.sinks ? P.sinks[i] : -INFINITY;
   }
 
-  if ((long long)blockIdx.x * U >= all) return;
-  const int c0 = blockIdx.x * U, c1 = min(all - c0, U) + c0;
+  if ((long long)cta * U >= all) return;
+  const int c0 = cta * U, c1 = min(all - c0, U) + c0;
 
   // CTAs that hold a part of a row; one more part of it is written (the last
   // to say so gets true, and clears the counter for the next launch)
@@ -518,7 +520,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) attend_kernel(const Params P) 
     return (it.begin + it.tiles - 1) / U - it.begin / U + 1;
   };
   auto arrive = [&](const Item<S>& it) -> int {
-    uint32_t* count = P.arrived + it.r * per + it.sub;
+    uint32_t* count = P.arrived + (it.r * per + it.sub) * P.row_tiles + rt;
     __threadfence();
     const bool last = atomicAdd(count, 1u) + 1 == (uint32_t)pieces_of(it);
     if (last) *count = 0;
@@ -588,7 +590,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) attend_kernel(const Params P) 
     cc = item_at<S>(P, s_prefix, s_len, per, p0);
     const int p1 = min(c1, cc.end);
     const int real = min(p1, cc.begin + cc.tiles);     // tiles beyond are padding
-    const int kvh = cc.sub / P.row_tiles, row0 = (cc.sub % P.row_tiles) * S::kRows;
+    const int kvh = cc.sub, row0 = rt * S::kRows;
     const int rows_here = min(S::kRows, P.group - row0);
     const int head0 = kvh * P.group + row0;
 
@@ -660,7 +662,10 @@ __global__ void __launch_bounds__(S::kThreads, 1) attend_kernel(const Params P) 
       const int* pos = s_pos + (wid * S::kStages + out_stage) * kMt;
       out_stage = out_stage + 1 == S::kStages ? 0 : out_stage + 1;
       if (t >= real) continue;
-      if (pos[0] >= cc.row.len && pos[kMt - 1] >= cc.row.len) continue;   // no page there
+      bool any = false;
+#pragma unroll
+      for (int s = 0; s < kMt; ++s) any |= pos[s] < cc.row.len;
+      if (!any) continue;                              // no page there
 
       // S^T = K Q^T, as kSplitK sums where the tile alone gives one chain of products
       constexpr int kSplitK = NT * kMt == 1 ? 2 : 1;
@@ -909,7 +914,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) attend_kernel(const Params P) 
   }
 
   // ---- the share's last piece: all warps at once ----
-  const int kvh = cc.sub / P.row_tiles, row0 = (cc.sub % P.row_tiles) * S::kRows;
+  const int kvh = cc.sub, row0 = rt * S::kRows;
   const int rows_here = min(S::kRows, P.group - row0);
   const int head0 = kvh * P.group + row0;
   __syncthreads();                                     // no turn uses the shared state any more
@@ -998,7 +1003,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) attend_kernel(const Params P) 
   for (int e = 0; e < 2; ++e) {
     if (!s_last[e]) continue;
     const Item<S> it = item_at<S>(P, s_prefix, s_len, per, e ? c1 - 1 : c0);
-    join_row<S>(P, it, U, pieces_of(it), s_sum, s_mul);
+    join_row<S>(P, it, rt, U, pieces_of(it), s_sum, s_mul);
   }
   if (bad) atomicOr(P.err, bad);
 }
@@ -1013,8 +1018,9 @@ void launch(const Params& P, const moe_reader_kv& kv, const moe_reader_kv_attend
             cudaStream_t s) {
   // one CTA per SM, fewer where even full tables cannot fill them
   const long long keys = (long long)(a.pages ? a.keep : a.width) << P.shift;
-  const long long tiles = (keys + S::kKeys - 1) / S::kKeys * a.requests * P.kv_heads * P.row_tiles;
-  const int grid = (int)std::min<long long>(kv.sms, (tiles + S::kWarps - 1) / S::kWarps);
+  const long long tiles = (keys + S::kKeys - 1) / S::kKeys * a.requests * P.kv_heads;
+  const int grid = P.row_tiles * (int)std::min<long long>(std::max(1, kv.sms / P.row_tiles),
+                                                         (tiles + S::kWarps - 1) / S::kWarps);
   launch_early(attend_kernel<S>, dim3(grid), S::kThreads, S::kSmem, s, P);
 }
 

@@ -649,8 +649,7 @@ int moe_reader_kv_attend(moe_reader_kv_t* kv, const moe_reader_kv_attend_args* a
   if ((long long)a->width << kv->page_shift >= (1LL << 30)) return MOE_READER_EINVAL;
   // the work list is indexed with 32 bits
   const long long pages = a->pages ? a->keep : a->width;
-  const long long items = (long long)a->requests * kv->cfg.num_kv_heads *
-                          mr::attend_row_tiles(kv->cfg);
+  const long long items = (long long)a->requests * kv->cfg.num_kv_heads;
   if (items * (pages << kv->page_shift) >= (1LL << 34)) return MOE_READER_EINVAL;
   if (a->requests == 0) return MOE_READER_OK;
   if (!a->q || !a->table || !a->lens || !a->out) return MOE_READER_EINVAL;
