@@ -45,7 +45,11 @@ struct Shape {
   static constexpr int kMt = kRow >= 256 ? 1 : kRow == 128 ? 2 : 4;   // 16-key subtiles per tile
   static constexpr int kKeys = 16 * kMt;                     // keys per tile
   static constexpr int kTile = 2 * kKeys * kRow;             // bytes of a tile, K then V
-  static constexpr int kWarps = kRow >= 512 ? 4 : 8;
+  // An e4m3 tile costs its conversions: a warp is busy with it for longer than
+  // HBM takes to bring it, so such rows get more warps where the registers
+  // allow (128 requests, 8 heads per KV head: D 64 151.5 -> 137.1 us, D 128 227.4
+  // -> 221.7).
+  static constexpr int kWarps = kRow >= 512 ? 4 : CT == kE4m3 && NT == 1 && D <= 128 ? 12 : 8;
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kStages = 192 * 1024 / (kWarps * kTile);   // copies in flight: all but one
     static constexpr int kSplit = 64;                          // tiles that a join is worth
@@ -63,7 +67,7 @@ struct Shape {
   static constexpr int kPos = kWarps * kStages * kMt * 4;
   static constexpr int kSmem = kPipe + kSum + kMl + kPos + (2 * kMaxRequests + 1) * 4;
   static_assert(kRows * kMaxSms * 4 <= kSum, "join weights of a piece per CTA");
-  static_assert(kSmem + 2048 <= 227 * 1024, "shared memory");
+  static_assert(kSmem + 2048 <= 227 * 1024 && kStages >= 2, "shared memory");
 };
 
 struct Params {
