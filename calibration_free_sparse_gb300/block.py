@@ -295,13 +295,46 @@ class PagedCache:
 def _matrix(t, what, shape, device):
     """(address, row stride, type code) of a float matrix with contiguous rows."""
     try:
-        if t.dtype in _FLOATS and t.shape == shape and t.get_device() == device:
+        code = TYPES[t.dtype]
+        if code < 3 and t.shape == shape and t.get_device() == device:
+            if t.is_contiguous():
+                return t.data_ptr(), shape[1], code
             s = t.stride()
             if s[1] == 1:
-                return t.data_ptr(), s[0] if shape[0] > 1 else 0, TYPES[t.dtype]
-    except AttributeError:
+                return t.data_ptr(), s[0] if shape[0] > 1 else 0, code
+    except (AttributeError, KeyError):
         pass
     _refuse(t, _FLOATS, shape, what + "'s rows", device)
+
+
+def _weight(w, what, shape, device):
+    """(address, type code) of a weight vector."""
+    try:
+        code = TYPES[w.dtype]
+        if code < 3 and w.shape == shape and w.get_device() == device and w.is_contiguous():
+            return w.data_ptr(), code
+    except (AttributeError, KeyError):
+        pass
+    _refuse(w, _FLOATS, shape, what, device)
+
+
+def _gate(g, rows, hidden, device):
+    """(address, row stride, column stride, type code) of a gate."""
+    try:
+        code, shape = TYPES[g.dtype], g.shape
+        if code < 3 and g.get_device() == device:
+            s = g.stride()
+            if shape == (rows, hidden):
+                return g.data_ptr(), s[0] if rows > 1 else 0, s[1], code
+            if shape == (hidden,):
+                return g.data_ptr(), 0, s[0], code
+            if shape == (rows, 1):
+                return g.data_ptr(), s[0], 0, code
+            raise ValueError(f"gate must be [hidden], [rows][1] or [rows][hidden], got "
+                             f"{tuple(shape)}")
+    except (AttributeError, KeyError):
+        pass
+    _refuse(g, _FLOATS, getattr(g, "shape", ()), "gate", device)
 
 
 def residual_norm(h, x=None, y=None, post_weight=None, gate=None, scale=1.0, pre_weight=None,
@@ -312,15 +345,17 @@ def residual_norm(h, x=None, y=None, post_weight=None, gate=None, scale=1.0, pre
     h, y, x, h_out: [rows][hidden], float32, bfloat16 or float16 each (h_out as
     h; it may be h).  gate: [hidden], [rows][1] or [rows][hidden].  Weights:
     [hidden] of one dtype.  x or h_out may be left out, not both."""
-    if not isinstance(h, torch.Tensor) or h.dim() != 2 or not h.is_cuda:
-        raise TypeError("h must be a CUDA tensor [rows][hidden]")
-    dev, shape = h.get_device(), h.shape
+    try:
+        dev, shape = h.get_device(), h.shape
+        rows, hidden = shape
+    except (AttributeError, ValueError):
+        raise TypeError("h must be a CUDA tensor [rows][hidden]") from None
     if dev != _device():
+        if dev < 0:
+            raise TypeError("h must be a CUDA tensor [rows][hidden]")
         raise ValueError(f"h is on cuda:{dev}, not the current device")
-    rows, hidden = shape
     hp, hs, ht = _matrix(h, "h", shape, dev)
-    yp = ys = gp = grow = gcol = op = os_ = xp = xs = 0
-    yt = xt = gt = wt = 0
+    yp = ys = yt = xp = xs = xt = op = os_ = gp = grow = gcol = gt = pp = qp = wt = 0
     if y is not None:
         yp, ys, yt = _matrix(y, "y", shape, dev)
     if x is not None:
@@ -330,31 +365,16 @@ def residual_norm(h, x=None, y=None, post_weight=None, gate=None, scale=1.0, pre
         if ot != ht:
             raise TypeError("h_out must have h's dtype")
     if gate is not None:
-        if not isinstance(gate, torch.Tensor) or gate.dtype not in _FLOATS:
-            raise TypeError("gate must be a float32, bfloat16 or float16 CUDA tensor")
-        if not gate.is_cuda or gate.get_device() != dev:
-            raise ValueError(f"gate must be on cuda:{dev}")
-        gp, gt, g = gate.data_ptr(), TYPES[gate.dtype], gate.shape
-        if g == (hidden,):
-            gcol = gate.stride(0)
-        elif g == shape:
-            grow, gcol = gate.stride()
-            grow = grow if rows > 1 else 0
-        elif g == (rows, 1):
-            grow = gate.stride(0)
-        else:
-            raise ValueError(f"gate must be [hidden], [rows][1] or [rows][hidden], got {tuple(g)}")
-    wp = [0, 0]
-    for i, (w, name) in enumerate(((post_weight, "post_weight"), (pre_weight, "pre_weight"))):
-        if w is not None:
-            if not isinstance(w, torch.Tensor) or w.dtype not in _FLOATS:
-                raise TypeError(f"{name} must be a float32, bfloat16 or float16 CUDA tensor")
-            wp[i], wt = _whole(w, w.dtype, (hidden,), name, dev), TYPES[w.dtype]
-    if post_weight is not None and pre_weight is not None and \
-            post_weight.dtype != pre_weight.dtype:
-        raise TypeError("post_weight and pre_weight must have one dtype")
-    args = _NORM.pack(hp, yp, gp, wp[0], wp[1], op, xp, hs, ys, os_, xs, grow, gcol, rows, hidden,
-                      ht, yt, xt, gt, wt, scale, eps)
+        gp, grow, gcol, gt = _gate(gate, rows, hidden, dev)
+    if post_weight is not None:
+        pp, wt = _weight(post_weight, "post_weight", (hidden,), dev)
+    if pre_weight is not None:
+        qp, qt = _weight(pre_weight, "pre_weight", (hidden,), dev)
+        if pp and qt != wt:
+            raise TypeError("post_weight and pre_weight must have one dtype")
+        wt = qt
+    args = _NORM.pack(hp, yp, gp, pp, qp, op, xp, hs, ys, os_, xs, grow, gcol, rows, hidden, ht, yt,
+                      xt, gt, wt, scale, eps)
     code = _rd._lib().moe_reader_residual_norm(
         args, _current(dev) if stream is None else _handle(stream))
     if code:

@@ -520,6 +520,31 @@ def test_append_extreme_values(dtype):
     assert not c.codes[at].any() and float(c.steps[at, 0]) == 2.0 ** -106
 
 
+@pytest.mark.parametrize("rows", [BF, HF])
+def test_append_quotients_are_the_divisions(rows):
+    """Every bit pattern of the rows' type, over scales of every size: what is
+    stored is the rounded, saturated quotient."""
+    patterns = torch.arange(65536, dtype=torch.int32, device="cuda").to(torch.int16).view(rows)
+    x = patterns.reshape(1024, 1, 64)
+    k = torch.zeros((64, 1, 16, 64), dtype=E4, device="cuda")
+    v = torch.zeros_like(k)
+    slots = torch.arange(1024, dtype=torch.int32, device="cuda")
+    g = torch.Generator().manual_seed(5)
+    scales = [1.0, 0.0173, 3.0, 2.0 ** -100, 2.0 ** 100, 2.0 ** -101, 2.0 ** 101, 1e-38, 2e-45, 3e38]
+    scales += [float(10 ** (8 * torch.rand((), generator=g) - 4)) for _ in range(20)]
+    for scale in scales:
+        ks = torch.tensor([scale], device="cuda")
+        vs = torch.tensor([scale * 1.5 if scale < 2e38 else scale], device="cuda")
+        cache = block.PagedCache(k, v, 1, max_requests=1, k_scale=ks, v_scale=vs)
+        cache.append(x, x, slots)
+        for got, s in ((k, ks), (v, vs)):
+            want = (x.float() / s).clamp(-448, 448).to(E4).float().reshape(-1)
+            have = got.float().reshape(-1)
+            assert torch.equal(torch.isnan(have), torch.isnan(want)), scale
+            assert torch.equal(torch.nan_to_num(have), torch.nan_to_num(want)), scale
+        cache.close()
+
+
 def test_append_bad_slots():
     c = Cache([16], 1, 64, 16, BF, q_heads=1)
     before = c.k.clone()
