@@ -152,6 +152,7 @@ plan_kernel(moe_reader_kv_plan_args a, int shift, int num_pages, uint32_t* err) 
 // append
 // ---------------------------------------------------------------------------
 constexpr int kAppendThreads = 128;
+constexpr int kKeyWindow = 64;       // tokens that a CTA's two ballots hold
 
 template <int CT> struct Cell { using type = uint16_t; };
 template <> struct Cell<MOE_READER_TYPE_E4M3> { using type = uint8_t; };
@@ -191,20 +192,26 @@ template <typename P> __device__ __forceinline__ uint32_t bits_of(P v) {
 __device__ __forceinline__ float2 widen2(__half2 v) { return __half22float2(v); }
 __device__ __forceinline__ float2 widen2(__nv_bfloat162 v) { return __bfloat1622float2(v); }
 
-// Eight new values of a row as the cache stores them: 16 bytes, or 8 of e4m3
-// (in words 0 and 1).
-template <int CT, int IT>
-__device__ __forceinline__ uint4 load_new(const uint16_t* p, bool wide, const Divider& by) {
-  uint4 in;
-  if (wide) {
-    in = __ldg(reinterpret_cast<const uint4*>(p));
-  } else {
-    uint32_t w[4];
+// Loads go out for several rows before the first is used (volatile: between the
+// branches that tell rows apart, the compiler would wait for each).
+__device__ __forceinline__ uint4 load16(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+// Eight new values of a row as they come in.
+__device__ __forceinline__ uint4 fetch_new(const uint16_t* p, bool wide) {
+  if (wide) return load16(p);
+  uint32_t w[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      w[i] = (uint32_t)__ldg(p + 2 * i) | (uint32_t)__ldg(p + 2 * i + 1) << 16;
-    in = make_uint4(w[0], w[1], w[2], w[3]);
-  }
+  for (int i = 0; i < 4; ++i)
+    w[i] = (uint32_t)__ldg(p + 2 * i) | (uint32_t)__ldg(p + 2 * i + 1) << 16;
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+// The same as the cache stores them: 16 bytes, or 8 of e4m3 (in words 0 and 1).
+template <int CT, int IT>
+__device__ __forceinline__ uint4 stored(const uint4& in, const Divider& by) {
   if constexpr (CT == MOE_READER_TYPE_E4M3) {
     const uint32_t w[4] = {in.x, in.y, in.z, in.w};
     uint32_t r[4];
@@ -227,12 +234,13 @@ template <int CT> __device__ __forceinline__ void put8(void* p, uint4 v) {
   if constexpr (CT == MOE_READER_TYPE_E4M3) *static_cast<uint2*>(p) = make_uint2(v.x, v.y);
   else *static_cast<uint4*>(p) = v;
 }
-template <int CT> __device__ __forceinline__ uint4 get8(const void* p) {
+template <int CT> __device__ __forceinline__ uint4 fetch_old(const void* p) {
   if constexpr (CT == MOE_READER_TYPE_E4M3) {
-    const uint2 v = *static_cast<const uint2*>(p);
-    return make_uint4(v.x, v.y, 0, 0);
+    uint4 v = make_uint4(0, 0, 0, 0);
+    asm volatile("ld.global.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+    return v;
   } else {
-    return *static_cast<const uint4*>(p);
+    return load16(p);
   }
 }
 // The four pairs of a row's eight stored values.
@@ -253,30 +261,32 @@ __device__ __forceinline__ void pairs_of(uint4 v, typename Pair<CT>::type (&p)[4
   }
 }
 
-// One CTA looks at `window` (at most 32) consecutive tokens for one KV head,
-// for their keys (blockIdx.z 0) or their values (1), so that a prompt's pages
-// are twice as many independent chains of loads.  Values are copied row by row.
-// Keys are taken once per page: for the token that is the last new one of its
-// page, with the run of new tokens that ends there (their slots are
-// consecutive).  It copies the run's rows and, over the page's rows up to that
-// token -- the older ones read from the cache, the new ones from the input --
-// forms the largest and smallest key per coordinate, so the summary needs no
-// second pass and no other CTA's writes.  D / 8 lanes share a row, 8 values
-// each; a thread has kAhead rows in flight.
+// The first `key_ctas` CTAs of a KV head look at `key_window` (at most 64)
+// consecutive tokens each for their keys, the others at `value_window` each for
+// their values: a prompt's pages are twice as many independent chains of loads.
+// Values are copied row by row.  Keys are taken once per page: for the token
+// that is the last new one of its page, with the run of new tokens that ends
+// there (their slots are consecutive).  It copies the run's rows and, over the
+// page's rows up to that token -- the older ones read from the cache, the new
+// ones from the input -- forms the largest and smallest key per coordinate, so
+// the summary needs no second pass and no other CTA's writes.  D / 8 lanes share
+// a row, 8 values each; a thread has kAhead rows in flight.
 //
 // Measured: 2.5 us for one token of 16 requests (4 KV heads of 128, pages of
-// 16); 13.4 us for 10 thousand tokens into an e4m3 cache (31 MB, 2.3 TB/s: the
+// 16); 12.4 us for 10 thousand tokens into an e4m3 cache (31 MB, 2.5 TB/s: the
 // quotients and conversions keep the issue slots half busy, the rest is the
-// latency of slot, row and summary), 19.5 us for 9 thousand tokens of 8 heads of
-// 128 in bf16 (75 MB, 3.8 TB/s).  Keys and values in one CTA took 21 us for the
-// first of these, plain divisions and a scan per token 28.
+// latency of slot, row and summary); 17.6 us for 9 thousand tokens of 8 heads of
+// 128 in bf16 (75 MB, 4.2 TB/s).  On the way, for the e4m3 case: plain divisions
+// and a scan per token 28.3 us, keys and values in one CTA 21.0, rows loaded one
+// after the other 15.0, windows of 32 keys 12.9 and of 16 values 13.6.
 template <int D, int CT, int IT>
 __global__ void __launch_bounds__(kAppendThreads)
 append_kernel(moe_reader_kv_append_args a, typename Cell<CT>::type* __restrict__ kc,
               typename Cell<CT>::type* __restrict__ vc, int8_t* __restrict__ codes,
               float* __restrict__ steps, const float* __restrict__ k_scale,
-              const float* __restrict__ v_scale, int heads, int shift, int num_pages, int window,
-              bool wide_k, bool wide_v, uint32_t* err) {
+              const float* __restrict__ v_scale, int heads, int shift, int num_pages,
+              int key_ctas, int key_window, int value_window, bool wide_k, bool wide_v,
+              uint32_t* err) {
   using P2 = typename Pair<CT>::type;
   constexpr int kLanes = D / 8;                          // lanes of a row
   constexpr int kRows = kAppendThreads / kLanes;         // rows at a time
@@ -284,64 +294,79 @@ append_kernel(moe_reader_kv_append_args a, typename Cell<CT>::type* __restrict__
   constexpr int kAhead = 4;
   __shared__ uint32_t s_hi[kWarps][D / 2], s_lo[kWarps][D / 2];
   __shared__ float s_max[kWarps];
+  __shared__ int s_slot[256 + kKeyWindow + 1];
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
   const int head = blockIdx.y, ps = 1 << shift;
   const int col = (tid % kLanes) * 8, row0 = tid / kLanes;
   const long long slots_all = (long long)num_pages << shift;
 
-  const long long first = (long long)blockIdx.x * window;
-  if (blockIdx.z) {
+  if ((int)blockIdx.x >= key_ctas) {
+    const long long first = (long long)(blockIdx.x - key_ctas) * value_window;
     const Divider vd(CT == MOE_READER_TYPE_E4M3 ? v_scale[head] : 1.f);
     const uint16_t* vin = static_cast<const uint16_t*>(a.v) + head * a.v_head_stride + col;
-    const int n = (int)min((long long)window, a.tokens - first);
-#pragma unroll 2
-    for (int i = row0; i < n; i += kRows) {
-      const int slot = __ldg(a.slots + first + i);
-      const uint4 v = load_new<CT, IT>(vin + (first + i) * a.v_token_stride, wide_v, vd);
-      if (slot < 0 || slot >= slots_all) continue;
-      const size_t row = (((size_t)(slot >> shift) * heads + head) << shift) + (slot & (ps - 1));
-      put8<CT>(vc + row * D + col, v);
+    const int n = (int)min((long long)value_window, a.tokens - first);
+    for (int i0 = row0; i0 < n; i0 += kRows * kAhead) {
+      int slot[kAhead];
+      uint4 vr[kAhead];
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        const int i = i0 + j * kRows;
+        slot[j] = -1;
+        if (i < n) {
+          slot[j] = __ldg(a.slots + first + i);
+          vr[j] = fetch_new(vin + (first + i) * a.v_token_stride, wide_v);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        if (slot[j] < 0 || slot[j] >= slots_all) continue;
+        const size_t row =
+            (((size_t)(slot[j] >> shift) * heads + head) << shift) + (slot[j] & (ps - 1));
+        put8<CT>(vc + row * D + col, stored<CT, IT>(vr[j], vd));
+      }
     }
     return;
   }
 
-  // the tokens of the window that close their page's run (the same in every warp)
-  const long long mine = first + lane;
-  int slot_l = -1;
-  bool closes = false;
-  if (lane < window && mine < a.tokens) {
-    slot_l = __ldg(a.slots + mine);
-    const int after = mine + 1 < a.tokens ? __ldg(a.slots + mine + 1) : -1;
-    if (slot_l >= 0 && slot_l < slots_all)
-      closes = (slot_l & (ps - 1)) == ps - 1 || after != slot_l + 1;
-    else if (slot_l != -1 && wid == 0)
-      atomicOr(err, kErrPage);
+  // the window's slots, a page before them and one behind, in one round of loads
+  const long long first = (long long)blockIdx.x * key_window;
+  for (int i = tid; i <= ps + key_window; i += kAppendThreads) {
+    const long long t = first - ps + i;
+    s_slot[i] = t >= 0 && t < a.tokens ? __ldg(a.slots + t) : -1;
   }
-  uint32_t todo = __ballot_sync(0xffffffffu, closes);
+  __syncthreads();
+  // the tokens of the window that close their page's run (the same in every warp)
+  unsigned long long todo = 0;
+#pragma unroll
+  for (int half = 0; half < kKeyWindow; half += 32) {
+    const int i = half + lane;
+    bool closes = false;
+    if (i < key_window && first + i < a.tokens) {
+      const int slot = s_slot[ps + i];
+      if (slot >= 0 && slot < slots_all)
+        closes = (slot & (ps - 1)) == ps - 1 || s_slot[ps + i + 1] != slot + 1;
+      else if (slot != -1 && wid == 0)
+        atomicOr(err, kErrPage);
+    }
+    todo |= (unsigned long long)__ballot_sync(0xffffffffu, closes) << half;
+  }
   if (!todo) return;
 
   const Divider kd(CT == MOE_READER_TYPE_E4M3 ? k_scale[head] : 1.f);
   const uint16_t* kin = static_cast<const uint16_t*>(a.k) + head * a.k_head_stride + col;
   for (; todo; todo &= todo - 1) {
-    const int w = __ffs(todo) - 1;
+    const int w = __ffsll(todo) - 1;
     const long long t = first + w;
-    const int slot = __shfl_sync(0xffffffffu, slot_l, w), off = slot & (ps - 1);
-    // the run of new tokens that ends here: its first offset in the page (the
-    // loads of up to 256 slots before it go out together)
+    const int slot = s_slot[ps + w], off = slot & (ps - 1);
+    // the run of new tokens that ends here: its first offset in the page
     int run0 = 0;
-    if (off) {
-      int before[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int back = 32 * i + 1 + lane;
-        before[i] = -1;
-        if (back <= off && t >= back) before[i] = __ldg(a.slots + t - back);
-      }
-#pragma unroll
-      for (int i = 7; i >= 0; --i) {
-        const int back = 32 * i + 1 + lane;
-        const uint32_t out = __ballot_sync(0xffffffffu, before[i] != slot - back);
-        if (out) run0 = max(0, off - (32 * i + __ffs(out) - 1));
+    for (int b = 1; b <= off; b += 32) {
+      const int back = b + lane;
+      const bool in = back <= off && s_slot[ps + w - min(back, ps)] == slot - back;
+      const uint32_t out = __ballot_sync(0xffffffffu, !in);
+      if (out) {
+        run0 = off - (b + __ffs(out) - 1) + 1;
+        break;
       }
     }
     const size_t page = ((size_t)(slot >> shift) * heads + head) << shift;   // first row
@@ -356,16 +381,19 @@ append_kernel(moe_reader_kv_append_args a, typename Cell<CT>::type* __restrict__
         if (o > off) continue;
         if (o >= run0) {
           const long long tt = t - (off - o);
-          kr[j] = load_new<CT, IT>(kin + tt * a.k_token_stride, wide_k, kd);
+          kr[j] = fetch_new(kin + tt * a.k_token_stride, wide_k);
         } else {
-          kr[j] = get8<CT>(kc + (page + o) * D + col);
+          kr[j] = fetch_old<CT>(kc + (page + o) * D + col);
         }
       }
 #pragma unroll
       for (int j = 0; j < kAhead; ++j) {
         const int o = o0 + j * kRows;
         if (o > off) continue;
-        if (o >= run0) put8<CT>(kc + (page + o) * D + col, kr[j]);
+        if (o >= run0) {
+          kr[j] = stored<CT, IT>(kr[j], kd);
+          put8<CT>(kc + (page + o) * D + col, kr[j]);
+        }
         if (codes) {
           P2 p[4];
           pairs_of<CT>(kr[j], p);
@@ -446,19 +474,24 @@ append_kernel(moe_reader_kv_append_args a, typename Cell<CT>::type* __restrict__
 template <int D, int CT, int IT>
 void append_as(const moe_reader_kv& kv, const moe_reader_kv_append_args& a, cudaStream_t s) {
   using C = typename Cell<CT>::type;
-  // A window of one token while that is a few CTAs per SM (a decode step: every
-  // token closes its page's run); longer windows keep a prompt's grid from
-  // being mostly CTAs whose token closes nothing.
+  // Windows of one token while that is a few CTAs per SM (a decode step: every
+  // token closes its page's run).  Else a page of keys a CTA, up to what its
+  // ballot holds, so that few CTAs find nothing to close and none closes several
+  // pages in turn; and enough values for a thread's loads to overlap.
   const int heads = kv.cfg.num_kv_heads;
-  const int window =
-      (int)std::min(32LL, std::max(1LL, (long long)a.tokens * heads / (16 * kv.sms)));
+  const bool few = (long long)a.tokens * heads <= 16LL * kv.sms;
+  const int key_window = few ? 1 : std::min(kKeyWindow, kv.cfg.page_size);
+  const int value_window = few ? 1 : 8 * kAppendThreads * 8 / D;
+  const unsigned key_ctas = (unsigned)((a.tokens + key_window - 1) / key_window);
+  const unsigned value_ctas = (unsigned)((a.tokens + value_window - 1) / value_window);
   auto wide = [](const void* p, int64_t ts, int64_t hs) {
     return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ts % 8 == 0 && hs % 8 == 0;
   };
-  const dim3 grid((unsigned)((a.tokens + window - 1) / window), (unsigned)heads, 2);
+  const dim3 grid(key_ctas + value_ctas, (unsigned)heads);
   append_kernel<D, CT, IT><<<grid, kAppendThreads, 0, s>>>(
       a, static_cast<C*>(kv.k), static_cast<C*>(kv.v), kv.codes, kv.steps, kv.k_scale, kv.v_scale,
-      heads, kv.page_shift, kv.cfg.num_pages, window, wide(a.k, a.k_token_stride, a.k_head_stride),
+      heads, kv.page_shift, kv.cfg.num_pages, (int)key_ctas, key_window, value_window,
+      wide(a.k, a.k_token_stride, a.k_head_stride),
       wide(a.v, a.v_token_stride, a.v_head_stride), kv.err);
 }
 
