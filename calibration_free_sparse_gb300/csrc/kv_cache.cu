@@ -474,14 +474,22 @@ append_kernel(moe_reader_kv_append_args a, typename Cell<CT>::type* __restrict__
 template <int D, int CT, int IT>
 void append_as(const moe_reader_kv& kv, const moe_reader_kv_append_args& a, cudaStream_t s) {
   using C = typename Cell<CT>::type;
-  // Windows of one token while that is a few CTAs per SM (a decode step: every
-  // token closes its page's run).  Else a page of keys a CTA, up to what its
-  // ballot holds, so that few CTAs find nothing to close and none closes several
-  // pages in turn; and enough values for a thread's loads to overlap.
-  const int heads = kv.cfg.num_kv_heads;
-  const bool few = (long long)a.tokens * heads <= 16LL * kv.sms;
-  const int key_window = few ? 1 : std::min(kKeyWindow, kv.cfg.page_size);
-  const int value_window = few ? 1 : 8 * kAppendThreads * 8 / D;
+  // Windows of one token while that is a few CTAs per SM: in a small decode step
+  // every token closes its page's run.  A prompt closes a page only every
+  // page_size tokens, so its windows are as long as its runs can be expected to
+  // be, tokens / max_requests at least, up to a page and what the ballots hold:
+  // few CTAs find nothing to close.  (A decode step of many requests must not
+  // get long windows: a CTA closes one page after the other.  With windows of a
+  // page 1024 requests of 8 heads took 125 us, with these 23.)
+  const int heads = kv.cfg.num_kv_heads, at_once = kAppendThreads * 8 / D;
+  const long long rows = (long long)a.tokens * heads;
+  const bool few = rows <= 16LL * kv.sms;
+  const long long run = std::max(a.tokens / kv.cfg.max_requests, 1);
+  const int key_window =
+      few ? 1 : (int)std::min<long long>(std::min(kKeyWindow, kv.cfg.page_size),
+                                         std::max(run, rows / (16 * kv.sms)));
+  const int value_window =
+      few ? 1 : at_once * (int)std::min<long long>(8, 1 + rows / (4 * kv.sms * at_once));
   const unsigned key_ctas = (unsigned)((a.tokens + key_window - 1) / key_window);
   const unsigned value_ctas = (unsigned)((a.tokens + value_window - 1) / value_window);
   auto wide = [](const void* p, int64_t ts, int64_t hs) {
