@@ -12,8 +12,9 @@
 //
 // Work is a list of (row, tile of keys), a row being a request, a KV head and
 // up to 16 of its query heads.  The lengths are on the device, so every CTA
-// counts the tiles itself and takes an equal contiguous share of the list (or,
-// with few rows, a whole number of CTAs per row).  Inside a CTA every warp
+// counts the tiles itself and takes an equal contiguous share of the list (with
+// few rows a whole number of CTAs per row, with many short ones whole rows per
+// CTA or per warp).  Inside a CTA every warp
 // takes every kWarps-th tile with a private cp.async pipeline, softmax state
 // and output, and its copies run on across rows: no barrier until the share
 // ends.  Where a row ends before the share does, the warps add their states to
@@ -351,6 +352,49 @@ __device__ __forceinline__ void store_out(const Params& P, int r, int head, int 
   *at = P.q_type == kBf16 ? pack<true>(a, b) : pack<false>(a, b);
 }
 
+// Writes a row that one warp has computed.  The accumulators' 8 x 8 blocks
+// (coordinate by head) are transposed, so that a lane has neighbouring
+// coordinates of one head.
+template <class S>
+__device__ __forceinline__ void store_row(const Params& P, int r, int kvh, int head0, int rows,
+                                          const float (&o)[S::D / 16][S::NT][4],
+                                          const float (&m)[S::NT][2],
+                                          const float (&l)[S::NT][2]) {
+  constexpr int D = S::D;
+  const int lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
+#pragma unroll
+  for (int n = 0; n < S::NT; ++n) {
+    float mul[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int h = n * 8 + 2 * t4 + i;
+      float lse;
+      finish<S>(P, kvh, head0 + (h < rows ? h : 0), m[n][i], l[n][i], mul[i], lse);
+      if (g == 0 && h < rows && P.lse) P.lse[(size_t)r * P.heads + head0 + h] = lse;
+    }
+    const int h = n * 8 + g;
+    uint16_t* out = static_cast<uint16_t*>(P.out) + ((size_t)r * P.heads + head0 + h) * D;
+#pragma unroll
+    for (int x = 0; x < D / 16; ++x) {
+      uint32_t v[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float a = o[x][n][2 * i] * mul[0], b = o[x][n][2 * i + 1] * mul[1];
+        v[i] = transpose8(P.q_type == kBf16 ? pack<true>(a, b) : pack<false>(a, b));
+      }
+      if (h >= rows) continue;
+      if constexpr (S::CT == kE4m3) {
+        // rows g and g + 8 of the block are coordinates 2g and 2g + 1
+        *reinterpret_cast<uint2*>(out + x * 16 + 4 * t4) =
+            make_uint2(__byte_perm(v[0], v[1], 0x5410), __byte_perm(v[0], v[1], 0x7632));
+      } else {
+        *reinterpret_cast<uint32_t*>(out + x * 16 + 2 * t4) = v[0];
+        *reinterpret_cast<uint32_t*>(out + x * 16 + 8 + 2 * t4) = v[1];
+      }
+    }
+  }
+}
+
 // Sums the pieces of a row that several CTAs wrote, in order; all of the CTA.
 template <class S>
 __device__ __forceinline__ void join_row(const Params& P, const Item<S>& it, int rt, int U, int pieces,
@@ -482,6 +526,20 @@ __global__ void __launch_bounds__(S::kThreads, 1) attend_kernel(const Params P) 
     }
     if (W <= U + kSplit) whole = true, U = max(W, 1);
   }
+  // More rows than CTAs.  In tiles of a warp's time (about 0.75 us): what its
+  // share takes, seven for each row that a CTA's warps add up, fifteen for the
+  // rows that equal shares cut.  Short rows are dealt whole, to the CTAs in whose
+  // part of the list they begin, which costs half a row in balance; the shortest
+  // to single warps (solo), which then meet nobody, but carry the longest row
+  // alone.  128 requests of up to 100 / 500 / 1000 / 2000 tokens, 8 KV heads:
+  // equal shares 47 / 62 / 84 / 128 us, whole rows per CTA - / - / - / 120, per
+  // warp 15 / 41 / 70 / 132; 40 requests of up to 600, 4 KV heads: 26 / 18 / 27.
+  const int each = total / (grid * kWarps), added = 7 * (items / grid);
+  const bool many = items > grid;
+  const bool aligned = many && most < 20 * kWarps;
+  const int meeting = each + added + (aligned ? 7 + most / (2 * kWarps) : 15);
+  const bool solo = many && max(most, each) + most / 4 + items * 3 / (2 * grid * kWarps) < meeting;
+  if (many && (solo || aligned)) U = 1 << 30;       // no row is cut
   // prefix of the (padded) tiles of a request's one item
   {
     int run = 0;
@@ -522,8 +580,24 @@ __global__ void __launch_bounds__(S::kThreads, 1) attend_kernel(const Params P) 
         P.lse[(size_t)r * P.heads + i] = P.sinks ? P.sinks[i] : -INFINITY;
   }
 
-  if ((long long)cta * U >= all) return;
-  const int c0 = cta * U, c1 = min(all - c0, U) + c0;
+  // [c0, c1): the share of the CTA or (solo) the warp
+  int c0, c1;
+  if (many && (solo || aligned)) {
+    const int part = solo ? cta * kWarps + wid : cta, parts = solo ? grid * kWarps : grid;
+    auto row_from = [&](long long t) {               // the first row from t on
+      if (t >= all) return all;
+      const Item<S> it = item_at<S>(P, s_prefix, s_len, per, (int)t);
+      return it.begin < t ? it.end : it.begin;
+    };
+    c0 = row_from((long long)part * all / parts);
+    c1 = row_from((long long)(part + 1) * all / parts);
+    if (c0 >= c1) return;                            // the CTA, or a warp that meets no other
+  } else {
+    if ((long long)cta * U >= all) return;
+    c0 = cta * U;
+    c1 = min(all - c0, U) + c0;
+  }
+  const int step = solo ? 1 : kWarps, from0 = solo ? c0 : c0 + wid;   // this warp's tiles
 
   // CTAs that hold a part of a row; one more part of it is written (the last
   // to say so gets true, and clears the counter for the next launch)
@@ -548,7 +622,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) attend_kernel(const Params P) 
   Source now, next;
   long long now_at = 0;    // byte offset of the lane's subtile
   auto look = [&](int n) { // the batch that begins with the warp's tile n
-    const int t = c0 + wid + (n + lane / kMt) * kWarps;
+    const int t = from0 + (n + lane / kMt) * step;
     next.pos = kNowhere;
     next.id = next.head = next.in = next.lo = next.len = 0;
     if (t < c1) next = source_at<S>(P, s_prefix, s_len, per, t, lane % kMt, bad);
@@ -565,7 +639,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) attend_kernel(const Params P) 
       now_at = ((((long long)now.id * P.kv_heads + now.head) << P.shift) + now.in) * S::kRow;
       look(copied + kBatch);
     }
-    if (c0 + wid + copied * kWarps < c1) {
+    if (from0 + copied * step < c1) {
       const uint32_t base = pipe + in_stage * S::kTile;
 #pragma unroll
       for (int s = 0; s < kMt; ++s) {
@@ -596,7 +670,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) attend_kernel(const Params P) 
   // ---- pieces: the rows, or parts of rows, of this share ----
   float o[D / 16][NT][4], m[NT][2], l[NT][2];
   Item<S> cc;
-  int p0 = c0, t = c0 + wid;
+  int p0 = c0, t = from0;
   for (int k = 0;; ++k) {
     cc = item_at<S>(P, s_prefix, s_len, per, p0);
     const int p1 = min(c1, cc.end);
@@ -665,7 +739,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) attend_kernel(const Params P) 
     }
 
 #pragma unroll 1
-    for (; t < p1; t += kWarps) {
+    for (; t < p1; t += step) {
       cp_wait<S::kStages - 2>();
       __syncwarp();
       issue();          // into the stage that the previous tile left
@@ -852,6 +926,15 @@ __global__ void __launch_bounds__(S::kThreads, 1) attend_kernel(const Params P) 
       for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int x = 4; x < 32; x <<= 1) l[n][i] += __shfl_xor_sync(0xffffffffu, l[n][i], x);
+    if (solo) {
+      store_row<S>(P, cc.r, kvh, head0, rows_here, o, m, l);
+      if (p1 == c1) {
+        if (bad) atomicOr(P.err, bad);
+        return;
+      }
+      p0 = p1;
+      continue;
+    }
     if (p1 == c1) break;
 
     // ---- the row ends here, the share does not: add to its state in turn ----

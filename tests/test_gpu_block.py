@@ -87,12 +87,12 @@ class Cache:
 
     def rows(self, r, head, positions):
         """(k, v) float64 rows of request r at positions."""
-        ids = self.table_np[r, positions // self.page]
-        off = positions % self.page
+        ids = torch.from_numpy(self.table_np[r, positions // self.page]).long().cuda()
+        off = torch.from_numpy(positions % self.page).long().cuda()
         out = []
         for c, s in ((self.k, self.scales[0]), (self.v, self.scales[1])):
-            picked = torch.stack([c[int(i), head, int(o)].float() for i, o in zip(ids, off)])
-            x = f64(picked)
+            bits = c if c.element_size() > 1 else c.view(torch.uint8)
+            x = f64(bits[ids, head, off].view(c.dtype).float())
             out.append(x if s is None else x * float(s[head]))
         return out
 
@@ -196,6 +196,26 @@ def test_attend_splits(lens, kv, dtype):
     c.cache.attend(q, c.table, c.lens_t, again)
     assert torch.equal(out, again)
     check_attend(c, q, out, lse)
+
+
+@pytest.mark.parametrize("dim,dtype,qt,group", [(64, HF, HF, 16), (128, BF, BF, 8), (128, E4, BF, 5),
+                                                (256, BF, BF, 3)])
+@pytest.mark.parametrize("lens", [
+    [2700 - 40 * i for i in range(20)],                   # rows cut by equal shares
+    [1200 - 50 * i for i in range(20)],                   # whole rows per CTA
+    [0, 1, 500] + [17 + 3 * i for i in range(61)],        # whole rows per warp
+    [3000] + [5] * 40])                                   # one long row among short ones
+def test_attend_many_rows(dim, dtype, qt, group, lens):
+    """More rows than CTAs, in each way that they are dealt out."""
+    c = Cache(lens, 8, dim, 64, dtype, seed=len(lens), q_heads=8 * group, summaries=False)
+    q = queries(len(lens), 8 * group, dim, qt)
+    out, again = torch.full_like(q, math.nan), torch.empty_like(q)
+    lse = torch.full(q.shape[:2], math.nan, device="cuda")
+    sinks = torch.linspace(-4, 4, 8 * group).cuda()
+    c.cache.attend(q, c.table, c.lens_t, out, lse=lse, sinks=sinks)
+    c.cache.attend(q, c.table, c.lens_t, again, sinks=sinks)
+    assert torch.equal(out, again) and c.cache.status() == (0, 0)
+    check_attend(c, q, out, lse, sinks=sinks)
 
 
 @pytest.mark.parametrize("window", [1, 5, 16, 100, 300, 100000])
