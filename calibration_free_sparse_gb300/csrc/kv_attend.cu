@@ -60,7 +60,7 @@ struct Shape {
   static constexpr int kWarps = kRow >= 512 ? 4 : CT == kE4m3 && NT == 1 && D <= 128 ? 12 : 8;
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kStages = 192 * 1024 / (kWarps * kTile);   // copies in flight: all but one
-    static constexpr int kSplit = 64;                          // tiles that a join is worth
+  static constexpr int kSplit = 64;                          // tiles that a join is worth
   static constexpr int kRows = 8 * NT;                       // query heads of a row
   // the sum over the warps at the end runs over slices of the coordinates
   static constexpr int kSlice = kWarps * kRows >= 96 ? 32 : 64;
