@@ -14,8 +14,9 @@
 // up to 16 of its query heads.  The lengths are on the device, so every CTA
 // counts the tiles itself and takes an equal contiguous share of the list (with
 // few rows a whole number of CTAs per row, with many short ones whole rows per
-// CTA or per warp).  Inside a CTA every warp
-// takes every kWarps-th tile with a private cp.async pipeline, softmax state
+// CTA or per warp; where lengths differ much, the short rows go to single warps,
+// which take them before their CTA's share of the others).  Inside a CTA every
+// warp takes every kWarps-th tile with a private cp.async pipeline, softmax state
 // and output, and its copies run on across rows: no barrier until the share
 // ends.  Where a row ends before the share does, the warps add their states to
 // one in shared memory in turns, beginning with another warp each time, and go
@@ -73,7 +74,8 @@ struct Shape {
   static constexpr int kSum = kSumA > kSumB ? kSumA : kSumB;
   static constexpr int kMl = kWarps * kRows * 2 * 4;
   static constexpr int kPos = kWarps * kStages * kMt * 4;
-  static constexpr int kSmem = kPipe + kSum + kMl + kPos + (2 * kMaxRequests + 1) * 4;
+  static constexpr int kSmem = kPipe + kSum + kMl + kPos + (2 * kMaxRequests + 1) * 4 +
+                               kMaxRequests * 2;
   static_assert(kRows * kMaxSms * 4 <= kSum, "join weights of a piece per CTA");
   static_assert(kSmem + 2048 <= 227 * 1024 && kStages >= 2, "shared memory");
 };
@@ -223,16 +225,17 @@ struct Item {
 };
 
 template <class S>
-__device__ __forceinline__ Item<S> item_at(const Params& P, const int* prefix, const int* lens,
-                                           int per, int t) {
+__device__ __forceinline__ Item<S> item_at(const Params& P, const int* prefix,
+                                           const uint16_t* order, const int* lens, int per,
+                                           int t) {
   int lo = 0, hi = P.requests - 1;
   while (lo < hi) {                      // the last request that begins at t or before
     const int mid = (lo + hi + 1) >> 1;
     if (prefix[mid] * per <= t) lo = mid; else hi = mid - 1;
   }
   Item<S> o;
-  o.r = lo;
-  o.row = row_of(P, lens[lo]);
+  o.r = order[lo];
+  o.row = row_of(P, lens[o.r]);
   o.tiles = tiles_of<S>(o.row);
   const int first = prefix[lo] * per, padded = prefix[lo + 1] - prefix[lo];
   o.sub = (t - first) / padded;
@@ -251,10 +254,11 @@ constexpr int kNowhere = INT32_MAX - 64;
 // Source of subtile s of the tile at index t.  The page id is used by the
 // caller only later, so that its load is in flight meanwhile.
 template <class S>
-__device__ __forceinline__ Source source_at(const Params& P, const int* prefix, const int* lens,
-                                            int per, int t, int s, uint32_t& bad) {
+__device__ __forceinline__ Source source_at(const Params& P, const int* prefix,
+                                            const uint16_t* order, const int* lens, int per,
+                                            int t, int s, uint32_t& bad) {
   Source o;
-  const Item<S> it = item_at<S>(P, prefix, lens, per, t);
+  const Item<S> it = item_at<S>(P, prefix, order, lens, per, t);
   o.id = 0;
   o.pos = kNowhere;
   o.lo = it.row.lo;
@@ -462,6 +466,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) attend_kernel(const Params P) 
   int* s_pos = reinterpret_cast<int*>(smem + S::kPipe + S::kSum + S::kMl);
   int* s_prefix = s_pos + S::kPos / 4;
   int* s_len = s_prefix + kMaxRequests + 1;
+  uint16_t* s_order = reinterpret_cast<uint16_t*>(s_len + kMaxRequests);   // requests of the list
   __shared__ int4 s_scan[kWarps];
   __shared__ int s_before[kWarps];
   __shared__ uint32_t s_turn[2];
@@ -476,7 +481,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) attend_kernel(const Params P) 
 
   if (tid < 2) s_turn[tid] = 0, s_last[tid] = 0;
   wait_for_earlier_launch();
-  // ---- shares: U tiles per CTA ----
+  // ---- shares of the rows that CTAs share: U tiles per CTA ----
   constexpr int kPer = (kMaxRequests + S::kThreads - 1) / S::kThreads;
   int mine[kPer], sum = 0, rows = 0, most = 0;
 #pragma unroll
@@ -497,82 +502,147 @@ __global__ void __launch_bounds__(S::kThreads, 1) attend_kernel(const Params P) 
   }
   if (blockIdx.x == 0 && bad) atomicOr(P.err, bad);
   bad = 0;
-  sum = __reduce_add_sync(0xffffffffu, sum);
-  rows = __reduce_add_sync(0xffffffffu, rows);
-  most = __reduce_max_sync(0xffffffffu, most);
-  if (lane == 0) s_scan[wid] = make_int4(sum, rows, most, 0);
-  __syncthreads();
-  sum = rows = most = 0;
+  auto block_sums = [&](int& a, int& b, int& top) {    // two sums and a maximum
+    a = __reduce_add_sync(0xffffffffu, a);
+    b = __reduce_add_sync(0xffffffffu, b);
+    top = __reduce_max_sync(0xffffffffu, top);
+    if (lane == 0) s_scan[wid] = make_int4(a, b, top, 0);
+    __syncthreads();
+    a = b = top = 0;
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    const int4 v = s_scan[w];
-    sum += v.x;
-    rows += v.y;
-    most = max(most, v.z);
-  }
+    for (int w = 0; w < kWarps; ++w) {
+      const int4 v = s_scan[w];
+      a += v.x;
+      b += v.y;
+      top = max(top, v.z);
+    }
+  };
+  block_sums(sum, rows, most);
   const int grid = (int)gridDim.x / P.row_tiles;
-  const int total = sum * per, items = rows * per;
-  // Shares of equal size: best where the cache is long.  A row of its own per
-  // CTA (or a whole number of CTAs per row) where that costs no CTA more than
-  // kSplit tiles extra: a row that is split costs its CTAs the join.
+  int total = sum * per, items = rows * per;
+
+  // Times below are in tiles of a warp's time (about 0.75 us).  A row that the
+  // warps of a CTA share costs them about seven beside its tiles, a row that
+  // CTAs share fifteen; a row that a single warp has to itself costs one and a
+  // half, but all of its tiles are that warp's.
+  int short_most = 0;             // rows of at most so many tiles are single warps'
+  const bool differ = items >= 16 && (long long)most * items >= 2LL * total;
+  if (items > grid || differ) {
+    const int each = total / (grid * kWarps);          // a warp's part
+    if (items > grid) {
+      const int meeting = each + 7 * (items / grid) +
+                          (most < 20 * kWarps ? 7 + most / (2 * kWarps) : 15);
+      if (max(most, each) + most / 4 + items * 3 / (2 * grid * kWarps) < meeting)
+        short_most = most;
+    }
+    if (short_most == 0 && differ) {
+      // The short rows go to single warps, where they are many, the others are
+      // shared.  8 KV heads of 128, 128 requests: lengths lognormal around 500
+      // (sigma 1) 109 -> 80 us, around 100 (1.2) 79 -> 40, one of 8192 tokens
+      // and 127 of 5 96 -> 18.  Up to half a part instead: 89 us for the first.
+      const int limit = max(each, 16);
+      int b_sum = 0, b_rows = 0, none = 0;
+#pragma unroll
+      for (int j = 0; j < kPer; ++j)
+        if (mine[j] > 0 && mine[j] <= limit) b_sum += mine[j], ++b_rows;
+      __syncthreads();                                 // s_scan is read above
+      block_sums(b_sum, b_rows, none);
+      if (b_rows * per * 2 >= grid && b_rows < rows) {
+        short_most = limit;
+        total -= b_sum * per;
+        items -= b_rows * per;
+      }
+    }
+  }
+  // The other rows.  Equal shares: best where the cache is long.  A row of its
+  // own per CTA (or a whole number of CTAs per row) where that costs no CTA more
+  // than kSplit tiles extra.  More rows than CTAs, but short ones: whole rows, to
+  // the CTAs in whose part of the list they begin, which costs half a row in
+  // balance.  Measured, 8 KV heads of 128, 128 requests of up to 100 / 500 / 1000 /
+  // 2000 tokens: equal shares 47 / 62 / 84 / 128 us, whole rows per CTA - / - / - /
+  // 120, per warp 15 / 41 / 70 / 132; 40 requests of up to 600, 4 KV heads: 26 /
+  // 18 / 27.
   constexpr int kSplit = S::kSplit;
   int U = max((total + grid - 1) / grid, kWarps);
-  bool whole = false;
+  bool whole = false, aligned = false;
   if (items <= grid) {
-    int W = most;                                 // no row split
+    int W = most;                                      // no row split
     if (items < grid) {
       const int cut = max((total + (grid - items) - 1) / (grid - items), kWarps);
       if (cut + kSplit < W) W = cut;
     }
     if (W <= U + kSplit) whole = true, U = max(W, 1);
+  } else if (most < 20 * kWarps) {
+    aligned = true;
+    U = 1 << 30;                                       // no row is cut
   }
-  // More rows than CTAs.  In tiles of a warp's time (about 0.75 us): what its
-  // share takes, seven for each row that a CTA's warps add up, fifteen for the
-  // rows that equal shares cut.  Short rows are dealt whole, to the CTAs in whose
-  // part of the list they begin, which costs half a row in balance; the shortest
-  // to single warps (solo), which then meet nobody, but carry the longest row
-  // alone.  128 requests of up to 100 / 500 / 1000 / 2000 tokens, 8 KV heads:
-  // equal shares 47 / 62 / 84 / 128 us, whole rows per CTA - / - / - / 120, per
-  // warp 15 / 41 / 70 / 132; 40 requests of up to 600, 4 KV heads: 26 / 18 / 27.
-  const int each = total / (grid * kWarps), added = 7 * (items / grid);
-  const bool many = items > grid;
-  const bool aligned = many && most < 20 * kWarps;
-  const int meeting = each + added + (aligned ? 7 + most / (2 * kWarps) : 15);
-  const bool solo = many && max(most, each) + most / 4 + items * 3 / (2 * grid * kWarps) < meeting;
-  if (many && (solo || aligned)) U = 1 << 30;       // no row is cut
-  // prefix of the (padded) tiles of a request's one item
-  {
-    int run = 0;
+  // The list: requests whose rows are shared, padded to whole shares, then those
+  // whose rows are single warps'.
+  int at_b = 0, at_n = 0, all_n = 0;                   // short requests: tiles and their number
+  if (short_most > 0) {
+    int b = 0, n = 0;
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-      if (whole) mine[j] = (mine[j] + U - 1) / U * U;
-      run += mine[j];
-    }
-    int in = run;
+    for (int j = 0; j < kPer; ++j)
+      if (mine[j] > 0 && mine[j] <= short_most) b += mine[j], ++n;
+    int ib = b, in = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int u = __shfl_up_sync(0xffffffffu, in, o);
-      if (lane >= o) in += u;
+      const int ub = __shfl_up_sync(0xffffffffu, ib, o), un = __shfl_up_sync(0xffffffffu, in, o);
+      if (lane >= o) ib += ub, in += un;
     }
-    if (lane == 31) s_before[wid] = in;
+    __syncthreads();                                   // s_scan is read above
+    if (lane == 31) s_scan[wid] = make_int4(ib, in, 0, 0);
     __syncthreads();
-    int at = in - run;
+    at_b = ib - b;
+    at_n = in - n;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) at += w < wid ? s_before[w] : 0;
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-      const int r = tid * kPer + j;
-      if (r < P.requests) s_prefix[r] = at;
-      at += mine[j];
+    for (int w = 0; w < kWarps; ++w) {
+      const int4 v = s_scan[w];
+      if (w < wid) at_b += v.x, at_n += v.y;
+      all_n += v.y;
     }
-    if (tid == S::kThreads - 1) s_prefix[P.requests] = at;
   }
+  int a = 0;
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    if (whole && mine[j] > short_most) mine[j] = (mine[j] + U - 1) / U * U;
+    if (mine[j] > short_most) a += mine[j];
+  }
+  int ia = a;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int up = __shfl_up_sync(0xffffffffu, ia, o);
+    if (lane >= o) ia += up;
+  }
+  if (lane == 31) s_before[wid] = ia;
   __syncthreads();
-  const int all = s_prefix[P.requests] * per;
+  int at_a = ia - a, all_a = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    const int v = s_before[w];
+    if (w < wid) at_a += v;
+    all_a += v;
+  }
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    const int r = tid * kPer + j;
+    const bool brief = mine[j] > 0 && mine[j] <= short_most;
+    if (r < P.requests) {
+      const int i = brief ? P.requests - all_n + at_n : r - at_n;
+      s_order[i] = (uint16_t)r;
+      s_prefix[i] = brief ? all_a + at_b : at_a;
+    }
+    if (brief) at_b += mine[j], ++at_n;
+    else at_a += mine[j];
+  }
+  if (tid == S::kThreads - 1) s_prefix[P.requests] = all_a + at_b;
+  __syncthreads();
+  const int shared_end = all_a * per, all = s_prefix[P.requests] * per;
 
   // rows with nothing to read
-  for (int r = blockIdx.x; r < P.requests; r += gridDim.x) {
-    if (s_prefix[r + 1] != s_prefix[r]) continue;
+  for (int e = blockIdx.x; e < P.requests; e += gridDim.x) {
+    if (s_prefix[e + 1] != s_prefix[e]) continue;
+    const int r = s_order[e];
     uint4* o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(P.out) + (size_t)r * P.heads * D);
     for (int i = tid; i < P.heads * D / 8; i += S::kThreads) o[i] = make_uint4(0, 0, 0, 0);
     if (P.lse)
@@ -580,24 +650,31 @@ __global__ void __launch_bounds__(S::kThreads, 1) attend_kernel(const Params P) 
         P.lse[(size_t)r * P.heads + i] = P.sinks ? P.sinks[i] : -INFINITY;
   }
 
-  // [c0, c1): the share of the CTA or (solo) the warp
-  int c0, c1;
-  if (many && (solo || aligned)) {
-    const int part = solo ? cta * kWarps + wid : cta, parts = solo ? grid * kWarps : grid;
-    auto row_from = [&](long long t) {               // the first row from t on
-      if (t >= all) return all;
-      const Item<S> it = item_at<S>(P, s_prefix, s_len, per, (int)t);
-      return it.begin < t ? it.end : it.begin;
-    };
-    c0 = row_from((long long)part * all / parts);
-    c1 = row_from((long long)(part + 1) * all / parts);
-    if (c0 >= c1) return;                            // the CTA, or a warp that meets no other
-  } else {
-    if ((long long)cta * U >= all) return;
+  // [c0, c1): the CTA's share; [b0, b1): the rows that are this warp's own
+  auto row_from = [&](long long t) {                   // the first row from t on
+    if (t >= all) return all;
+    const Item<S> it = item_at<S>(P, s_prefix, s_order, s_len, per, (int)t);
+    return it.begin < t ? it.end : it.begin;
+  };
+  int c0 = 0, c1 = 0, b0 = 0, b1 = 0;
+  if (aligned) {
+    if (shared_end > 0) {
+      c0 = min(row_from((long long)cta * shared_end / grid), shared_end);
+      c1 = min(row_from((long long)(cta + 1) * shared_end / grid), shared_end);
+    }
+  } else if ((long long)cta * U < shared_end) {
     c0 = cta * U;
-    c1 = min(all - c0, U) + c0;
+    c1 = min(shared_end - c0, U) + c0;
   }
-  const int step = solo ? 1 : kWarps, from0 = solo ? c0 : c0 + wid;   // this warp's tiles
+  if (all > shared_end) {
+    const long long part = cta * kWarps + wid, parts = grid * kWarps, own = all - shared_end;
+    b0 = row_from(shared_end + part * own / parts);
+    b1 = row_from(shared_end + (part + 1) * own / parts);
+  }
+  const int n_own = max(b1 - b0, 0);                   // the warp's tiles: its own rows first
+  const int tiles = n_own + (c1 > c0 + wid ? (c1 - c0 - wid + kWarps - 1) / kWarps : 0);
+  if (n_own == 0 && c0 >= c1) return;                  // all warps of a CTA share or none
+  auto tile_at = [&](int n) { return n < n_own ? b0 + n : c0 + wid + (n - n_own) * kWarps; };
 
   // CTAs that hold a part of a row; one more part of it is written (the last
   // to say so gets true, and clears the counter for the next launch)
@@ -622,10 +699,11 @@ __global__ void __launch_bounds__(S::kThreads, 1) attend_kernel(const Params P) 
   Source now, next;
   long long now_at = 0;    // byte offset of the lane's subtile
   auto look = [&](int n) { // the batch that begins with the warp's tile n
-    const int t = from0 + (n + lane / kMt) * step;
+    const int i = n + lane / kMt;
     next.pos = kNowhere;
     next.id = next.head = next.in = next.lo = next.len = 0;
-    if (t < c1) next = source_at<S>(P, s_prefix, s_len, per, t, lane % kMt, bad);
+    if (i < tiles)
+      next = source_at<S>(P, s_prefix, s_order, s_len, per, tile_at(i), lane % kMt, bad);
   };
   int in_stage = 0, out_stage = 0;
   auto issue = [&]() {
@@ -639,7 +717,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) attend_kernel(const Params P) 
       now_at = ((((long long)now.id * P.kv_heads + now.head) << P.shift) + now.in) * S::kRow;
       look(copied + kBatch);
     }
-    if (from0 + copied * step < c1) {
+    if (copied < tiles) {
       const uint32_t base = pipe + in_stage * S::kTile;
 #pragma unroll
       for (int s = 0; s < kMt; ++s) {
@@ -670,10 +748,11 @@ __global__ void __launch_bounds__(S::kThreads, 1) attend_kernel(const Params P) 
   // ---- pieces: the rows, or parts of rows, of this share ----
   float o[D / 16][NT][4], m[NT][2], l[NT][2];
   Item<S> cc;
-  int p0 = c0, t = from0;
-  for (int k = 0;; ++k) {
-    cc = item_at<S>(P, s_prefix, s_len, per, p0);
-    const int p1 = min(c1, cc.end);
+  bool own = n_own > 0;
+  int p0 = own ? b0 : c0, t = own ? b0 : c0 + wid;
+  for (int k = 0;;) {                                  // k: shared pieces so far
+    cc = item_at<S>(P, s_prefix, s_order, s_len, per, p0);
+    const int p1 = own ? cc.end : min(c1, cc.end), step = own ? 1 : kWarps;
     const int real = min(p1, cc.begin + cc.tiles);     // tiles beyond are padding
     const int kvh = cc.sub, row0 = rt * S::kRows;
     const int rows_here = min(S::kRows, P.group - row0);
@@ -926,13 +1005,17 @@ __global__ void __launch_bounds__(S::kThreads, 1) attend_kernel(const Params P) 
       for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int x = 4; x < 32; x <<= 1) l[n][i] += __shfl_xor_sync(0xffffffffu, l[n][i], x);
-    if (solo) {
+    if (own) {
       store_row<S>(P, cc.r, kvh, head0, rows_here, o, m, l);
-      if (p1 == c1) {
+      p0 = p1;
+      if (p1 < b1) continue;
+      if (c0 >= c1) {
         if (bad) atomicOr(P.err, bad);
         return;
       }
-      p0 = p1;
+      own = false;
+      p0 = c0;
+      t = c0 + wid;
       continue;
     }
     if (p1 == c1) break;
@@ -1005,6 +1088,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) attend_kernel(const Params P) 
     }
     if (lane == 0) pass_turn(&s_turn[b], turn + 1);
     p0 = p1;
+    ++k;
   }
 
   // ---- the share's last piece: all warps at once ----
@@ -1096,7 +1180,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) attend_kernel(const Params P) 
 #pragma unroll 1
   for (int e = 0; e < 2; ++e) {
     if (!s_last[e]) continue;
-    const Item<S> it = item_at<S>(P, s_prefix, s_len, per, e ? c1 - 1 : c0);
+    const Item<S> it = item_at<S>(P, s_prefix, s_order, s_len, per, e ? c1 - 1 : c0);
     join_row<S>(P, it, rt, U, pieces_of(it), s_sum, s_mul);
   }
   if (bad) atomicOr(P.err, bad);

@@ -204,7 +204,8 @@ def test_attend_splits(lens, kv, dtype):
     [2700 - 40 * i for i in range(20)],                   # rows cut by equal shares
     [1200 - 50 * i for i in range(20)],                   # whole rows per CTA
     [0, 1, 500] + [17 + 3 * i for i in range(61)],        # whole rows per warp
-    [3000] + [5] * 40])                                   # one long row among short ones
+    [3000] + [5] * 40,                                    # one long row among short ones
+    [3, 0, 1900] + [40 + i for i in range(50)] + [0, 5000, 1] + [30] * 20 + [7000]])
 def test_attend_many_rows(dim, dtype, qt, group, lens):
     """More rows than CTAs, in each way that they are dealt out."""
     c = Cache(lens, 8, dim, 64, dtype, seed=len(lens), q_heads=8 * group, summaries=False)
