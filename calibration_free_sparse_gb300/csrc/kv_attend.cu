@@ -946,9 +946,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) attend_kernel(const Params P) 
       // O^T += V^T P^T.  The products' type would round the weights as coarsely
       // as the output is rounded, which made the result's error 1.42 times that
       // of one rounding; so what the rounding left goes through a second
-      // product (an e4m3 cache's fp16 weights are finer than bf16 outputs and
-      // need it for fp16 outputs only).
-      const bool two = !k8 || P.q_type == kF16;
+      // product.
 #pragma unroll
       for (int s = 0; s < kMt; ++s) {
         uint32_t pf[NT][2], pr[NT][2];
@@ -958,11 +956,9 @@ __global__ void __launch_bounds__(S::kThreads, 1) attend_kernel(const Params P) 
           for (int i = 0; i < 2; ++i) {
             const float a = sc[s][n][2 * i], b = sc[s][n][2 * i + 1];
             const uint32_t r = pack<kBf>(a, b);
+            const float2 f = unpack<kBf>(r);
             pf[n][i] = transpose8(r);
-            if (two) {
-              const float2 f = unpack<kBf>(r);
-              pr[n][i] = transpose8(pack<kBf>(a - f.x, b - f.y));
-            }
+            pr[n][i] = transpose8(pack<kBf>(a - f.x, b - f.y));
           }
         const uint32_t vb = vs + s * 16 * S::kRow + v_lane;
         if constexpr (!k8) {
@@ -991,7 +987,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) attend_kernel(const Params P) 
 #pragma unroll
               for (int n = 0; n < NT; ++n) {
                 mma<false>(o[2 * d + j][n], a, pf[n][0], pf[n][1]);
-                if (two) mma<false>(o[2 * d + j][n], a, pr[n][0], pr[n][1]);
+                mma<false>(o[2 * d + j][n], a, pr[n][0], pr[n][1]);
               }
             }
           }

@@ -1,0 +1,103 @@
+"""Numerical edges of the decode-step operators: what the weights of attention
+keep, infinities and NaN among the rows that are read, and the range of the
+page summaries.  References are in 64 bits; tolerances follow from the
+arithmetic, as each test says (u: half an ulp of a type, d: the bound
+(D + 16) 2^-24 scale sum |q k| of a logit's error in fp32)."""
+
+import math
+
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from tests import test_gpu_block as T  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+
+if torch.cuda.is_available():
+    from calibration_free_sparse_gb300 import block
+    from calibration_free_sparse_gb300 import reader as rd
+
+BF, HF, F32, E4 = T.BF, T.HF, T.F32, T.E4
+U = T.HALF_ULP
+
+
+@pytest.fixture(autouse=True)
+def need_gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+
+
+def given_cache(k, v, dtype, page=16, q_heads=None, scale=1.0):
+    """A Cache of requests [R][n][kv][dim] float64 whose rows are given (all of
+    one length, exact in the cache's type); 8-bit caches have one scale."""
+    R, n, kv, dim = k.shape
+    c = T.Cache([n] * R, kv, dim, page, dtype, q_heads=q_heads, summaries=False)
+    if dtype == E4:
+        c.k_scale.fill_(scale), c.v_scale.fill_(scale)
+        c.scales[0].fill_(scale), c.scales[1].fill_(scale)
+    pos = np.arange(n)
+    for r in range(R):
+        ids = torch.from_numpy(c.table_np[r, pos // page]).long().cuda()
+        off = torch.from_numpy(pos % page).long().cuda()
+        for cache, rows in ((c.k, k[r]), (c.v, v[r])):
+            x = torch.from_numpy(rows / (scale if dtype == E4 else 1.0)).to(dtype).cuda()
+            if dtype == E4:
+                cache.view(torch.uint8)[ids, :, off] = x.view(torch.uint8)
+            else:
+                cache[ids, :, off] = x
+    return c
+
+
+def exact(c, q, r, h, scale):
+    """(out [G][dim], lse [G], A, d, n) of a request and KV head in 64 bits; A is
+    the weighted mean of |v| over the finite v, d the bound of a logit's error."""
+    G, dim = q.shape[1] // c.k.shape[1], q.shape[2]
+    mine = slice(h * G, h * G + G)
+    k, v = c.rows(r, h, np.arange(c.lens[r]))
+    x = T.f64(q[r, mine])
+    with np.errstate(all="ignore"):
+        s = scale * x @ k.T
+        top = s.max(1, keepdims=True)
+        p = np.exp(s - top)
+        den = p.sum(1, keepdims=True)
+        out = np.where(np.isinf(v).any(0), (p[:, :, None] * v).sum(1), p @ np.where(np.isinf(v), 0, v))
+        A = p @ np.abs(np.where(np.isfinite(v), v, 0)) / den
+        d = ((dim + 16) * 2.0 ** -24 * scale * (np.abs(x) @ np.abs(k).T)).max(1, keepdims=True)
+        return out / den, (np.log(den) + top)[:, 0], A, d, len(v)
+
+
+def attended(c, q, scale=None, **kw):
+    out = torch.full_like(q, 7.0)
+    lse = torch.full(q.shape[:2], 7.0, device="cuda")
+    c.cache.attend(q, c.table, c.lens_t, out, lse=lse, scale=scale, **kw)
+    assert c.cache.status() == (0, 0)
+    return T.f64(out), T.f64(lse)
+
+
+# --------------------------------------------------------------------------
+# the weights of attention
+# --------------------------------------------------------------------------
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("dtype,qt", [(BF, BF), (HF, HF), (E4, HF), (E4, BF)])
+def test_attend_weights_keep_their_bits(dim, dtype, qt):
+    """Two keys whose weights nearly cancel: out = tanh(delta / 2), far below
+    the weights, so what their rounding loses stands out.  A weight may be off
+    by the fp32 forms of its logit and exponential and by 2^-20 of itself, the
+    output by its own rounding.  (Weights of 8 or 11 bits would be off by 2^-9
+    or 2^-12: an output by half that.)"""
+    g = torch.Generator().manual_seed(dim)
+    R, G = 40, 8
+    k, v = np.zeros((R, 2, 1, dim)), np.ones((R, 2, 1, dim))
+    k[:, 0, :, 0], v[:, 1] = 1, -1
+    c = given_cache(k, v, dtype, q_heads=G)
+    q = torch.zeros((R, G, dim))
+    q[:, :, 0] = 2.0 ** -(6 + 3 * torch.rand((R, G), generator=g)) * \
+        torch.sign(torch.randn((R, G), generator=g))
+    q = q.to(qt).cuda()
+    out, _ = attended(c, q, 1.0)
+    for r in range(R):
+        ref, _, A, d, _ = exact(c, q, r, 0, 1.0)
+        tol = (2.0 ** -19 + 2 * d) * A + U[qt] * np.abs(ref)
+        assert np.all(np.abs(out[r] - ref) <= tol), r
