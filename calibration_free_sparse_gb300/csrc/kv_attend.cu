@@ -62,6 +62,16 @@ struct Shape {
   static constexpr int kThreads = 32 * kWarps;
   static constexpr int kStages = 192 * 1024 / (kWarps * kTile);   // copies in flight: all but one
   static constexpr int kSplit = 64;                          // tiles that a join is worth
+  // Weights are formed relative to a reference that lies 2^kLift below the
+  // largest logit when it is set and follows that only when it has grown by
+  // more than 2^kSlack: the sums stay exact to a common factor, and nearly
+  // every tile saves the rescaling.  fp16 weights so reach 2^15, and what lies
+  // 2^-35 below the largest is still a multiple of their least value (with the
+  // reference at the largest, everything below 2^-25 of it was lost: 200 keys
+  // beside a dominant one).  bf16 has fp32's range: there the weights stay below
+  // one, so that no sum exceeds what the values allow.
+  static constexpr float kLift = CT == kBf16 ? -8.f : 11.f;
+  static constexpr float kSlack = CT == kBf16 ? 8.f : 4.f;
   static constexpr int kRows = 8 * NT;                       // query heads of a row
   // the sum over the warps at the end runs over slices of the coordinates
   static constexpr int kSlice = kWarps * kRows >= 96 ? 32 : 64;
@@ -329,7 +339,7 @@ __device__ __forceinline__ void pass_turn(uint32_t* turn, uint32_t next) {
 
 // What scales a row's weighted sum to its output, and the log of its
 // denominator: here the sink joins.  top and den: the row's reference (in
-// units of log2) and the sum of its weights.
+// units of log2; -infinity where nothing was seen) and the sum of its weights.
 template <class S>
 __device__ __forceinline__ void finish(const Params& P, int kvh, int head, float top, float den,
                                        float& mul, float& lse) {
@@ -893,11 +903,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) attend_kernel(const Params P) 
               if (!(i < 2 ? in0 : in1)) sc[s][n1][i] = -INFINITY;
         }
       }
-      // The weights are taken relative to a reference that follows the maximum
-      // only when that has grown by more than 2^kSlack: the sums stay exact to
-      // a common factor, and nearly every tile saves the rescaling.  fp16
-      // weights reach 2^kSlack at most, far from their end.
-      constexpr float kSlack = 8.f;
+      // weights relative to the reference m, which follows the maximum lazily
       float top[NT][2];
       bool grown = false;
 #pragma unroll
@@ -908,7 +914,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) attend_kernel(const Params P) 
 #pragma unroll
           for (int s = 1; s < kMt; ++s) v = fmaxf(v, fmaxf(sc[s][n1][i], sc[s][n1][i + 2]));
           top[n1][i] = v;
-          grown |= v > m[n1][i] + kSlack;
+          grown |= v > m[n1][i] + (S::kLift + S::kSlack);
         }
       }
       if (__any_sync(0xffffffffu, grown)) {
@@ -917,7 +923,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) attend_kernel(const Params P) 
           float a[2];
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            float v = fmaxf(top[n1][i], m[n1][i]);
+            float v = fmaxf(top[n1][i] - S::kLift, m[n1][i]);
 #pragma unroll
             for (int x = 4; x < 32; x <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, x));
             a[i] = exp2_fast(m[n1][i] - (v == -INFINITY ? 0.f : v));

@@ -101,3 +101,28 @@ def test_attend_weights_keep_their_bits(dim, dtype, qt):
         ref, _, A, d, _ = exact(c, q, r, 0, 1.0)
         tol = (2.0 ** -19 + 2 * d) * A + U[qt] * np.abs(ref)
         assert np.all(np.abs(out[r] - ref) <= tol), r
+
+
+@pytest.mark.parametrize("dim,dtype,qt", [(64, HF, HF), (128, HF, HF), (256, HF, HF), (128, E4, BF),
+                                          (64, E4, HF), (128, BF, BF)])
+@pytest.mark.parametrize("R,kv,n", [(64, 8, 200), (1, 1, 700), (1, 2, 9000), (25, 8, 1500)])
+def test_attend_small_weights_beside_a_dominant_key(dim, dtype, qt, R, kv, n):
+    """One key, the first, takes nearly all the weight and its value is zero;
+    the others weigh 2^-24 to 2^-30 of it each and make the output.  Weights
+    in fp16 keep 2^-35 of the largest: n 2^-35 max |v| is what they may lose."""
+    g = torch.Generator().manual_seed(dim + n)
+    k, v = np.zeros((R, n, kv, dim)), np.zeros((R, n, kv, dim))
+    k[:, 0, :, 0] = 3
+    v[:, 1:] = (2.0 ** 10 * (1 + torch.randint(0, 8, (R, n - 1, kv, dim), generator=g))).numpy()
+    c = given_cache(k, v, dtype, q_heads=4 * kv, scale=64.0 if dtype == E4 else 1.0)
+    q = torch.zeros((R, 4 * kv, dim))
+    q[:, :, 0] = torch.tensor([5.5, 6.0, 6.5, 7.0]).repeat(kv)
+    q = q.to(qt).cuda()
+    out, _ = attended(c, q, 1.0)
+    for r in range(R):
+        for h in range(kv):
+            ref, _, A, d, m = exact(c, q, r, h, 1.0)
+            tol = (2.0 ** -19 + 2 * d) * A + U[qt] * np.abs(ref)
+            if dtype != BF:
+                tol = tol + m * 2.0 ** -35 * 2.0 ** 13
+            assert np.all(np.abs(out[r, 4 * h:4 * h + 4] - ref) <= tol), (r, h)
