@@ -550,7 +550,8 @@ int moe_reader_kv_append(moe_reader_kv_t* kv, const moe_reader_kv_append_args* a
  * A row with nothing to attend to is zeros, its lse the sink or -infinity.
  * Rows outside [max(0, len - window), len) are not read, whatever they hold.
  * Logits, references and sums are fp32; the weights enter the product with V
- * as a value of the cache's type (for E4M3 in fp16) and what its rounding left.
+ * as a value of the cache's type (for E4M3 in fp16) and what that cut off.  A V
+ * of infinity makes its coordinate infinite, unless the key's weight is 0.
  * A length below 0 counts as 0, one beyond the table is cut (ERR_LENGTH); a
  * page that is not in the pool is skipped (ERR_PAGE).  EINVAL where width *
  * page_size >= 2^30 (in plan and select too), or where requests *

@@ -126,3 +126,60 @@ def test_attend_small_weights_beside_a_dominant_key(dim, dtype, qt, R, kv, n):
             if dtype != BF:
                 tol = tol + m * 2.0 ** -35 * 2.0 ** 13
             assert np.all(np.abs(out[r, 4 * h:4 * h + 4] - ref) <= tol), (r, h)
+
+
+# --------------------------------------------------------------------------
+# infinities and NaN in rows that are read
+# --------------------------------------------------------------------------
+DEALT = [([40, 1, 33], 2), ([5000], 1), ([3, 700], 1), ([200] * 64, 8),
+         ([2700 - 40 * i for i in range(20)], 8), ([3000] + [5] * 40, 8)]
+
+
+def infinite_values(c, rows):
+    """An infinity in some coordinates of the last and of a middle key."""
+    for r in rows:
+        n = c.lens[r]
+        for pos, coord, value in ((n - 1, 3, math.inf), (n // 2, 5, -math.inf), (n - 1, 7, math.inf),
+                                  (0, 7, -math.inf), (n // 3, 9, math.inf)):
+            c.v[c.table_np[r, pos // c.page], :, pos % c.page, coord] = value
+
+
+@pytest.mark.parametrize("lens,kv", DEALT)
+@pytest.mark.parametrize("dim,dtype,group", [(64, HF, 4), (128, BF, 16), (128, HF, 12), (256, BF, 3)])
+def test_attend_infinite_values(lens, kv, dim, dtype, group):
+    """A value of infinity makes its coordinate infinite, whatever its key's
+    weight; infinities of both signs make it NaN; the others stay finite."""
+    c = T.Cache(lens, kv, dim, 32, dtype, seed=11, q_heads=group * kv, summaries=False)
+    rows = range(0, len(lens), max(1, len(lens) // 3))
+    infinite_values(c, rows)
+    # in the first request one of them belongs to a key of nearly no weight
+    c.k[c.table_np[0, (lens[0] // 3) // 32], :, (lens[0] // 3) % 32] *= 4
+    q = T.queries(len(lens), group * kv, dim, dtype)
+    out, _ = attended(c, q)
+    for r in rows:
+        for h in range(kv):
+            ref, _, A, d, m = exact(c, q, r, h, dim ** -0.5)
+            got = out[r, h * group:h * group + group]
+            assert np.array_equal(np.isnan(got), np.isnan(ref)), (r, h)
+            assert np.array_equal(np.where(np.isinf(got), got, 0), np.where(np.isinf(ref), ref, 0))
+            fine = np.isfinite(ref)
+            tol = (2.0 ** -16 + 2 * d) * A + U[dtype] * np.abs(np.where(fine, ref, 0)) + \
+                m * 2.0 ** -34 * 8 + 2.0 ** -25
+            assert np.all(np.abs(np.where(fine, got, 0) - np.where(fine, ref, 0)) <= tol), (r, h)
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+def test_attend_infinite_value_of_a_key_without_weight(dtype):
+    """A key whose logit lies 40 below the largest still has a weight: its
+    value of infinity counts.  One whose logit is -infinity has none."""
+    k, v = np.zeros((2, 40, 1, 64)), np.ones((2, 40, 1, 64))
+    k[:, 7, :, 0] = -4
+    v[:, 7, :, 2] = math.inf
+    k[1, 7, :, 0] = -math.inf
+    c = given_cache(k, v, dtype, q_heads=2)
+    q = torch.zeros((2, 2, 64))
+    q[:, :, 0] = 10
+    out, _ = attended(c, q.to(dtype).cuda(), 1.0)
+    want = np.ones((2, 2, 64))
+    want[0, :, 2], want[1, :, 2] = math.inf, math.nan
+    assert np.array_equal(out, want, equal_nan=True)
