@@ -363,7 +363,7 @@ __device__ __forceinline__ void finish(const Params& P, int kvh, int head, float
   } else {
     mul = den == 0.f ? 0.f : vs / den;
   }
-  lse = ref == -INFINITY ? -INFINITY : (ref + log2f(den)) * kLn2;
+  lse = (ref + log2f(den)) * kLn2;          // of a sum of 0: -infinity
 }
 
 // Two neighbouring outputs of a query head.
@@ -1021,6 +1021,13 @@ __global__ void __launch_bounds__(S::kThreads, 1) attend_kernel(const Params P) 
       for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int x = 4; x < 32; x <<= 1) l[n][i] += __shfl_xor_sync(0xffffffffu, l[n][i], x);
+    // The maximum passes over NaN: where all logits are, the reference says
+    // "nothing seen" while the sum is NaN.  Any finite reference carries the sum on.
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        if (l[n][i] != l[n][i]) m[n][i] = fmaxf(m[n][i], 0.f);
     if (own) {
       store_row<S>(P, cc.r, kvh, head0, rows_here, o, m, l);
       p0 = p1;
@@ -1067,7 +1074,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) attend_kernel(const Params P) 
           const int h = n * 8 + 2 * t4 + (i & 1);
           float* at = acc + h * S::kAccPitch + x * 16 + (k8 ? 2 * g + (i >> 1) : g + 8 * (i >> 1));
           const float v = o[x][n][i] * add[i & 1];
-          *at = keep[i & 1] != 0.f ? *at * keep[i & 1] + v : v;
+          *at = place_in_turn ? *at * keep[i & 1] + v : v;
         }
     }
     __syncwarp();

@@ -548,6 +548,7 @@ int moe_reader_kv_append(moe_reader_kv_t* kv, const moe_reader_kv_append_args* a
  *   lse      dev, fp32 [requests][Hq] or NULL: log of the denominator.
  *
  * A row with nothing to attend to is zeros, its lse the sink or -infinity.
+ * A logit of NaN makes the head's row and its lse NaN.
  * Rows outside [max(0, len - window), len) are not read, whatever they hold.
  * Logits, references and sums are fp32; the weights enter the product with V
  * as a value of the cache's type (for E4M3 in fp16) and what that cut off.  A V

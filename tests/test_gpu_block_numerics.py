@@ -183,3 +183,46 @@ def test_attend_infinite_value_of_a_key_without_weight(dtype):
     want = np.ones((2, 2, 64))
     want[0, :, 2], want[1, :, 2] = math.inf, math.nan
     assert np.array_equal(out, want, equal_nan=True)
+
+
+@pytest.mark.parametrize("lens,kv", DEALT + [([513] * 30, 8), ([65] * 160, 2)])
+@pytest.mark.parametrize("dim,dtype,group", [(64, HF, 4), (128, BF, 16), (128, E4, 5), (256, BF, 3)])
+@pytest.mark.parametrize("sinks", [False, True])
+def test_attend_nan_logits(lens, kv, dim, dtype, group, sinks):
+    """A key of NaN makes its KV head's outputs and lse NaN wherever it stands
+    (alone in the last tile, in the first, in the middle); a query of NaN its own head's."""
+    c = T.Cache(lens, kv, dim, 32, dtype, seed=12, q_heads=group * kv, summaries=False)
+    qt = BF if dtype == E4 else dtype
+    q = T.queries(len(lens), group * kv, dim, qt)
+    rows = list(range(0, len(lens), max(1, len(lens) // 5)))
+    bad = np.zeros((len(lens), group * kv), bool)
+    for i, r in enumerate(rows):
+        h, pos = i % kv, (c.lens[r] - 1, 0, c.lens[r] // 2)[i % 3]
+        at = c.table_np[r, pos // 32], h, pos % 32
+        if dtype == E4:
+            c.k.view(torch.uint8)[at] = 0x7f
+        else:
+            c.k[at] = math.nan
+        bad[r, h * group:h * group + group] = True
+        q[r, (i + 1) % kv * group, 4] = math.nan
+        bad[r, (i + 1) % kv * group] = True
+    sk = torch.linspace(-2, 2, group * kv).cuda() if sinks else None
+    out, lse = attended(c, q, sinks=sk)
+    assert np.array_equal(np.isnan(out), np.broadcast_to(bad[:, :, None], out.shape))
+    assert np.array_equal(np.isnan(lse), bad) and np.all(np.isfinite(lse[~bad]))
+
+
+@pytest.mark.parametrize("lens,kv", DEALT)
+def test_attend_nan_values_stay_in_their_coordinate(lens, kv):
+    """NaN in a value: that coordinate only, also where the key's weight is
+    far below those of the other warps and CTAs."""
+    c = T.Cache(lens, kv, 128, 32, BF, seed=13, q_heads=4 * kv, summaries=False)
+    for r in range(len(lens)):
+        pos = lens[r] - 1
+        c.v[c.table_np[r, pos // 32], :, pos % 32, 6] = math.nan
+        c.k[c.table_np[r, 0], :, 0] *= 8
+    q = T.queries(len(lens), 4 * kv, 128, BF)
+    out, lse = attended(c, q)
+    want = np.zeros(out.shape, bool)
+    want[:, :, 6] = True
+    assert np.array_equal(np.isnan(out), want) and np.all(np.isfinite(lse))
