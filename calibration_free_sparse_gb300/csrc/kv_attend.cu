@@ -798,8 +798,8 @@ __global__ void __launch_bounds__(S::kThreads, 1) attend_kernel(const Params P) 
             }
           fac[n][0] = fac[n][1] = base;
         } else {
-          // q as fp16: a power of two brings the head's largest value to [1, 2),
-          // which keeps every bit of it (what underflows is 2^-24 of the largest)
+          // q as fp16: a power of two brings the head's largest value to [2^14,
+          // 2^15), and what lies 2^-28 (fp16) or 2^-31 (bf16) below it keeps every bit
           float top = 0.f;
           float f[D / 16][4];
 #pragma unroll
@@ -811,7 +811,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) attend_kernel(const Params P) 
             }
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-          const int e = floor_log2_held(top);
+          const int e = max((__float_as_int(top) >> 23) - 127 - 14, -126);
           const float down = two_to(-e);
 #pragma unroll
           for (int k = 0; k < D / 16; ++k) {

@@ -226,3 +226,27 @@ def test_attend_nan_values_stay_in_their_coordinate(lens, kv):
     want = np.zeros(out.shape, bool)
     want[:, :, 6] = True
     assert np.array_equal(np.isnan(out), want) and np.all(np.isfinite(lse))
+
+
+@pytest.mark.parametrize("qt", [BF, HF])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_attend_small_queries_beside_a_large_one(dim, qt):
+    """8-bit cache: coordinates 2^-20 to 2^-26 below the query's largest keep
+    all their bits (the largest one meets keys of zero)."""
+    g = torch.Generator().manual_seed(dim)
+    R, G, n = 6, 8, 40
+    k = torch.randint(-14, 15, (R, n, 1, dim), generator=g).double().numpy()
+    v = torch.randint(-14, 15, (R, n, 1, dim), generator=g).double().numpy()
+    k[:, :, :, 0] = 0
+    c = given_cache(k, v, E4, q_heads=G)
+    q = 2.0 ** -20 * torch.randn((R, G, dim), generator=g)
+    q[:, 1::2] *= 2.0 ** (-6 if qt == BF else 4)
+    q[:, :, 0] = 1.7
+    q = q.to(qt).cuda()
+    for scale, heads in ((2.0 ** 14, slice(0, G, 2)), (2.0 ** (20 if qt == BF else 10), slice(1, G, 2))):
+        out, lse = attended(c, q, scale)
+        for r in range(R):
+            ref, want, A, d, _ = exact(c, q, r, 0, scale)
+            tol = (2.0 ** -18 + 2 * d) * A + U[qt] * np.abs(ref)
+            assert np.all(np.abs(out[r] - ref)[heads] <= tol[heads]), r
+            assert np.all(np.abs(lse[r] - want)[heads] <= (2 * d[:, 0] + 2.0 ** -19 * (1 + np.abs(want)))[heads])
