@@ -195,7 +195,10 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const Params P) {
       }
     }
     if (owns && page < p_end) {
-      uint32_t key = id < 0 ? 0u : order_key((float)dot[0] * unit);
+      // NaN (a step that nothing has written) ranks with the pages outside the
+      // pool: its key would be the forced pages' and the list overrun
+      const float score = (float)dot[0] * unit;
+      uint32_t key = id < 0 || score != score ? 0u : order_key(score);
       if (page < a.first || page >= held - a.last) key = kForced;
       keys[page] = key;
     }

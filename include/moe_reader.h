@@ -595,8 +595,9 @@ int moe_reader_kv_attend(moe_reader_kv_t* kv, const moe_reader_kv_attend_args* a
  *   pages    dev, int32 [requests][Hkv][keep]: chosen pages (indices into the
  *            request's table row), ascending, -1 behind the last one.
  * q, table, lens, errors as for moe_reader_kv_attend.  A page that is not in
- * the pool ranks last (ERR_PAGE).  EINVAL on a cache without summaries;
- * width <= 49152.
+ * the pool ranks last (ERR_PAGE), and so does one whose score is NaN (a step
+ * that append never wrote holds what the caller's memory held).  EINVAL on a
+ * cache without summaries; width <= 49152.
  */
 typedef struct {
   const void* q;

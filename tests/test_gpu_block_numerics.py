@@ -250,3 +250,69 @@ def test_attend_small_queries_beside_a_large_one(dim, qt):
             tol = (2.0 ** -18 + 2 * d) * A + U[qt] * np.abs(ref)
             assert np.all(np.abs(out[r] - ref)[heads] <= tol[heads]), r
             assert np.all(np.abs(lse[r] - want)[heads] <= (2 * d[:, 0] + 2.0 ** -19 * (1 + np.abs(want)))[heads])
+
+
+# --------------------------------------------------------------------------
+# page selection
+# --------------------------------------------------------------------------
+def ranked(score, keep, first, last):
+    """Pages in the order of the definition: forced, by score, NaN last, ties to
+    the lower page; the first `keep` of them, ascending."""
+    n = len(score)
+    forced = (np.arange(n) < first) | (np.arange(n) >= n - last)
+    order = np.lexsort((np.arange(n), np.where(np.isnan(score), 0, -score), np.isnan(score), ~forced))
+    best = np.sort(order[:keep])
+    return np.concatenate([best, np.full(keep - len(best), -1)]).astype(np.int32)
+
+
+def query_codes(x):
+    """P and N of a group's queries [G][dim], as the header defines them."""
+    f = np.rint(x * 2.0 ** (14 - math.frexp(np.abs(x).max())[1]))
+    P, N = np.maximum(f, 0).sum(0), np.maximum(-f, 0).sum(0)
+    t = math.frexp(max(P.max(), N.max(), 1.0))[1] - 1
+    return [np.minimum(np.rint(z * 2.0 ** (6 - t)), 127) for z in (P, N)]
+
+
+@pytest.mark.parametrize("lens,page", [([640, 900], 16), ([60000], 16), ([300, 40, 20000], 32)])
+@pytest.mark.parametrize("first,last", [(1, 1), (0, 0)])
+def test_select_steps_that_are_not_finite(lens, page, first, last):
+    """Steps of NaN rank last and infinite ones as their scores say (zero times
+    infinity is NaN), in the first, a middle and the last head: the list holds
+    `keep` pages and nothing is written behind it."""
+    kv, G, keep = 3, 2, 6
+    c = T.Cache(lens, kv, 64, page, BF, seed=21, q_heads=G * kv)
+    c.summarise()
+    g = torch.Generator().manual_seed(5)
+    for h in range(kv):
+        at = torch.randperm(c.steps.shape[0], generator=g)[:c.steps.shape[0] // 2].cuda()
+        c.steps[at[0::4], h] = math.nan
+        c.steps[at[1::4], h] = math.inf
+        c.steps[at[2::4], h] = -math.nan
+        c.steps[at[3::4], h] = math.inf
+        c.codes[at[3::4], h] = 0
+    q = T.queries(len(lens), G * kv, 64, BF, seed=6)
+    room = torch.full((len(lens) * kv * keep + 400,), -77, dtype=torch.int32, device="cuda")
+    pages = room[200:-200].view(len(lens), kv, keep)
+    c.cache.select(q, c.table, c.lens_t, pages, first=first, last=last)
+    assert c.cache.status() == (0, 0)
+    codes, steps = T.f64(c.codes.float()), T.f64(c.steps)
+    for r, n in enumerate(lens):
+        for h in range(kv):
+            P, N = query_codes(T.f64(q[r, G * h:G * h + G]))
+            at = c.table_np[r, :-(-n // page)]
+            with np.errstate(invalid="ignore"):
+                score = (codes[at, h, 0] @ P - codes[at, h, 1] @ N) * steps[at, h]
+            want = ranked(score, keep, min(first, len(at)), min(last, len(at)))
+            assert np.array_equal(pages[r, h].cpu().numpy(), want), (r, h)
+    assert bool((room[:200] == -77).all()) and bool((room[-200:] == -77).all())
+
+
+def test_select_every_step_unwritten():
+    """No score at all: the forced pages and the lowest others."""
+    c = T.Cache([640], 2, 64, 16, BF, seed=22, q_heads=2)
+    c.steps.fill_(math.nan)
+    room = torch.full((2 * 5 + 100,), -77, dtype=torch.int32, device="cuda")
+    pages = room[50:-50].view(1, 2, 5)
+    c.cache.select(T.queries(1, 2, 64, BF), c.table, c.lens_t, pages)
+    assert pages.tolist() == [[[0, 1, 2, 3, 39]] * 2]
+    assert bool((room[:50] == -77).all()) and bool((room[-50:] == -77).all())
