@@ -700,9 +700,10 @@ int moe_reader_kv_attend(moe_reader_kv_t* kv, const moe_reader_kv_attend_args* a
   if (!type_fits(kv->cfg.cache_type, a->q_type)) return MOE_READER_EINVAL;
   if (a->width < 1 || a->window < 0 || (a->pages && a->keep < 1)) return MOE_READER_EINVAL;
   if ((long long)a->width << kv->page_shift >= (1LL << 30)) return MOE_READER_EINVAL;
-  // the work list is indexed with 32 bits
+  // a row's keys and the work list are indexed with 32 bits
   const long long pages = a->pages ? a->keep : a->width;
   const long long items = (long long)a->requests * kv->cfg.num_kv_heads;
+  if (pages << kv->page_shift >= (1LL << 30)) return MOE_READER_EINVAL;
   if (items * (pages << kv->page_shift) >= (1LL << 34)) return MOE_READER_EINVAL;
   if (a->requests == 0) return MOE_READER_OK;
   if (!a->q || !a->table || !a->lens || !a->out) return MOE_READER_EINVAL;

@@ -555,8 +555,8 @@ int moe_reader_kv_append(moe_reader_kv_t* kv, const moe_reader_kv_append_args* a
  * of infinity makes its coordinate infinite, unless the key's weight is 0.
  * A length below 0 counts as 0, one beyond the table is cut (ERR_LENGTH); a
  * page that is not in the pool is skipped (ERR_PAGE).  EINVAL where width *
- * page_size >= 2^30 (in plan and select too), or where requests *
- * Hkv * width (keep with pages) * page_size >= 2^34.
+ * page_size >= 2^30 (in plan and select too), or keep * page_size with pages,
+ * or where requests * Hkv * width (keep with pages) * page_size >= 2^34.
  */
 typedef struct {
   const void* q;

@@ -316,3 +316,18 @@ def test_select_every_step_unwritten():
     c.cache.select(T.queries(1, 2, 64, BF), c.table, c.lens_t, pages)
     assert pages.tolist() == [[[0, 1, 2, 3, 39]] * 2]
     assert bool((room[:50] == -77).all()) and bool((room[-50:] == -77).all())
+
+
+# --------------------------------------------------------------------------
+# refusals
+# --------------------------------------------------------------------------
+@pytest.mark.parametrize("keep", [1 << 22, 1 << 23, (1 << 24) + 1])
+def test_attend_refuses_a_list_beyond_32_bits(keep):
+    """keep * page_size from 2^30 on: the row's keys are counted in 32 bits."""
+    c = T.Cache([300], 1, 64, 256, BF, q_heads=2, summaries=False)
+    q = T.queries(1, 2, 64, BF)
+    out = torch.full_like(q, 7.0)
+    pages = torch.full((1, 1, keep), -1, dtype=torch.int32, device="cuda")
+    with pytest.raises(rd.ReaderError) as e:
+        c.cache.attend(q, c.table, c.lens_t, out, pages=pages)
+    assert e.value.code == rd.EINVAL and bool((out == 7).all())
