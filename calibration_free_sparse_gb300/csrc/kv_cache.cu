@@ -578,6 +578,17 @@ bool type_fits(int cache, int type) {
   return type == cache;
 }
 
+// An array of 32-bit words.
+struct Words {
+  const int32_t* at;
+  long long count;
+};
+bool share_a_word(const Words& a, const Words& b) {
+  if (a.count == 0 || b.count == 0) return false;
+  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a.at), b0 = reinterpret_cast<uintptr_t>(b.at);
+  return a0 < b0 + 4 * b.count && b0 < a0 + 4 * a.count;
+}
+
 // Launches go to the calling thread's device: it has to be the handle's.
 bool on_device(const moe_reader_kv* kv) {
   int dev = -1;
@@ -671,12 +682,17 @@ int moe_reader_kv_plan(moe_reader_kv_t* kv, const moe_reader_kv_plan_args* a, vo
                          a->slots, a->positions, a->token_requests, a->taken};
   for (const void* p : words)
     if (!at_multiple(p, 4)) return MOE_READER_EINVAL;
-  // other CTAs still read the lengths while the first one writes its outputs
-  const void* outs[] = {a->lens, a->starts, a->slots, a->positions, a->token_requests, a->taken,
-                        a->table};
-  for (const void* o : outs)
-    if (o && (o == a->prev_lens || o == a->new_lens || o == a->free_pages))
-      return MOE_READER_EINVAL;
+  // CTAs still read the inputs while others write the outputs
+  const long long R = a->requests, T = a->max_tokens;
+  const Words ins[] = {{a->prev_lens, R}, {a->new_lens, R}, {a->free_pages, a->num_free}};
+  const Words outs[] = {{a->table, R * a->width}, {a->lens, R}, {a->starts, R + 1}, {a->slots, T},
+                        {a->positions, T}, {a->token_requests, T}, {a->taken, 1}};
+  for (const Words& o : outs) {
+    for (const Words& i : ins)
+      if (share_a_word(o, i)) return MOE_READER_EINVAL;
+    for (const Words* p = outs; p != &o; ++p)
+      if (share_a_word(o, *p)) return MOE_READER_EINVAL;
+  }
   if (!on_device(kv)) return MOE_READER_EINVAL;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   return done(kv, mr::launch_kv_plan(*kv, *a, s), s);

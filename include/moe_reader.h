@@ -467,12 +467,14 @@ int moe_reader_kv_create(const moe_reader_kv_config* cfg, void* k, void* v, int8
  *   prev_lens, new_lens  dev, int32 [requests], >= 0.
  *   table       dev, int32 [requests][width]: updated in place.
  *   free_pages  dev, int32 [num_free].
- *   lens        dev, int32 [requests]: prev + new (may not alias prev_lens).
+ *   lens        dev, int32 [requests]: prev + new.
  *   starts      dev, int32 [requests + 1]: a request's first new token.
  *   slots, positions, token_requests  dev, int32 [max_tokens]: each new
  *               token's slot, position and request, in request order; -1
  *               behind the last one.
  *   taken       dev, int32 [1]: free pages used, from the front.
+ * No output (the table among them) may overlap an input or another output
+ * (EINVAL).
  *
  * Device-side errors (moe_reader_kv_status): a negative length counts as 0;
  * a request that outgrows `width` pages is cut there; tokens beyond

@@ -331,3 +331,44 @@ def test_attend_refuses_a_list_beyond_32_bits(keep):
     with pytest.raises(rd.ReaderError) as e:
         c.cache.attend(q, c.table, c.lens_t, out, pages=pages)
     assert e.value.code == rd.EINVAL and bool((out == 7).all())
+
+
+def test_plan_refuses_arrays_that_overlap():
+    """An input that is part of an output (not only one that begins with it),
+    and outputs that share words; neighbours that only touch are taken."""
+    kv = torch.zeros((8, 1, 16, 64), dtype=BF, device="cuda")
+    cache = block.PagedCache(kv, kv.clone(), 1, max_requests=4)
+    i32 = T.to_i32
+    table = i32(np.full((4, 3), -1))
+    plan = cache.plan(table, 8)
+    two, free = i32([1, 1]), i32(np.arange(8))
+    flat = table.view(-1)
+    for prev, new, pool in [(plan._lens[1:3], two, free), (plan._starts[1:3], two, free),
+                            (plan._starts[2:4], two, free), (two, plan._lens[1:3], free),
+                            (two, plan.slots[3:5], free), (plan.positions[6:], two, free),
+                            (two, two, plan.requests[2:5]), (two, two, flat[5:7]),
+                            (flat[1:3], two, free), (two, two, plan.taken)]:
+        before = [t.clone() for t in (table, plan._lens, plan._starts, plan.slots)]
+        with pytest.raises(rd.ReaderError) as e:
+            plan.update(prev, new, pool)
+        assert e.value.code == rd.EINVAL
+        for a, b in zip(before, (table, plan._lens, plan._starts, plan.slots)):
+            assert torch.equal(a, b)
+    shared = torch.zeros(40, dtype=torch.int32, device="cuda")
+    call = block._rd._lib().moe_reader_kv_plan
+    base = shared.data_ptr()
+    for at in ([0, 2, 5, 13, 20, 28], [0, 1, 5, 13, 21, 29], [0, 2, 5, 13, 21, 28], [6, 0, 3, 11, 19, 27]):
+        out = [base + 4 * i for i in at]       # lens 2, starts 3, slots, positions, requests 8 each, taken 1
+        args = block._PLAN.pack(two.data_ptr(), two.data_ptr(), table.data_ptr(), free.data_ptr(),
+                                *out, 2, 3, 8, 8)
+        assert call(cache._h, args, None) == rd.EINVAL
+    # lens behind the lengths that it is made of, everything else side by side
+    lens = i32([3, 4, 0, 0])
+    out = [lens.data_ptr() + 8] + [base + 4 * i for i in (2, 5, 13, 21, 29)]
+    args = block._PLAN.pack(lens.data_ptr(), two.data_ptr(), table.data_ptr(), free.data_ptr(), *out,
+                            2, 3, 8, 8)
+    torch.cuda.synchronize()
+    assert call(cache._h, args, torch.cuda.current_stream().cuda_stream) == rd.OK
+    torch.cuda.synchronize()
+    assert lens.tolist() == [3, 4, 4, 5] and shared.tolist()[2:5] == [0, 1, 2]
+    cache.status()
