@@ -261,6 +261,162 @@ __device__ __forceinline__ void pairs_of(uint4 v, typename Pair<CT>::type (&p)[4
   }
 }
 
+// A summary's step is 2^step_exponent(the largest magnitude).
+__device__ __forceinline__ int step_exponent(float top) {
+  top = fminf(fmaxf(top, two_to(-100)), two_to(100));
+  const int e = floor_log2_held(top) - 6;
+  return top > 127.f * two_to(e) ? e + 1 : e;
+}
+// Codes of the largest and the smallest key; inv: 1 / step.  A power-of-two
+// step: the quotients are exact, but for those that underflow, which still round
+// away from zero.
+__device__ __forceinline__ int code_up(float v, float inv) {
+  const float c = fminf(fmaxf(ceilf(v * inv), -127.f), 127.f);
+  return (int)(v > 0.f ? fmaxf(c, 1.f) : c);
+}
+__device__ __forceinline__ int code_down(float v, float inv) {
+  const float c = fminf(fmaxf(floorf(v * inv), -127.f), 127.f);
+  return (int)(v < 0.f ? fminf(c, -1.f) : c);
+}
+
+// One new value as the cache stores it, and a stored value widened.
+template <int CT, int IT>
+__device__ __forceinline__ typename Cell<CT>::type stored1(uint16_t in, const Divider& by) {
+  if constexpr (CT == MOE_READER_TYPE_E4M3) {
+    const float f = IT == MOE_READER_TYPE_BF16 ? __uint_as_float((uint32_t)in << 16)
+                                               : __half2float(__ushort_as_half(in));
+    return __nv_cvt_float_to_fp8(by(f), __NV_SATFINITE, __NV_E4M3);
+  } else {
+    return in;
+  }
+}
+template <int CT>
+__device__ __forceinline__ float widen1(typename Cell<CT>::type v) {
+  if constexpr (CT == MOE_READER_TYPE_E4M3)
+    return __half2float(__half(__nv_cvt_fp8_to_halfraw(v, __NV_E4M3)));
+  else if constexpr (CT == MOE_READER_TYPE_BF16)
+    return __uint_as_float((uint32_t)v << 16);
+  else
+    return __half2float(__ushort_as_half(v));
+}
+
+// A window of keys.
+struct Window {
+  int slots[256 + kKeyWindow + 1];     // of its tokens, a page of them before and one behind
+  unsigned long long ends;             // tokens that end a run
+  unsigned long long followed, follows;   // those with another run of their page behind, before
+  uint16_t back[256];                  // a row's token, counted back from the run's last; 0: none
+  float top[kAppendThreads / 32];
+};
+
+// The keys of a window near which tokens are skipped: false, and nothing done,
+// unless that cuts the new tokens of a page into several runs.  Then each run
+// copies its rows, and the last one of a page sums the page up: other CTAs write
+// the others' rows meanwhile, so it takes them from the input, too.  A thread per
+// coordinate, and a function apart with its state in shared memory: this is
+// rare, and registers of its own would cost the kernel occupancy.
+template <int D, int CT, int IT>
+__device__ __noinline__ bool append_cut_runs(Window& c, const moe_reader_kv_append_args& a,
+                                             typename Cell<CT>::type* kc, int8_t* codes,
+                                             float* steps, const float* k_scale, int heads, int shift,
+                                             int pool, int first) {
+  const int lane = threadIdx.x & 31, ps = 1 << shift;
+  auto live = [&](int slot) { return (unsigned)slot < (unsigned)pool; };
+  auto same_page = [&](int x, int y) { return (x ^ y) < ps; };
+  __syncthreads();
+  // runs with another of their page behind them, or before them
+#pragma unroll 1
+  for (int w = threadIdx.x >> 5; w < kKeyWindow; w += kAppendThreads / 32) {
+    if (!(c.ends >> w & 1)) continue;
+    const int slot = c.slots[ps + w];
+#pragma unroll 1
+    for (int b = 1; b <= ps; b += 32) {
+      const int t = first + w + b + lane;
+      const int at = b + lane <= ps && t < a.tokens ? __ldg(a.slots + t) : -1;
+      const uint32_t any = __ballot_sync(0xffffffffu, live(at));
+      if (!any) continue;
+      if (lane == __ffs(any) - 1 && at > slot && same_page(at, slot))
+        atomicOr(&c.followed, 1ull << w);
+      break;
+    }
+    bool ended = false;
+#pragma unroll 1
+    for (int b = 1; b <= ps; b += 32) {
+      const int back = min(b + lane, ps), at = c.slots[ps + w - back];
+      const uint32_t out = __ballot_sync(0xffffffffu, ended || at != slot - back);
+      const bool other = live(at) && !same_page(at, slot);
+      if (out && live(at) && !other && at < slot && lane >= __ffs(out) - 1)
+        atomicOr(&c.follows, 1ull << w);
+      if (__any_sync(0xffffffffu, other)) break;
+      ended |= out != 0;
+    }
+  }
+  __syncthreads();
+  if (!(c.followed | c.follows)) return false;
+
+  const int head = blockIdx.y;
+#pragma unroll 1
+  for (int w = 0; w < kKeyWindow; ++w) {
+    if (!(c.ends >> w & 1)) continue;
+    const int slot = c.slots[ps + w], off = slot & (ps - 1);
+    const size_t summary = (size_t)(slot >> shift) * heads + head;
+    const bool sums = !(c.followed >> w & 1);
+    __syncthreads();
+    for (int o = threadIdx.x; o < ps; o += kAppendThreads) c.back[o] = 0;
+    __syncthreads();
+    for (int back = 1 + threadIdx.x; back <= ps; back += kAppendThreads) {
+      const int at = c.slots[ps + w - back];
+      if (live(at) && at < slot && same_page(at, slot)) c.back[at & (ps - 1)] = (uint16_t)back;
+    }
+    __syncthreads();
+    constexpr int kPer = (D + kAppendThreads - 1) / kAppendThreads;
+    float hi[kPer], lo[kPer], top = 0.f;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int d = threadIdx.x + i * kAppendThreads;
+      hi[i] = -INFINITY;
+      lo[i] = INFINITY;
+      bool run = true;                                 // the rows of this run
+#pragma unroll 1
+      for (int o = off; o >= 0 && d < D; --o) {
+        const int back = o == off ? 0 : c.back[o];
+        run &= back == off - o;
+        if (!run && !sums) break;
+        auto* at = kc + ((summary << shift) + o) * D + d;
+        typename Cell<CT>::type v;
+        if (o == off || back) {
+          const Divider by(CT == MOE_READER_TYPE_E4M3 ? k_scale[head] : 1.f);
+          v = stored1<CT, IT>(__ldg(static_cast<const uint16_t*>(a.k) + head * a.k_head_stride +
+                                    (first + w - back) * a.k_token_stride + d), by);
+          if (run) *at = v;
+        } else {
+          v = *at;
+        }
+        hi[i] = fmaxf(hi[i], widen1<CT>(v));
+        lo[i] = fminf(lo[i], widen1<CT>(v));
+      }
+      if (d < D) top = fmaxf(top, fmaxf(fabsf(hi[i]), fabsf(lo[i])));
+    }
+    if (!sums) continue;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if (lane == 0) c.top[threadIdx.x >> 5] = top;
+    __syncthreads();
+#pragma unroll
+    for (int v = 0; v < kAppendThreads / 32; ++v) top = fmaxf(top, c.top[v]);
+    const int e = step_exponent(top);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int d = threadIdx.x + i * kAppendThreads;
+      if (d >= D) continue;
+      codes[summary * 2 * D + d] = (int8_t)code_up(hi[i], two_to(-e));
+      codes[summary * 2 * D + D + d] = (int8_t)code_down(lo[i], two_to(-e));
+    }
+    if (threadIdx.x == 0) steps[summary] = two_to(e);
+  }
+  return true;
+}
+
 // The first `key_ctas` CTAs of a KV head look at `key_window` (at most 64)
 // consecutive tokens each for their keys, the others at `value_window` each for
 // their values: a prompt's pages are twice as many independent chains of loads.
@@ -269,8 +425,9 @@ __device__ __forceinline__ void pairs_of(uint4 v, typename Pair<CT>::type (&p)[4
 // there (their slots are consecutive).  It copies the run's rows and, over the
 // page's rows up to that token -- the older ones read from the cache, the new
 // ones from the input -- forms the largest and smallest key per coordinate, so
-// the summary needs no second pass and no other CTA's writes.  D / 8 lanes share
-// a row, 8 values each; a thread has kAhead rows in flight.
+// the summary needs no second pass and no other CTA's writes (append_cut_runs
+// sees to pages whose new tokens have skipped ones between them).  D / 8 lanes
+// share a row, 8 values each; a thread has kAhead rows in flight.
 //
 // Measured: 2.5 us for one token of 16 requests (4 KV heads of 128, pages of
 // 16); 12.4 us for 10 thousand tokens into an e4m3 cache (31 MB, 2.5 TB/s: the
@@ -281,7 +438,7 @@ __device__ __forceinline__ void pairs_of(uint4 v, typename Pair<CT>::type (&p)[4
 // after the other 15.0, windows of 32 keys 12.9 and of 16 values 13.6.
 template <int D, int CT, int IT>
 __global__ void __launch_bounds__(kAppendThreads)
-append_kernel(moe_reader_kv_append_args a, typename Cell<CT>::type* __restrict__ kc,
+append_kernel(const __grid_constant__ moe_reader_kv_append_args a, typename Cell<CT>::type* __restrict__ kc,
               typename Cell<CT>::type* __restrict__ vc, int8_t* __restrict__ codes,
               float* __restrict__ steps, const float* __restrict__ k_scale,
               const float* __restrict__ v_scale, int heads, int shift, int num_pages,
@@ -294,7 +451,10 @@ append_kernel(moe_reader_kv_append_args a, typename Cell<CT>::type* __restrict__
   constexpr int kAhead = 4;
   __shared__ uint32_t s_hi[kWarps][D / 2], s_lo[kWarps][D / 2];
   __shared__ float s_max[kWarps];
-  __shared__ int s_slot[256 + kKeyWindow + 1];
+  __shared__ Window s_window;
+  __shared__ __align__(4) bool s_skips[kWarps];
+  static_assert(kWarps == 4, "read as one word");
+  int* s_slot = s_window.slots;
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
   const int head = blockIdx.y, ps = 1 << shift;
   const int col = (tid % kLanes) * 8, row0 = tid / kLanes;
@@ -330,11 +490,19 @@ append_kernel(moe_reader_kv_append_args a, typename Cell<CT>::type* __restrict__
 
   // the window's slots, a page before them and one behind, in one round of loads
   const long long first = (long long)blockIdx.x * key_window;
+  int out = 0;
   for (int i = tid; i <= ps + key_window; i += kAppendThreads) {
     const long long t = first - ps + i;
-    s_slot[i] = t >= 0 && t < a.tokens ? __ldg(a.slots + t) : -1;
+    const bool in = t >= 0 && t < a.tokens;
+    const int slot = in ? __ldg(a.slots + t) : -1;
+    s_slot[i] = slot;
+    out |= in ? slot | (int)(slots_all - 1 - slot) : 0;
   }
+  // a sign: a skipped token among them (a barrier that reduces costs prompts 5 %)
+  const bool some = __any_sync(0xffffffffu, out < 0);
+  if (lane == 0) s_skips[wid] = some;
   __syncthreads();
+  const bool skips = *reinterpret_cast<const uint32_t*>(s_skips) != 0;
   // the tokens of the window that close their page's run (the same in every warp)
   unsigned long long todo = 0;
 #pragma unroll
@@ -351,6 +519,12 @@ append_kernel(moe_reader_kv_append_args a, typename Cell<CT>::type* __restrict__
     todo |= (unsigned long long)__ballot_sync(0xffffffffu, closes) << half;
   }
   if (!todo) return;
+  if (skips && codes) {
+    if (tid == 0) s_window.ends = todo, s_window.followed = s_window.follows = 0;
+    if (append_cut_runs<D, CT, IT>(s_window, a, kc, codes, steps, k_scale, heads, shift,
+                                   (int)slots_all, (int)first))
+      return;
+  }
 
   const Divider kd(CT == MOE_READER_TYPE_E4M3 ? k_scale[head] : 1.f);
   const uint16_t* kin = static_cast<const uint16_t*>(a.k) + head * a.k_head_stride + col;
@@ -446,25 +620,13 @@ append_kernel(moe_reader_kv_append_args a, typename Cell<CT>::type* __restrict__
     __syncthreads();
 #pragma unroll
     for (int v = 0; v < kWarps; ++v) top = fmaxf(top, s_max[v]);
-    top = fminf(fmaxf(top, two_to(-100)), two_to(100));
-    int e = floor_log2_held(top) - 6;
-    if (top > 127.f * two_to(e)) ++e;
+    const int e = step_exponent(top);
     const float inv = two_to(-e);
     const size_t at = (size_t)(slot >> shift) * heads + head;
     if (tid < D / 2) {
-      // a power-of-two step: the quotients are exact, but for those that
-      // underflow, which still round away from zero
-      auto up = [&](float v) {
-        const float c = fminf(fmaxf(ceilf(v * inv), -127.f), 127.f);
-        return (int)(v > 0.f ? fmaxf(c, 1.f) : c);
-      };
-      auto down = [&](float v) {
-        const float c = fminf(fmaxf(floorf(v * inv), -127.f), 127.f);
-        return (int)(v < 0.f ? fminf(c, -1.f) : c);
-      };
       char2* out = reinterpret_cast<char2*>(codes + at * 2 * D);
-      out[tid] = make_char2((char)up(h.x), (char)up(h.y));
-      out[D / 2 + tid] = make_char2((char)down(l.x), (char)down(l.y));
+      out[tid] = make_char2((char)code_up(h.x, inv), (char)code_up(h.y, inv));
+      out[D / 2 + tid] = make_char2((char)code_down(l.x, inv), (char)code_down(l.y, inv));
     }
     if (tid == 0) steps[at] = two_to(e);
     __syncthreads();   // s_hi, s_lo and s_max are free again

@@ -510,6 +510,9 @@ int moe_reader_kv_plan(moe_reader_kv_t* kv, const moe_reader_kv_plan_args* a, vo
  *   slots     dev, int32 [tokens]; -1 skips the token, a slot outside the
  *             pool too (ERR_PAGE).  A request's tokens are consecutive and
  *             ascending, as moe_reader_kv_plan writes them; no slot twice.
+ *             Skipped tokens may stand anywhere, also between tokens of a page
+ *             (whose rows need not follow one another then), but those of one
+ *             page lie within page_size places of the list.
  *
  * E4M3 stores rn(clamp(x / scale, -448, 448)), NaN stays NaN.  The summary of
  * a page and head covers its rows up to the newest written: per coordinate

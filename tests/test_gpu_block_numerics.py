@@ -372,3 +372,79 @@ def test_plan_refuses_arrays_that_overlap():
     torch.cuda.synchronize()
     assert lens.tolist() == [3, 4, 4, 5] and shared.tolist()[2:5] == [0, 1, 2]
     cache.status()
+
+
+# --------------------------------------------------------------------------
+# append
+# --------------------------------------------------------------------------
+def written(c, positions, seed, rows=BF, skip=0.3, other=None):
+    """Appends rows at `positions` (a list per request, ascending) with skipped
+    tokens strewn between, or (skip 0) in the place of each position left out,
+    and slots outside the pool, if `other` is given; checks every row and every
+    touched page's summary."""
+    rng = np.random.default_rng(seed)
+    kv, page, dim = c.k.shape[1:]
+    slots = []
+    for r, pos in enumerate(positions):
+        for i, p in enumerate(pos):
+            slots += [-1] * (int(rng.geometric(1 - skip) - 1) if skip else p - pos[max(i - 1, 0)] - 1)
+            if other is not None and rng.random() < 0.1:
+                slots.append(other)
+            slots.append(int(c.table_np[r, p // page]) * page + p % page)
+        slots += [-1] * int(rng.integers(0, 3))
+    slots = np.array(slots)
+    for page_id in np.unique(slots[slots >= 0] // page):       # the contract
+        at = np.flatnonzero((slots // page == page_id) & (slots >= 0))
+        assert at[-1] - at[0] <= page or page_id * page >= c.k.shape[0] * page
+    x = torch.from_numpy(3 * rng.standard_normal((2, len(slots), kv, dim))).to(rows).cuda()
+    want = [c.k.float(), c.v.float()]
+    c.cache.append(x[0], x[1], T.to_i32(slots))
+    status = c.cache.status()
+    live = (slots >= 0) & (slots < c.k.shape[0] * page)
+    assert status == ((0, 0) if (live | (slots == -1)).all() else (rd.EDEVICE, block.ERR_PAGE))
+    at = torch.from_numpy(slots[live]).cuda()
+    for w, got, y, s in zip(want, (c.k, c.v), x, c.scales):
+        y = y.float() if s is None else (y.float() / s[:, None]).clamp(-448, 448)
+        w[at // page, :, at % page] = y[torch.from_numpy(live).cuda()].to(c.k.dtype).float()
+        assert torch.equal(torch.nan_to_num(got.float(), nan=7e4), torch.nan_to_num(w, nan=7e4))
+    if c.codes is None:
+        return
+    keys, codes, steps = T.f64(c.k.float()), c.codes.cpu().numpy(), T.f64(c.steps)
+    for page_id in np.unique(slots[live] // page):
+        top = (slots[live] % page)[slots[live] // page == page_id].max()
+        for h in range(kv):
+            hi, lo, step = T.ref_summary(keys[page_id, h, :top + 1])
+            assert steps[page_id, h] == step, (page_id, h)
+            assert np.array_equal(codes[page_id, h], np.stack([hi, lo])), (page_id, h)
+
+
+@pytest.mark.parametrize("dim,dtype,rows,page", [(64, BF, BF, 16), (128, E4, BF, 16), (256, HF, HF, 32),
+                                                 (64, E4, HF, 64), (128, BF, BF, 256)])
+@pytest.mark.parametrize("other", [False, True])
+@pytest.mark.parametrize("summaries", [True, False])
+def test_append_skipped_tokens_inside_a_run(dim, dtype, rows, page, other, summaries):
+    """Skipped tokens between tokens of one page, rows that are left out, runs
+    across page ends: the summary of a page covers all its new rows."""
+    lens = [3 * page] * 5
+    half = page // 2
+    positions = [[0, 1, 2], [half - 1, half, half + 2, half + 5], list(range(page - 3, page + half - 2)),
+                 [page + 1, page + 4, 2 * page - 1, 2 * page, 2 * page + 1], [7]]
+    c = T.Cache(lens, 3, dim, page, dtype, seed=31, q_heads=3, summaries=summaries)
+    outside = c.k.shape[0] * page + 5 if other else None
+    for seed in range(6):
+        written(c, positions, seed, rows, skip=0.25, other=outside)
+
+
+@pytest.mark.parametrize("dtype,page", [(BF, 16), (E4, 64), (BF, 128)])
+def test_append_skipped_tokens_in_long_lists(dtype, page):
+    """The same where a CTA looks at many tokens: prompts with a few gaps."""
+    n = 700
+    c = T.Cache([n] * 6, 8, 64, page, dtype, seed=32, q_heads=8, max_requests=6)
+    rng = np.random.default_rng(9)
+    for seed in range(3):
+        positions = []
+        for r in range(6):
+            keep = np.ones(n, bool)
+            keep[rng.integers(0, n, 25)] = False
+            positions.append(list(np.flatnonzero(keep)))
+        written(c, positions, seed, skip=0)
