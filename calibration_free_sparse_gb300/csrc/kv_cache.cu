@@ -395,6 +395,7 @@ __device__ __noinline__ bool append_cut_runs(Window& c, const moe_reader_kv_appe
         hi[i] = fmaxf(hi[i], widen1<CT>(v));
         lo[i] = fminf(lo[i], widen1<CT>(v));
       }
+      if (hi[i] < lo[i]) hi[i] = lo[i] = 0.f;          // all NaN
       if (d < D) top = fmaxf(top, fmaxf(fabsf(hi[i]), fabsf(lo[i])));
     }
     if (!sums) continue;
@@ -609,9 +610,9 @@ append_kernel(const __grid_constant__ moe_reader_kv_append_args a, typename Cell
       }
       h = widen2(hp);
       l = widen2(lp);
-      // a coordinate whose keys are all NaN: the empty range
-      if (h.x != h.x) h.x = -INFINITY, l.x = INFINITY;
-      if (h.y != h.y) h.y = -INFINITY, l.y = INFINITY;
+      // a coordinate whose keys are all NaN says nothing, to the step neither
+      if (h.x != h.x) h.x = l.x = 0.f;
+      if (h.y != h.y) h.y = l.y = 0.f;
       top = fmaxf(fmaxf(fabsf(h.x), fabsf(l.x)), fmaxf(fabsf(h.y), fabsf(l.y)));
     }
 #pragma unroll

@@ -516,10 +516,11 @@ int moe_reader_kv_plan(moe_reader_kv_t* kv, const moe_reader_kv_plan_args* a, vo
  *
  * E4M3 stores rn(clamp(x / scale, -448, 448)), NaN stays NaN.  The summary of
  * a page and head covers its rows up to the newest written: per coordinate
- * the largest and the smallest key (a NaN key is passed over), as codes
- * ceil(hi / step) and floor(lo / step) clamped to +-127, where a = max(|hi|,
- * |lo|) over the coordinates (clamped to 2^-100 .. 2^100) and step =
- * 2^(floor(log2 a) - 6), doubled if a > 127 step.
+ * the largest and the smallest key (a NaN key is passed over; 0 and 0 where
+ * all are), as codes ceil(hi / step) and floor(lo / step) clamped to +-127,
+ * where a = max(|hi|, |lo|) over the coordinates (clamped to 2^-100 .. 2^100)
+ * and step = 2^(floor(log2 a) - 6), doubled if a > 127 step.  A key of infinity
+ * so makes the step 2^94, and the page's score a bound that says little.
  */
 typedef struct {
   const void* k;

@@ -448,3 +448,42 @@ def test_append_skipped_tokens_in_long_lists(dtype, page):
             keep[rng.integers(0, n, 25)] = False
             positions.append(list(np.flatnonzero(keep)))
         written(c, positions, seed, skip=0)
+
+
+def summary_of(rows):
+    """Codes and step of keys [rows][dim] by the header's definition."""
+    number = ~np.isnan(rows)
+    seen = number.any(0)
+    hi = np.where(seen, np.where(number, rows, -np.inf).max(0), 0)
+    lo = np.where(seen, np.where(number, rows, np.inf).min(0), 0)
+    a = min(max(np.abs(hi).max(), np.abs(lo).max(), 2.0 ** -100), 2.0 ** 100)
+    step = 2.0 ** (math.frexp(a)[1] - 7)
+    step = 2 * step if a > 127 * step else step
+    return np.clip(np.ceil(hi / step), -127, 127), np.clip(np.floor(lo / step), -127, 127), step
+
+
+@pytest.mark.parametrize("dtype", [BF, HF, E4])
+@pytest.mark.parametrize("gap", [False, True])
+def test_append_coordinates_that_are_nan_throughout(dtype, gap):
+    """Such a coordinate is passed over: the others keep their step and codes."""
+    c = T.Cache([3 * 16] * 3, 2, 64, 16, dtype, seed=33, q_heads=2)
+    rows = HF if dtype == HF else BF
+    g = torch.Generator().manual_seed(1)
+    k = torch.randn((16, 2, 64), generator=g)
+    k[:, 0, 5] = k[:, 1, 63] = math.nan
+    k[3:9, 0, 7] = math.nan
+    k[:, 1, 0:62] = math.nan
+    k = k.to(rows).cuda()
+    for r, every in enumerate((k, torch.full_like(k, math.nan))):
+        slots = c.table_np[r, 1] * 16 + np.arange(16)
+        if gap:                        # two runs, the second from the ninth row on
+            slots = np.insert(slots, 8, -1)
+            every = torch.cat([every[:8], every[:1], every[8:]])
+        c.cache.append(every, every, T.to_i32(slots))
+        keys = T.f64(c.k[int(c.table_np[r, 1])].float())
+        for h in range(2):
+            hi, lo, step = summary_of(keys[h])
+            assert float(c.steps[c.table_np[r, 1], h]) == step
+            assert np.array_equal(c.codes[c.table_np[r, 1], h].cpu().numpy(), np.stack([hi, lo]))
+    # no stored value is above 448: no step above 4
+    assert float(c.steps[c.table_np[0, 1], 0]) <= 4 and c.cache.status() == (0, 0)
