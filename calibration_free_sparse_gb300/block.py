@@ -203,7 +203,7 @@ class PagedCache:
             pass
 
     def status(self):
-        """(code, error bits) since the last status; synchronizes the stream."""
+        """(code, error bits) since the last status; synchronizes the device."""
         bits = ctypes.c_uint32(0)
         code = _rd._lib().moe_reader_kv_status(self._h, ctypes.byref(bits))
         return code, bits.value

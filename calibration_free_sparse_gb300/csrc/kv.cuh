@@ -28,8 +28,6 @@ struct moe_reader_kv {
   uint32_t* arrived;          // [rows]           pieces written; zero between launches
   size_t arrived_bytes;
   uint32_t* err;              // [1]              device error word
-  cudaStream_t last_stream;
-  int used;
 };
 
 namespace mr {

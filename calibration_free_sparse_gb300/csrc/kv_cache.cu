@@ -758,13 +758,6 @@ bool on_device(const moe_reader_kv* kv) {
   return cudaGetDevice(&dev) == cudaSuccess && dev == kv->device;
 }
 
-int done(moe_reader_kv* kv, cudaError_t e, cudaStream_t s) {
-  if (e != cudaSuccess) return status_of(e);
-  kv->last_stream = s;
-  kv->used = 1;
-  return MOE_READER_OK;
-}
-
 }  // namespace
 
 extern "C" {
@@ -858,7 +851,7 @@ int moe_reader_kv_plan(moe_reader_kv_t* kv, const moe_reader_kv_plan_args* a, vo
   }
   if (!on_device(kv)) return MOE_READER_EINVAL;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return done(kv, mr::launch_kv_plan(*kv, *a, s), s);
+  return status_of(mr::launch_kv_plan(*kv, *a, s));
 }
 
 int moe_reader_kv_append(moe_reader_kv_t* kv, const moe_reader_kv_append_args* a, void* stream) {
@@ -870,7 +863,7 @@ int moe_reader_kv_append(moe_reader_kv_t* kv, const moe_reader_kv_append_args* a
     return MOE_READER_EINVAL;
   if (!on_device(kv)) return MOE_READER_EINVAL;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return done(kv, mr::launch_kv_append(*kv, *a, s), s);
+  return status_of(mr::launch_kv_append(*kv, *a, s));
 }
 
 int moe_reader_kv_attend(moe_reader_kv_t* kv, const moe_reader_kv_attend_args* a, void* stream) {
@@ -901,7 +894,7 @@ int moe_reader_kv_attend(moe_reader_kv_t* kv, const moe_reader_kv_attend_args* a
     if (!at_multiple(p, 4)) return MOE_READER_EINVAL;
   if (!on_device(kv)) return MOE_READER_EINVAL;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return done(kv, mr::launch_kv_attend(*kv, *a, s), s);
+  return status_of(mr::launch_kv_attend(*kv, *a, s));
 }
 
 int moe_reader_kv_select(moe_reader_kv_t* kv, const moe_reader_kv_select_args* a, void* stream) {
@@ -920,23 +913,28 @@ int moe_reader_kv_select(moe_reader_kv_t* kv, const moe_reader_kv_select_args* a
     return MOE_READER_EINVAL;
   if (!on_device(kv)) return MOE_READER_EINVAL;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return done(kv, mr::launch_kv_select(*kv, *a, s), s);
+  return status_of(mr::launch_kv_select(*kv, *a, s));
 }
 
 int moe_reader_kv_status(moe_reader_kv_t* kv, uint32_t* bits_out) {
-  if (!kv) return MOE_READER_EINVAL;
-  cudaError_t ce = kv->used ? cudaStreamSynchronize(kv->last_stream) : cudaDeviceSynchronize();
+  if (!kv || !on_device(kv)) return MOE_READER_EINVAL;
+  // the whole device: a captured call runs on whichever stream replays it
+  cudaError_t ce = cudaDeviceSynchronize();
   if (ce != cudaSuccess) return status_of(ce);
   uint32_t bits = 0;
   if ((ce = cudaMemcpy(&bits, kv->err, 4, cudaMemcpyDeviceToHost)) != cudaSuccess)
     return status_of(ce);
-  if ((ce = cudaMemset(kv->err, 0, 4)) != cudaSuccess) return status_of(ce);
-  if (bits_out) *bits_out = bits;
-  if (bits & MOE_READER_ERR_TIMEOUT) {
-    // what the launch that gave up has counted does not hold for the next one
-    ce = cudaMemset(kv->arrived, 0, kv->arrived_bytes);
-    return ce == cudaSuccess ? MOE_READER_ETIMEOUT : status_of(ce);
+  if (bits) {
+    // cleared before this returns: streams need not wait for the default one.
+    // What a launch that gave up has counted does not hold for the next one.
+    ce = cudaMemsetAsync(kv->err, 0, 4, cudaStreamLegacy);
+    if (ce == cudaSuccess && (bits & MOE_READER_ERR_TIMEOUT))
+      ce = cudaMemsetAsync(kv->arrived, 0, kv->arrived_bytes, cudaStreamLegacy);
+    if (ce == cudaSuccess) ce = cudaStreamSynchronize(cudaStreamLegacy);
+    if (ce != cudaSuccess) return status_of(ce);
   }
+  if (bits_out) *bits_out = bits;
+  if (bits & MOE_READER_ERR_TIMEOUT) return MOE_READER_ETIMEOUT;
   return bits ? MOE_READER_EDEVICE : MOE_READER_OK;
 }
 

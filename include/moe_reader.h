@@ -619,10 +619,11 @@ typedef struct {
 } moe_reader_kv_select_args;
 int moe_reader_kv_select(moe_reader_kv_t* kv, const moe_reader_kv_select_args* a, void* stream);
 
-/* moe_reader_kv_status -- synchronize the stream of the last call on the
- * handle, read and clear its device error word.  *bits (host, may be NULL)
+/* moe_reader_kv_status -- synchronize the handle's device (a captured call runs
+ * on whichever stream replays it), read and clear the device error word: calls
+ * made after it returns report into a clean one.  *bits (host, may be NULL)
  * receives the MOE_READER_ERR_* bits.  Returns OK, EDEVICE, ETIMEOUT (a bounded
- * wait inside a kernel ran out) or ECUDA. */
+ * wait inside a kernel ran out), EINVAL or ECUDA. */
 int moe_reader_kv_status(moe_reader_kv_t* kv, uint32_t* bits);
 
 /* moe_reader_kv_destroy -- free the handle and its workspace (NULL is a

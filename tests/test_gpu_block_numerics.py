@@ -487,3 +487,44 @@ def test_append_coordinates_that_are_nan_throughout(dtype, gap):
             assert np.array_equal(c.codes[c.table_np[r, 1], h].cpu().numpy(), np.stack([hi, lo]))
     # no stored value is above 448: no step above 4
     assert float(c.steps[c.table_np[0, 1], 0]) <= 4 and c.cache.status() == (0, 0)
+
+
+# --------------------------------------------------------------------------
+# status
+# --------------------------------------------------------------------------
+def test_status_waits_for_a_replay_on_another_stream():
+    """A step that was captured on one stream and is replayed on a stream that
+    does not wait for others: status sees the replay's errors, and clears them."""
+    c = T.Cache([40, 30], 1, 64, 16, BF, q_heads=2, summaries=False)
+    q = T.queries(2, 2, 64, BF)
+    out = torch.empty_like(q)
+    lens = c.lens_t.clone()
+    c.cache.attend(q, c.table, lens, out)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        c.cache.attend(q, c.table, lens, out)
+    side = torch.cuda.Stream()
+    for bad in (True, False, True):
+        lens.copy_(T.to_i32([-1 if bad else 40, 30]))
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(100_000_000)             # some 50 ms
+            graph.replay()
+        assert c.cache.status() == ((rd.EDEVICE, block.ERR_LENGTH) if bad else (0, 0))
+    torch.cuda.synchronize()
+    assert c.cache.status() == (0, 0)
+
+
+def test_status_does_not_clear_what_a_later_call_reports():
+    """Calls on another stream straight after status, over and over."""
+    c = T.Cache([40], 1, 64, 16, BF, q_heads=2, summaries=False)
+    q = T.queries(1, 2, 64, BF)
+    out, bad = torch.empty_like(q), T.to_i32([-1])
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        for _ in range(300):
+            c.cache.attend(q, c.table, bad, out)
+            assert c.cache.status() == (rd.EDEVICE, block.ERR_LENGTH)
+    assert c.cache.status() == (0, 0)
