@@ -128,6 +128,15 @@ const void* export_ptr(const moe_reader* h, int which) {
   }
 }
 
+// Clears the reported error bits, and the counters that a timed-out decode leaves
+// behind, before it returns: streams need not wait for the default one.
+cudaError_t clear_errors(const moe_reader* h, uint32_t bits) {
+  cudaError_t ce = cudaMemsetAsync(h->ws.err, 0, 4, cudaStreamLegacy);
+  if (ce == cudaSuccess && (bits & mr::kErrTimeout))
+    ce = cudaMemsetAsync(h->ws.sync, 0, mr::sync_words(h->d) * 4, cudaStreamLegacy);
+  return ce == cudaSuccess ? cudaStreamSynchronize(cudaStreamLegacy) : ce;
+}
+
 int check_decode_args(const moe_reader* h, const void* x, int32_t B, const void* ids,
                       const void* w, int32_t k, const void* y) {
   if (!h) return MOE_READER_EINVAL;
@@ -476,9 +485,8 @@ int moe_reader_decode_host(moe_reader_t* h, const float* x_host, int32_t B,
     return cuda_status(ce);
   if ((ce = cudaStreamSynchronize(s)) != cudaSuccess) return cuda_status(ce);
   if (bits & mr::kErrTimeout) {
-    cudaMemset(h->ws.sync, 0, mr::sync_words(d) * 4);
-    cudaMemset(h->ws.err, 0, 4);
-    return MOE_READER_ETIMEOUT;
+    ce = clear_errors(h, bits);
+    return ce == cudaSuccess ? MOE_READER_ETIMEOUT : cuda_status(ce);
   }
   if (bits) return MOE_READER_EDEVICE;
   return MOE_READER_OK;
@@ -552,17 +560,13 @@ int moe_reader_inject_fault(moe_reader_t* h, uint32_t what) {
 
 int moe_reader_status(moe_reader_t* h, uint32_t* bits_out) {
   if (!h) return MOE_READER_EINVAL;
-  cudaError_t ce = h->has_decode ? cudaStreamSynchronize(h->last_stream) : cudaDeviceSynchronize();
+  // the whole device: a captured decode runs on whichever stream replays it
+  cudaError_t ce = cudaDeviceSynchronize();
   if (ce != cudaSuccess) return cuda_status(ce);
   uint32_t bits = 0;
   if ((ce = cudaMemcpy(&bits, h->ws.err, 4, cudaMemcpyDeviceToHost)) != cudaSuccess)
     return cuda_status(ce);
-  if ((ce = cudaMemset(h->ws.err, 0, 4)) != cudaSuccess) return cuda_status(ce);
-  if (bits & mr::kErrTimeout) {
-    // a timed-out decode leaves its counters behind: clear them for the next call
-    if ((ce = cudaMemset(h->ws.sync, 0, mr::sync_words(h->d) * 4)) != cudaSuccess)
-      return cuda_status(ce);
-  }
+  if (bits && (ce = clear_errors(h, bits)) != cudaSuccess) return cuda_status(ce);
   if (bits_out) *bits_out = bits;
   if (bits & mr::kErrTimeout) return MOE_READER_ETIMEOUT;
   if (bits) return MOE_READER_EDEVICE;

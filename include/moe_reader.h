@@ -299,9 +299,11 @@ int moe_reader_set_wait_limit(moe_reader_t* h, uint64_t ns);
 #define MOE_READER_INJECT_ALLOC_FAIL    0x4u
 int moe_reader_inject_fault(moe_reader_t* h, uint32_t what);
 
-/* moe_reader_status -- synchronize the stream of the last decode, read and
- * clear the device error word.  *bits (host, may be NULL) receives the
- * MOE_READER_ERR_* bits.  Returns OK, EDEVICE (input check) or ETIMEOUT. */
+/* moe_reader_status -- synchronize the device (a captured decode runs on
+ * whichever stream replays it), read and clear the device error word: decodes
+ * enqueued after it returns report into a clean one.  *bits (host, may be NULL)
+ * receives the MOE_READER_ERR_* bits.  Returns OK, EDEVICE (input check) or
+ * ETIMEOUT. */
 int moe_reader_status(moe_reader_t* h, uint32_t* bits);
 
 /* moe_reader_get_stats -- read accounting of the last decode (synchronizes
