@@ -42,8 +42,14 @@ class Config(ctypes.Structure):
                 ("cache_type", ctypes.c_int32), ("flags", ctypes.c_int32)]
 
 
-_current = torch._C._cuda_getCurrentRawStream   # the current stream's handle on a device
-_device = torch._C._cuda_getDevice              # the current device
+def _no_cuda(*_):
+    raise RuntimeError("this build of torch has no CUDA")
+
+
+# the current stream's handle on a device, and the current device; a torch built
+# without CUDA lacks both, and the first call that needs one says so
+_current = getattr(torch._C, "_cuda_getCurrentRawStream", _no_cuda)
+_device = getattr(torch._C, "_cuda_getDevice", _no_cuda)
 
 
 def _handle(stream):
@@ -350,9 +356,9 @@ def residual_norm(h, x=None, y=None, post_weight=None, gate=None, scale=1.0, pre
         rows, hidden = shape
     except (AttributeError, ValueError):
         raise TypeError("h must be a CUDA tensor [rows][hidden]") from None
+    if dev < 0:
+        raise TypeError("h must be a CUDA tensor [rows][hidden]")
     if dev != _device():
-        if dev < 0:
-            raise TypeError("h must be a CUDA tensor [rows][hidden]")
         raise ValueError(f"h is on cuda:{dev}, not the current device")
     hp, hs, ht = _matrix(h, "h", shape, dev)
     yp = ys = yt = xp = xs = xt = op = os_ = gp = grow = gcol = gt = pp = qp = wt = 0
