@@ -15,6 +15,7 @@ namespace {
 // Pending one-shot fault injections that are not tied to a handle.
 std::atomic<int> g_fail_next_alloc{0};
 std::atomic<int> g_stall_next_prepare{0};
+std::atomic<int> g_stall_next_attend{0};
 
 using mr::Dims;
 
@@ -175,6 +176,9 @@ cudaError_t device_alloc(void** p, size_t bytes) {
 }
 
 bool take_prepare_stall() { return g_stall_next_prepare.exchange(0) != 0; }
+bool take_attend_stall() {
+  return g_stall_next_attend.load(std::memory_order_relaxed) && g_stall_next_attend.exchange(0) != 0;
+}
 
 }  // namespace mr
 
@@ -546,7 +550,8 @@ int moe_reader_set_wait_limit(moe_reader_t* h, uint64_t ns) {
 
 int moe_reader_inject_fault(moe_reader_t* h, uint32_t what) {
   const uint32_t handle_bits = MOE_READER_INJECT_DECODE_STALL;
-  const uint32_t global_bits = MOE_READER_INJECT_PREPARE_STALL | MOE_READER_INJECT_ALLOC_FAIL;
+  const uint32_t global_bits = MOE_READER_INJECT_PREPARE_STALL | MOE_READER_INJECT_ALLOC_FAIL |
+                               MOE_READER_INJECT_ATTEND_STALL;
   if (what == 0 || (what & ~(handle_bits | global_bits))) return MOE_READER_EINVAL;
   if (h ? (what & global_bits) != 0 : (what & handle_bits) != 0) return MOE_READER_EINVAL;
   if (h) {
@@ -555,6 +560,7 @@ int moe_reader_inject_fault(moe_reader_t* h, uint32_t what) {
   }
   if (what & MOE_READER_INJECT_PREPARE_STALL) g_stall_next_prepare.store(1);
   if (what & MOE_READER_INJECT_ALLOC_FAIL) g_fail_next_alloc.store(1);
+  if (what & MOE_READER_INJECT_ATTEND_STALL) g_stall_next_attend.store(1);
   return MOE_READER_OK;
 }
 

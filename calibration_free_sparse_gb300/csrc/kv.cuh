@@ -48,6 +48,8 @@ cudaError_t launch_kv_append(const moe_reader_kv& kv, const moe_reader_kv_append
 cudaError_t launch_kv_attend(const moe_reader_kv& kv, const moe_reader_kv_attend_args& a,
                              cudaStream_t s);
 cudaError_t configure_kv_attend(const moe_reader_kv& kv);
+// One-shot injection of a turn that never comes in the next attend.
+bool take_attend_stall();
 // Items of attend: (request, KV head, tile of the group's query heads).
 int attend_row_tiles(const moe_reader_kv_config& c);
 cudaError_t launch_kv_select(const moe_reader_kv& kv, const moe_reader_kv_select_args& a,

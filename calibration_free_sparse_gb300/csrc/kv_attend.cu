@@ -110,6 +110,8 @@ struct Params {
   float* part_ml;
   uint32_t* arrived;
   uint32_t* err;
+  int polls;               // of a turn, at most
+  uint32_t stall;          // added to the turn that is waited for: 0, or never reached
 };
 
 // ---- instructions ---------------------------------------------------------
@@ -329,17 +331,28 @@ __device__ __forceinline__ void copy_subtile(const Params& P, long long at, int 
   }
 }
 
-// Waits until shared word `turn` reaches `want`; gives up after a fraction of
-// a second (the warps that it waits for only compute, so this cannot happen).
-__device__ __forceinline__ void wait_turn(const uint32_t* turn, uint32_t want, uint32_t& bad) {
-  const uint32_t a = smem_addr(turn);
-  for (int n = 0; n < (1 << 21); ++n) {
-    uint32_t v;
-    asm volatile("ld.acquire.cta.shared.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
-    if (v == want) return;
+__device__ __forceinline__ uint32_t load_acquire(const uint32_t* p) {
+  uint32_t v;
+  asm volatile("ld.acquire.cta.shared.u32 %0, [%1];" : "=r"(v) : "r"(smem_addr(p)) : "memory");
+  return v;
+}
+// Waits until shared word `turn` reaches `want`; all lanes.  False where that
+// took `most` polls (a fraction of a second; the warps that it waits for only
+// compute, so only an injected stall gets there) or another wait of the CTA gave
+// up: the turn is then not passed on, so that all later ones end soon, too, and
+// the call ends with an error.
+__device__ __forceinline__ bool wait_turn(const uint32_t* turn, uint32_t want, uint32_t* gave_up,
+                                          int most) {
+  bool mine = false;
+  for (int n = 0; n < most; ++n) {
+    mine = load_acquire(turn) == want;
+    if (mine || ((n & 63) == 63 && load_acquire(gave_up))) break;
     __nanosleep(64);
   }
-  bad |= MOE_READER_ERR_TIMEOUT;
+  mine = __all_sync(0xffffffffu, mine);
+  if (!mine)
+    asm volatile("st.release.cta.shared.u32 [%0], 1;" ::"r"(smem_addr(gave_up)) : "memory");
+  return mine;
 }
 __device__ __forceinline__ void pass_turn(uint32_t* turn, uint32_t next) {
   asm volatile("st.release.cta.shared.u32 [%0], %1;" ::"r"(smem_addr(turn)), "r"(next) : "memory");
@@ -487,7 +500,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) attend_kernel(const Params P) 
   uint16_t* s_order = reinterpret_cast<uint16_t*>(s_len + kMaxRequests);   // requests of the list
   __shared__ int4 s_scan[kWarps];
   __shared__ int s_before[kWarps];
-  __shared__ uint32_t s_turn[2];
+  __shared__ uint32_t s_turn[2], s_gave_up;
   __shared__ int s_last[2];
   __shared__ float s_mul[S::kRows];
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
@@ -498,6 +511,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) attend_kernel(const Params P) 
   uint32_t bad = 0;
 
   if (tid < 2) s_turn[tid] = 0, s_last[tid] = 0;
+  if (tid == 0) s_gave_up = 0;
   wait_for_earlier_launch();
   // ---- shares of the rows that CTAs share: U tiles per CTA ----
   constexpr int kPer = (kMaxRequests + S::kThreads - 1) / S::kThreads;
@@ -1049,36 +1063,41 @@ __global__ void __launch_bounds__(S::kThreads, 1) attend_kernel(const Params P) 
     float* ref = s_ml + b * S::kRows;
     float* den = s_ml + (2 + b) * S::kRows;
     const uint32_t turn = (uint32_t)(k >> 1) * kWarps + place_in_turn;
-    wait_turn(&s_turn[b], turn, bad);
+    const bool my_turn = wait_turn(&s_turn[b], turn + P.stall, &s_gave_up, P.polls);
+    if (!my_turn) bad |= MOE_READER_ERR_TIMEOUT;
+    if (my_turn) {
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      float keep[2] = {0.f, 0.f}, add[2];              // factors of the state and of this warp
+      for (int n = 0; n < NT; ++n) {
+        float keep[2] = {0.f, 0.f}, add[2];            // factors of the state and of this warp
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int h = n * 8 + 2 * t4 + i;
-        const float before = place_in_turn ? ref[h] : -INFINITY;
-        const float now_ref = fmaxf(before, m[n][i]);
-        add[i] = m[n][i] == -INFINITY ? 0.f : exp2_fast(m[n][i] - now_ref);
-        float d = l[n][i] * add[i];
-        if (before != -INFINITY) {
-          keep[i] = exp2_fast(before - now_ref);
-          d += den[h] * keep[i];
+        for (int i = 0; i < 2; ++i) {
+          const int h = n * 8 + 2 * t4 + i;
+          const float before = place_in_turn ? ref[h] : -INFINITY;
+          const float now_ref = fmaxf(before, m[n][i]);
+          add[i] = m[n][i] == -INFINITY ? 0.f : exp2_fast(m[n][i] - now_ref);
+          float d = l[n][i] * add[i];
+          if (before != -INFINITY) {
+            keep[i] = exp2_fast(before - now_ref);
+            d += den[h] * keep[i];
+          }
+          __syncwarp();                                // all lanes of the column have read
+          if (g == 0) ref[h] = now_ref, den[h] = d;
         }
-        __syncwarp();                                  // all lanes of the column have read
-        if (g == 0) ref[h] = now_ref, den[h] = d;
+#pragma unroll
+        for (int x = 0; x < D / 16; ++x)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int h = n * 8 + 2 * t4 + (i & 1);
+            float* at = acc + h * S::kAccPitch + x * 16 + (k8 ? 2 * g + (i >> 1) : g + 8 * (i >> 1));
+            const float v = o[x][n][i] * add[i & 1];
+            *at = place_in_turn ? *at * keep[i & 1] + v : v;
+          }
       }
-#pragma unroll
-      for (int x = 0; x < D / 16; ++x)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int h = n * 8 + 2 * t4 + (i & 1);
-          float* at = acc + h * S::kAccPitch + x * 16 + (k8 ? 2 * g + (i >> 1) : g + 8 * (i >> 1));
-          const float v = o[x][n][i] * add[i & 1];
-          *at = place_in_turn ? *at * keep[i & 1] + v : v;
-        }
     }
     __syncwarp();
-    if (place_in_turn == kWarps - 1) {
+    if (place_in_turn == kWarps - 1 && !my_turn) {     // the row's other CTAs still count this one
+      if (cc.begin < c0 && lane == 0) s_last[0] = arrive(cc);
+    } else if (place_in_turn == kWarps - 1) {
       if (cc.begin >= c0) {                            // the whole row
         if (lane < S::kRows) {
           float mul, lse;
@@ -1109,7 +1128,7 @@ __global__ void __launch_bounds__(S::kThreads, 1) attend_kernel(const Params P) 
       }
       __syncwarp();
     }
-    if (lane == 0) pass_turn(&s_turn[b], turn + 1);
+    if (my_turn && lane == 0) pass_turn(&s_turn[b], turn + 1);
     p0 = p1;
     ++k;
   }
@@ -1299,6 +1318,9 @@ cudaError_t launch_kv_attend(const moe_reader_kv& kv, const moe_reader_kv_attend
   P.part_ml = kv.part_ml;
   P.arrived = kv.arrived;
   P.err = kv.err;
+  const bool stall = take_attend_stall();
+  P.polls = stall ? 1 << 12 : 1 << 21;
+  P.stall = stall ? 1u << 30 : 0u;
   with_shape(kv.cfg, [&](auto sh) { launch<decltype(sh)>(P, kv, a, s); return 0; });
   return cudaGetLastError();
 }

@@ -21,6 +21,7 @@ FLAG_TRIT5 = 0x2      # sketch codes stored five trits per byte
 ERR_EXPERT_RANGE, ERR_EXPERT_DUP, ERR_WEIGHT, ERR_X_NONFINITE, ERR_TIMEOUT = 1, 2, 4, 8, 16
 # one-shot fault injections for tests of failure detection (moe_reader_inject_fault)
 INJECT_DECODE_STALL, INJECT_PREPARE_STALL, INJECT_ALLOC_FAIL = 0x1, 0x2, 0x4
+INJECT_ATTEND_STALL = 0x10
 ARRAYS = ("codes", "scales", "dnorm", "G", "V", "Dt", "b", "U")
 
 EXPORT = {
@@ -217,8 +218,8 @@ def topk_noalloc(scores, k, kept, ids=None, stream=None):
 
 def inject_fault(what, reader=None):
     """Arm a one-shot failure (INJECT_* bits): a decode stall on `reader`, or,
-    with reader None, a stall in the next prepare or a failed next device
-    allocation.  Nothing faults the GPU; the failure surfaces as a status."""
+    with reader None, a stall in the next prepare or cache attention or a failed
+    next device allocation.  Nothing faults the GPU; the failure surfaces as a status."""
     _check(_lib().moe_reader_inject_fault(None if reader is None else reader.handle, int(what)),
            "moe_reader_inject_fault")
 

@@ -292,11 +292,16 @@ int moe_reader_set_wait_limit(moe_reader_t* h, uint64_t ns);
  *   MOE_READER_INJECT_ALLOC_FAIL     (h = NULL) the library's next device
  *       allocation reports failure as if the device were out of memory; the
  *       call that made it returns ENOMEM after freeing what it holds.
+ *   MOE_READER_INJECT_ATTEND_STALL   (h = NULL) the next moe_reader_kv_attend
+ *       waits, where a row ends inside a CTA's share of keys, for a turn that
+ *       does not come; the wait runs out after about a millisecond, the CTA
+ *       adds up no more rows and the call ends with MOE_READER_ERR_TIMEOUT.
  * Each injection fires once.  EINVAL for an unknown bit or a wrong h.
  */
 #define MOE_READER_INJECT_DECODE_STALL  0x1u
 #define MOE_READER_INJECT_PREPARE_STALL 0x2u
 #define MOE_READER_INJECT_ALLOC_FAIL    0x4u
+#define MOE_READER_INJECT_ATTEND_STALL  0x10u
 int moe_reader_inject_fault(moe_reader_t* h, uint32_t what);
 
 /* moe_reader_status -- synchronize the device (a captured decode runs on

@@ -5,6 +5,7 @@ arithmetic, as each test says (u: half an ulp of a type, d: the bound
 (D + 16) 2^-24 scale sum |q k| of a logit's error in fp32)."""
 
 import math
+import time
 
 import numpy as np
 import pytest
@@ -528,3 +529,25 @@ def test_status_does_not_clear_what_a_later_call_reports():
             c.cache.attend(q, c.table, bad, out)
             assert c.cache.status() == (rd.EDEVICE, block.ERR_LENGTH)
     assert c.cache.status() == (0, 0)
+
+
+@pytest.mark.parametrize("dim,dtype,group", [(64, HF, 4), (128, BF, 16), (128, E4, 5), (256, BF, 3)])
+def test_attend_turn_that_does_not_come(dim, dtype, group):
+    """Rows cut by equal shares, so that they end inside them: the waits there
+    run out, a timeout within a moment and not one per row, and the next call on
+    the handle is right and clean."""
+    lens = [2700 - 40 * i for i in range(20)]
+    c = T.Cache(lens, 8, dim, 64, dtype, seed=41, q_heads=8 * group, summaries=False)
+    q = T.queries(len(lens), 8 * group, dim, BF if dtype == E4 else dtype)
+    good, out = torch.empty_like(q), torch.empty_like(q)
+    c.cache.attend(q, c.table, c.lens_t, good)
+    assert c.cache.status() == (0, 0)
+    for _ in range(2):
+        rd.inject_fault(rd.INJECT_ATTEND_STALL)
+        start = time.perf_counter()
+        c.cache.attend(q, c.table, c.lens_t, out)
+        assert c.cache.status() == (rd.ETIMEOUT, rd.ERR_TIMEOUT)
+        assert time.perf_counter() - start < 1.0
+        out.fill_(7.0)
+        c.cache.attend(q, c.table, c.lens_t, out)
+        assert c.cache.status() == (0, 0) and torch.equal(out, good)
