@@ -10,6 +10,7 @@
 // above 16384 elements (8192 with fp32 or mixed types) do not fit the registers
 // that way: their kernel reads the row again (from L2) for each of its passes.
 #include <algorithm>
+#include <cstdlib>
 #include <type_traits>
 
 #include "kv.cuh"
@@ -317,19 +318,34 @@ bool rows_fit(const void* p, int type, int64_t stride) {
   return float_type(type) && reinterpret_cast<uintptr_t>(p) % 16 == 0 && stride % 8 == 0;
 }
 
-// Whether two row-strided matrices share a byte (by their outer extents).
-bool overlap(const void* p, int pt, int64_t ps, const void* q, int qt, int64_t qs, int rows,
-             int hidden) {
-  if (!p || !q) return false;
-  auto extent = [&](const void* m, int t, int64_t s, uintptr_t& lo, uintptr_t& hi) {
-    const long long step = (long long)(rows - 1) * s * bytes_of(t);
-    lo = reinterpret_cast<uintptr_t>(m) + (step < 0 ? step : 0);
-    hi = reinterpret_cast<uintptr_t>(m) + (step > 0 ? step : 0) + hidden * bytes_of(t);
+// Rows of `width` bytes, `step` bytes apart.
+struct Bytes {
+  const void* at;
+  long long step, width;
+  int rows;
+};
+Bytes matrix(const void* p, int type, int64_t stride, int rows, int hidden) {
+  return {p, stride * bytes_of(type), hidden * bytes_of(type), rows};
+}
+
+// Whether two of them share a byte: by their outer extents, but column slices of
+// one buffer do not.
+bool overlap(const Bytes& p, const Bytes& q) {
+  if (!p.at || !q.at) return false;
+  auto extent = [](const Bytes& m, long long& lo, long long& hi) {
+    const long long last = (m.rows - 1) * m.step;
+    lo = static_cast<long long>(reinterpret_cast<uintptr_t>(m.at)) + std::min(last, 0LL);
+    hi = static_cast<long long>(reinterpret_cast<uintptr_t>(m.at)) + std::max(last, 0LL) + m.width;
   };
-  uintptr_t a0, a1, b0, b1;
-  extent(p, pt, ps, a0, a1);
-  extent(q, qt, qs, b0, b1);
-  return a0 < b1 && b0 < a1;
+  long long a0, a1, b0, b1;
+  extent(p, a0, a1);
+  extent(q, b0, b1);
+  if (a0 >= b1 || b0 >= a1) return false;
+  if (p.step == q.step && p.step > 0) {
+    const long long apart = ((b0 - a0) % p.step + p.step) % p.step;
+    if (apart >= p.width && apart + q.width <= p.step) return false;
+  }
+  return true;
 }
 
 int check(const Args& a) {
@@ -354,16 +370,23 @@ int check(const Args& a) {
       return MOE_READER_EINVAL;
     }
   }
+  const Bytes h = matrix(a.h, a.h_type, a.h_stride, a.rows, a.hidden);
+  const Bytes y = matrix(a.y, a.y_type, a.y_stride, a.rows, a.hidden);
+  const Bytes h_out = matrix(a.h_out, a.h_type, a.h_out_stride, a.rows, a.hidden);
+  const Bytes x = matrix(a.x, a.x_type, a.x_stride, a.rows, a.hidden);
+  const Bytes gate = matrix(a.gate, a.gate_type, a.gate_row_stride, a.rows,
+                            a.gate_col_stride ? a.hidden : 1);
+  const Bytes post = matrix(a.post_weight, a.weight_type, 0, 1, a.hidden);
+  const Bytes pre = matrix(a.pre_weight, a.weight_type, 0, 1, a.hidden);
+  // an output's rows are its own
+  for (const Bytes* o : {&h_out, &x})
+    if (o->at && a.rows > 1 && std::abs(o->step) < o->width) return MOE_READER_EINVAL;
   // h' may replace h in place; any other overlap would be read after a write
   const bool in_place = a.h_out == a.h && a.h_out_stride == a.h_stride;
-  if (a.h_out && !in_place &&
-      overlap(a.h, a.h_type, a.h_stride, a.h_out, a.h_type, a.h_out_stride, a.rows, a.hidden))
-    return MOE_READER_EINVAL;
-  if (overlap(a.y, a.y_type, a.y_stride, a.h_out, a.h_type, a.h_out_stride, a.rows, a.hidden) ||
-      overlap(a.h, a.h_type, a.h_stride, a.x, a.x_type, a.x_stride, a.rows, a.hidden) ||
-      overlap(a.y, a.y_type, a.y_stride, a.x, a.x_type, a.x_stride, a.rows, a.hidden) ||
-      overlap(a.h_out, a.h_type, a.h_out_stride, a.x, a.x_type, a.x_stride, a.rows, a.hidden))
-    return MOE_READER_EINVAL;
+  if (!in_place && overlap(h, h_out)) return MOE_READER_EINVAL;
+  for (const Bytes* in : {&y, &gate, &post, &pre})
+    if (overlap(*in, h_out) || overlap(*in, x)) return MOE_READER_EINVAL;
+  if (overlap(h, x) || overlap(h_out, x)) return MOE_READER_EINVAL;
   return MOE_READER_OK;
 }
 

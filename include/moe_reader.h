@@ -653,8 +653,10 @@ void moe_reader_kv_destroy(moe_reader_kv_t* kv);
  *              0 broadcasts, gate_col_stride is 0 or 1.
  *   post_weight, pre_weight  dev, [hidden] of weight_type, or NULL.
  *   h_out      dev, [rows][hidden] of h_type, or NULL (not written); may be h.
- *   x          dev, [rows][hidden] of x_type, or NULL (not written); may not
- *              overlap h, y or h_out.
+ *   x          dev, [rows][hidden] of x_type, or NULL (not written).
+ *              No other input may overlap an output, nor an output the other,
+ *              nor a row of an output the next (column slices of one buffer do
+ *              not).
  *
  * hidden is a multiple of 8, 8..65536.  Everything is held in fp32 and rounded
  * once, on the way out: x is formed from the unrounded h'.  Asynchronous; one

@@ -551,3 +551,28 @@ def test_attend_turn_that_does_not_come(dim, dtype, group):
         out.fill_(7.0)
         c.cache.attend(q, c.table, c.lens_t, out)
         assert c.cache.status() == (0, 0) and torch.equal(out, good)
+
+
+# --------------------------------------------------------------------------
+# residual norm
+# --------------------------------------------------------------------------
+def test_residual_norm_between_column_slices_of_one_buffer():
+    """Inputs and outputs side by side in the rows of one buffer, also where the
+    rows' end touches the next row's beginning; a gate beside them."""
+    g = torch.Generator(device="cuda").manual_seed(2)
+    rows, H = 37, 264
+    wide = torch.randn((rows, 5 * H), generator=g, device="cuda")
+    h, y, x, h_out, gate = (wide[:, i * H:(i + 1) * H] for i in (1, 0, 2, 4, 3))
+    before = wide.clone()
+    pre = torch.randn(H, generator=g, device="cuda")
+    want = T.ref_norm(T.f64(h), T.f64(y), None, T.f64(gate), 0.5, T.f64(pre), 1e-6)
+    block.residual_norm(h, x, y=y, gate=gate, scale=0.5, pre_weight=pre, h_out=h_out)
+    hh, xx, size, inv = want                # as test_residual_norm bounds them, in fp32
+    assert np.all(np.abs(T.f64(h_out) - hh) <= 2.0 ** -18 * size + 2.0 ** -24 * (1 + np.abs(hh)))
+    assert np.all(np.abs(T.f64(x) - xx) <= 2.0 ** -17 * (size * inv * np.abs(T.f64(pre)) + np.abs(xx)) +
+                  2.0 ** -24)
+    for i in (0, 1, 3):
+        assert torch.equal(wide[:, i * H:(i + 1) * H], before[:, i * H:(i + 1) * H])
+    # one value for all rows is no place to write to
+    with pytest.raises(rd.ReaderError):
+        block.residual_norm(h, torch.empty((1, H), device="cuda").expand(rows, H))
