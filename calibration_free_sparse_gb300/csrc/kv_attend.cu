@@ -25,7 +25,7 @@
 // All sums have a fixed order: the result does not depend on timing.
 //
 // Measured on a GB300 (read-only streams reach 7.3 TB/s there): 128 requests of
-// up to 8192 tokens, 16 heads of 128 on each of 4 KV heads, bf16: 205 us for
+// up to 8192 tokens, 16 heads of 128 on each of 4 KV heads, bf16: 206 us for
 // 1.28 GB, 6.2 TB/s, the tensor pipe 27 % busy (so a wider matrix instruction
 // would not shorten it); 131071 tokens of e4m3 alone: 49 us for 268 MB; one
 // request of 301 tokens: 7 us, of which 2 are the launch, 3 the lengths, shares,
@@ -556,7 +556,10 @@ __global__ void __launch_bounds__(S::kThreads, 1) attend_kernel(const Params P) 
   // Times below are in tiles of a warp's time (about 0.75 us).  A row that the
   // warps of a CTA share costs them about seven beside its tiles, a row that
   // CTAs share fifteen; a row that a single warp has to itself costs one and a
-  // half, but all of its tiles are that warp's.
+  // half, but all of its tiles are that warp's.  (Fitted to bf16 heads of 128,
+  // eight warps; the other shapes use the same numbers.  128 requests lognormal
+  // around 500 tokens, 8 KV heads: bf16 heads of 128 80 us of 55 at the measured
+  // bandwidth, of 256 159 / 111; e4m3 heads of 128 79 / 28, of 64 52 / 14.)
   int short_most = 0;             // rows of at most so many tiles are single warps'
   const bool differ = items >= 16 && (long long)most * items >= 2LL * total;
   if (items > grid || differ) {

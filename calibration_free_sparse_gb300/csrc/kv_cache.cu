@@ -430,11 +430,12 @@ __device__ __noinline__ bool append_cut_runs(Window& c, const moe_reader_kv_appe
 // sees to pages whose new tokens have skipped ones between them).  D / 8 lanes
 // share a row, 8 values each; a thread has kAhead rows in flight.
 //
-// Measured: 2.5 us for one token of 16 requests (4 KV heads of 128, pages of
-// 16); 12.4 us for 10 thousand tokens into an e4m3 cache (31 MB, 2.5 TB/s: the
-// quotients and conversions keep the issue slots half busy, the rest is the
+// Measured: 2.6 us for one token of 16 requests (4 KV heads of 128, pages of
+// 16); 12.6 us for 10 thousand tokens into an e4m3 cache (31 MB, 2.4 TB/s: the
+// quotients and conversions keep the issue slots 60 % busy, the rest is the
 // latency of slot, row and summary); 17.6 us for 9 thousand tokens of 8 heads of
-// 128 in bf16 (75 MB, 4.2 TB/s).  On the way, for the e4m3 case: plain divisions
+// 128 in bf16 (75 MB, 4.2 TB/s: one page in flight per CTA, whose next rows wait
+// for the reduction).  On the way, for the e4m3 case: plain divisions
 // and a scan per token 28.3 us, keys and values in one CTA 21.0, rows loaded one
 // after the other 15.0, windows of 32 keys 12.9 and of 16 values 13.6.
 template <int D, int CT, int IT>
@@ -643,7 +644,9 @@ void append_as(const moe_reader_kv& kv, const moe_reader_kv_append_args& a, cuda
   // be, tokens / max_requests at least, up to a page and what the ballots hold:
   // few CTAs find nothing to close.  (A decode step of many requests must not
   // get long windows: a CTA closes one page after the other.  With windows of a
-  // page 1024 requests of 8 heads took 125 us, with these 23.)
+  // page 1024 requests of 8 heads of 128 in e4m3 took 125 us, with these 22: each
+  // token reads the older keys of its page back, and a CTA does one page after
+  // the other.)
   const int heads = kv.cfg.num_kv_heads, at_once = kAppendThreads * 8 / D;
   const long long rows = (long long)a.tokens * heads;
   const bool few = rows <= 16LL * kv.sms;
