@@ -21,7 +21,7 @@ import torch
 from . import reader as _rd
 
 TYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2, torch.float8_e4m3fn: 3}
-ERR_LENGTH, ERR_PAGE, ERR_POOL = 0x20, 0x40, 0x80
+ERR_LENGTH, ERR_PAGE, ERR_POOL, ERR_ROW = 0x20, 0x40, 0x80, 0x100
 
 _I32 = torch.int32
 _FLOATS = (torch.float32, torch.bfloat16, torch.float16)
@@ -32,6 +32,10 @@ _PLAN = struct.Struct("10Q4i")
 _APPEND = struct.Struct("3Q4q2i")
 _ATTEND = struct.Struct("7Q2q5if")
 _SELECT = struct.Struct("4Q2q6i")
+_CHUNK = struct.Struct("7Q2q5if")
+_PAGES = struct.Struct("8Q2i")
+_FORK = struct.Struct("8Q4i")
+_COPY = struct.Struct("3Qi4x")
 _NORM = struct.Struct("7Q6q7i2f4x")
 
 
@@ -149,6 +153,83 @@ class PagePlan:
         return self
 
 
+class PagePool:
+    """The pages of a pool that one page table refers to (see
+    ``PagedCache.pool``): which are free, rows forked from others, and the ones
+    in use moved to the front.  A table serves all layers, so these calls are
+    made once, and the copies that they ask for (``src``, ``dst``) once a layer
+    by ``PagedCache.copy_pages``.
+
+    ``refs`` [pages], ``free`` [pages] (-1 behind the last) and ``count`` [1]
+    are written by ``collect`` and ``compact``; ``src`` and ``dst`` by
+    ``compact`` (with ``moves`` [1]) and ``fork`` (with ``taken`` [1])."""
+
+    def __init__(self, cache, max_forks):
+        n = cache.num_pages
+        new = lambda n: torch.empty(n, dtype=_I32, device=cache.k.device)  # noqa: E731
+        self.cache, self.max_forks = cache, int(max_forks)
+        self.refs, self.free, self.count = new(n), new(n), new(1)
+        self.moves, self.taken = new(1), new(1)
+        self._moves = (new(n // 2), new(n // 2))
+        self._forks = (new(max(self.max_forks, 1)), new(max(self.max_forks, 1)))
+        self.src, self.dst = self._moves[0][:0], self._moves[1][:0]
+        lib = _rd._lib()
+        self._collect, self._compact = lib.moe_reader_kv_collect, lib.moe_reader_kv_compact
+        self._fork = lib.moe_reader_kv_fork
+
+    def _pages(self, call, name, table, lens, moves, stream):
+        dev = self.cache.device
+        R = _length(lens, "lens")
+        tab, width = _table(table, R, dev)
+        ln = _whole(lens, _I32, (R,), "lens", dev)
+        args = _PAGES.pack(tab, ln, self.refs.data_ptr(), self.free.data_ptr(),
+                           self.count.data_ptr(), *moves, R, width)
+        code = call(self.cache._h, args, _current(dev) if stream is None else _handle(stream))
+        if code:
+            _check(code, name)
+        return self
+
+    def collect(self, table, lens, stream=None):
+        """References and free pages of table (int32 [>= R][width]) with lens
+        (int32 [R]; 0 frees a request's pages)."""
+        return self._pages(self._collect, "moe_reader_kv_collect", table, lens, (0, 0, 0), stream)
+
+    def compact(self, table, lens, stream=None):
+        """``collect``, then the pages in use renumbered to the front of the
+        pool: table is updated in place, src and dst list the moves (-1 behind
+        the last of the pages // 2 that there can be)."""
+        src, dst = self._moves
+        self._pages(self._compact, "moe_reader_kv_compact", table, lens,
+                    (src.data_ptr(), dst.data_ptr(), self.moves.data_ptr()), stream)
+        self.src, self.dst = src, dst
+        return self
+
+    def fork(self, parents, children, table, lens, free_pages, stream=None):
+        """Rows children (int32 [F]) of table continue rows parents (int32
+        [F]): they share full pages, and a last page that is not full becomes a
+        fresh one from the front of free_pages.  Updates table and lens (int32
+        [rows]) in place; src and dst [F] list the copies, -1 for none."""
+        dev = self.cache.device
+        F = _length(parents, "parents")
+        par = _whole(parents, _I32, (F,), "parents", dev)
+        chi = _whole(children, _I32, (F,), "children", dev)
+        if F > self.max_forks:
+            raise ValueError(f"{F} forks for a pool of at most {self.max_forks}")
+        R = _length(lens, "lens")
+        tab, width = _table(table, R, dev)
+        ln = _whole(lens, _I32, (R,), "lens", dev)
+        N = _length(free_pages, "free_pages")
+        free = _whole(free_pages, _I32, (N,), "free_pages", dev)
+        src, dst = self._forks
+        args = _FORK.pack(par, chi, tab, ln, free, src.data_ptr(), dst.data_ptr(),
+                          self.taken.data_ptr(), F, R, width, N)
+        code = self._fork(self.cache._h, args, _current(dev) if stream is None else _handle(stream))
+        if code:
+            _check(code, "moe_reader_kv_fork")
+        self.src, self.dst = src[:F], dst[:F]
+        return self
+
+
 class PagedCache:
     """One layer's paged key/value cache.
 
@@ -173,6 +254,7 @@ class PagedCache:
         _whole(k, k.dtype, shape, "k", self.device)
         _whole(v, k.dtype, shape, "v", self.device)
         pages, self.kv_heads, self.page_size, self.head_dim = shape
+        self.k, self.v, self.num_pages = k, v, pages
         self.dtype, self.q_heads, self.max_requests = k.dtype, int(q_heads), int(max_requests)
         # rows and queries have the cache's type; an 8-bit cache takes either 16-bit one
         self._row_types = _FLOATS[1:] if k.dtype is torch.float8_e4m3fn else (k.dtype,)
@@ -189,7 +271,8 @@ class PagedCache:
         cfg = Config(self.q_heads, self.kv_heads, self.head_dim, self.page_size, pages,
                      self.max_requests, TYPES[k.dtype], 0)
         self._append, self._attend = lib.moe_reader_kv_append, lib.moe_reader_kv_attend
-        self._select = lib.moe_reader_kv_select
+        self._chunk = lib.moe_reader_kv_chunk
+        self._select, self._copy = lib.moe_reader_kv_select, lib.moe_reader_kv_copy
         h = ctypes.c_void_p()
         at = _current(self.device) if stream is None else _handle(stream)
         _check(lib.moe_reader_kv_create(ctypes.byref(cfg), k.data_ptr(), v.data_ptr(), *ptr, at,
@@ -219,6 +302,24 @@ class PagedCache:
         """A PagePlan over table (int32 [requests][width], updated in place)
         for steps of at most max_tokens new tokens."""
         return PagePlan(self, table, max_tokens)
+
+    def pool(self, max_forks=0):
+        """A PagePool over this cache's pages, for calls of at most max_forks
+        forks."""
+        return PagePool(self, max_forks)
+
+    def copy_pages(self, src, dst, count=None, stream=None):
+        """Copy whole pages, keys, values and summaries: page src[i] to page
+        dst[i] (int32 [n], -1 skips; a page stands once in dst at most and not
+        in src too).  count (int32 [1]): only the first count[0] of them."""
+        n = _length(src, "src")
+        s = _whole(src, _I32, (n,), "src", self.device)
+        d = _whole(dst, _I32, (n,), "dst", self.device)
+        c = 0 if count is None else _whole(count, _I32, (1,), "count", self.device)
+        code = self._copy(self._h, _COPY.pack(s, d, c, n),
+                          _current(self.device) if stream is None else _handle(stream))
+        if code:
+            _check(code, "moe_reader_kv_copy")
 
     def append(self, k, v, slots, stream=None):
         """Write rows k, v ([tokens][kv_heads][head_dim], rows contiguous,
@@ -262,6 +363,32 @@ class PagedCache:
         code = self._attend(self._h, args, _current(dev) if stream is None else _handle(stream))
         if code:
             _check(code, "moe_reader_kv_attend")
+
+    def attend_chunk(self, q, table, lens, starts, out, scale=None, window=0, sinks=None, lse=None,
+                     stream=None):
+        """Attention of several new tokens per request, already appended: q,
+        out [T][q_heads][head_dim], table int32 [>= R][width], lens int32 [R],
+        starts int32 [R + 1] (a request's first row of q, as ``PagePlan.update``
+        writes them; the rows are the last of its lens[r] tokens, and each sees
+        itself and those before).  Rows outside of starts are left alone.  scale,
+        window, sinks as for ``attend``; lse float32 [T][q_heads]."""
+        T, R, dev = _length(q, "q"), _length(lens, "lens"), self.device
+        shape = (T, self.q_heads, self.head_dim)
+        qp, s, qt = self._rows(q, "q", shape)
+        o = _whole(out, q.dtype, shape, "out", dev)
+        tab, width = _table(table, R, dev)
+        ln = _whole(lens, _I32, (R,), "lens", dev)
+        st = _whole(starts, _I32, (R + 1,), "starts", dev)
+        sk = ls = 0
+        if sinks is not None:
+            sk = _whole(sinks, torch.float32, (self.q_heads,), "sinks", dev)
+        if lse is not None:
+            ls = _whole(lse, torch.float32, (T, self.q_heads), "lse", dev)
+        args = _CHUNK.pack(qp, tab, ln, st, sk, o, ls, s[0], s[1], qt, R, T, width, window,
+                           self._scale if scale is None else scale)
+        code = self._chunk(self._h, args, _current(dev) if stream is None else _handle(stream))
+        if code:
+            _check(code, "moe_reader_kv_chunk")
 
     def select(self, q, table, lens, pages, first=1, last=1, stream=None):
         """Choose pages.shape[2] pages per request and KV head by the page

@@ -55,6 +55,46 @@ int attend_row_tiles(const moe_reader_kv_config& c);
 cudaError_t launch_kv_select(const moe_reader_kv& kv, const moe_reader_kv_select_args& a,
                              cudaStream_t s);
 cudaError_t configure_kv_select(const moe_reader_kv& kv);
+cudaError_t launch_kv_chunk(const moe_reader_kv& kv, const moe_reader_kv_chunk_args& a,
+                            cudaStream_t s);
+cudaError_t launch_kv_collect(const moe_reader_kv& kv, const moe_reader_kv_pages_args& a,
+                              cudaStream_t s);
+cudaError_t launch_kv_compact(const moe_reader_kv& kv, const moe_reader_kv_pages_args& a,
+                              cudaStream_t s);
+cudaError_t launch_kv_fork(const moe_reader_kv& kv, const moe_reader_kv_fork_args& a,
+                           cudaStream_t s);
+cudaError_t launch_kv_copy(const moe_reader_kv& kv, const moe_reader_kv_copy_args& a,
+                           cudaStream_t s);
+cudaError_t configure_kv_pages();
+
+// An array of 32-bit words.
+struct Words {
+  const int32_t* at;
+  long long count;
+};
+inline bool share_a_word(const Words& a, const Words& b) {
+  if (a.count == 0 || b.count == 0) return false;
+  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a.at), b0 = reinterpret_cast<uintptr_t>(b.at);
+  return a0 < b0 + 4 * b.count && b0 < a0 + 4 * a.count;
+}
+
+// Rows and queries have the cache's type; an 8-bit cache takes either 16-bit one.
+inline bool type_fits(int cache, int type) {
+  if (cache == MOE_READER_TYPE_E4M3)
+    return type == MOE_READER_TYPE_BF16 || type == MOE_READER_TYPE_F16;
+  return type == cache;
+}
+
+inline int status_of(cudaError_t e) {
+  if (e == cudaSuccess) return MOE_READER_OK;
+  return e == cudaErrorMemoryAllocation ? MOE_READER_ENOMEM : MOE_READER_ECUDA;
+}
+
+// Launches go to the calling thread's device: it has to be the handle's.
+inline bool on_device(const moe_reader_kv* kv) {
+  int dev = -1;
+  return cudaGetDevice(&dev) == cudaSuccess && dev == kv->device;
+}
 
 // Launch that may start while the stream's previous kernel ends: it has to
 // call wait_for_earlier_launch() before it touches global memory, which returns

@@ -713,12 +713,13 @@ cudaError_t launch_kv_append(const moe_reader_kv& kv, const moe_reader_kv_append
 // ---------------------------------------------------------------------------
 namespace {
 
-bool at_multiple(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+using mr::on_device;
+using mr::share_a_word;
+using mr::status_of;
+using mr::type_fits;
+using mr::Words;
 
-int status_of(cudaError_t e) {
-  if (e == cudaSuccess) return MOE_READER_OK;
-  return e == cudaErrorMemoryAllocation ? MOE_READER_ENOMEM : MOE_READER_ECUDA;
-}
+bool at_multiple(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 
 int check_kv_config(const moe_reader_kv_config* c) {
   if (!c || c->flags != 0) return MOE_READER_EINVAL;
@@ -735,30 +736,6 @@ int check_kv_config(const moe_reader_kv_config* c) {
       c->cache_type != MOE_READER_TYPE_E4M3)
     return MOE_READER_EINVAL;
   return MOE_READER_OK;
-}
-
-// Rows and queries have the cache's type; an 8-bit cache takes either 16-bit one.
-bool type_fits(int cache, int type) {
-  if (cache == MOE_READER_TYPE_E4M3)
-    return type == MOE_READER_TYPE_BF16 || type == MOE_READER_TYPE_F16;
-  return type == cache;
-}
-
-// An array of 32-bit words.
-struct Words {
-  const int32_t* at;
-  long long count;
-};
-bool share_a_word(const Words& a, const Words& b) {
-  if (a.count == 0 || b.count == 0) return false;
-  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a.at), b0 = reinterpret_cast<uintptr_t>(b.at);
-  return a0 < b0 + 4 * b.count && b0 < a0 + 4 * a.count;
-}
-
-// Launches go to the calling thread's device: it has to be the handle's.
-bool on_device(const moe_reader_kv* kv) {
-  int dev = -1;
-  return cudaGetDevice(&dev) == cudaSuccess && dev == kv->device;
 }
 
 }  // namespace
@@ -814,6 +791,7 @@ int moe_reader_kv_create(const moe_reader_kv_config* cfg, void* k, void* v, int8
     kv->sms = std::min(kv->sms, mr::kMaxSms);
     if ((ce = mr::configure_kv_attend(*kv)) != cudaSuccess) break;
     if ((ce = mr::configure_kv_select(*kv)) != cudaSuccess) break;
+    if ((ce = mr::configure_kv_pages()) != cudaSuccess) break;
     if ((ce = cudaMemsetAsync(kv->base, 0, bytes, s)) != cudaSuccess) break;
     ce = cudaStreamSynchronize(s);
   } while (0);

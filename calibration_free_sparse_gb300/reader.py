@@ -37,6 +37,10 @@ EXPORTED_SYMBOLS = (
     "moe_reader_set_wait_limit", "moe_reader_inject_fault",
     "moe_reader_kv_create", "moe_reader_kv_plan", "moe_reader_kv_append", "moe_reader_kv_attend",
     "moe_reader_kv_select", "moe_reader_kv_status", "moe_reader_kv_destroy",
+    "moe_reader_kv_chunk", "moe_reader_kv_collect", "moe_reader_kv_compact", "moe_reader_kv_fork",
+    "moe_reader_kv_copy", "moe_reader_experts_create", "moe_reader_experts_plan",
+    "moe_reader_experts_activate", "moe_reader_experts_combine", "moe_reader_experts_status",
+    "moe_reader_experts_destroy",
     "moe_reader_residual_norm",
 )
 PHASES = ("decode", "screen", "score_topk", "exact", "out")
@@ -123,16 +127,25 @@ def _lib():
         # the decode-step calls take packed argument structs (block.py)
         lib.moe_reader_kv_create.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, ctypes.POINTER(vp)]
         lib.moe_reader_kv_create.restype = ctypes.c_int
-        for name in ("plan", "append", "attend", "select"):
-            fn = getattr(lib, "moe_reader_kv_" + name)
+        lib.moe_reader_experts_create.argtypes = [vp, vp, vp, vp, vp, ctypes.POINTER(vp)]
+        lib.moe_reader_experts_create.restype = ctypes.c_int
+        lib.moe_reader_experts_status.argtypes = [vp, ctypes.POINTER(ctypes.c_uint32)]
+        lib.moe_reader_experts_status.restype = ctypes.c_int
+        lib.moe_reader_experts_destroy.argtypes = [vp]
+        lib.moe_reader_experts_destroy.restype = None
+        for name in ("kv_plan", "kv_append", "kv_attend", "kv_select", "kv_chunk", "kv_collect",
+                     "kv_compact", "kv_fork", "kv_copy", "experts_activate", "experts_combine"):
+            fn = getattr(lib, "moe_reader_" + name)
             fn.argtypes = [vp, ctypes.c_char_p, vp]
             fn.restype = ctypes.c_int
         lib.moe_reader_kv_status.argtypes = [vp, ctypes.POINTER(ctypes.c_uint32)]
         lib.moe_reader_kv_status.restype = ctypes.c_int
         lib.moe_reader_kv_destroy.argtypes = [vp]
         lib.moe_reader_kv_destroy.restype = None
-        lib.moe_reader_residual_norm.argtypes = [ctypes.c_char_p, vp]
-        lib.moe_reader_residual_norm.restype = ctypes.c_int
+        for name in ("residual_norm", "experts_plan"):
+            fn = getattr(lib, "moe_reader_" + name)
+            fn.argtypes = [ctypes.c_char_p, vp]
+            fn.restype = ctypes.c_int
         lib.moe_reader_abi_version.argtypes = []
         lib.moe_reader_abi_version.restype = ctypes.c_int
         _LIB = lib

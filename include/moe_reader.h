@@ -427,7 +427,8 @@ void moe_reader_destroy(moe_reader_t* h);
 /* Device error bits reported by moe_reader_kv_status(). */
 #define MOE_READER_ERR_LENGTH  0x20u  /* a length negative or above the table, or too many tokens */
 #define MOE_READER_ERR_PAGE    0x40u  /* a page, slot or selected page out of range (skipped) */
-#define MOE_READER_ERR_POOL    0x80u  /* fewer free pages than the plan needs */
+#define MOE_READER_ERR_POOL    0x80u  /* fewer free pages than the plan or the forks need */
+#define MOE_READER_ERR_ROW     0x100u /* a fork's row out of range or in use by another fork */
 
 typedef struct moe_reader_kv moe_reader_kv_t;   /* opaque handle of one layer's cache */
 
@@ -590,6 +591,56 @@ typedef struct {
 int moe_reader_kv_attend(moe_reader_kv_t* kv, const moe_reader_kv_attend_args* a, void* stream);
 
 /*
+ * moe_reader_kv_chunk -- attention of several new tokens per request over its
+ * cached tokens (a prompt, a chunk of one, drafted tokens): the new tokens'
+ * keys and values are in the cache already, and each sees those before it.
+ * Asynchronous; one launch, deterministic.
+ *
+ * Request r has new tokens starts[r] .. starts[r + 1] - 1, the last ones of its
+ * lens[r]; with p = lens[r] - (starts[r + 1] - t) the position of row t,
+ *   s_j = scale * q_t . k_j,  j in [max(0, p + 1 - window), p]  (window 0: all)
+ *   out = sum_j exp(s_j) v_j / (sum_j exp(s_j) + exp(sink))
+ *
+ *   q        dev, [tokens][Hq][D] of q_type (the cache's type; BF16 or F16 for
+ *            an E4M3 cache), D contiguous, strides in elements.
+ *   table    dev, int32 [requests][width];  lens dev, int32 [requests].
+ *   starts   dev, int32 [requests + 1], ascending, as moe_reader_kv_plan writes
+ *            them.  Rows outside [starts[0], starts[requests]) are left alone.
+ *   sinks    dev, fp32 [Hq] or NULL.
+ *   out      dev, [tokens][Hq][D] of q_type, contiguous, 16-byte aligned; may
+ *            not overlap the span of q.
+ *   lse      dev, fp32 [tokens][Hq] or NULL: log of the denominator.
+ *
+ * A row with nothing to attend to is zeros, its lse the sink or -infinity; a
+ * logit of NaN makes the head's row and its lse NaN.  What a row does not see
+ * (later tokens, rows behind the last one) does not touch it, whatever it
+ * holds.  Logits, references and sums are fp32; the weights enter the product
+ * with V as values of q_type.  A V of infinity makes its coordinate infinite,
+ * unless the key's weight is 0.
+ * A negative length counts as 0, starts are cut to [0, tokens], a request with
+ * fewer tokens than new ones has rows of nothing in front, and keys beyond the
+ * table do not exist (all ERR_LENGTH); a page that is not in the pool is skipped
+ * (ERR_PAGE).  EINVAL where width * page_size >= 2^30 or tokens * Hq >= 2^31.
+ */
+typedef struct {
+  const void* q;
+  const int32_t* table;
+  const int32_t* lens;
+  const int32_t* starts;
+  const float* sinks;
+  void* out;
+  float* lse;
+  int64_t q_token_stride, q_head_stride;
+  int32_t q_type;
+  int32_t requests;
+  int32_t tokens;           /* rows of q and out */
+  int32_t width;
+  int32_t window;           /* >= 0 */
+  float scale;
+} moe_reader_kv_chunk_args;
+int moe_reader_kv_chunk(moe_reader_kv_t* kv, const moe_reader_kv_chunk_args* a, void* stream);
+
+/*
  * moe_reader_kv_select -- choose `keep` pages per request and KV head for
  * moe_reader_kv_attend by a score of their summaries (the reader's screen,
  * applied to attention).  Asynchronous; one launch.
@@ -625,6 +676,108 @@ typedef struct {
   int32_t first, last;      /* >= 0 */
 } moe_reader_kv_select_args;
 int moe_reader_kv_select(moe_reader_kv_t* kv, const moe_reader_kv_select_args* a, void* stream);
+
+/*
+ * moe_reader_kv_collect -- which pages the requests hold: a page is free when
+ * no request's table row holds it, so a request is freed by setting its length
+ * to 0.  Asynchronous; one launch.
+ *
+ *   table       dev, int32 [requests][width];  lens dev, int32 [requests].
+ *               Request r holds the first ceil(lens[r] / page_size) entries of
+ *               its row; several rows may hold one page (moe_reader_kv_fork).
+ *   refs        dev, int32 [num_pages]: entries that hold each page.
+ *   free_pages  dev, int32 [num_pages]: the pages without any, ascending, -1
+ *               behind the last one (what moe_reader_kv_plan takes from).
+ *   count       dev, int32 [1]: how many they are.
+ *   src, dst, moves  NULL.
+ *
+ * moe_reader_kv_compact -- the same, and the pages in use moved to the front
+ * of the pool: with n of them, the k-th one at or behind page n goes to the
+ * k-th free page before it, both ascending, so that the fewest pages move.
+ *
+ *   table       renumbered in place.  refs, free_pages, count: as they are
+ *               after the moves (pages n and up are free).
+ *   src, dst    dev, int32 [num_pages / 2]: the moves, -1 behind the last one,
+ *               for one moe_reader_kv_copy per layer whose cache this table
+ *               is for.
+ *   moves       dev, int32 [1]: how many they are.
+ *
+ * No output may overlap an input or another output (EINVAL).  A negative
+ * length counts as 0, one beyond the table is cut (ERR_LENGTH); an entry that
+ * is not in the pool is passed over (ERR_PAGE).
+ */
+typedef struct {
+  int32_t* table;
+  const int32_t* lens;
+  int32_t* refs;
+  int32_t* free_pages;
+  int32_t* count;
+  int32_t* src;
+  int32_t* dst;
+  int32_t* moves;
+  int32_t requests;         /* 0..max_requests */
+  int32_t width;            /* pages per table row, >= 1 */
+} moe_reader_kv_pages_args;
+int moe_reader_kv_collect(moe_reader_kv_t* kv, const moe_reader_kv_pages_args* a, void* stream);
+int moe_reader_kv_compact(moe_reader_kv_t* kv, const moe_reader_kv_pages_args* a, void* stream);
+
+/*
+ * moe_reader_kv_fork -- continue requests in several ways: row children[i]
+ * gets the tokens of row parents[i].  It shares the parent's full pages; a
+ * last page that is not full becomes a fresh one from free_pages, in order of
+ * i, and a copy of the parent's (src, dst: one moe_reader_kv_copy per layer).
+ * Asynchronous; one launch.
+ *
+ *   parents, children  dev, int32 [forks]: rows of the table.  A parent may
+ *               stand several times, a child once, and no child is a parent:
+ *               forks that break this do nothing (of equal children all but
+ *               the first), and neither do rows out of range (ERR_ROW).
+ *   table       dev, int32 [rows][width]: the children's first entries are
+ *               overwritten, the others left alone.
+ *   lens        dev, int32 [rows]: the children's become their parents'.
+ *   free_pages  dev, int32 [num_free].
+ *   src, dst    dev, int32 [forks]: fork i's copy, or -1.
+ *   taken       dev, int32 [1]: free pages used, from the front.
+ *
+ * No output may overlap an input or another output (EINVAL).  A parent's
+ * length is cut as in moe_reader_kv_collect (ERR_LENGTH); a fresh page that
+ * free_pages does not have, or that is not in the pool, is -1 in the table
+ * (ERR_POOL); a last page that is not in the pool is not copied (ERR_PAGE).
+ */
+typedef struct {
+  const int32_t* parents;
+  const int32_t* children;
+  int32_t* table;
+  int32_t* lens;
+  const int32_t* free_pages;
+  int32_t* src;
+  int32_t* dst;
+  int32_t* taken;
+  int32_t forks;            /* 0..max_requests */
+  int32_t rows;             /* 0..max_requests */
+  int32_t width;            /* pages per table row, >= 1 */
+  int32_t num_free;
+} moe_reader_kv_fork_args;
+int moe_reader_kv_fork(moe_reader_kv_t* kv, const moe_reader_kv_fork_args* a, void* stream);
+
+/*
+ * moe_reader_kv_copy -- copy whole pages of this layer's cache, keys, values
+ * and summaries: page src[i] to page dst[i].  Asynchronous; one launch.
+ *
+ *   src, dst  dev, int32 [pages]; where either is -1, or both are equal,
+ *             nothing is copied.  A page stands once in dst at most, and not in
+ *             src too (as the calls above write them).
+ *   count     dev, int32 [1] or NULL: only the first count[0] are copied.
+ *
+ * A page that is not in the pool is skipped (ERR_PAGE).
+ */
+typedef struct {
+  const int32_t* src;
+  const int32_t* dst;
+  const int32_t* count;
+  int32_t pages;
+} moe_reader_kv_copy_args;
+int moe_reader_kv_copy(moe_reader_kv_t* kv, const moe_reader_kv_copy_args* a, void* stream);
 
 /* moe_reader_kv_status -- synchronize the handle's device (a captured call runs
  * on whichever stream replays it), read and clear the device error word: calls
@@ -678,6 +831,127 @@ typedef struct {
   float scale, eps;
 } moe_reader_residual_norm_args;
 int moe_reader_residual_norm(const moe_reader_residual_norm_args* a, void* stream);
+
+/* ------------------------------------------------------------------------
+ * A prompt's experts.  The reader decodes few tokens by reading few channels;
+ * a prompt's tokens want nearly all of them, and their experts are dense
+ * products grouped by expert.  With pairs (token t, slot s) numbered t * topk
+ * + s and sorted by expert, row j of `act` belongs to pair order[j]:
+ *
+ *   act_j = silu(G_e x_t) * (V_e x_t)                e = ids[t][s]
+ *   y_t   = sum_s w_ts D_e act_(places[t][s])        (slots in order)
+ * ------------------------------------------------------------------------ */
+typedef struct moe_reader_experts moe_reader_experts_t;   /* opaque handle of one layer's experts */
+
+typedef struct {
+  int32_t hidden;             /* H: a multiple of 8, 8..65536 */
+  int32_t inter;              /* I: a multiple of 8, 8..65536 */
+  int32_t num_experts;        /* E: 1..1024 */
+  int32_t type;               /* MOE_READER_TYPE_BF16 or _F16: weights, x and act */
+  int32_t flags;              /* 0 */
+} moe_reader_experts_config;
+
+/*
+ * moe_reader_experts_create -- a handle on one layer's expert weights.
+ *
+ *   gate, up  dev, [E][I][H] of type, 16-byte aligned (as moe_reader_prepare
+ *             takes them), or both NULL: no activate.
+ *   down      dev, [E][H][I] of type, 16-byte aligned, or NULL: no combine.
+ *
+ * They are the caller's and must outlive the handle, which owns an error word
+ * only.  The calling thread's current device has to be the handle's in every
+ * call (EINVAL).  Errors: EINVAL, ENOMEM, ECUDA.
+ */
+int moe_reader_experts_create(const moe_reader_experts_config* cfg, const void* gate,
+                              const void* up, const void* down, void* stream,
+                              moe_reader_experts_t** out);
+
+/*
+ * moe_reader_experts_plan -- sort a batch's pairs by expert (stable: those of
+ * an expert ascend).  Asynchronous; one launch.
+ *
+ *   ids      dev, int32 [tokens][topk].  An id outside [0, E) belongs to no
+ *            expert: its pair has no row, place -1 and adds nothing to y.
+ *   order    dev, int32 [tokens * topk]: the pair of each row, -1 behind the
+ *            last.
+ *   offsets  dev, int32 [E + 1]: each expert's first row; offsets[E] rows in all.
+ *   places   dev, int32 [tokens][topk]: each pair's row, or -1.
+ *   skipped  dev, int32 [1]: pairs without an expert.
+ * No output may overlap ids or another output (EINVAL).
+ */
+typedef struct {
+  const int32_t* ids;
+  int32_t* order;
+  int32_t* offsets;
+  int32_t* places;
+  int32_t* skipped;
+  int32_t tokens;             /* tokens * topk < 2^30 */
+  int32_t experts_per_token;  /* topk, 1..64 */
+  int32_t num_experts;
+} moe_reader_experts_plan_args;
+int moe_reader_experts_plan(const moe_reader_experts_plan_args* a, void* stream);
+
+/*
+ * moe_reader_experts_activate -- the gated activations of every row of a plan.
+ * Asynchronous; one launch, deterministic.
+ *
+ *   x               dev, [tokens][H] of type, 16-byte aligned; the row stride
+ *                   (in elements) is a multiple of 8.
+ *   order, offsets  dev, as moe_reader_experts_plan writes them.
+ *   act             dev, [tokens * topk][I] of type, contiguous, 16-byte
+ *                   aligned, apart from all inputs.  Rows behind the last are
+ *                   left alone.
+ * Sums are fp32, silu and the product too; one rounding, on the way out.
+ */
+typedef struct {
+  const void* x;
+  const int32_t* order;
+  const int32_t* offsets;
+  void* act;
+  int64_t x_stride;
+  int32_t tokens;
+  int32_t experts_per_token;
+} moe_reader_experts_activate_args;
+int moe_reader_experts_activate(moe_reader_experts_t* h, const moe_reader_experts_activate_args* a,
+                                void* stream);
+
+/*
+ * moe_reader_experts_combine -- the down products of every row, weighted and
+ * summed per token.  Asynchronous; two launches, deterministic.
+ *
+ *   act              dev, [tokens * topk][I] of type, contiguous, 16-byte aligned.
+ *   offsets, places  dev, as moe_reader_experts_plan writes them.
+ *   weights          dev, fp32 [tokens][topk].
+ *   slots            dev, fp32 [tokens * topk][H], 16-byte aligned: scratch (the
+ *                    rows' products; layers may share it).
+ *   y                dev, [tokens][H] of y_type (F32, BF16 or F16), 16-byte
+ *                    aligned; the row stride is a multiple of 8, rows apart.
+ * slots and y may not overlap an input or one another (EINVAL).  Sums are fp32,
+ * over the slots in order; one rounding, on the way out.  A token whose pairs
+ * have no row gets zeros.
+ */
+typedef struct {
+  const void* act;
+  const int32_t* offsets;
+  const int32_t* places;
+  const float* weights;
+  float* slots;
+  void* y;
+  int64_t y_stride;
+  int32_t tokens;
+  int32_t experts_per_token;
+  int32_t y_type;
+} moe_reader_experts_combine_args;
+int moe_reader_experts_combine(moe_reader_experts_t* h, const moe_reader_experts_combine_args* a,
+                               void* stream);
+
+/* moe_reader_experts_status -- as moe_reader_kv_status: synchronizes the
+ * device, reads and clears the handle's error word. */
+int moe_reader_experts_status(moe_reader_experts_t* h, uint32_t* bits);
+
+/* moe_reader_experts_destroy -- free the handle (NULL is a no-op).
+ * Synchronizes the handle's device first. */
+void moe_reader_experts_destroy(moe_reader_experts_t* h);
 
 /* moe_reader_strerror -- static text of a status code. */
 const char* moe_reader_strerror(int code);
