@@ -7,6 +7,7 @@
 #include "device_util.cuh"
 #include "internal.cuh"
 #include "moe_reader.h"
+#include "tc.cuh"
 
 struct moe_reader_experts {
   moe_reader_experts_config cfg;
@@ -15,6 +16,7 @@ struct moe_reader_experts {
   const void* gate;          // caller-owned [E][I][H]
   const void* up;
   const void* down;          // caller-owned [E][H][I]
+  CUtensorMap gate_map, up_map, down_map;
   uint32_t* err;             // [1] device error word
 };
 
@@ -92,106 +94,384 @@ experts_plan_kernel(moe_reader_experts_plan_args a) {
 // ---------------------------------------------------------------------------
 // products
 // ---------------------------------------------------------------------------
-template <int T> __device__ __forceinline__ float wide(const void* p, long long i) {
-  if constexpr (T == MOE_READER_TYPE_BF16)
-    return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
-  else if constexpr (T == MOE_READER_TYPE_F16)
-    return __half2float(static_cast<const __half*>(p)[i]);
-  else
-    return static_cast<const float*>(p)[i];
-}
-template <int T> __device__ __forceinline__ void put(void* p, long long i, float v) {
-  if constexpr (T == MOE_READER_TYPE_BF16)
-    static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
-  else if constexpr (T == MOE_READER_TYPE_F16)
-    static_cast<__half*>(p)[i] = __float2half_rn(v);
-  else
-    static_cast<float*>(p)[i] = v;
-}
+// The weights' rows lie on the tensor core's 128 rows and the plan's rows on
+// its columns, of which a product may have any multiple of 16: ragged numbers
+// of rows cost few columns of nothing, and an expert with three tokens is read
+// at the speed of its weights.  A tile is 2 x 128 weight rows (gate and up of
+// 128 channels; 256 channels of down) by up to N plan rows; a persistent CTA per SM
+// takes tiles in turn.  One warp brings weights by tensor copies, four gather
+// the plan rows' inputs by 16-byte copies (a token's row stands wherever the
+// caller has it), one issues the products, eight write a finished tile out while
+// the next one is summed (two sets of accumulators where they fit).
+constexpr int kGroupThreads = 512;
+constexpr int kBoxBytes = 128 * 128;          // 128 weight rows of 64 values
 
-__device__ __forceinline__ int expert_of(const int32_t* offsets, int E, int row) {
-  int lo = 0, hi = E;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (__ldg(offsets + mid) <= row) lo = mid; else hi = mid - 1;
+template <int N> struct GroupShape {
+  static constexpr int kStageBytes = 2 * kBoxBytes + N * 128;
+  static constexpr int kStages = N >= 256 ? 3 : N >= 128 ? 4 : N >= 64 ? 5 : 6;
+  static constexpr int kLag = kStages > 3 ? 2 : 1;     // copies under way behind the newest
+  static constexpr int kSets = N <= 128 ? 2 : 1;       // sets of accumulators
+  static constexpr size_t kSmem = (size_t)kStages * kStageBytes + 1024;
+};
+
+struct GroupArgs {
+  const char* in;            // rows of the right operand
+  long long in_stride;       // bytes
+  const int32_t* order;      // the pair of each row (in = token rows), or null (in = plan rows)
+  const int32_t* offsets;
+  void* out;                 // act, or slots
+  int experts, k, channels;  // channels: I, or H
+  int pairs, topk;
+};
+
+template <int N, bool kBf16, bool kAct>
+__global__ void __launch_bounds__(kGroupThreads, 1)
+group_kernel(const __grid_constant__ CUtensorMap map0, const __grid_constant__ CUtensorMap map1,
+             GroupArgs a, uint32_t* err) {
+  using S = GroupShape<N>;
+  extern __shared__ char raw[];
+  __shared__ int s_first[kMaxExperts + 1], s_tiles[kMaxExperts + 1];
+  __shared__ uint64_t s_bar[3 * S::kStages + 2 * S::kSets + 1];
+  __shared__ uint32_t s_tmem;
+  __shared__ volatile uint32_t s_quit;
+  const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+  const uint32_t base = (tc::smem_at(raw) + 1023) & ~1023u, bars = tc::smem_at(s_bar);
+  auto stage_at = [&](int s) { return base + s * S::kStageBytes; };
+  auto weights_in = [&](int s) { return bars + 8 * s; };
+  auto rows_in = [&](int s) { return bars + 8 * (S::kStages + s); };
+  auto stage_free = [&](int s) { return bars + 8 * (2 * S::kStages + s); };
+  auto sums_done = [&](int s) { return bars + 8 * (3 * S::kStages + s); };
+  auto sums_free = [&](int s) { return bars + 8 * (3 * S::kStages + S::kSets + s); };
+  const uint32_t drained = bars + 8 * (3 * S::kStages + 2 * S::kSets);
+
+  // the experts' first rows and tiles
+  for (int e = tid; e <= a.experts; e += kGroupThreads)
+    s_first[e] = min(max(__ldg(a.offsets + e), 0), a.pairs);
+  if (tid == 0) {
+    for (int s = 0; s < S::kStages; ++s) {
+      tc::bar_init(weights_in(s), 1);
+      tc::bar_init(rows_in(s), 128);
+      tc::bar_init(stage_free(s), 1);
+    }
+    for (int s = 0; s < S::kSets; ++s) {
+      tc::bar_init(sums_done(s), 1);
+      tc::bar_init(sums_free(s), 256);
+    }
+    tc::bar_init(drained, 1);
+    s_quit = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  return lo;
-}
-
-constexpr int kChannels = 256;
-
-template <int T>
-__global__ void __launch_bounds__(kChannels)
-activate_kernel(moe_reader_experts_activate_args a, const void* gate, const void* up, int H, int I,
-                int E, int topk) {
-  const int row = blockIdx.x, ch = blockIdx.y * kChannels + threadIdx.x;
-  const int e = expert_of(a.offsets, E, row), pair = __ldg(a.order + row);
-  if (e >= E || pair < 0 || pair >= (long long)a.tokens * topk || ch >= I) return;
-  const long long x = (long long)(pair / topk) * a.x_stride, w = ((long long)e * I + ch) * H;
-  float g = 0.f, v = 0.f;
-  for (int i = 0; i < H; ++i) {
-    const float xi = wide<T>(a.x, x + i);
-    g += xi * wide<T>(gate, w + i);
-    v += xi * wide<T>(up, w + i);
+  if (wid == 1) tc::tmem_alloc(tc::smem_at(&s_tmem), 512);
+  __syncthreads();
+  const int per_tile = kAct ? 128 : 256;
+  const int m_tiles = (a.channels + per_tile - 1) / per_tile;
+  if (wid == 0) {
+    int sum = 0;
+    for (int e0 = 0; e0 <= a.experts; e0 += 32) {
+      const int e = e0 + lane;
+      int n = 0;
+      if (e < a.experts) n = (max(s_first[e + 1] - s_first[e], 0) + N - 1) / N * m_tiles;
+      int at = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, at, o);
+        if (lane >= o) at += u;
+      }
+      if (e <= a.experts) s_tiles[e] = sum + at - n;
+      sum += __shfl_sync(0xffffffffu, at, 31);
+    }
   }
-  put<T>(a.act, (long long)row * I + ch, silu_f(g) * v);
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  const uint32_t tmem = s_tmem;
+  const int tiles = s_tiles[a.experts];
+  const int k_steps = (a.k + 63) / 64;
+
+  struct Tile {
+    int expert, m, first, rows;      // weight tile, first plan row and number of them
+  };
+  auto tile_at = [&](int t) {
+    int lo = 0, hi = a.experts - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (s_tiles[mid] <= t) lo = mid; else hi = mid - 1;
+    }
+    const int all = s_first[lo + 1] - s_first[lo], n_tiles = (all + N - 1) / N;
+    const int at = t - s_tiles[lo], n = at % n_tiles;
+    return Tile{lo, at / n_tiles, s_first[lo] + n * N, min(N, all - n * N)};
+  };
+
+  if (wid == 0) {
+    // weights
+    int s = 0, used = 0;
+    uint32_t phase = 1;
+    if (lane == 0) {
+      for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
+        const Tile x = tile_at(t);
+        for (int k = 0; k < k_steps; ++k) {
+          if (!tc::bar_wait(stage_free(s), phase, &s_quit)) goto weights_end;
+          tc::bar_expect(weights_in(s), 2 * kBoxBytes);
+          tc::load_box(stage_at(s), &map0, k * 64, x.m * per_tile, x.expert, weights_in(s));
+          tc::load_box(stage_at(s) + kBoxBytes, &map1, k * 64,
+                       x.m * per_tile + (kAct ? 0 : 128), x.expert, weights_in(s));
+          used++;
+          if (++s == S::kStages) s = 0, phase ^= 1;
+        }
+      }
+    weights_end:
+      // no copy is left under way
+      for (int i = 0; i < min(used, S::kStages); ++i) {
+        if (--s < 0) s = S::kStages - 1, phase ^= 1;
+        volatile uint32_t ignore = 0;
+        tc::bar_wait(weights_in(s), phase ^ 1, &ignore);
+      }
+    }
+    __syncwarp();
+  } else if (wid == 1) {
+    // products
+    if (lane == 0) {
+      int s = 0, set = 0;
+      uint32_t phase = 0, set_phase = 1;
+      bool go = true;
+      for (int t = blockIdx.x; go && t < tiles; t += gridDim.x) {
+        const Tile x = tile_at(t);
+        const uint32_t idesc = tc::instr<kBf16>((x.rows + 15) & ~15);
+        const uint32_t d = tmem + set * 2 * N;
+        if (!(go = tc::bar_wait(sums_free(set), set_phase, &s_quit))) break;
+        tc::fence_after();
+        for (int k = 0; k < k_steps; ++k) {
+          if (!(go = tc::bar_wait(weights_in(s), phase, &s_quit) &&
+                     tc::bar_wait(rows_in(s), phase, &s_quit)))
+            break;
+          tc::fence_after();
+          const uint64_t a0 = tc::desc_k(stage_at(s)), a1 = tc::desc_k(stage_at(s) + kBoxBytes);
+          const uint64_t b = tc::desc_k(stage_at(s) + 2 * kBoxBytes);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            tc::mma(d, a0 + 2 * i, b + 2 * i, idesc, k + i > 0);
+            tc::mma(d + N, a1 + 2 * i, b + 2 * i, idesc, k + i > 0);
+          }
+          tc::commit(stage_free(s));
+          if (++s == S::kStages) s = 0, phase ^= 1;
+        }
+        if (!go) break;
+        tc::commit(sums_done(set));
+        if (++set == S::kSets) set = 0, set_phase ^= 1;
+      }
+      tc::commit(drained);
+      volatile uint32_t ignore = 0;
+      tc::bar_wait(drained, 0, &ignore);
+    }
+    __syncwarp();
+  } else if (wid >= 4 && wid < 8) {
+    // the plan rows' inputs: eight threads a row of 128 bytes, 16 rows at once
+    const int id = tid - 128, piece = id & 7, sub = id >> 3;
+    int s = 0, late = 0, behind = 0;       // `late`: oldest stage not yet handed over
+    uint32_t phase = 1;
+    for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
+      const Tile x = tile_at(t);
+      const int n16 = (x.rows + 15) & ~15;
+      const char* from[N / 16];
+      uint32_t in = 0;
+#pragma unroll
+      for (int i = 0; i < N / 16; ++i) {
+        const int r = i * 16 + sub;
+        long long at = 0;
+        if (r < x.rows) {
+          int row = x.first + r;
+          if (kAct) {
+            row = __ldg(a.order + row);
+            if ((unsigned)row < (unsigned)a.pairs) in |= 1u << i, at = row / a.topk;
+          } else {
+            in |= 1u << i;
+            at = row;
+          }
+        }
+        from[i] = a.in + at * a.in_stride + piece * 16;
+      }
+      for (int k = 0; k < k_steps; ++k) {
+        if (!tc::bar_wait(stage_free(s), phase, &s_quit)) goto rows_end;
+        const uint32_t to = stage_at(s) + 2 * kBoxBytes + tc::swizzled(sub, piece);
+        const bool k_in = k * 64 + piece * 8 < a.k;
+#pragma unroll
+        for (int i = 0; i < N / 16; ++i)
+          if (i * 16 < n16) {
+            const bool there = k_in && (in >> i & 1);
+            tc::copy16(to + i * 2048, there ? from[i] + k * 128 : a.in, there);
+          }
+        tc::copies_commit();
+        if (behind == S::kLag) {
+          tc::copies_wait<S::kLag>();
+          tc::publish_smem();
+          tc::bar_arrive(rows_in(late));
+          if (++late == S::kStages) late = 0;
+        } else {
+          behind++;
+        }
+        if (++s == S::kStages) s = 0, phase ^= 1;
+      }
+    }
+  rows_end:
+    tc::copies_wait<0>();
+    tc::publish_smem();
+    for (; behind > 0; --behind) {
+      tc::bar_arrive(rows_in(late));
+      if (++late == S::kStages) late = 0;
+    }
+  } else if (wid >= 8) {
+    // a finished tile: a thread has one channel (row) and half of the columns
+    const int quarter = wid & 3, half = (wid - 8) >> 2;
+    int set = 0;
+    uint32_t set_phase = 0;
+    for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
+      const Tile x = tile_at(t);
+      if (!tc::bar_wait(sums_done(set), set_phase, &s_quit)) break;
+      tc::fence_after();
+      const int n16 = (x.rows + 15) >> 4;
+      const int ch = x.m * per_tile + quarter * 32 + lane;
+      const uint32_t at = tmem + set * 2 * N + ((uint32_t)(quarter * 32) << 16);
+      for (int c = half; c < n16; c += 2) {
+        uint32_t u[16], v[16];
+        tc::ld16(at + c * 16, u);
+        tc::ld16(at + N + c * 16, v);
+        tc::ld_wait();
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int col = c * 16 + i;
+          if (col >= x.rows) break;
+          const long long row = x.first + col;
+          const float f = __uint_as_float(u[i]), g = __uint_as_float(v[i]);
+          if constexpr (kAct) {
+            // silu(gate) * up in fp32, rounded once
+            const float y = f / (1.f + __expf(-f)) * g;
+            if (ch < a.channels) {
+              if constexpr (kBf16)
+                static_cast<__nv_bfloat16*>(a.out)[row * a.channels + ch] = __float2bfloat16_rn(y);
+              else
+                static_cast<__half*>(a.out)[row * a.channels + ch] = __float2half_rn(y);
+            }
+          } else {
+            float* out = static_cast<float*>(a.out) + row * a.channels + ch;
+            if (ch < a.channels) out[0] = f;
+            if (ch + 128 < a.channels) out[128] = g;
+          }
+        }
+      }
+      tc::fence_before();
+      tc::bar_arrive(sums_free(set));
+      if (++set == S::kSets) set = 0, set_phase ^= 1;
+    }
+  }
+  __syncthreads();
+  if (wid == 1) tc::tmem_free(tmem, 512);
+  if (tid == 0 && s_quit) atomicOr(err, kErrTimeout);
 }
 
+// y_t: a thread has four columns of a token and adds its slots in order.
 template <int T>
-__global__ void __launch_bounds__(kChannels)
-down_kernel(moe_reader_experts_combine_args a, const void* down, int H, int I, int E) {
-  const int row = blockIdx.x, ch = blockIdx.y * kChannels + threadIdx.x;
-  const int e = expert_of(a.offsets, E, row);
-  if (e >= E || ch >= H) return;
-  const long long w = ((long long)e * H + ch) * I;
-  float z = 0.f;
-  for (int i = 0; i < I; ++i) z += wide<T>(a.act, (long long)row * I + i) * wide<T>(down, w + i);
-  a.slots[(long long)row * H + ch] = z;
-}
-
-template <int T>
-__global__ void __launch_bounds__(kChannels)
+__global__ void __launch_bounds__(256)
 combine_kernel(moe_reader_experts_combine_args a, int H, int topk) {
-  const int t = blockIdx.x, ch = blockIdx.y * kChannels + threadIdx.x;
-  if (ch >= H) return;
-  float y = 0.f;
+  const int t = blockIdx.x, c = (blockIdx.y * 256 + threadIdx.x) * 4;
+  if (c >= H) return;
+  const int pairs = a.tokens * topk;
+  float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int s = 0; s < topk; ++s) {
     const int row = __ldg(a.places + (long long)t * topk + s);
-    if (row >= 0 && row < (long long)a.tokens * topk)
-      y += __ldg(a.weights + (long long)t * topk + s) * a.slots[(long long)row * H + ch];
+    if ((unsigned)row >= (unsigned)pairs) continue;
+    const float w = __ldg(a.weights + (long long)t * topk + s);
+    const float4 z = *reinterpret_cast<const float4*>(a.slots + (long long)row * H + c);
+    y.x += w * z.x;
+    y.y += w * z.y;
+    y.z += w * z.z;
+    y.w += w * z.w;
   }
-  put<T>(a.y, t * a.y_stride + ch, y);
+  const long long at = t * a.y_stride + c;
+  if constexpr (T == MOE_READER_TYPE_F32) {
+    *reinterpret_cast<float4*>(static_cast<float*>(a.y) + at) = y;
+  } else if constexpr (T == MOE_READER_TYPE_BF16) {
+    __nv_bfloat162 v[2] = {__floats2bfloat162_rn(y.x, y.y), __floats2bfloat162_rn(y.z, y.w)};
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.y) + at) =
+        *reinterpret_cast<const uint2*>(v);
+  } else {
+    __half2 v[2] = {__floats2half2_rn(y.x, y.y), __floats2half2_rn(y.z, y.w)};
+    *reinterpret_cast<uint2*>(static_cast<__half*>(a.y) + at) = *reinterpret_cast<const uint2*>(v);
+  }
 }
 
-template <int T>
+template <int N, bool kBf16, bool kAct>
+cudaError_t group_as(const moe_reader_experts& h, const GroupArgs& a, cudaStream_t s) {
+  const CUtensorMap& m0 = kAct ? h.gate_map : h.down_map;
+  const CUtensorMap& m1 = kAct ? h.up_map : h.down_map;
+  group_kernel<N, kBf16, kAct><<<h.sms, kGroupThreads, GroupShape<N>::kSmem, s>>>(m0, m1, a, h.err);
+  return cudaGetLastError();
+}
+
+// Columns of a tile: about as many as an expert has rows on average (a tile
+// of more leaves less shared memory for the weights under way, one of fewer
+// reads them again).
+template <bool kBf16, bool kAct>
+cudaError_t group(const moe_reader_experts& h, const GroupArgs& a, cudaStream_t s) {
+  const int mean = a.pairs / a.experts;
+  if (mean <= 32) return group_as<32, kBf16, kAct>(h, a, s);
+  if (mean <= 64) return group_as<64, kBf16, kAct>(h, a, s);
+  return group_as<128, kBf16, kAct>(h, a, s);
+}
+
+template <bool kBf16>
 cudaError_t activate_as(const moe_reader_experts& h, const moe_reader_experts_activate_args& a,
                         cudaStream_t s) {
-  const dim3 grid((unsigned)(a.tokens * a.experts_per_token),
-                  (unsigned)((h.cfg.inter + kChannels - 1) / kChannels));
-  activate_kernel<T><<<grid, kChannels, 0, s>>>(a, h.gate, h.up, h.cfg.hidden, h.cfg.inter,
-                                                h.cfg.num_experts, a.experts_per_token);
+  const GroupArgs g = {static_cast<const char*>(a.x), 2 * a.x_stride, a.order, a.offsets, a.act,
+                       h.cfg.num_experts, h.cfg.hidden, h.cfg.inter,
+                       a.tokens * a.experts_per_token, a.experts_per_token};
+  return group<kBf16, true>(h, g, s);
+}
+
+template <bool kBf16>
+cudaError_t combine_as(const moe_reader_experts& h, const moe_reader_experts_combine_args& a,
+                       cudaStream_t s) {
+  const int H = h.cfg.hidden, topk = a.experts_per_token;
+  const GroupArgs g = {static_cast<const char*>(a.act), 2LL * h.cfg.inter, nullptr, a.offsets,
+                       a.slots, h.cfg.num_experts, h.cfg.inter, H, a.tokens * topk, topk};
+  const cudaError_t e = group<kBf16, false>(h, g, s);
+  if (e != cudaSuccess) return e;
+  const dim3 grid((unsigned)a.tokens, (unsigned)((H + 1023) / 1024));
+  switch (a.y_type) {
+    case MOE_READER_TYPE_BF16: combine_kernel<MOE_READER_TYPE_BF16><<<grid, 256, 0, s>>>(a, H, topk); break;
+    case MOE_READER_TYPE_F16: combine_kernel<MOE_READER_TYPE_F16><<<grid, 256, 0, s>>>(a, H, topk); break;
+    default: combine_kernel<MOE_READER_TYPE_F32><<<grid, 256, 0, s>>>(a, H, topk);
+  }
   return cudaGetLastError();
 }
 
-template <int T>
-cudaError_t combine_as(const moe_reader_experts& h, const moe_reader_experts_combine_args& a,
-                       cudaStream_t s) {
-  const unsigned chunks = (unsigned)((h.cfg.hidden + kChannels - 1) / kChannels);
-  const int topk = a.experts_per_token;
-  down_kernel<T><<<dim3((unsigned)(a.tokens * topk), chunks), kChannels, 0, s>>>(
-      a, h.down, h.cfg.hidden, h.cfg.inter, h.cfg.num_experts);
-  const dim3 grid((unsigned)a.tokens, chunks);
-  switch (a.y_type) {
-    case MOE_READER_TYPE_BF16:
-      combine_kernel<MOE_READER_TYPE_BF16><<<grid, kChannels, 0, s>>>(a, h.cfg.hidden, topk);
-      break;
-    case MOE_READER_TYPE_F16:
-      combine_kernel<MOE_READER_TYPE_F16><<<grid, kChannels, 0, s>>>(a, h.cfg.hidden, topk);
-      break;
-    default:
-      combine_kernel<MOE_READER_TYPE_F32><<<grid, kChannels, 0, s>>>(a, h.cfg.hidden, topk);
+template <int N, bool kBf16, bool kAct>
+cudaError_t configure_one() {
+  return cudaFuncSetAttribute(group_kernel<N, kBf16, kAct>,
+                              cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              (int)GroupShape<N>::kSmem);
+}
+template <bool kBf16, bool kAct>
+cudaError_t configure_group() {
+  cudaError_t e = configure_one<32, kBf16, kAct>();
+  if (e == cudaSuccess) e = configure_one<64, kBf16, kAct>();
+  if (e == cudaSuccess) e = configure_one<128, kBf16, kAct>();
+  return e;
+}
+cudaError_t configure_experts(moe_reader_experts& h) {
+  const bool bf16 = h.cfg.type == MOE_READER_TYPE_BF16;
+  const uint64_t H = h.cfg.hidden, I = h.cfg.inter, E = h.cfg.num_experts;
+  cudaError_t e = cudaSuccess;
+  if (h.gate) {
+    e = tc::make_map(&h.gate_map, h.gate, bf16, H, I, E, 128);
+    if (e == cudaSuccess) e = tc::make_map(&h.up_map, h.up, bf16, H, I, E, 128);
+    if (e == cudaSuccess) e = bf16 ? configure_group<true, true>() : configure_group<false, true>();
   }
-  return cudaGetLastError();
+  if (e == cudaSuccess && h.down) {
+    e = tc::make_map(&h.down_map, h.down, bf16, I, H, E, 128);
+    if (e == cudaSuccess)
+      e = bf16 ? configure_group<true, false>() : configure_group<false, false>();
+  }
+  return e;
 }
 
 }  // namespace
@@ -273,6 +553,7 @@ int moe_reader_experts_create(const moe_reader_experts_config* c, const void* ga
     if ((ce = cudaDeviceGetAttribute(&h->sms, cudaDevAttrMultiProcessorCount, h->device)) !=
         cudaSuccess)
       break;
+    if ((ce = mr::configure_experts(*h)) != cudaSuccess) break;
     if ((ce = cudaMemsetAsync(p, 0, 256, s)) != cudaSuccess) break;
     ce = cudaStreamSynchronize(s);
   } while (0);
@@ -327,8 +608,8 @@ int moe_reader_experts_activate(moe_reader_experts_t* h, const moe_reader_expert
   if (!apart(ins, outs) || !on_device(h)) return MOE_READER_EINVAL;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   return status_of(c.type == MOE_READER_TYPE_BF16
-                       ? mr::activate_as<MOE_READER_TYPE_BF16>(*h, *a, s)
-                       : mr::activate_as<MOE_READER_TYPE_F16>(*h, *a, s));
+                       ? mr::activate_as<true>(*h, *a, s)
+                       : mr::activate_as<false>(*h, *a, s));
 }
 
 int moe_reader_experts_combine(moe_reader_experts_t* h, const moe_reader_experts_combine_args* a,
@@ -359,8 +640,8 @@ int moe_reader_experts_combine(moe_reader_experts_t* h, const moe_reader_experts
   if (!apart(ins, outs) || !on_device(h)) return MOE_READER_EINVAL;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   return status_of(c.type == MOE_READER_TYPE_BF16
-                       ? mr::combine_as<MOE_READER_TYPE_BF16>(*h, *a, s)
-                       : mr::combine_as<MOE_READER_TYPE_F16>(*h, *a, s));
+                       ? mr::combine_as<true>(*h, *a, s)
+                       : mr::combine_as<false>(*h, *a, s));
 }
 
 int moe_reader_experts_status(moe_reader_experts_t* h, uint32_t* bits_out) {
