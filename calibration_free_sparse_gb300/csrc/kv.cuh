@@ -27,6 +27,9 @@ struct moe_reader_kv {
   float* part_ml;             // [sms][2][2][16]  their references and sums of weights
   uint32_t* arrived;          // [rows]           pieces written; zero between launches
   size_t arrived_bytes;
+  float* chunk_o;             // [sms][chunk_rows][D]  unnormalised outputs of a chunk's pieces
+  float* chunk_ml;            // [sms][2][chunk_rows]  their references and sums of weights
+  uint32_t* chunk_arrived;    // [kMaxSms]        pieces written, behind `arrived`
   uint32_t* err;              // [1]              device error word
 };
 
@@ -57,6 +60,8 @@ cudaError_t launch_kv_select(const moe_reader_kv& kv, const moe_reader_kv_select
 cudaError_t configure_kv_select(const moe_reader_kv& kv);
 cudaError_t launch_kv_chunk(const moe_reader_kv& kv, const moe_reader_kv_chunk_args& a,
                             cudaStream_t s);
+cudaError_t configure_kv_chunk(const moe_reader_kv& kv);
+int chunk_rows(const moe_reader_kv_config& c);      // rows of an item of kv_chunk
 cudaError_t launch_kv_collect(const moe_reader_kv& kv, const moe_reader_kv_pages_args& a,
                               cudaStream_t s);
 cudaError_t launch_kv_compact(const moe_reader_kv& kv, const moe_reader_kv_pages_args& a,

@@ -771,9 +771,14 @@ int moe_reader_kv_create(const moe_reader_kv_config* cfg, void* k, void* v, int8
   const size_t o_bytes = (size_t)mr::kMaxSms * 2 * 16 * cfg->head_dim * sizeof(float);
   const size_t ml_bytes = (size_t)mr::kMaxSms * 2 * 2 * 16 * sizeof(float);
   const size_t items = (size_t)cfg->max_requests * cfg->num_kv_heads * mr::attend_row_tiles(*cfg);
-  const size_t c_bytes = (items * 4 + 255) & ~(size_t)255;
-  const size_t bytes = o_bytes + ml_bytes + c_bytes + 256;
-  cudaError_t ce = mr::device_alloc(&kv->base, bytes);
+  const size_t item_bytes = (items * 4 + 255) & ~(size_t)255;
+  const size_t c_bytes = item_bytes + mr::kMaxSms * 4;
+  cudaError_t ce = cudaDeviceGetAttribute(&kv->sms, cudaDevAttrMultiProcessorCount, kv->device);
+  kv->sms = std::min(kv->sms, mr::kMaxSms);
+  const size_t chunk_rows = (size_t)kv->sms * mr::chunk_rows(*cfg);
+  const size_t zeroed = o_bytes + ml_bytes + c_bytes + 256;
+  const size_t bytes = zeroed + chunk_rows * (cfg->head_dim + 2) * sizeof(float);
+  if (ce == cudaSuccess) ce = mr::device_alloc(&kv->base, bytes);
   if (ce != cudaSuccess) {
     free(kv);
     return status_of(ce);
@@ -783,16 +788,16 @@ int moe_reader_kv_create(const moe_reader_kv_config* cfg, void* k, void* v, int8
   kv->part_ml = reinterpret_cast<float*>(b + o_bytes);
   kv->arrived = reinterpret_cast<uint32_t*>(b + o_bytes + ml_bytes);
   kv->arrived_bytes = c_bytes;
+  kv->chunk_arrived = kv->arrived + item_bytes / 4;
   kv->err = reinterpret_cast<uint32_t*>(b + o_bytes + ml_bytes + c_bytes);
+  kv->chunk_o = reinterpret_cast<float*>(b + zeroed);
+  kv->chunk_ml = kv->chunk_o + chunk_rows * cfg->head_dim;
   do {
-    if ((ce = cudaDeviceGetAttribute(&kv->sms, cudaDevAttrMultiProcessorCount, kv->device)) !=
-        cudaSuccess)
-      break;
-    kv->sms = std::min(kv->sms, mr::kMaxSms);
     if ((ce = mr::configure_kv_attend(*kv)) != cudaSuccess) break;
     if ((ce = mr::configure_kv_select(*kv)) != cudaSuccess) break;
     if ((ce = mr::configure_kv_pages()) != cudaSuccess) break;
-    if ((ce = cudaMemsetAsync(kv->base, 0, bytes, s)) != cudaSuccess) break;
+    if ((ce = mr::configure_kv_chunk(*kv)) != cudaSuccess) break;
+    if ((ce = cudaMemsetAsync(kv->base, 0, zeroed, s)) != cudaSuccess) break;
     ce = cudaStreamSynchronize(s);
   } while (0);
   if (ce != cudaSuccess) {

@@ -4,19 +4,37 @@
 #include "device_util.cuh"
 #include "internal.cuh"
 #include "kv.cuh"
+#include "tc.cuh"
 
 namespace mr {
 namespace {
 
+constexpr int kBf16 = MOE_READER_TYPE_BF16, kF16 = MOE_READER_TYPE_F16,
+              kE4m3 = MOE_READER_TYPE_E4M3;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
 template <int CT>
 __device__ __forceinline__ float cell(const void* base, long long at) {
-  if constexpr (CT == MOE_READER_TYPE_E4M3)
+  if constexpr (CT == kE4m3)
     return __half2float(__half(__nv_cvt_fp8_to_halfraw(
         static_cast<const __nv_fp8_storage_t*>(base)[at], __NV_E4M3)));
-  else if constexpr (CT == MOE_READER_TYPE_BF16)
+  else if constexpr (CT == kBf16)
     return __bfloat162float(static_cast<const __nv_bfloat16*>(base)[at]);
   else
     return __half2float(static_cast<const __half*>(base)[at]);
+}
+template <int QT> __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  uint32_t r;
+  if constexpr (QT == kBf16)
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  else
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
 // A request's part of the call.
@@ -35,91 +53,867 @@ __device__ __forceinline__ Span span_of(const moe_reader_kv_chunk_args& a, int r
   return x;
 }
 
-constexpr int kRowWarps = 8;
+// ---------------------------------------------------------------------------
+// Both products run on the tensor core: S = Q K^T with 128 rows (token, head
+// of the group) a tile, and O += P V with P read from tensor memory, where it
+// replaces S.  A CTA has two row tiles, so that one's softmax runs while the
+// other's products do, and both share the keys (heads of 256: one tile, whose S
+// has two buffers).  Four warps a row tile: a thread has a row, so maxima and
+// sums need no exchange.  Three warps bring pages, one issues products.
+// ---------------------------------------------------------------------------
+constexpr int kLoaderWarps = 3;
+constexpr int kLoaders = 32 * kLoaderWarps;
+constexpr int kChunkThreads = 256 + kLoaders + 32;     // 12 warps: 168 registers a thread
+constexpr int kMaxPieces = kMaxSms;
 
-// A warp per row (token, query head): online softmax, lanes over coordinates.
+template <int D> struct ChunkShape {
+  static constexpr int kTiles = D <= 128 ? 2 : 1;        // row tiles
+  static constexpr int kRows = 128 * kTiles;
+  static constexpr int kKeys = D <= 128 ? 128 : 64;      // keys of a step
+  static constexpr int kBlocks = D / 64;                 // 128-byte blocks of a row
+  static constexpr int kQBytes = kRows * D * 2;
+  static constexpr int kSlotBytes = kKeys * D * 2;       // keys or values of a step
+  static constexpr int kSlots = D == 64 ? 8 : 4;
+  static constexpr size_t kSmem = kQBytes + (size_t)kSlots * kSlotBytes + 1024;
+  // tensor memory: two S, then O
+  static constexpr int kO = 2 * kKeys;
+};
+
+struct ChunkCall {
+  moe_reader_kv_chunk_args a;
+  const char* k;
+  const char* v;
+  const float* k_scale;
+  const float* v_scale;
+  float* part_o;             // [piece][kRows][D]
+  float* part_ml;            // [piece][2][kRows]
+  uint32_t* arrived;         // [item]
+  uint32_t* err;
+  int heads, kv_heads, group, shift, pool;
+  int wide;                  // q can be copied 16 bytes at a time
+};
+
+// Part of an item: the rows [row, row + rows) of a request's (token, head of
+// the group) list, one KV head, the steps [step, last) of its keys.
+struct Piece {
+  Span sp;
+  int request, head, row, rows;
+  int p0, p1;                // positions of the first and the last row
+  int lo, hi;                // keys that some row sees
+  int step, last;
+  int item, index, count;    // index-th of the item's `count` pieces
+  int slot;                  // where its partial result goes
+};
+
+template <int D>
+__device__ __forceinline__ void item_range(const ChunkCall& c, Piece& x) {
+  using S = ChunkShape<D>;
+  const int before = x.sp.len - x.sp.tokens;
+  x.p0 = before + x.row / c.group;
+  x.p1 = before + (x.row + x.rows - 1) / c.group;
+  x.lo = c.a.window ? max(0, x.p0 + 1 - c.a.window) : 0;
+  x.hi = (int)min((long long)x.p1 + 1, (long long)c.a.width << c.shift);
+  x.step = x.lo / S::kKeys;
+  x.last = x.hi > x.lo ? (x.hi + S::kKeys - 1) / S::kKeys : x.step;
+}
+
+// Item i: block of rows and KV head; the longest rows of a request first.
+template <int D>
+__device__ __forceinline__ Piece item_at(const ChunkCall& c, const int* blocks, int i) {
+  using S = ChunkShape<D>;
+  const int b = i / c.kv_heads;
+  int lo = 0, hi = c.a.requests - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (blocks[mid] <= b) lo = mid; else hi = mid - 1;
+  }
+  uint32_t ignore = 0;
+  Piece x;
+  x.sp = span_of(c.a, lo, ignore);
+  x.request = lo;
+  x.head = i - b * c.kv_heads;
+  x.row = (blocks[lo + 1] - 1 - b) * S::kRows;
+  x.rows = min(S::kRows, x.sp.tokens * c.group - x.row);
+  x.item = i;
+  x.index = 0;
+  x.count = 1;
+  x.slot = 0;
+  item_range<D>(c, x);
+  return x;
+}
+
+// One row without the tensor core, for pieces whose masked values are not
+// finite (0 times those is not 0): a warp, lanes over coordinates.  Same
+// reference and scaling as the tensor path's.
 template <int D, int CT, int QT>
-__global__ void __launch_bounds__(kRowWarps * 32)
-chunk_row_kernel(moe_reader_kv_chunk_args a, const void* k, const void* v, const float* k_scale,
-                 const float* v_scale, int heads, int kv_heads, int shift, int pool,
-                 uint32_t* err) {
-  constexpr int kPer = D / 32;
-  const int lane = threadIdx.x & 31;
-  const long long row = (long long)blockIdx.x * kRowWarps + (threadIdx.x >> 5);
-  const int t = (int)(row / heads), head = (int)(row % heads);
-  if (t >= a.tokens) return;
-  const int kvh = head / (heads / kv_heads);
+__device__ __noinline__ void plain_row(const ChunkCall& c, const Piece& x, int row, float factor,
+                                       int klo, int khi, float lift, float* o, float& m, float& l) {
+  const int lane = threadIdx.x & 31, t = x.sp.first + row / c.group;
+  const int head = x.head * c.group + row % c.group;
+  const long long q = t * c.a.q_token_stride + head * c.a.q_head_stride + lane;
+  const float sign = c.a.scale < 0.f ? -1.f : 1.f;
+  m = -INFINITY;
+  l = 0.f;
+  for (int i = 0; i < D / 32; ++i) o[i] = 0.f;
+  for (int j = klo; j < khi; ++j) {
+    const int page = __ldg(c.a.table + (size_t)x.request * c.a.width + (j >> c.shift));
+    if ((unsigned)page >= (unsigned)c.pool) continue;
+    const long long at =
+        ((((long long)page * c.kv_heads + x.head) << c.shift) + (j & ((1 << c.shift) - 1))) * D +
+        lane;
+    float s = 0.f;
+    for (int i = 0; i < D / 32; ++i)
+      s += sign * cell<QT>(c.a.q, q + 32 * i) * cell<CT>(c.k, at + 32 * i);
+    s = warp_sum(s) * factor;
+    const float top = fmaxf(m, s), ref = top == -INFINITY ? 0.f : top;
+    const float f = exp2_fast(m - ref), p = exp2_fast(s - ref + lift);
+    m = top;
+    l = l * f + p;
+    for (int i = 0; i < D / 32; ++i) o[i] = o[i] * f + p * cell<CT>(c.v, at + 32 * i);
+  }
+}
+
+// Eight values of 16 bits, any of which is infinite or NaN.
+template <int QT> __device__ __forceinline__ bool odd8(uint4 v) {
+  constexpr uint32_t e = QT == kBf16 ? 0x7f80u : 0x7c00u;
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  bool odd = false;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    odd |= (w[i] & e) == e || (w[i] >> 16 & e) == e;
+  return odd;
+}
+
+// What a row adds up to with its sink: the factor of its sums, lse.
+struct Close {
+  float scale, lse;
+};
+__device__ __forceinline__ Close close_row(float m, float l, float sink, float lift) {
+  sink *= kLog2e;
+  const float top = fmaxf(m, sink);
+  if (top == -INFINITY && !(l != l)) return {0.f, -INFINITY};
+  if (sink == INFINITY) return {0.f, INFINITY};
+  const float f = m == -INFINITY ? 0.f : exp2_fast(m - top);
+  const float all = l * f + exp2_fast(sink - top + lift);
+  return {f / all, (top - lift + log2f(all)) * kLn2};
+}
+
+template <int D, int CT, int QT>
+__global__ void __launch_bounds__(kChunkThreads, 1)
+chunk_kernel(const __grid_constant__ ChunkCall c) {
+  using S = ChunkShape<D>;
+  constexpr float kLift = QT == kF16 ? 11.f : 0.f;     // fp16 weights reach down to 2^-35
+  constexpr float kSlack = QT == kF16 ? 4.f : 8.f;     // how far a logit may pass the reference
+  extern __shared__ char raw[];
+  __shared__ int s_blocks[kMaxRequests + 1], s_pieces[kMaxPieces + 1];
+  __shared__ uint64_t s_bar[2 * S::kSlots + 10];
+  // by piece with keys and by step, in turn: loaders are at most two pieces and
+  // kSlots / 2 + 1 steps ahead of softmax
+  __shared__ volatile uint32_t s_odd[4], s_bad[8];
+  __shared__ uint32_t s_tmem, s_last;
+  __shared__ volatile uint32_t s_quit;
+  const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+  const int grid = gridDim.x;
+  const uint32_t q_at = (tc::smem_at(raw) + 1023) & ~1023u, kv_at = q_at + S::kQBytes;
+  const uint32_t bars = tc::smem_at(s_bar);
+  auto slot_full = [&](int s) { return bars + 8 * s; };
+  auto slot_free = [&](int s) { return bars + 8 * (S::kSlots + s); };
+  const uint32_t more = bars + 16 * S::kSlots;
+  auto s_full = [&](int t) { return more + 8 * t; };          // logits of a tile are there
+  auto p_full = [&](int t) { return more + 16 + 8 * t; };     // its weights are
+  auto o_full = [&](int t) { return more + 32 + 8 * t; };     // they are added up
+  const uint32_t q_full = more + 48, q_free = more + 56, join = more + 64, drained = more + 72;
+
+  // ---- what there is to do: every CTA finds it out for itself ----
   uint32_t bad = 0;
-  int r = 0;
-  Span sp = {};
-  for (; r < a.requests; ++r) {
-    sp = span_of(a, r, bad);
-    if (t >= sp.first && t < sp.first + sp.tokens) break;
+  for (int r = tid; r < c.a.requests; r += kChunkThreads) {
+    const Span sp = span_of(c.a, r, bad);
+    if (sp.len > ((long long)c.a.width << c.shift)) bad |= kErrLength;
+    s_blocks[r] = (int)(((long long)sp.tokens * c.group + S::kRows - 1) / S::kRows);
   }
-  if (r < a.requests) {
-    const long long room = (long long)a.width << shift;
-    if (sp.len > room) bad |= kErrLength;
-    const int pos = sp.len - sp.tokens + t - sp.first;
-    const int hi = (int)min((long long)pos + 1, room), lo = a.window ? max(0, pos + 1 - a.window) : 0;
-    float q[kPer], o[kPer], m = -INFINITY, l = 0.f;
-    for (int i = 0; i < kPer; ++i) {
-      q[i] = cell<QT>(a.q, t * a.q_token_stride + head * a.q_head_stride + lane + 32 * i);
-      o[i] = 0.f;
+  if (bad && blockIdx.x == 0) atomicOr(c.err, bad);
+  if (tid == 0) {
+    for (int s = 0; s < S::kSlots; ++s) {
+      tc::bar_init(slot_full(s), kLoaders);
+      tc::bar_init(slot_free(s), 1);
     }
-    const float scale = a.scale * (k_scale ? k_scale[kvh] : 1.f);
-    for (int j = lo; j < hi; ++j) {
-      const int page = __ldg(a.table + (size_t)r * a.width + (j >> shift));
-      if ((unsigned)page >= (unsigned)pool) {
-        bad |= kErrPage;
-        continue;
+    for (int t = 0; t < 2; ++t) {
+      tc::bar_init(s_full(t), 1);
+      tc::bar_init(p_full(t), 128);
+      tc::bar_init(o_full(t), 1);
+    }
+    tc::bar_init(q_full, kLoaders);
+    tc::bar_init(q_free, 1);
+    tc::bar_init(join, 256);
+    tc::bar_init(drained, 1);
+    for (int i = 0; i < 4; ++i) s_odd[i] = 0;
+    s_quit = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (wid == 11) tc::tmem_alloc(tc::smem_at(&s_tmem), 512);
+  __syncthreads();
+  if (wid == 0) {
+    int sum = 0;
+    for (int r0 = 0; r0 <= c.a.requests; r0 += 32) {
+      const int r = r0 + lane, n = r < c.a.requests ? s_blocks[r] : 0;
+      int at = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, at, o);
+        if (lane >= o) at += u;
       }
-      const long long at =
-          ((((long long)page * kv_heads + kvh) << shift) + (j & ((1 << shift) - 1))) * D + lane;
-      float s = 0.f;
-      for (int i = 0; i < kPer; ++i) s += q[i] * cell<CT>(k, at + 32 * i);
-      s = warp_sum(s) * scale;
-      const float top = fmaxf(m, s), ref = top == -INFINITY ? 0.f : top;
-      const float f = expf(m - ref), p = expf(s - ref);
-      m = top;
-      l = l * f + p;
-      for (int i = 0; i < kPer; ++i) o[i] = o[i] * f + p * cell<CT>(v, at + 32 * i);
+      if (r <= c.a.requests) s_blocks[r] = sum + at - n;
+      sum += __shfl_sync(0xffffffffu, at, 31);
     }
-    const float sink = a.sinks ? __ldg(a.sinks + head) : -INFINITY;
-    const float top = fmaxf(m, sink), ref = top == -INFINITY ? 0.f : top;
-    const float f = expf(m - ref);
-    l = l * f + expf(sink - ref);
-    const float inv = hi > lo && l != 0.f ? f / l * (v_scale ? v_scale[kvh] : 1.f) : 0.f;
-    for (int i = 0; i < kPer; ++i) {
-      const long long at = ((long long)t * heads + head) * D + lane + 32 * i;
-      const float y = inv == 0.f ? 0.f : o[i] * inv;
-      if constexpr (QT == MOE_READER_TYPE_BF16)
-        static_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16_rn(y);
-      else
-        static_cast<__half*>(a.out)[at] = __float2half_rn(y);
-    }
-    if (a.lse && lane == 0) a.lse[(long long)t * heads + head] = logf(l) + ref;
   }
-  if (bad && lane == 0) atomicOr(err, bad);
+  __syncthreads();
+  const long long items = (long long)s_blocks[c.a.requests] * c.kv_heads;
+  const bool split = items <= min(grid, kMaxPieces);
+  int pieces = (int)items;
+  if (split) {
+    // Few items: each is cut into pieces of at most `most` steps, the fewest
+    // for which there are no more pieces than CTAs.
+    for (int i = tid; i < items; i += kChunkThreads) {
+      const Piece x = item_at<D>(c, s_blocks, i);
+      s_pieces[i] = x.last - x.step;
+    }
+    __syncthreads();
+    if (wid == 0) {
+      int low = 4, high = 4;
+      for (int i = lane; i < items; i += 32) high = max(high, s_pieces[i]);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) high = max(high, __shfl_xor_sync(0xffffffffu, high, o));
+      while (low < high) {
+        const int mid = (low + high) >> 1;
+        int n = 0;
+        for (int i = lane; i < items; i += 32) n += max(1, (s_pieces[i] + mid - 1) / mid);
+        if (warp_sum_i(n) <= min(grid, kMaxPieces)) high = mid; else low = mid + 1;
+      }
+      int sum = 0;
+      for (int i0 = 0; i0 <= items; i0 += 32) {
+        const int i = i0 + lane;
+        const int n = i < items ? max(1, (s_pieces[i] + high - 1) / high) : 0;
+        int at = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int u = __shfl_up_sync(0xffffffffu, at, o);
+          if (lane >= o) at += u;
+        }
+        __syncwarp();
+        if (i <= items) s_pieces[i] = sum + at - n;
+        sum += __shfl_sync(0xffffffffu, at, 31);
+      }
+    }
+    __syncthreads();
+    pieces = s_pieces[items];
+  }
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  const uint32_t tmem = s_tmem;
+
+  // Pieces are dealt to the CTAs in turn, every other round backwards: those
+  // of a request get shorter, so that a CTA's long ones meet its short ones.
+  const int rounds = (pieces + grid - 1) / grid;
+  auto piece_at = [&](int round, Piece& x) {
+    const int i = round * grid + (round & 1 ? grid - 1 - (int)blockIdx.x : (int)blockIdx.x);
+    if (i >= pieces) return false;
+    if (!split) {
+      x = item_at<D>(c, s_blocks, i);
+      return true;
+    }
+    int lo = 0, hi = (int)items - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (s_pieces[mid] <= i) lo = mid; else hi = mid - 1;
+    }
+    x = item_at<D>(c, s_blocks, lo);
+    x.index = i - s_pieces[lo];
+    x.count = s_pieces[lo + 1] - s_pieces[lo];
+    x.slot = i;
+    const int n = x.last - x.step, first = x.step;
+    x.step = first + (int)((long long)n * x.index / x.count);
+    x.last = first + (int)((long long)n * (x.index + 1) / x.count);
+    return true;
+  };
+
+  if (wid >= 8 && wid < 11) {
+    // ------------------------------------------------------------------
+    // loaders
+    // ------------------------------------------------------------------
+    // a warp's copy covers four rows of 128 bytes; the warps take those in turn
+    const int id = tid - 256, who = wid - 8, piece = lane & 7, sub = lane >> 3;
+    constexpr int kTurns = (S::kKeys / 4 + kLoaderWarps - 1) / kLoaderWarps;
+    int s = 0, late = 0, behind = 0;
+    uint32_t phase = 1, q_phase = 1, check = 0, err = 0;   // check: bit i: i-th oldest late slot
+    uint32_t late_work[2] = {0, 0}, work = 0, steps = 0;
+    constexpr int kLag = 2;
+    // hands the oldest slot over (16-bit caches: its copies have landed)
+    auto hand_over = [&]() {
+      if (check & 1) {
+        bool odd = false;
+        for (int b = 0; b < S::kBlocks; ++b)
+          for (int r = who * 4 + sub; r < S::kKeys; r += kLoaderWarps * 4) {
+            const uint32_t at = kv_at + late * S::kSlotBytes + b * S::kKeys * 128 +
+                                tc::swizzled(r, piece);
+            uint4 v;
+            asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                         : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at));
+            odd |= odd8<QT>(v);
+          }
+        if (odd) s_odd[late_work[0] & 3] = late_work[0];
+      }
+      check >>= 1;
+      late_work[0] = late_work[1];
+      tc::publish_smem();
+      tc::bar_arrive(slot_full(late));
+      if (++late == S::kSlots) late = 0;
+    };
+    for (int round = 0; round < rounds; ++round) {
+      Piece x;
+      if (!piece_at(round, x)) break;
+      if (x.step >= x.last) continue;
+      work++;
+      // queries; the last products with those before want their keys first
+      tc::copies_wait<0>();
+      for (; behind > 0; --behind) hand_over();
+      if (!tc::bar_wait(q_free, q_phase, &s_quit)) goto loaders_end;
+      q_phase ^= 1;
+      {
+        const uint16_t flip = c.a.scale < 0.f ? 0x8000 : 0;
+        for (int r = who * 4 + sub; r < S::kRows; r += kLoaderWarps * 4) {
+          const int row = x.row + r;
+          const bool in = r < x.rows;
+          const long long at = in ? (long long)(x.sp.first + row / c.group) * c.a.q_token_stride +
+                                        (long long)(x.head * c.group + row % c.group) *
+                                            c.a.q_head_stride + piece * 8
+                                  : 0;
+          const uint16_t* from = static_cast<const uint16_t*>(c.a.q) + at;
+          const uint32_t to = q_at + (r >> 7) * (S::kBlocks << 14) + tc::swizzled(r & 127, piece);
+          if (c.wide) {
+#pragma unroll
+            for (int b = 0; b < S::kBlocks; ++b)
+              tc::copy16(to + (b << 14), in ? from + b * 64 : from, in);
+          } else {
+            for (int b = 0; b < S::kBlocks; ++b) {
+              uint32_t w[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const uint16_t e0 = in ? __ldg(from + b * 64 + 2 * i) ^ flip : 0;
+                const uint16_t e1 = in ? __ldg(from + b * 64 + 2 * i + 1) ^ flip : 0;
+                w[i] = (uint32_t)e0 | (uint32_t)e1 << 16;
+              }
+              asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};"
+                           :: "r"(to + (b << 14)), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
+                           : "memory");
+            }
+          }
+        }
+        tc::copies_commit();
+        tc::copies_wait<0>();
+        tc::publish_smem();
+        tc::bar_arrive(q_full);
+      }
+      // keys and values: lane l has the page of keys 16 l.. of the step
+      const int32_t* row = c.a.table + (size_t)x.request * c.a.width;
+      auto page_of = [&](int step) {
+        const int key = step * S::kKeys + lane * 16;
+        // a page all of whose rows are out of sight may be gone
+        if (lane < S::kKeys / 16 && key < x.hi && ((key >> c.shift) + 1) << c.shift > x.lo) {
+          const int p = __ldg(row + (key >> c.shift));
+          if ((unsigned)p < (unsigned)c.pool) return p;
+          return -2;
+        }
+        return -1;
+      };
+      int next = page_of(x.step);
+      const int clear_lo = c.a.window ? max(0, x.p1 + 1 - c.a.window) : 0;
+      const int clear_hi = min(x.p0 + 1, x.hi);
+      for (int step = x.step; step < x.last; ++step) {
+        const int page = next, k0 = step * S::kKeys;
+        if (step + 1 < x.last) next = page_of(step + 1);
+        const uint32_t lost = __ballot_sync(0xffffffffu, page == -2);
+        if (lost) err |= kErrPage;
+        const bool partial = k0 < clear_lo || k0 + S::kKeys > clear_hi;
+        if (id == 0) s_bad[steps & 7] = lost;
+        steps++;
+#pragma unroll 1
+        for (int kind = 0; kind < 2; ++kind) {
+          const char* base = kind ? c.v : c.k;
+          if constexpr (CT != kE4m3) {
+            if (!tc::bar_wait(slot_free(s), phase, &s_quit)) goto loaders_end;
+            const uint32_t to = kv_at + s * S::kSlotBytes;
+#pragma unroll
+            for (int i = 0; i < kTurns; ++i) {
+              const int r = (i * kLoaderWarps + who) * 4 + sub;
+              if ((i + 1) * kLoaderWarps * 4 > S::kKeys && r >= S::kKeys) break;
+              const int p = __shfl_sync(0xffffffffu, page, r >> 4);
+              const int key = k0 + r;
+              const bool in = p >= 0 && key >= x.lo && key < x.hi;
+              const char* from = base;
+              if (in)
+                from += (((((long long)p * c.kv_heads + x.head) << c.shift) +
+                          (key & ((1 << c.shift) - 1))) * D + piece * 8) * 2;
+#pragma unroll
+              for (int b = 0; b < S::kBlocks; ++b)
+                tc::copy16(to + b * S::kKeys * 128 + tc::swizzled(r, piece),
+                           in ? from + b * 128 : from, in);
+            }
+            tc::copies_commit();
+            if (behind == kLag) {
+              tc::copies_wait<kLag>();
+              hand_over();
+            } else {
+              behind++;
+            }
+            late_work[behind - 1] = work;
+            if (kind && partial) check |= 1u << (behind - 1);
+          } else {
+            // 16 e4m3 values a thread and row piece, widened on the way: both
+            // 16-bit types hold them exactly
+            constexpr int kRow = D / 16, kSub = 32 / kRow;
+            constexpr int kN = (S::kKeys / kSub + kLoaderWarps - 1) / kLoaderWarps;
+            const int piece = lane % kRow, sub = lane / kRow;
+            uint4 v[kN];
+#pragma unroll
+            for (int i = 0; i < kN; ++i) {
+              const int r = (i * kLoaderWarps + who) * kSub + sub, key = k0 + r;
+              const int p = __shfl_sync(0xffffffffu, page, (r >> 4) & 31);
+              v[i] = make_uint4(0, 0, 0, 0);
+              if (r < S::kKeys && p >= 0 && key >= x.lo && key < x.hi)
+                v[i] = ldg_stream(reinterpret_cast<const uint4*>(
+                    base + ((((long long)p * c.kv_heads + x.head) << c.shift) +
+                            (key & ((1 << c.shift) - 1))) * D + piece * 16));
+            }
+            if (!tc::bar_wait(slot_free(s), phase, &s_quit)) goto loaders_end;
+            const uint32_t to = kv_at + s * S::kSlotBytes + (piece >> 2) * S::kKeys * 128;
+            bool odd = false;
+#pragma unroll
+            for (int i = 0; i < kN; ++i) {
+              const int r = (i * kLoaderWarps + who) * kSub + sub;
+              if (r >= S::kKeys) break;
+              const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+              uint32_t o[8];
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                const uint32_t two = w[j >> 1] >> (16 * (j & 1)) & 0xffff;
+                const __half2 h(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3));
+                odd |= (two & 0x7f) == 0x7f || (two & 0x7f00) == 0x7f00;
+                if constexpr (QT == kBf16) {
+                  const float2 f = __half22float2(h);
+                  o[j] = pack2<kBf16>(f.x, f.y);
+                } else {
+                  o[j] = *reinterpret_cast<const uint32_t*>(&h);
+                }
+              }
+#pragma unroll
+              for (int j = 0; j < 2; ++j)
+                asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};"
+                             :: "r"(to + tc::swizzled(r, (piece & 3) * 2 + j)),
+                                "r"(o[4 * j]), "r"(o[4 * j + 1]), "r"(o[4 * j + 2]),
+                                "r"(o[4 * j + 3])
+                             : "memory");
+            }
+            if (odd && kind && partial) s_odd[work & 3] = work;
+            tc::publish_smem();
+            tc::bar_arrive(slot_full(s));
+          }
+          if (++s == S::kSlots) s = 0, phase ^= 1;
+        }
+      }
+    }
+  loaders_end:
+    tc::copies_wait<0>();
+    for (; behind > 0; --behind) hand_over();
+    if (err && id == 0) atomicOr(c.err, err);
+  } else if (wid == 11) {
+    // ------------------------------------------------------------------
+    // products
+    // ------------------------------------------------------------------
+    if (lane == 0) {
+      constexpr uint32_t s_desc = tc::instr<QT == kBf16>(S::kKeys);
+      constexpr uint32_t o_desc = tc::instr<QT == kBf16>(D, true);
+      int s = 0;
+      uint32_t phase = 0, q_phase = 0, p_phase[2] = {0, 0};
+      auto next_slot = [&]() { if (++s == S::kSlots) s = 0, phase ^= 1; };
+      auto logits = [&](int tile, int at, int slot) {
+        const uint32_t q = q_at + tile * (S::kBlocks << 14), k = kv_at + slot * S::kSlotBytes;
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i)
+          tc::mma(tmem + at * S::kKeys, tc::desc_k(q + (i >> 2 << 14)) + 2 * (i & 3),
+                  tc::desc_k(k + (i >> 2) * S::kKeys * 128) + 2 * (i & 3), s_desc, i > 0);
+        tc::commit(s_full(at));
+      };
+      auto outputs = [&](int tile, int at, int slot, bool first) {
+        const uint32_t v = kv_at + slot * S::kSlotBytes;
+#pragma unroll
+        for (int i = 0; i < S::kKeys / 16; ++i)
+          tc::mma_ta(tmem + S::kO + tile * D, tmem + at * S::kKeys + i * 8,
+                     tc::desc_mn(v + i * 2048, S::kKeys * 128), o_desc, !first || i > 0);
+        tc::commit(o_full(tile));
+      };
+      bool go = true;
+      for (int round = 0; go && round < rounds; ++round) {
+        Piece x;
+        if (!piece_at(round, x)) break;
+        if (x.step >= x.last) continue;
+        const int tiles = x.rows > 128 ? 2 : 1, n = x.last - x.step;
+        if (!(go = tc::bar_wait(q_full, q_phase, &s_quit))) break;
+        q_phase ^= 1;
+        if (!(go = tc::bar_wait(slot_full(s), phase, &s_quit))) break;
+        tc::fence_after();
+        if constexpr (S::kTiles == 2) {
+          for (int t = 0; t < tiles; ++t) logits(t, t, s);
+          tc::commit(slot_free(s));
+          if (n == 1) tc::commit(q_free);
+          next_slot();
+          for (int j = 0; go && j < n; ++j) {
+            const int v_slot = s;
+            if (!(go = tc::bar_wait(slot_full(s), phase, &s_quit))) break;
+            next_slot();
+            if (j + 1 < n && !(go = tc::bar_wait(slot_full(s), phase, &s_quit))) break;
+            for (int t = 0; t < tiles; ++t) {
+              if (!(go = tc::bar_wait(p_full(t), p_phase[t], &s_quit))) break;
+              p_phase[t] ^= 1;
+              tc::fence_after();
+              outputs(t, t, v_slot, j == 0);
+              if (t == tiles - 1) tc::commit(slot_free(v_slot));
+              if (j + 1 < n) logits(t, t, s);
+            }
+            if (!go) break;
+            if (j + 1 < n) {
+              tc::commit(slot_free(s));
+              if (j + 2 == n) tc::commit(q_free);
+              next_slot();
+            }
+          }
+        } else {
+          logits(0, 0, s);
+          tc::commit(slot_free(s));
+          if (n == 1) tc::commit(q_free);
+          next_slot();
+          for (int j = 0; go && j < n; ++j) {
+            const int v_slot = s;
+            if (!(go = tc::bar_wait(slot_full(s), phase, &s_quit))) break;
+            next_slot();
+            if (j + 1 < n) {
+              if (!(go = tc::bar_wait(slot_full(s), phase, &s_quit))) break;
+              tc::fence_after();
+              logits(0, (j + 1) & 1, s);
+              tc::commit(slot_free(s));
+              if (j + 2 == n) tc::commit(q_free);
+              next_slot();
+            }
+            if (!(go = tc::bar_wait(p_full(j & 1), p_phase[j & 1], &s_quit))) break;
+            p_phase[j & 1] ^= 1;
+            tc::fence_after();
+            outputs(0, j & 1, v_slot, j == 0);
+            tc::commit(slot_free(v_slot));
+          }
+        }
+      }
+      // no product is left under way
+      volatile uint32_t ignore = 0;
+      tc::commit(drained);
+      tc::bar_wait(drained, 0, &ignore);
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------------
+    // softmax: a thread has a row
+    // ------------------------------------------------------------------
+    const int tile = wid >> 2, quarter = wid & 3;
+    const int r = tile * 128 + quarter * 32 + lane;
+    const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
+    const uint32_t o_at = tmem + S::kO + tile * D + lanes;
+    uint32_t full_phase[2] = {0, 0}, sums = 0, join_phase = 0;
+    uint32_t work = 0, steps = 0;
+    for (int round = 0; round < rounds; ++round) {
+      Piece x;
+      if (!piece_at(round, x)) break;
+      const int n = x.last - x.step;
+      const bool mine = tile * 128 < x.rows;       // uniform in the four warps
+      const int row = x.row + r;
+      const int pos = x.sp.len - x.sp.tokens + row / c.group;
+      const int khi = min(pos + 1, x.hi), klo = c.a.window ? max(0, pos + 1 - c.a.window) : 0;
+      // logits in powers of two: |scale| (its sign went into q) times log2 e
+      float factor = fabsf(c.a.scale) * kLog2e * (c.k_scale ? __ldg(c.k_scale + x.head) : 1.f);
+      factor = fmaxf(factor, 1.1754943508222875e-38f);   // 0 times a masked -infinity is NaN
+      float m = -INFINITY, l = 0.f;
+      if (mine && n > 0) {
+        // keys that all of the tile's rows see
+        const int t1 = x.sp.len - x.sp.tokens + (x.row + min(x.rows, tile * 128 + 128) - 1) / c.group;
+        const int t0 = x.sp.len - x.sp.tokens + (x.row + tile * 128) / c.group;
+        const int clear_lo = c.a.window ? max(0, t1 + 1 - c.a.window) : 0;
+        const int clear_hi = min(t0 + 1, x.hi);
+        for (int j = 0; j < n; ++j) {
+          const int at = S::kTiles == 2 ? tile : j & 1;
+          const int k0 = (x.step + j) * S::kKeys;
+          if (!tc::bar_wait(s_full(at), full_phase[at], &s_quit)) goto softmax_end;
+          full_phase[at] ^= 1;
+          tc::fence_after();
+          const uint32_t s_at = tmem + at * S::kKeys + lanes;
+          uint32_t v[S::kKeys];
+#pragma unroll
+          for (int i = 0; i < S::kKeys; i += 32) tc::ld32(s_at + i, v + i);
+          tc::ld_wait();
+          const uint32_t lost = s_bad[(steps + j) & 7];
+          if (k0 < clear_lo || k0 + S::kKeys > clear_hi || lost) {
+            const int a0 = klo - k0, a1 = khi - k0;
+#pragma unroll
+            for (int i = 0; i < S::kKeys; ++i)
+              if (i < a0 || i >= a1 || (lost >> (i >> 4) & 1)) v[i] = 0xff800000u;
+          }
+          float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int i = 0; i < S::kKeys; i += 4) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) top[e] = fmaxf(top[e], __uint_as_float(v[i + e]));
+          }
+          const float high = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * factor;
+          const bool moves = high > m + kSlack;
+          if (__any_sync(0xffffffffu, moves)) {
+            // the reference follows the maximum; what is added up so far with it
+            const float f = moves ? exp2_fast(m - high) : 1.f;
+            if (moves) m = high;
+            l *= f;
+            if (j > 0) {
+              if (S::kTiles == 1 && !tc::bar_wait(o_full(0), (sums + j - 1) & 1, &s_quit))
+                goto softmax_end;
+              tc::fence_after();
+#pragma unroll 1
+              for (int i = 0; i < D; i += 16) {
+                uint32_t o[16];
+                tc::ld16(o_at + i, o);
+                tc::ld_wait();
+#pragma unroll
+                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                tc::st16(o_at + i, o);
+              }
+            }
+          }
+          const float bias = kLift - (m == -INFINITY ? 0.f : m);
+          float add[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int i = 0; i < S::kKeys; i += 32) {
+            uint32_t w[16];
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) {
+              const float p0 = exp2_fast(fmaf(__uint_as_float(v[i + e]), factor, bias));
+              const float p1 = exp2_fast(fmaf(__uint_as_float(v[i + e + 1]), factor, bias));
+              add[e & 2] += p0;
+              add[(e & 2) + 1] += p1;
+              w[e / 2] = pack2<QT>(p0, p1);
+            }
+            tc::st16(s_at + i / 2, w);
+          }
+          l += (add[0] + add[1]) + (add[2] + add[3]);
+          tc::st_wait();
+          tc::fence_before();
+          tc::bar_arrive(p_full(at));
+        }
+        sums += n;
+        if (S::kTiles == 1 && n > 1 && !tc::bar_wait(o_full(0), sums & 1, &s_quit)) goto softmax_end;
+        if (!tc::bar_wait(o_full(tile), (sums - 1) & 1, &s_quit)) goto softmax_end;
+        tc::fence_after();
+      }
+      steps += n;
+      work += n > 0;
+      const bool odd = n > 0 && s_odd[work & 3] == work;
+      const bool whole = x.count == 1;
+      const float v_scale = c.v_scale ? __ldg(c.v_scale + x.head) : 1.f;
+      if (mine && !odd) {
+        const bool in = r < x.rows;
+        const int t = x.sp.first + row / c.group, head = x.head * c.group + row % c.group;
+        const long long line = (long long)t * c.heads + head;
+        if (whole) {
+          const float sink = in && c.a.sinks ? __ldg(c.a.sinks + head) : -INFINITY;
+          const Close z = close_row(m, l, sink, kLift);
+          const float f = z.scale * v_scale;
+          if (in && c.a.lse) c.a.lse[line] = z.lse;
+          uint4* out = reinterpret_cast<uint4*>(static_cast<uint16_t*>(c.a.out) + line * D);
+#pragma unroll 1
+          for (int i = 0; i < D; i += 16) {
+            uint32_t o[16];
+            tc::ld16(o_at + i, o);
+            tc::ld_wait();
+            uint32_t w[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              w[e] = z.scale == 0.f ? 0u
+                                    : pack2<QT>(__uint_as_float(o[2 * e]) * f,
+                                                __uint_as_float(o[2 * e + 1]) * f);
+            if (in) {
+              out[i / 8] = make_uint4(w[0], w[1], w[2], w[3]);
+              out[i / 8 + 1] = make_uint4(w[4], w[5], w[6], w[7]);
+            }
+          }
+        } else {
+          float* part = c.part_o + ((size_t)x.slot * S::kRows + r) * D;
+#pragma unroll 1
+          for (int i = 0; i < D; i += 16) {
+            uint32_t o[16];
+            tc::ld16(o_at + i, o);
+            tc::ld_wait();
+            if (in) {
+#pragma unroll
+              for (int e = 0; e < 16; e += 4)
+                *reinterpret_cast<uint4*>(part + i + e) =
+                    make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+            }
+          }
+          if (in) {
+            float* ml = c.part_ml + (size_t)x.slot * 2 * S::kRows + r;
+            ml[0] = m;
+            ml[S::kRows] = l;
+          }
+        }
+        tc::fence_before();
+      } else if (mine) {
+        // row by row: the warp's 32 rows
+        for (int i = 0; i < 32; ++i) {
+          const int rr = tile * 128 + quarter * 32 + i, one = x.row + rr;
+          if (rr >= x.rows) break;
+          const int p = x.sp.len - x.sp.tokens + one / c.group;
+          const int h1 = min(min(p + 1, x.hi), x.last * S::kKeys);
+          const int h0 = max(c.a.window ? max(0, p + 1 - c.a.window) : 0, x.step * S::kKeys);
+          float o[D / 32], m1, l1;
+          plain_row<D, CT, QT>(c, x, one, factor, h0, h1, kLift, o, m1, l1);
+          const int t = x.sp.first + one / c.group, head = x.head * c.group + one % c.group;
+          const long long line = (long long)t * c.heads + head;
+          if (whole) {
+            const float sink = c.a.sinks ? __ldg(c.a.sinks + head) : -INFINITY;
+            const Close z = close_row(m1, l1, sink, kLift);
+            if (lane == 0 && c.a.lse) c.a.lse[line] = z.lse;
+            for (int e = 0; e < D / 32; ++e) {
+              const float y = z.scale == 0.f ? 0.f : o[e] * z.scale * v_scale;
+              static_cast<uint16_t*>(c.a.out)[line * D + lane + 32 * e] =
+                  (uint16_t)pack2<QT>(y, 0.f);
+            }
+          } else {
+            for (int e = 0; e < D / 32; ++e)
+              c.part_o[((size_t)x.slot * S::kRows + rr) * D + lane + 32 * e] = o[e];
+            if (lane == 0) {
+              float* ml = c.part_ml + (size_t)x.slot * 2 * S::kRows + rr;
+              ml[0] = m1;
+              ml[S::kRows] = l1;
+            }
+          }
+        }
+      }
+      if (!whole) {
+        // the last piece of an item to arrive adds them up, in order
+        __threadfence();
+        tc::bar_arrive(join);
+        if (!tc::bar_wait(join, join_phase, &s_quit)) goto softmax_end;
+        join_phase ^= 1;
+        if (tid == 0) {
+          const uint32_t before = atomicAdd(c.arrived + x.item, 1);
+          s_last = before == (uint32_t)x.count - 1;
+          if (s_last) c.arrived[x.item] = 0;
+          __threadfence();
+        }
+        tc::bar_arrive(join);
+        if (!tc::bar_wait(join, join_phase, &s_quit)) goto softmax_end;
+        join_phase ^= 1;
+        if (s_last) {
+          __threadfence();
+          constexpr int kPer = D / 32;
+          const int first = x.slot - x.index;
+          for (int rr = wid; rr < x.rows; rr += 8) {
+            const int one = x.row + rr;
+            const int t = x.sp.first + one / c.group, head = x.head * c.group + one % c.group;
+            const long long line = (long long)t * c.heads + head;
+            float top = -INFINITY, all = 0.f, o[kPer];
+            for (int e = 0; e < kPer; ++e) o[e] = 0.f;
+            for (int i = 0; i < x.count; ++i)
+              top = fmaxf(top, __ldcg(c.part_ml + (size_t)(first + i) * 2 * S::kRows + rr));
+            const float ref = top == -INFINITY ? 0.f : top;
+            for (int i = 0; i < x.count; ++i) {
+              const float* ml = c.part_ml + (size_t)(first + i) * 2 * S::kRows + rr;
+              const float f = exp2_fast(__ldcg(ml) - ref);
+              const float li = __ldcg(ml + S::kRows);
+              all += li * f;
+              const float* part = c.part_o + ((size_t)(first + i) * S::kRows + rr) * D + lane * kPer;
+              if (f == 0.f && li == li) continue;
+#pragma unroll
+              for (int e = 0; e < kPer; ++e) o[e] += __ldcg(part + e) * f;
+            }
+            const float sink = c.a.sinks ? __ldg(c.a.sinks + head) : -INFINITY;
+            const Close z = close_row(top, all, sink, kLift);
+            if (lane == 0 && c.a.lse) c.a.lse[line] = z.lse;
+            uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(c.a.out) + line * D +
+                                                        lane * kPer);
+            const float f = z.scale * v_scale;
+#pragma unroll
+            for (int e = 0; e < kPer; e += 2)
+              out[e / 2] = z.scale == 0.f ? 0u : pack2<QT>(o[e] * f, o[e + 1] * f);
+          }
+        }
+      }
+    }
+  softmax_end:
+    (void)0;
+  }
+  __syncthreads();
+  if (wid == 11) tc::tmem_free(tmem, 512);
+  if (tid == 0 && s_quit) atomicOr(c.err, kErrTimeout);
 }
 
 template <int D, int CT, int QT>
 cudaError_t chunk_as(const moe_reader_kv& kv, const moe_reader_kv_chunk_args& a, cudaStream_t s) {
-  const long long rows = (long long)a.tokens * kv.cfg.num_q_heads;
-  chunk_row_kernel<D, CT, QT><<<(unsigned)((rows + kRowWarps - 1) / kRowWarps), kRowWarps * 32, 0,
-                                s>>>(a, kv.k, kv.v, kv.k_scale, kv.v_scale, kv.cfg.num_q_heads,
-                                     kv.cfg.num_kv_heads, kv.page_shift, kv.cfg.num_pages, kv.err);
+  ChunkCall c;
+  c.a = a;
+  c.k = static_cast<const char*>(kv.k);
+  c.v = static_cast<const char*>(kv.v);
+  c.k_scale = kv.k_scale;
+  c.v_scale = kv.v_scale;
+  c.part_o = kv.chunk_o;
+  c.part_ml = kv.chunk_ml;
+  c.arrived = kv.chunk_arrived;
+  c.err = kv.err;
+  c.heads = kv.cfg.num_q_heads;
+  c.kv_heads = kv.cfg.num_kv_heads;
+  c.group = kv.group;
+  c.shift = kv.page_shift;
+  c.pool = kv.cfg.num_pages;
+  c.wide = reinterpret_cast<uintptr_t>(a.q) % 16 == 0 && a.q_token_stride % 8 == 0 &&
+           a.q_head_stride % 8 == 0 && !(a.scale < 0.f);
+  chunk_kernel<D, CT, QT><<<kv.sms, kChunkThreads, ChunkShape<D>::kSmem, s>>>(c);
   return cudaGetLastError();
 }
 
 template <int D>
 cudaError_t chunk_dim(const moe_reader_kv& kv, const moe_reader_kv_chunk_args& a, cudaStream_t s) {
-  constexpr int B = MOE_READER_TYPE_BF16, H = MOE_READER_TYPE_F16, E = MOE_READER_TYPE_E4M3;
-  if (kv.cfg.cache_type == B) return chunk_as<D, B, B>(kv, a, s);
-  if (kv.cfg.cache_type == H) return chunk_as<D, H, H>(kv, a, s);
-  return a.q_type == B ? chunk_as<D, E, B>(kv, a, s) : chunk_as<D, E, H>(kv, a, s);
+  if (kv.cfg.cache_type == kBf16) return chunk_as<D, kBf16, kBf16>(kv, a, s);
+  if (kv.cfg.cache_type == kF16) return chunk_as<D, kF16, kF16>(kv, a, s);
+  return a.q_type == kBf16 ? chunk_as<D, kE4m3, kBf16>(kv, a, s) : chunk_as<D, kE4m3, kF16>(kv, a, s);
+}
+
+template <int D, int CT, int QT> cudaError_t configure_as() {
+  return cudaFuncSetAttribute(chunk_kernel<D, CT, QT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              (int)ChunkShape<D>::kSmem);
+}
+template <int D> cudaError_t configure_dim(int type) {
+  if (type == kBf16) return configure_as<D, kBf16, kBf16>();
+  if (type == kF16) return configure_as<D, kF16, kF16>();
+  const cudaError_t e = configure_as<D, kE4m3, kBf16>();
+  return e != cudaSuccess ? e : configure_as<D, kE4m3, kF16>();
 }
 
 }  // namespace
+
+int chunk_rows(const moe_reader_kv_config& c) {
+  return c.head_dim <= 128 ? ChunkShape<128>::kRows : ChunkShape<256>::kRows;
+}
+
+cudaError_t configure_kv_chunk(const moe_reader_kv& kv) {
+  switch (kv.cfg.head_dim) {
+    case 64: return configure_dim<64>(kv.cfg.cache_type);
+    case 128: return configure_dim<128>(kv.cfg.cache_type);
+    default: return configure_dim<256>(kv.cfg.cache_type);
+  }
+}
 
 cudaError_t launch_kv_chunk(const moe_reader_kv& kv, const moe_reader_kv_chunk_args& a,
                             cudaStream_t s) {
