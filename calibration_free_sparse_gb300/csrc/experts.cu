@@ -1,6 +1,7 @@
 // A prompt's experts: pairs (token, slot) sorted by expert, and products grouped
 // by expert over ragged numbers of rows.
 #include <stdlib.h>
+#include <string.h>
 
 #include <algorithm>
 
@@ -462,12 +463,12 @@ cudaError_t configure_experts(moe_reader_experts& h) {
   const uint64_t H = h.cfg.hidden, I = h.cfg.inter, E = h.cfg.num_experts;
   cudaError_t e = cudaSuccess;
   if (h.gate) {
-    e = tc::make_map(&h.gate_map, h.gate, bf16, H, I, E, 128);
-    if (e == cudaSuccess) e = tc::make_map(&h.up_map, h.up, bf16, H, I, E, 128);
+    e = tc::make_map(&h.gate_map, h.gate, bf16, H, I, E, 0, 128);
+    if (e == cudaSuccess) e = tc::make_map(&h.up_map, h.up, bf16, H, I, E, 0, 128);
     if (e == cudaSuccess) e = bf16 ? configure_group<true, true>() : configure_group<false, true>();
   }
   if (e == cudaSuccess && h.down) {
-    e = tc::make_map(&h.down_map, h.down, bf16, I, H, E, 128);
+    e = tc::make_map(&h.down_map, h.down, bf16, I, H, E, 0, 128);
     if (e == cudaSuccess)
       e = bf16 ? configure_group<true, false>() : configure_group<false, false>();
   }
@@ -534,8 +535,11 @@ int moe_reader_experts_create(const moe_reader_experts_config* c, const void* ga
   if (!gate != !up || (!gate && !down)) return MOE_READER_EINVAL;
   if (!at_multiple(gate, 16) || !at_multiple(up, 16) || !at_multiple(down, 16))
     return MOE_READER_EINVAL;
-  moe_reader_experts* h = static_cast<moe_reader_experts*>(calloc(1, sizeof(moe_reader_experts)));
+  // (tensor maps want 64-byte alignment)
+  moe_reader_experts* h = static_cast<moe_reader_experts*>(
+      aligned_alloc(alignof(moe_reader_experts), sizeof(moe_reader_experts)));
   if (!h) return MOE_READER_ENOMEM;
+  memset(h, 0, sizeof(moe_reader_experts));
   h->cfg = *c;
   h->gate = gate;
   h->up = up;

@@ -1,6 +1,7 @@
 // Declarations shared by the paged cache's translation units.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -29,6 +30,7 @@ struct moe_reader_kv {
   size_t arrived_bytes;
   float* chunk_o;             // [sms][chunk_rows][D]  unnormalised outputs of a chunk's pieces
   float* chunk_ml;            // [sms][2][chunk_rows]  their references and sums of weights
+  CUtensorMap chunk_maps[2];  // of keys and values, 16-bit caches
   uint32_t* chunk_arrived;    // [kMaxSms]        pieces written, behind `arrived`
   uint32_t* err;              // [1]              device error word
 };
@@ -60,7 +62,7 @@ cudaError_t launch_kv_select(const moe_reader_kv& kv, const moe_reader_kv_select
 cudaError_t configure_kv_select(const moe_reader_kv& kv);
 cudaError_t launch_kv_chunk(const moe_reader_kv& kv, const moe_reader_kv_chunk_args& a,
                             cudaStream_t s);
-cudaError_t configure_kv_chunk(const moe_reader_kv& kv);
+cudaError_t configure_kv_chunk(moe_reader_kv& kv);
 int chunk_rows(const moe_reader_kv_config& c);      // rows of an item of kv_chunk
 cudaError_t launch_kv_collect(const moe_reader_kv& kv, const moe_reader_kv_pages_args& a,
                               cudaStream_t s);

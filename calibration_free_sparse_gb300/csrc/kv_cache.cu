@@ -755,8 +755,11 @@ int moe_reader_kv_create(const moe_reader_kv_config* cfg, void* k, void* v, int8
   const bool e4m3 = cfg->cache_type == MOE_READER_TYPE_E4M3;
   if (e4m3 != (k_scale != nullptr) || e4m3 != (v_scale != nullptr)) return MOE_READER_EINVAL;
   if (!at_multiple(k_scale, 4) || !at_multiple(v_scale, 4)) return MOE_READER_EINVAL;
-  moe_reader_kv* kv = static_cast<moe_reader_kv*>(calloc(1, sizeof(moe_reader_kv)));
+  // (tensor maps want 64-byte alignment)
+  moe_reader_kv* kv =
+      static_cast<moe_reader_kv*>(aligned_alloc(alignof(moe_reader_kv), sizeof(moe_reader_kv)));
   if (!kv) return MOE_READER_ENOMEM;
+  memset(kv, 0, sizeof(moe_reader_kv));
   kv->cfg = *cfg;
   kv->k = k;
   kv->v = v;
@@ -773,12 +776,13 @@ int moe_reader_kv_create(const moe_reader_kv_config* cfg, void* k, void* v, int8
   const size_t items = (size_t)cfg->max_requests * cfg->num_kv_heads * mr::attend_row_tiles(*cfg);
   const size_t item_bytes = (items * 4 + 255) & ~(size_t)255;
   const size_t c_bytes = item_bytes + mr::kMaxSms * 4;
-  cudaError_t ce = cudaDeviceGetAttribute(&kv->sms, cudaDevAttrMultiProcessorCount, kv->device);
+  const cudaError_t counted =
+      cudaDeviceGetAttribute(&kv->sms, cudaDevAttrMultiProcessorCount, kv->device);
   kv->sms = std::min(kv->sms, mr::kMaxSms);
   const size_t chunk_rows = (size_t)kv->sms * mr::chunk_rows(*cfg);
   const size_t zeroed = o_bytes + ml_bytes + c_bytes + 256;
   const size_t bytes = zeroed + chunk_rows * (cfg->head_dim + 2) * sizeof(float);
-  if (ce == cudaSuccess) ce = mr::device_alloc(&kv->base, bytes);
+  cudaError_t ce = mr::device_alloc(&kv->base, bytes);
   if (ce != cudaSuccess) {
     free(kv);
     return status_of(ce);
@@ -793,6 +797,7 @@ int moe_reader_kv_create(const moe_reader_kv_config* cfg, void* k, void* v, int8
   kv->chunk_o = reinterpret_cast<float*>(b + zeroed);
   kv->chunk_ml = kv->chunk_o + chunk_rows * cfg->head_dim;
   do {
+    if ((ce = counted) != cudaSuccess) break;
     if ((ce = mr::configure_kv_attend(*kv)) != cudaSuccess) break;
     if ((ce = mr::configure_kv_select(*kv)) != cudaSuccess) break;
     if ((ce = mr::configure_kv_pages()) != cudaSuccess) break;

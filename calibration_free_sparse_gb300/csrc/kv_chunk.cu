@@ -61,9 +61,7 @@ __device__ __forceinline__ Span span_of(const moe_reader_kv_chunk_args& a, int r
 // has two buffers).  Four warps a row tile: a thread has a row, so maxima and
 // sums need no exchange.  Three warps bring pages, one issues products.
 // ---------------------------------------------------------------------------
-constexpr int kLoaderWarps = 3;
-constexpr int kLoaders = 32 * kLoaderWarps;
-constexpr int kChunkThreads = 256 + kLoaders + 32;     // 12 warps: 168 registers a thread
+constexpr int kChunkThreads = 384;                     // 12 warps: 168 registers a thread
 constexpr int kMaxPieces = kMaxSms;
 
 template <int D> struct ChunkShape {
@@ -91,6 +89,7 @@ struct ChunkCall {
   uint32_t* err;
   int heads, kv_heads, group, shift, pool;
   int wide;                  // q can be copied 16 bytes at a time
+  CUtensorMap k_map, v_map;  // of 16-bit caches
 };
 
 // Part of an item: the rows [row, row + rows) of a request's (token, head of
@@ -140,6 +139,25 @@ __device__ __forceinline__ Piece item_at(const ChunkCall& c, const int* blocks, 
   x.slot = 0;
   item_range<D>(c, x);
   return x;
+}
+
+// Whether some row of the piece does not see all of a step's keys.
+template <int D>
+__device__ __forceinline__ bool partial_step(const ChunkCall& c, const Piece& x, int k0) {
+  const int lo = c.a.window ? max(0, x.p1 + 1 - c.a.window) : 0, hi = min(x.p0 + 1, x.hi);
+  return k0 < lo || k0 + ChunkShape<D>::kKeys > hi;
+}
+
+__device__ __forceinline__ void put_smem(uint32_t at, uint32_t x, uint32_t y, uint32_t z,
+                                         uint32_t w) {
+  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};"
+               :: "r"(at), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+__device__ __forceinline__ uint4 get_smem(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+  return v;
 }
 
 // One row without the tensor core, for pieces whose masked values are not
@@ -206,7 +224,7 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
   constexpr float kSlack = QT == kF16 ? 4.f : 8.f;     // how far a logit may pass the reference
   extern __shared__ char raw[];
   __shared__ int s_blocks[kMaxRequests + 1], s_pieces[kMaxPieces + 1];
-  __shared__ uint64_t s_bar[2 * S::kSlots + 10];
+  __shared__ uint64_t s_bar[4 * S::kSlots + 10];
   // by piece with keys and by step, in turn: loaders are at most two pieces and
   // kSlots / 2 + 1 steps ahead of softmax
   __shared__ volatile uint32_t s_odd[4], s_bad[8];
@@ -218,7 +236,9 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
   const uint32_t bars = tc::smem_at(s_bar);
   auto slot_full = [&](int s) { return bars + 8 * s; };
   auto slot_free = [&](int s) { return bars + 8 * (S::kSlots + s); };
-  const uint32_t more = bars + 16 * S::kSlots;
+  auto cleaned = [&](int s) { return bars + 8 * (2 * S::kSlots + s); };
+  auto landed = [&](int s) { return bars + 8 * (3 * S::kSlots + s); };
+  const uint32_t more = bars + 32 * S::kSlots;
   auto s_full = [&](int t) { return more + 8 * t; };          // logits of a tile are there
   auto p_full = [&](int t) { return more + 16 + 8 * t; };     // its weights are
   auto o_full = [&](int t) { return more + 32 + 8 * t; };     // they are added up
@@ -234,7 +254,9 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
   if (bad && blockIdx.x == 0) atomicOr(c.err, bad);
   if (tid == 0) {
     for (int s = 0; s < S::kSlots; ++s) {
-      tc::bar_init(slot_full(s), kLoaders);
+      tc::bar_init(slot_full(s), CT == kE4m3 ? 96 : 1);
+      tc::bar_init(cleaned(s), 64);
+      tc::bar_init(landed(s), 1);
       tc::bar_init(slot_free(s), 1);
     }
     for (int t = 0; t < 2; ++t) {
@@ -242,7 +264,7 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
       tc::bar_init(p_full(t), 128);
       tc::bar_init(o_full(t), 1);
     }
-    tc::bar_init(q_full, kLoaders);
+    tc::bar_init(q_full, CT == kE4m3 ? 96 : 64);
     tc::bar_init(q_free, 1);
     tc::bar_init(join, 256);
     tc::bar_init(drained, 1);
@@ -341,191 +363,226 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
     // ------------------------------------------------------------------
     // loaders
     // ------------------------------------------------------------------
-    // a warp's copy covers four rows of 128 bytes; the warps take those in turn
-    const int id = tid - 256, who = wid - 8, piece = lane & 7, sub = lane >> 3;
-    constexpr int kTurns = (S::kKeys / 4 + kLoaderWarps - 1) / kLoaderWarps;
-    int s = 0, late = 0, behind = 0;
-    uint32_t phase = 1, q_phase = 1, check = 0, err = 0;   // check: bit i: i-th oldest late slot
-    uint32_t late_work[2] = {0, 0}, work = 0, steps = 0;
-    constexpr int kLag = 2;
-    // hands the oldest slot over (16-bit caches: its copies have landed)
-    auto hand_over = [&]() {
-      if (check & 1) {
-        bool odd = false;
-        for (int b = 0; b < S::kBlocks; ++b)
-          for (int r = who * 4 + sub; r < S::kKeys; r += kLoaderWarps * 4) {
-            const uint32_t at = kv_at + late * S::kSlotBytes + b * S::kKeys * 128 +
-                                tc::swizzled(r, piece);
-            uint4 v;
-            asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-                         : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at));
-            odd |= odd8<QT>(v);
-          }
-        if (odd) s_odd[late_work[0] & 3] = late_work[0];
-      }
-      check >>= 1;
-      late_work[0] = late_work[1];
-      tc::publish_smem();
-      tc::bar_arrive(slot_full(late));
-      if (++late == S::kSlots) late = 0;
-    };
-    for (int round = 0; round < rounds; ++round) {
-      Piece x;
-      if (!piece_at(round, x)) break;
-      if (x.step >= x.last) continue;
-      work++;
-      // queries; the last products with those before want their keys first
-      tc::copies_wait<0>();
-      for (; behind > 0; --behind) hand_over();
-      if (!tc::bar_wait(q_free, q_phase, &s_quit)) goto loaders_end;
+    // 16-bit caches: one warp brings pages by tensor copies, two the queries,
+    // and these clear values that are in a page but not there (a page ends
+    // inside the step, or is gone).  e4m3: all three bring both.
+    constexpr bool kCopies = CT != kE4m3;
+    const int who = wid - (kCopies ? 9 : 8), warps = kCopies ? 2 : 3;
+    int s = 0;
+    uint32_t phase = 1, q_phase = 1, work = 0, steps = 0, err = 0;
+    uint32_t cleared = 0, clear_phase = 0;     // a bit per slot
+    // queries of a piece
+    auto queries = [&](const Piece& x) {
+      if (!tc::bar_wait(q_free, q_phase, &s_quit)) return false;
       q_phase ^= 1;
-      {
-        const uint16_t flip = c.a.scale < 0.f ? 0x8000 : 0;
-        for (int r = who * 4 + sub; r < S::kRows; r += kLoaderWarps * 4) {
-          const int row = x.row + r;
-          const bool in = r < x.rows;
-          const long long at = in ? (long long)(x.sp.first + row / c.group) * c.a.q_token_stride +
-                                        (long long)(x.head * c.group + row % c.group) *
-                                            c.a.q_head_stride + piece * 8
-                                  : 0;
-          const uint16_t* from = static_cast<const uint16_t*>(c.a.q) + at;
-          const uint32_t to = q_at + (r >> 7) * (S::kBlocks << 14) + tc::swizzled(r & 127, piece);
-          if (c.wide) {
+      const int piece = lane & 7;
+      const uint16_t flip = c.a.scale < 0.f ? 0x8000 : 0;
+      for (int r = who * 4 + (lane >> 3); r < S::kRows; r += warps * 4) {
+        const int row = x.row + r;
+        const bool in = r < x.rows;
+        const long long at = in ? (long long)(x.sp.first + row / c.group) * c.a.q_token_stride +
+                                      (long long)(x.head * c.group + row % c.group) *
+                                          c.a.q_head_stride + piece * 8
+                                : 0;
+        const uint16_t* from = static_cast<const uint16_t*>(c.a.q) + at;
+        const uint32_t to = q_at + (r >> 7) * (S::kBlocks << 14) + tc::swizzled(r & 127, piece);
+        if (c.wide) {
 #pragma unroll
-            for (int b = 0; b < S::kBlocks; ++b)
-              tc::copy16(to + (b << 14), in ? from + b * 64 : from, in);
-          } else {
-            for (int b = 0; b < S::kBlocks; ++b) {
-              uint32_t w[4];
+          for (int b = 0; b < S::kBlocks; ++b)
+            tc::copy16(to + (b << 14), in ? from + b * 64 : from, in);
+        } else {
+          for (int b = 0; b < S::kBlocks; ++b) {
+            uint32_t w[4];
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const uint16_t e0 = in ? __ldg(from + b * 64 + 2 * i) ^ flip : 0;
-                const uint16_t e1 = in ? __ldg(from + b * 64 + 2 * i + 1) ^ flip : 0;
-                w[i] = (uint32_t)e0 | (uint32_t)e1 << 16;
+            for (int i = 0; i < 4; ++i) {
+              const uint16_t e0 = in ? __ldg(from + b * 64 + 2 * i) ^ flip : 0;
+              const uint16_t e1 = in ? __ldg(from + b * 64 + 2 * i + 1) ^ flip : 0;
+              w[i] = (uint32_t)e0 | (uint32_t)e1 << 16;
+            }
+            put_smem(to + (b << 14), w[0], w[1], w[2], w[3]);
+          }
+        }
+      }
+      tc::copies_commit();
+      tc::copies_wait<0>();
+      tc::publish_smem();
+      tc::bar_arrive(q_full);
+      return true;
+    };
+    // lane l has the page of keys 16 l.. of a step: -2 not in the pool, -1 out
+    // of sight (it may be gone)
+    auto page_of = [&](const Piece& x, int step) {
+      const int key = step * S::kKeys + lane * 16;
+      if (lane < S::kKeys / 16 && key < x.hi && ((key >> c.shift) + 1) << c.shift > x.lo) {
+        const int p =
+            __ldg(c.a.table + (size_t)x.request * c.a.width + (key >> c.shift));
+        return (unsigned)p < (unsigned)c.pool ? p : -2;
+      }
+      return -1;
+    };
+    if constexpr (kCopies) {
+      if (wid == 8) {
+        const int rows = min(1 << c.shift, S::kKeys), boxes = S::kKeys / rows;
+        for (int round = 0; round < rounds; ++round) {
+          Piece x;
+          if (!piece_at(round, x)) break;
+          if (x.step >= x.last) continue;
+          int next = page_of(x, x.step);
+          for (int step = x.step; step < x.last; ++step) {
+            const int page = next, k0 = step * S::kKeys;
+            if (step + 1 < x.last) next = page_of(x, step + 1);
+            const uint32_t lost = __ballot_sync(0xffffffffu, page == -2);
+            if (lost) err |= kErrPage;
+            if (lane == 0) s_bad[steps & 7] = lost;
+            steps++;
+            // lane l has box l; pages that are not there are read as zeros
+            int from = __shfl_sync(0xffffffffu, page, (lane * rows >> 4) & 31);
+            if (from < 0) from = c.pool;
+            const bool partial = partial_step<D>(c, x, k0);
+#pragma unroll
+            for (int kind = 0; kind < 2; ++kind) {
+              if (!tc::bar_wait(slot_free(s), phase, &s_quit)) goto loaders_end;
+              // values to be cleared first have a barrier of their own
+              const bool clear = kind && partial;
+              const uint32_t bar = clear ? landed(s) : slot_full(s);
+              if (lane == 0) {
+                tc::bar_expect(bar, S::kSlotBytes);
+                if (clear) tc::bar_arrive(slot_full(s));
               }
-              asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};"
-                           :: "r"(to + (b << 14)), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
-                           : "memory");
+              if (clear) cleared |= 1u << s, clear_phase ^= 1u << s;
+              __syncwarp();
+              if (lane < boxes) {
+                const uint32_t to = kv_at + s * S::kSlotBytes + lane * rows * 128;
+#pragma unroll
+                for (int b = 0; b < S::kBlocks; ++b)
+                  tc::load_box(to + b * S::kKeys * 128, kind ? &c.v_map : &c.k_map, b * 64,
+                               k0 & ((1 << c.shift) - 1), x.head, from, bar);
+              }
+              if (++s == S::kSlots) s = 0, phase ^= 1;
             }
           }
         }
-        tc::copies_commit();
-        tc::copies_wait<0>();
-        tc::publish_smem();
-        tc::bar_arrive(q_full);
-      }
-      // keys and values: lane l has the page of keys 16 l.. of the step
-      const int32_t* row = c.a.table + (size_t)x.request * c.a.width;
-      auto page_of = [&](int step) {
-        const int key = step * S::kKeys + lane * 16;
-        // a page all of whose rows are out of sight may be gone
-        if (lane < S::kKeys / 16 && key < x.hi && ((key >> c.shift) + 1) << c.shift > x.lo) {
-          const int p = __ldg(row + (key >> c.shift));
-          if ((unsigned)p < (unsigned)c.pool) return p;
-          return -2;
-        }
-        return -1;
-      };
-      int next = page_of(x.step);
-      const int clear_lo = c.a.window ? max(0, x.p1 + 1 - c.a.window) : 0;
-      const int clear_hi = min(x.p0 + 1, x.hi);
-      for (int step = x.step; step < x.last; ++step) {
-        const int page = next, k0 = step * S::kKeys;
-        if (step + 1 < x.last) next = page_of(step + 1);
-        const uint32_t lost = __ballot_sync(0xffffffffu, page == -2);
-        if (lost) err |= kErrPage;
-        const bool partial = k0 < clear_lo || k0 + S::kKeys > clear_hi;
-        if (id == 0) s_bad[steps & 7] = lost;
-        steps++;
-#pragma unroll 1
-        for (int kind = 0; kind < 2; ++kind) {
-          const char* base = kind ? c.v : c.k;
-          if constexpr (CT != kE4m3) {
-            if (!tc::bar_wait(slot_free(s), phase, &s_quit)) goto loaders_end;
-            const uint32_t to = kv_at + s * S::kSlotBytes;
-#pragma unroll
-            for (int i = 0; i < kTurns; ++i) {
-              const int r = (i * kLoaderWarps + who) * 4 + sub;
-              if ((i + 1) * kLoaderWarps * 4 > S::kKeys && r >= S::kKeys) break;
-              const int p = __shfl_sync(0xffffffffu, page, r >> 4);
-              const int key = k0 + r;
-              const bool in = p >= 0 && key >= x.lo && key < x.hi;
-              const char* from = base;
-              if (in)
-                from += (((((long long)p * c.kv_heads + x.head) << c.shift) +
-                          (key & ((1 << c.shift) - 1))) * D + piece * 8) * 2;
-#pragma unroll
-              for (int b = 0; b < S::kBlocks; ++b)
-                tc::copy16(to + b * S::kKeys * 128 + tc::swizzled(r, piece),
-                           in ? from + b * 128 : from, in);
-            }
-            tc::copies_commit();
-            if (behind == kLag) {
-              tc::copies_wait<kLag>();
-              hand_over();
-            } else {
-              behind++;
-            }
-            late_work[behind - 1] = work;
-            if (kind && partial) check |= 1u << (behind - 1);
-          } else {
-            // 16 e4m3 values a thread and row piece, widened on the way: both
-            // 16-bit types hold them exactly
-            constexpr int kRow = D / 16, kSub = 32 / kRow;
-            constexpr int kN = (S::kKeys / kSub + kLoaderWarps - 1) / kLoaderWarps;
-            const int piece = lane % kRow, sub = lane / kRow;
-            uint4 v[kN];
-#pragma unroll
-            for (int i = 0; i < kN; ++i) {
-              const int r = (i * kLoaderWarps + who) * kSub + sub, key = k0 + r;
-              const int p = __shfl_sync(0xffffffffu, page, (r >> 4) & 31);
-              v[i] = make_uint4(0, 0, 0, 0);
-              if (r < S::kKeys && p >= 0 && key >= x.lo && key < x.hi)
-                v[i] = ldg_stream(reinterpret_cast<const uint4*>(
-                    base + ((((long long)p * c.kv_heads + x.head) << c.shift) +
-                            (key & ((1 << c.shift) - 1))) * D + piece * 16));
-            }
-            if (!tc::bar_wait(slot_free(s), phase, &s_quit)) goto loaders_end;
-            const uint32_t to = kv_at + s * S::kSlotBytes + (piece >> 2) * S::kKeys * 128;
-            bool odd = false;
-#pragma unroll
-            for (int i = 0; i < kN; ++i) {
-              const int r = (i * kLoaderWarps + who) * kSub + sub;
-              if (r >= S::kKeys) break;
-              const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-              uint32_t o[8];
-#pragma unroll
-              for (int j = 0; j < 8; ++j) {
-                const uint32_t two = w[j >> 1] >> (16 * (j & 1)) & 0xffff;
-                const __half2 h(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3));
-                odd |= (two & 0x7f) == 0x7f || (two & 0x7f00) == 0x7f00;
-                if constexpr (QT == kBf16) {
-                  const float2 f = __half22float2(h);
-                  o[j] = pack2<kBf16>(f.x, f.y);
-                } else {
-                  o[j] = *reinterpret_cast<const uint32_t*>(&h);
+      } else {
+        for (int round = 0; round < rounds; ++round) {
+          Piece x;
+          if (!piece_at(round, x)) break;
+          if (x.step >= x.last) continue;
+          work++;
+          if (!queries(x)) goto loaders_end;
+          for (int step = x.step; step < x.last; ++step) {
+            const int k0 = step * S::kKeys;
+            s = (s + 1) % S::kSlots;
+            if (partial_step<D>(c, x, k0)) {
+              const int page = page_of(x, step);
+              if (!tc::bar_wait(landed(s), clear_phase >> s & 1, &s_quit)) goto loaders_end;
+              clear_phase ^= 1u << s;
+              bool odd = false;
+              for (int r = who * 4 + (lane >> 3); r < S::kKeys; r += warps * 4) {
+                const int key = k0 + r;
+                const bool in = __shfl_sync(0xffffffffu, page, r >> 4) >= 0 && key >= x.lo &&
+                                key < x.hi;
+                for (int b = 0; b < S::kBlocks; ++b) {
+                  const uint32_t at = kv_at + s * S::kSlotBytes + b * S::kKeys * 128 +
+                                      tc::swizzled(r, lane & 7);
+                  if (in) odd |= odd8<QT>(get_smem(at));
+                  else put_smem(at, 0, 0, 0, 0);
                 }
               }
-#pragma unroll
-              for (int j = 0; j < 2; ++j)
-                asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};"
-                             :: "r"(to + tc::swizzled(r, (piece & 3) * 2 + j)),
-                                "r"(o[4 * j]), "r"(o[4 * j + 1]), "r"(o[4 * j + 2]),
-                                "r"(o[4 * j + 3])
-                             : "memory");
+              if (odd) s_odd[work & 3] = work;
+              tc::publish_smem();
+              tc::bar_arrive(cleaned(s));
             }
-            if (odd && kind && partial) s_odd[work & 3] = work;
-            tc::publish_smem();
-            tc::bar_arrive(slot_full(s));
+            s = (s + 1) % S::kSlots;
           }
-          if (++s == S::kSlots) s = 0, phase ^= 1;
+        }
+      }
+    } else {
+      // 16 values a thread and copy, widened on the way: both 16-bit types hold
+      // them exactly.  A step's values are requested before its keys are
+      // widened, the next step's keys before its values are.
+      constexpr int kRow = D / 16, kSub = 32 / kRow;
+      constexpr int kN = (S::kKeys / kSub + 2) / 3;
+      const int piece = lane % kRow, sub = lane / kRow;
+      auto fetch = [&](const Piece& x, const char* base, int k0, int page, uint4 (&v)[kN]) {
+#pragma unroll
+        for (int i = 0; i < kN; ++i) {
+          const int r = (i * 3 + who) * kSub + sub, key = k0 + r;
+          const int p = __shfl_sync(0xffffffffu, page, (r >> 4) & 31);
+          const bool in = p >= 0 && key >= x.lo && key < x.hi;
+          // (no branch: the loads go out together)
+          const long long at =
+              ((((long long)(in ? p : 0) * c.kv_heads + x.head) << c.shift) +
+               (key & ((1 << c.shift) - 1))) * D + piece * 16;
+          const uint4 w = ldg_stream(reinterpret_cast<const uint4*>(base + at));
+          v[i] = in && r < S::kKeys ? w : make_uint4(0, 0, 0, 0);
+        }
+      };
+      auto widen = [&](const uint4 (&v)[kN], bool watch) {
+        if (!tc::bar_wait(slot_free(s), phase, &s_quit)) return false;
+        const uint32_t to = kv_at + s * S::kSlotBytes + (piece >> 2) * S::kKeys * 128;
+        bool odd = false;
+#pragma unroll
+        for (int i = 0; i < kN; ++i) {
+          const int r = (i * 3 + who) * kSub + sub;
+          if (r >= S::kKeys) break;
+          const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+          uint32_t o[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const uint32_t two = w[j >> 1] >> (16 * (j & 1)) & 0xffff;
+            const __half2 h(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3));
+            odd |= (two & 0x7f) == 0x7f || (two & 0x7f00) == 0x7f00;
+            if constexpr (QT == kBf16) {
+              const float2 f = __half22float2(h);
+              o[j] = pack2<kBf16>(f.x, f.y);
+            } else {
+              o[j] = *reinterpret_cast<const uint32_t*>(&h);
+            }
+          }
+          put_smem(to + tc::swizzled(r, (piece & 3) * 2), o[0], o[1], o[2], o[3]);
+          put_smem(to + tc::swizzled(r, (piece & 3) * 2 + 1), o[4], o[5], o[6], o[7]);
+        }
+        if (odd && watch) s_odd[work & 3] = work;
+        tc::publish_smem();
+        tc::bar_arrive(slot_full(s));
+        if (++s == S::kSlots) s = 0, phase ^= 1;
+        return true;
+      };
+      uint4 keys[kN], values[kN];
+      for (int round = 0; round < rounds; ++round) {
+        Piece x;
+        if (!piece_at(round, x)) break;
+        if (x.step >= x.last) continue;
+        work++;
+        int next = page_of(x, x.step);
+        fetch(x, c.k, x.step * S::kKeys, next, keys);
+        if (!queries(x)) goto loaders_end;
+        for (int step = x.step; step < x.last; ++step) {
+          const int page = next, k0 = step * S::kKeys;
+          if (step + 1 < x.last) next = page_of(x, step + 1);
+          const uint32_t lost = __ballot_sync(0xffffffffu, page == -2);
+          if (lost) err |= kErrPage;
+          if (tid == 256) s_bad[steps & 7] = lost;
+          steps++;
+          fetch(x, c.v, k0, page, values);
+          if (!widen(keys, false)) goto loaders_end;
+          if (step + 1 < x.last) fetch(x, c.k, k0 + S::kKeys, next, keys);
+          if (!widen(values, partial_step<D>(c, x, k0))) goto loaders_end;
         }
       }
     }
   loaders_end:
     tc::copies_wait<0>();
-    for (; behind > 0; --behind) hand_over();
-    if (err && id == 0) atomicOr(c.err, err);
+    if (kCopies && wid == 8) {
+      // no copy is left under way
+      for (int i = 0; i < (int)min(2 * steps, (uint32_t)S::kSlots); ++i) {
+        if (--s < 0) s = S::kSlots - 1, phase ^= 1;
+        volatile uint32_t ignore = 0;
+        tc::bar_wait(slot_full(s), phase ^ 1, &ignore);
+        if (cleared >> s & 1) tc::bar_wait(landed(s), ~clear_phase >> s & 1, &ignore);
+      }
+    }
+    if (err && lane == 0 && wid == 8) atomicOr(c.err, err);
   } else if (wid == 11) {
     // ------------------------------------------------------------------
     // products
@@ -535,6 +592,15 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
       constexpr uint32_t o_desc = tc::instr<QT == kBf16>(D, true);
       int s = 0;
       uint32_t phase = 0, q_phase = 0, p_phase[2] = {0, 0};
+      uint32_t clean_phase = 0;                    // a bit per slot
+      // a step's values: there, and cleared where they have to be
+      auto values_in = [&](const Piece& x, int step) {
+        if (CT == kE4m3 || !partial_step<D>(c, x, step * S::kKeys))
+          return tc::bar_wait(slot_full(s), phase, &s_quit);
+        const uint32_t want = clean_phase >> s & 1;
+        clean_phase ^= 1u << s;
+        return tc::bar_wait(cleaned(s), want, &s_quit);
+      };
       auto next_slot = [&]() { if (++s == S::kSlots) s = 0, phase ^= 1; };
       auto logits = [&](int tile, int at, int slot) {
         const uint32_t q = q_at + tile * (S::kBlocks << 14), k = kv_at + slot * S::kSlotBytes;
@@ -569,7 +635,7 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
           next_slot();
           for (int j = 0; go && j < n; ++j) {
             const int v_slot = s;
-            if (!(go = tc::bar_wait(slot_full(s), phase, &s_quit))) break;
+            if (!(go = values_in(x, x.step + j))) break;
             next_slot();
             if (j + 1 < n && !(go = tc::bar_wait(slot_full(s), phase, &s_quit))) break;
             for (int t = 0; t < tiles; ++t) {
@@ -594,7 +660,7 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
           next_slot();
           for (int j = 0; go && j < n; ++j) {
             const int v_slot = s;
-            if (!(go = tc::bar_wait(slot_full(s), phase, &s_quit))) break;
+            if (!(go = values_in(x, x.step + j))) break;
             next_slot();
             if (j + 1 < n) {
               if (!(go = tc::bar_wait(slot_full(s), phase, &s_quit))) break;
@@ -879,6 +945,8 @@ cudaError_t chunk_as(const moe_reader_kv& kv, const moe_reader_kv_chunk_args& a,
   c.pool = kv.cfg.num_pages;
   c.wide = reinterpret_cast<uintptr_t>(a.q) % 16 == 0 && a.q_token_stride % 8 == 0 &&
            a.q_head_stride % 8 == 0 && !(a.scale < 0.f);
+  c.k_map = kv.chunk_maps[0];
+  c.v_map = kv.chunk_maps[1];
   chunk_kernel<D, CT, QT><<<kv.sms, kChunkThreads, ChunkShape<D>::kSmem, s>>>(c);
   return cudaGetLastError();
 }
@@ -907,7 +975,15 @@ int chunk_rows(const moe_reader_kv_config& c) {
   return c.head_dim <= 128 ? ChunkShape<128>::kRows : ChunkShape<256>::kRows;
 }
 
-cudaError_t configure_kv_chunk(const moe_reader_kv& kv) {
+cudaError_t configure_kv_chunk(moe_reader_kv& kv) {
+  const moe_reader_kv_config& g = kv.cfg;
+  const uint32_t keys = g.head_dim <= 128 ? 128 : 64;
+  for (int i = 0; i < 2 && g.cache_type != kE4m3; ++i) {
+    const cudaError_t e = tc::make_map(
+        &kv.chunk_maps[i], i ? kv.v : kv.k, g.cache_type == kBf16, g.head_dim, g.page_size,
+        g.num_kv_heads, g.num_pages, std::min<uint32_t>(g.page_size, keys));
+    if (e != cudaSuccess) return e;
+  }
   switch (kv.cfg.head_dim) {
     case 64: return configure_dim<64>(kv.cfg.cache_type);
     case 128: return configure_dim<128>(kv.cfg.cache_type);
