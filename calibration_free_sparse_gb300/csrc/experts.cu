@@ -231,40 +231,42 @@ group_kernel(const __grid_constant__ CUtensorMap map0, const __grid_constant__ C
     __syncwarp();
   } else if (wid == 1) {
     // products
-    if (lane == 0) {
-      int s = 0, set = 0;
-      uint32_t phase = 0, set_phase = 1;
-      bool go = true;
-      for (int t = blockIdx.x; go && t < tiles; t += gridDim.x) {
-        const Tile x = tile_at(t);
-        const uint32_t idesc = tc::instr<kBf16>((x.rows + 15) & ~15);
-        const uint32_t d = tmem + set * 2 * N;
-        if (!(go = tc::bar_wait(sums_free(set), set_phase, &s_quit))) break;
+    int s = 0, set = 0;
+    uint32_t phase = 0, set_phase = 1;
+    bool go = true;
+    for (int t = blockIdx.x; go && t < tiles; t += gridDim.x) {
+      const Tile x = tile_at(t);
+      const uint32_t idesc = tc::instr<kBf16>((x.rows + 15) & ~15);
+      const uint32_t d = tmem + set * 2 * N;
+      if (!(go = tc::bar_wait(sums_free(set), set_phase, &s_quit))) break;
+      tc::fence_after();
+      for (int k = 0; k < k_steps; ++k) {
+        if (!(go = tc::bar_wait(weights_in(s), phase, &s_quit) &&
+                   tc::bar_wait(rows_in(s), phase, &s_quit)))
+          break;
         tc::fence_after();
-        for (int k = 0; k < k_steps; ++k) {
-          if (!(go = tc::bar_wait(weights_in(s), phase, &s_quit) &&
-                     tc::bar_wait(rows_in(s), phase, &s_quit)))
-            break;
-          tc::fence_after();
-          const uint64_t a0 = tc::desc_k(stage_at(s)), a1 = tc::desc_k(stage_at(s) + kBoxBytes);
-          const uint64_t b = tc::desc_k(stage_at(s) + 2 * kBoxBytes);
+        const uint64_t a0 = tc::desc_k(stage_at(s)), a1 = tc::desc_k(stage_at(s) + kBoxBytes);
+        const uint64_t b = tc::desc_k(stage_at(s) + 2 * kBoxBytes);
+        const uint32_t bar = stage_free(s), last = k == k_steps - 1 ? sums_done(set) : 0;
+        if (tc::elected()) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             tc::mma(d, a0 + 2 * i, b + 2 * i, idesc, k + i > 0);
             tc::mma(d + N, a1 + 2 * i, b + 2 * i, idesc, k + i > 0);
           }
-          tc::commit(stage_free(s));
-          if (++s == S::kStages) s = 0, phase ^= 1;
+          tc::commit(bar);
+          if (last) tc::commit(last);
         }
-        if (!go) break;
-        tc::commit(sums_done(set));
-        if (++set == S::kSets) set = 0, set_phase ^= 1;
+        __syncwarp();
+        if (++s == S::kStages) s = 0, phase ^= 1;
       }
-      tc::commit(drained);
-      volatile uint32_t ignore = 0;
-      tc::bar_wait(drained, 0, &ignore);
+      if (!go) break;
+      if (++set == S::kSets) set = 0, set_phase ^= 1;
     }
+    if (tc::elected()) tc::commit(drained);
     __syncwarp();
+    volatile uint32_t ignore = 0;
+    tc::bar_wait(drained, 0, &ignore);
   } else if (wid >= 4 && wid < 8) {
     // the plan rows' inputs: eight threads a row of 128 bytes, 16 rows at once
     const int id = tid - 128, piece = id & 7, sub = id >> 3;

@@ -587,103 +587,106 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
     // ------------------------------------------------------------------
     // products
     // ------------------------------------------------------------------
-    if (lane == 0) {
-      constexpr uint32_t s_desc = tc::instr<QT == kBf16>(S::kKeys);
-      constexpr uint32_t o_desc = tc::instr<QT == kBf16>(D, true);
-      int s = 0;
-      uint32_t phase = 0, q_phase = 0, p_phase[2] = {0, 0};
-      uint32_t clean_phase = 0;                    // a bit per slot
-      // a step's values: there, and cleared where they have to be
-      auto values_in = [&](const Piece& x, int step) {
-        if (CT == kE4m3 || !partial_step<D>(c, x, step * S::kKeys))
-          return tc::bar_wait(slot_full(s), phase, &s_quit);
-        const uint32_t want = clean_phase >> s & 1;
-        clean_phase ^= 1u << s;
-        return tc::bar_wait(cleaned(s), want, &s_quit);
-      };
-      auto next_slot = [&]() { if (++s == S::kSlots) s = 0, phase ^= 1; };
-      auto logits = [&](int tile, int at, int slot) {
-        const uint32_t q = q_at + tile * (S::kBlocks << 14), k = kv_at + slot * S::kSlotBytes;
+    constexpr uint32_t s_desc = tc::instr<QT == kBf16>(S::kKeys);
+    constexpr uint32_t o_desc = tc::instr<QT == kBf16>(D, true);
+    int s = 0;
+    uint32_t phase = 0, q_phase = 0, p_phase[2] = {0, 0};
+    uint32_t clean_phase = 0;                    // a bit per slot
+    // a step's values: there, and cleared where they have to be
+    auto values_in = [&](const Piece& x, int step) {
+      if (CT == kE4m3 || !partial_step<D>(c, x, step * S::kKeys))
+        return tc::bar_wait(slot_full(s), phase, &s_quit);
+      const uint32_t want = clean_phase >> s & 1;
+      clean_phase ^= 1u << s;
+      return tc::bar_wait(cleaned(s), want, &s_quit);
+    };
+    auto next_slot = [&]() { if (++s == S::kSlots) s = 0, phase ^= 1; };
+    // S of a row tile; afterwards up to two barriers more
+    auto logits = [&](int tile, int at, int slot, uint32_t then, uint32_t then2) {
+      const uint64_t q = tc::desc_k(q_at + tile * (S::kBlocks << 14));
+      const uint64_t k = tc::desc_k(kv_at + slot * S::kSlotBytes);
+      const uint32_t d = tmem + at * S::kKeys, bar = s_full(at);
+      if (tc::elected()) {
 #pragma unroll
         for (int i = 0; i < D / 16; ++i)
-          tc::mma(tmem + at * S::kKeys, tc::desc_k(q + (i >> 2 << 14)) + 2 * (i & 3),
-                  tc::desc_k(k + (i >> 2) * S::kKeys * 128) + 2 * (i & 3), s_desc, i > 0);
-        tc::commit(s_full(at));
-      };
-      auto outputs = [&](int tile, int at, int slot, bool first) {
-        const uint32_t v = kv_at + slot * S::kSlotBytes;
+          tc::mma(d, q + ((i >> 2) << 10) + 2 * (i & 3), k + (i >> 2) * S::kKeys * 8 + 2 * (i & 3),
+                  s_desc, i > 0);
+        tc::commit(bar);
+        if (then) tc::commit(then);
+        if (then2) tc::commit(then2);
+      }
+      __syncwarp();
+    };
+    auto outputs = [&](int tile, int at, int slot, bool first, uint32_t then) {
+      const uint64_t v = tc::desc_mn(kv_at + slot * S::kSlotBytes, S::kKeys * 128);
+      const uint32_t d = tmem + S::kO + tile * D, p = tmem + at * S::kKeys, bar = o_full(tile);
+      if (tc::elected()) {
 #pragma unroll
         for (int i = 0; i < S::kKeys / 16; ++i)
-          tc::mma_ta(tmem + S::kO + tile * D, tmem + at * S::kKeys + i * 8,
-                     tc::desc_mn(v + i * 2048, S::kKeys * 128), o_desc, !first || i > 0);
-        tc::commit(o_full(tile));
-      };
-      bool go = true;
-      for (int round = 0; go && round < rounds; ++round) {
-        Piece x;
-        if (!piece_at(round, x)) break;
-        if (x.step >= x.last) continue;
-        const int tiles = x.rows > 128 ? 2 : 1, n = x.last - x.step;
-        if (!(go = tc::bar_wait(q_full, q_phase, &s_quit))) break;
-        q_phase ^= 1;
-        if (!(go = tc::bar_wait(slot_full(s), phase, &s_quit))) break;
-        tc::fence_after();
-        if constexpr (S::kTiles == 2) {
-          for (int t = 0; t < tiles; ++t) logits(t, t, s);
-          tc::commit(slot_free(s));
-          if (n == 1) tc::commit(q_free);
+          tc::mma_ta(d, p + i * 8, v + i * 128, o_desc, !first || i > 0);
+        tc::commit(bar);
+        if (then) tc::commit(then);
+      }
+      __syncwarp();
+    };
+    bool go = true;
+    for (int round = 0; go && round < rounds; ++round) {
+      Piece x;
+      if (!piece_at(round, x)) break;
+      if (x.step >= x.last) continue;
+      const int tiles = x.rows > 128 ? 2 : 1, n = x.last - x.step;
+      if (!(go = tc::bar_wait(q_full, q_phase, &s_quit))) break;
+      q_phase ^= 1;
+      if (!(go = tc::bar_wait(slot_full(s), phase, &s_quit))) break;
+      tc::fence_after();
+      if constexpr (S::kTiles == 2) {
+        for (int t = 0; t < tiles; ++t) {
+          const bool end = t == tiles - 1;
+          logits(t, t, s, end ? slot_free(s) : 0, end && n == 1 ? q_free : 0);
+        }
+        next_slot();
+        for (int j = 0; go && j < n; ++j) {
+          const int v_slot = s;
+          if (!(go = values_in(x, x.step + j))) break;
           next_slot();
-          for (int j = 0; go && j < n; ++j) {
-            const int v_slot = s;
-            if (!(go = values_in(x, x.step + j))) break;
-            next_slot();
-            if (j + 1 < n && !(go = tc::bar_wait(slot_full(s), phase, &s_quit))) break;
-            for (int t = 0; t < tiles; ++t) {
-              if (!(go = tc::bar_wait(p_full(t), p_phase[t], &s_quit))) break;
-              p_phase[t] ^= 1;
-              tc::fence_after();
-              outputs(t, t, v_slot, j == 0);
-              if (t == tiles - 1) tc::commit(slot_free(v_slot));
-              if (j + 1 < n) logits(t, t, s);
-            }
-            if (!go) break;
-            if (j + 1 < n) {
-              tc::commit(slot_free(s));
-              if (j + 2 == n) tc::commit(q_free);
-              next_slot();
-            }
-          }
-        } else {
-          logits(0, 0, s);
-          tc::commit(slot_free(s));
-          if (n == 1) tc::commit(q_free);
-          next_slot();
-          for (int j = 0; go && j < n; ++j) {
-            const int v_slot = s;
-            if (!(go = values_in(x, x.step + j))) break;
-            next_slot();
-            if (j + 1 < n) {
-              if (!(go = tc::bar_wait(slot_full(s), phase, &s_quit))) break;
-              tc::fence_after();
-              logits(0, (j + 1) & 1, s);
-              tc::commit(slot_free(s));
-              if (j + 2 == n) tc::commit(q_free);
-              next_slot();
-            }
-            if (!(go = tc::bar_wait(p_full(j & 1), p_phase[j & 1], &s_quit))) break;
-            p_phase[j & 1] ^= 1;
+          if (j + 1 < n && !(go = tc::bar_wait(slot_full(s), phase, &s_quit))) break;
+          for (int t = 0; t < tiles; ++t) {
+            const bool end = t == tiles - 1;
+            if (!(go = tc::bar_wait(p_full(t), p_phase[t], &s_quit))) break;
+            p_phase[t] ^= 1;
             tc::fence_after();
-            outputs(0, j & 1, v_slot, j == 0);
-            tc::commit(slot_free(v_slot));
+            outputs(t, t, v_slot, j == 0, end ? slot_free(v_slot) : 0);
+            if (j + 1 < n)
+              logits(t, t, s, end ? slot_free(s) : 0, end && j + 2 == n ? q_free : 0);
           }
+          if (!go) break;
+          if (j + 1 < n) next_slot();
+        }
+      } else {
+        logits(0, 0, s, slot_free(s), n == 1 ? q_free : 0);
+        next_slot();
+        for (int j = 0; go && j < n; ++j) {
+          const int v_slot = s;
+          if (!(go = values_in(x, x.step + j))) break;
+          next_slot();
+          if (j + 1 < n) {
+            if (!(go = tc::bar_wait(slot_full(s), phase, &s_quit))) break;
+            tc::fence_after();
+            logits(0, (j + 1) & 1, s, slot_free(s), j + 2 == n ? q_free : 0);
+            next_slot();
+          }
+          if (!(go = tc::bar_wait(p_full(j & 1), p_phase[j & 1], &s_quit))) break;
+          p_phase[j & 1] ^= 1;
+          tc::fence_after();
+          outputs(0, j & 1, v_slot, j == 0, slot_free(v_slot));
         }
       }
-      // no product is left under way
-      volatile uint32_t ignore = 0;
-      tc::commit(drained);
-      tc::bar_wait(drained, 0, &ignore);
     }
+    // no product is left under way
+    volatile uint32_t ignore = 0;
+    if (tc::elected()) tc::commit(drained);
     __syncwarp();
+    tc::bar_wait(drained, 0, &ignore);
   } else {
     // ------------------------------------------------------------------
     // softmax: a thread has a row

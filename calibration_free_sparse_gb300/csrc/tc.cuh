@@ -14,6 +14,15 @@ __device__ __forceinline__ uint32_t smem_at(const void* p) {
   return (uint32_t)__cvta_generic_to_shared(p);
 }
 
+// One lane of a warp that runs together: what only one may do stands behind
+// this, and all else is the warp's, so that operands stay in uniform registers.
+__device__ __forceinline__ bool elected() {
+  uint32_t ok;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+               : "=r"(ok));
+  return ok;
+}
+
 // ---- mbarriers ----
 __device__ __forceinline__ void bar_init(uint32_t bar, int arrivals) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" :: "r"(bar), "r"(arrivals) : "memory");
