@@ -37,6 +37,23 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return y;
 }
 
+// n / d and the remainder for 0 <= n < 2^31 by a product: the estimate is at
+// most one too small.
+struct Divisor {
+  uint32_t d, m;
+};
+__host__ __device__ __forceinline__ Divisor divisor(uint32_t d) { return {d, 0xffffffffu / d}; }
+__device__ __forceinline__ int quotient(int n, Divisor by, int& rest) {
+  uint32_t q = __umulhi((uint32_t)n, by.m), r = (uint32_t)n - q * by.d;
+  if (r >= by.d) q++, r -= by.d;
+  rest = (int)r;
+  return (int)q;
+}
+__device__ __forceinline__ int quotient(int n, Divisor by) {
+  int rest;
+  return quotient(n, by, rest);
+}
+
 // A request's part of the call.
 struct Span {
   int first;        // its first row of q
@@ -87,7 +104,8 @@ struct ChunkCall {
   float* part_ml;            // [piece][2][kRows]
   uint32_t* arrived;         // [item]
   uint32_t* err;
-  int heads, kv_heads, group, shift, pool;
+  int heads, kv_heads, shift, pool;
+  Divisor by_group, by_kv;   // query heads per KV head, KV heads
   int wide;                  // q can be copied 16 bytes at a time
   CUtensorMap k_map, v_map;  // of 16-bit caches
 };
@@ -108,31 +126,36 @@ template <int D>
 __device__ __forceinline__ void item_range(const ChunkCall& c, Piece& x) {
   using S = ChunkShape<D>;
   const int before = x.sp.len - x.sp.tokens;
-  x.p0 = before + x.row / c.group;
-  x.p1 = before + (x.row + x.rows - 1) / c.group;
+  x.p0 = before + quotient(x.row, c.by_group);
+  x.p1 = before + quotient(x.row + x.rows - 1, c.by_group);
   x.lo = c.a.window ? max(0, x.p0 + 1 - c.a.window) : 0;
   x.hi = (int)min((long long)x.p1 + 1, (long long)c.a.width << c.shift);
   x.step = x.lo / S::kKeys;
   x.last = x.hi > x.lo ? (x.hi + S::kKeys - 1) / S::kKeys : x.step;
 }
 
+// What every role looks its pieces up in.
+struct Work {
+  int blocks[kMaxRequests + 1];       // a request's first block of rows
+  int first[kMaxRequests], tokens[kMaxRequests], len[kMaxRequests];
+  int pieces[kMaxPieces + 1];         // an item's first piece, where items are cut
+};
+
 // Item i: block of rows and KV head; the longest rows of a request first.
 template <int D>
-__device__ __forceinline__ Piece item_at(const ChunkCall& c, const int* blocks, int i) {
+__device__ __forceinline__ Piece item_at(const ChunkCall& c, const Work& w, int i) {
   using S = ChunkShape<D>;
-  const int b = i / c.kv_heads;
+  Piece x;
+  const int b = quotient(i, c.by_kv, x.head);
   int lo = 0, hi = c.a.requests - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if (blocks[mid] <= b) lo = mid; else hi = mid - 1;
+    if (w.blocks[mid] <= b) lo = mid; else hi = mid - 1;
   }
-  uint32_t ignore = 0;
-  Piece x;
-  x.sp = span_of(c.a, lo, ignore);
+  x.sp = {w.first[lo], w.tokens[lo], w.len[lo]};
   x.request = lo;
-  x.head = i - b * c.kv_heads;
-  x.row = (blocks[lo + 1] - 1 - b) * S::kRows;
-  x.rows = min(S::kRows, x.sp.tokens * c.group - x.row);
+  x.row = (w.blocks[lo + 1] - 1 - b) * S::kRows;
+  x.rows = min(S::kRows, x.sp.tokens * (int)c.by_group.d - x.row);
   x.item = i;
   x.index = 0;
   x.count = 1;
@@ -166,8 +189,9 @@ __device__ __forceinline__ uint4 get_smem(uint32_t at) {
 template <int D, int CT, int QT>
 __device__ __noinline__ void plain_row(const ChunkCall& c, const Piece& x, int row, float factor,
                                        int klo, int khi, float lift, float* o, float& m, float& l) {
-  const int lane = threadIdx.x & 31, t = x.sp.first + row / c.group;
-  const int head = x.head * c.group + row % c.group;
+  int head;
+  const int lane = threadIdx.x & 31, t = x.sp.first + quotient(row, c.by_group, head);
+  head += x.head * c.by_group.d;
   const long long q = t * c.a.q_token_stride + head * c.a.q_head_stride + lane;
   const float sign = c.a.scale < 0.f ? -1.f : 1.f;
   m = -INFINITY;
@@ -202,6 +226,48 @@ template <int QT> __device__ __forceinline__ bool odd8(uint4 v) {
   return odd;
 }
 
+// Two e4m3 values in the high bytes of the halves, widened: their bits moved to
+// where the type has exponent and mantissa are the value times 2^-120 (bf16) or
+// 2^-8 (fp16), subnormal ones too, and a product with a power of two is exact.
+// (The conversion instructions took four times as long.)  NaN becomes 480: a
+// step that holds one goes row by row.
+template <int QT> __device__ __forceinline__ uint32_t widen2(uint32_t v) {
+  uint32_t r;
+  if constexpr (QT == kBf16) {
+    const uint32_t t = (v >> 4 & 0x07f007f0u) | (v & 0x80008000u);
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(t), "r"(0x7b807b80u));
+  } else {
+    const uint32_t t = (v >> 1 & 0x3f803f80u) | (v & 0x80008000u);
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(t), "r"(0x5c005c00u));
+  }
+  return r;
+}
+
+// Pairs of fp32 in one instruction.
+__device__ __forceinline__ uint64_t pair(float x, float y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t p, float& x, float& y) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(p));
+}
+__device__ __forceinline__ uint64_t fma_pair(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add_pair(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
 // What a row adds up to with its sink: the factor of its sums, lse.
 struct Close {
   float scale, lse;
@@ -223,10 +289,11 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
   constexpr float kLift = QT == kF16 ? 11.f : 0.f;     // fp16 weights reach down to 2^-35
   constexpr float kSlack = QT == kF16 ? 4.f : 8.f;     // how far a logit may pass the reference
   extern __shared__ char raw[];
-  __shared__ int s_blocks[kMaxRequests + 1], s_pieces[kMaxPieces + 1];
-  __shared__ uint64_t s_bar[4 * S::kSlots + 10];
+  __shared__ Work work_list;
+  __shared__ uint64_t s_bar[4 * S::kSlots + 14];
+  __shared__ float s_twin[2][128];
   // by piece with keys and by step, in turn: loaders are at most two pieces and
-  // kSlots / 2 + 1 steps ahead of softmax
+  // kSlots / 2 + 2 steps ahead of softmax
   __shared__ volatile uint32_t s_odd[4], s_bad[8];
   __shared__ uint32_t s_tmem, s_last;
   __shared__ volatile uint32_t s_quit;
@@ -243,13 +310,19 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
   auto p_full = [&](int t) { return more + 16 + 8 * t; };     // its weights are
   auto o_full = [&](int t) { return more + 32 + 8 * t; };     // they are added up
   const uint32_t q_full = more + 48, q_free = more + 56, join = more + 64, drained = more + 72;
+  auto p_half = [&](int t) { return more + 80 + 8 * t; };     // the first half of its weights
+  const uint32_t twin = more + 96, twin_done = more + 104;   // the second four's sums, taken
 
   // ---- what there is to do: every CTA finds it out for itself ----
   uint32_t bad = 0;
   for (int r = tid; r < c.a.requests; r += kChunkThreads) {
     const Span sp = span_of(c.a, r, bad);
     if (sp.len > ((long long)c.a.width << c.shift)) bad |= kErrLength;
-    s_blocks[r] = (int)(((long long)sp.tokens * c.group + S::kRows - 1) / S::kRows);
+    work_list.first[r] = sp.first;
+    work_list.tokens[r] = sp.tokens;
+    work_list.len[r] = sp.len;
+    work_list.blocks[r] =
+        (int)(((long long)sp.tokens * c.by_group.d + S::kRows - 1) / S::kRows);
   }
   if (bad && blockIdx.x == 0) atomicOr(c.err, bad);
   if (tid == 0) {
@@ -262,12 +335,15 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
     for (int t = 0; t < 2; ++t) {
       tc::bar_init(s_full(t), 1);
       tc::bar_init(p_full(t), 128);
+      tc::bar_init(p_half(t), 128);
       tc::bar_init(o_full(t), 1);
     }
     tc::bar_init(q_full, CT == kE4m3 ? 96 : 64);
     tc::bar_init(q_free, 1);
     tc::bar_init(join, 256);
     tc::bar_init(drained, 1);
+    tc::bar_init(twin, 128);
+    tc::bar_init(twin_done, 128);
     for (int i = 0; i < 4; ++i) s_odd[i] = 0;
     s_quit = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -277,44 +353,46 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
   if (wid == 0) {
     int sum = 0;
     for (int r0 = 0; r0 <= c.a.requests; r0 += 32) {
-      const int r = r0 + lane, n = r < c.a.requests ? s_blocks[r] : 0;
+      const int r = r0 + lane, n = r < c.a.requests ? work_list.blocks[r] : 0;
       int at = n;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int u = __shfl_up_sync(0xffffffffu, at, o);
         if (lane >= o) at += u;
       }
-      if (r <= c.a.requests) s_blocks[r] = sum + at - n;
+      if (r <= c.a.requests) work_list.blocks[r] = sum + at - n;
       sum += __shfl_sync(0xffffffffu, at, 31);
     }
   }
   __syncthreads();
-  const long long items = (long long)s_blocks[c.a.requests] * c.kv_heads;
+  const long long items = (long long)work_list.blocks[c.a.requests] * c.kv_heads;
   const bool split = items <= min(grid, kMaxPieces);
   int pieces = (int)items;
   if (split) {
     // Few items: each is cut into pieces of at most `most` steps, the fewest
     // for which there are no more pieces than CTAs.
     for (int i = tid; i < items; i += kChunkThreads) {
-      const Piece x = item_at<D>(c, s_blocks, i);
-      s_pieces[i] = x.last - x.step;
+      const Piece x = item_at<D>(c, work_list, i);
+      work_list.pieces[i] = x.last - x.step;
     }
     __syncthreads();
     if (wid == 0) {
       int low = 4, high = 4;
-      for (int i = lane; i < items; i += 32) high = max(high, s_pieces[i]);
+      for (int i = lane; i < items; i += 32) high = max(high, work_list.pieces[i]);
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) high = max(high, __shfl_xor_sync(0xffffffffu, high, o));
       while (low < high) {
         const int mid = (low + high) >> 1;
+        const Divisor by = divisor(mid);
         int n = 0;
-        for (int i = lane; i < items; i += 32) n += max(1, (s_pieces[i] + mid - 1) / mid);
+        for (int i = lane; i < items; i += 32)
+          n += max(1, quotient(work_list.pieces[i] + mid - 1, by));
         if (warp_sum_i(n) <= min(grid, kMaxPieces)) high = mid; else low = mid + 1;
       }
       int sum = 0;
       for (int i0 = 0; i0 <= items; i0 += 32) {
         const int i = i0 + lane;
-        const int n = i < items ? max(1, (s_pieces[i] + high - 1) / high) : 0;
+        const int n = i < items ? max(1, (work_list.pieces[i] + high - 1) / high) : 0;
         int at = n;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -322,12 +400,12 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
           if (lane >= o) at += u;
         }
         __syncwarp();
-        if (i <= items) s_pieces[i] = sum + at - n;
+        if (i <= items) work_list.pieces[i] = sum + at - n;
         sum += __shfl_sync(0xffffffffu, at, 31);
       }
     }
     __syncthreads();
-    pieces = s_pieces[items];
+    pieces = work_list.pieces[items];
   }
   tc::fence_before();
   __syncthreads();
@@ -341,17 +419,17 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
     const int i = round * grid + (round & 1 ? grid - 1 - (int)blockIdx.x : (int)blockIdx.x);
     if (i >= pieces) return false;
     if (!split) {
-      x = item_at<D>(c, s_blocks, i);
+      x = item_at<D>(c, work_list, i);
       return true;
     }
     int lo = 0, hi = (int)items - 1;
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
-      if (s_pieces[mid] <= i) lo = mid; else hi = mid - 1;
+      if (work_list.pieces[mid] <= i) lo = mid; else hi = mid - 1;
     }
-    x = item_at<D>(c, s_blocks, lo);
-    x.index = i - s_pieces[lo];
-    x.count = s_pieces[lo + 1] - s_pieces[lo];
+    x = item_at<D>(c, work_list, lo);
+    x.index = i - work_list.pieces[lo];
+    x.count = work_list.pieces[lo + 1] - work_list.pieces[lo];
     x.slot = i;
     const int n = x.last - x.step, first = x.step;
     x.step = first + (int)((long long)n * x.index / x.count);
@@ -377,12 +455,14 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
       q_phase ^= 1;
       const int piece = lane & 7;
       const uint16_t flip = c.a.scale < 0.f ? 0x8000 : 0;
+#pragma unroll 4
       for (int r = who * 4 + (lane >> 3); r < S::kRows; r += warps * 4) {
-        const int row = x.row + r;
         const bool in = r < x.rows;
-        const long long at = in ? (long long)(x.sp.first + row / c.group) * c.a.q_token_stride +
-                                      (long long)(x.head * c.group + row % c.group) *
-                                          c.a.q_head_stride + piece * 8
+        int g;
+        const int t = x.sp.first + quotient(x.row + r, c.by_group, g);
+        const long long at = in ? t * c.a.q_token_stride +
+                                      (int)(x.head * c.by_group.d + g) * c.a.q_head_stride +
+                                      piece * 8
                                 : 0;
         const uint16_t* from = static_cast<const uint16_t*>(c.a.q) + at;
         const uint32_t to = q_at + (r >> 7) * (S::kBlocks << 14) + tc::swizzled(r & 127, piece);
@@ -477,15 +557,21 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
               if (!tc::bar_wait(landed(s), clear_phase >> s & 1, &s_quit)) goto loaders_end;
               clear_phase ^= 1u << s;
               bool odd = false;
-              for (int r = who * 4 + (lane >> 3); r < S::kKeys; r += warps * 4) {
-                const int key = k0 + r;
-                const bool in = __shfl_sync(0xffffffffu, page, r >> 4) >= 0 && key >= x.lo &&
-                                key < x.hi;
-                for (int b = 0; b < S::kBlocks; ++b) {
-                  const uint32_t at = kv_at + s * S::kSlotBytes + b * S::kKeys * 128 +
-                                      tc::swizzled(r, lane & 7);
-                  if (in) odd |= odd8<QT>(get_smem(at));
-                  else put_smem(at, 0, 0, 0, 0);
+#pragma unroll
+              for (int b = 0; b < S::kBlocks; ++b) {
+                constexpr int kTurns = S::kKeys / 8;
+                uint4 v[kTurns];
+                const uint32_t at = kv_at + s * S::kSlotBytes + b * S::kKeys * 128;
+#pragma unroll
+                for (int i = 0; i < kTurns; ++i)
+                  v[i] = get_smem(at + tc::swizzled(i * 8 + who * 4 + (lane >> 3), lane & 7));
+#pragma unroll
+                for (int i = 0; i < kTurns; ++i) {
+                  const int r = i * 8 + who * 4 + (lane >> 3), key = k0 + r;
+                  const bool in = __shfl_sync(0xffffffffu, page, i >> 1) >= 0 && key >= x.lo &&
+                                  key < x.hi;
+                  if (in) odd |= odd8<QT>(v[i]);
+                  else put_smem(at + tc::swizzled(r, lane & 7), 0, 0, 0, 0);
                 }
               }
               if (odd) s_odd[work & 3] = work;
@@ -517,10 +603,10 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
           v[i] = in && r < S::kKeys ? w : make_uint4(0, 0, 0, 0);
         }
       };
-      auto widen = [&](const uint4 (&v)[kN], bool watch) {
+      auto widen = [&](const uint4 (&v)[kN]) {
         if (!tc::bar_wait(slot_free(s), phase, &s_quit)) return false;
         const uint32_t to = kv_at + s * S::kSlotBytes + (piece >> 2) * S::kKeys * 128;
-        bool odd = false;
+        uint32_t odd = 0;
 #pragma unroll
         for (int i = 0; i < kN; ++i) {
           const int r = (i * 3 + who) * kSub + sub;
@@ -528,21 +614,15 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
           const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
           uint32_t o[8];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const uint32_t two = w[j >> 1] >> (16 * (j & 1)) & 0xffff;
-            const __half2 h(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3));
-            odd |= (two & 0x7f) == 0x7f || (two & 0x7f00) == 0x7f00;
-            if constexpr (QT == kBf16) {
-              const float2 f = __half22float2(h);
-              o[j] = pack2<kBf16>(f.x, f.y);
-            } else {
-              o[j] = *reinterpret_cast<const uint32_t*>(&h);
-            }
+          for (int j = 0; j < 4; ++j) {
+            odd |= (w[j] & 0x7f7f7f7fu) + 0x01010101u;
+            o[2 * j] = widen2<QT>(__byte_perm(w[j], 0, 0x1404));
+            o[2 * j + 1] = widen2<QT>(__byte_perm(w[j], 0, 0x3424));
           }
           put_smem(to + tc::swizzled(r, (piece & 3) * 2), o[0], o[1], o[2], o[3]);
           put_smem(to + tc::swizzled(r, (piece & 3) * 2 + 1), o[4], o[5], o[6], o[7]);
         }
-        if (odd && watch) s_odd[work & 3] = work;
+        if (odd & 0x80808080u) s_odd[work & 3] = work;
         tc::publish_smem();
         tc::bar_arrive(slot_full(s));
         if (++s == S::kSlots) s = 0, phase ^= 1;
@@ -565,9 +645,9 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
           if (tid == 256) s_bad[steps & 7] = lost;
           steps++;
           fetch(x, c.v, k0, page, values);
-          if (!widen(keys, false)) goto loaders_end;
+          if (!widen(keys)) goto loaders_end;
           if (step + 1 < x.last) fetch(x, c.k, k0 + S::kKeys, next, keys);
-          if (!widen(values, partial_step<D>(c, x, k0))) goto loaders_end;
+          if (!widen(values)) goto loaders_end;
         }
       }
     }
@@ -617,17 +697,31 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
       }
       __syncwarp();
     };
+    // O += P V, the first half of the keys as soon as its weights are there
     auto outputs = [&](int tile, int at, int slot, bool first, uint32_t then) {
+      const uint32_t want = p_phase[at];
+      p_phase[at] ^= 1;
+      if (!tc::bar_wait(p_half(at), want, &s_quit)) return false;
+      tc::fence_after();
       const uint64_t v = tc::desc_mn(kv_at + slot * S::kSlotBytes, S::kKeys * 128);
       const uint32_t d = tmem + S::kO + tile * D, p = tmem + at * S::kKeys, bar = o_full(tile);
       if (tc::elected()) {
 #pragma unroll
-        for (int i = 0; i < S::kKeys / 16; ++i)
+        for (int i = 0; i < S::kKeys / 32; ++i)
           tc::mma_ta(d, p + i * 8, v + i * 128, o_desc, !first || i > 0);
+      }
+      __syncwarp();
+      if (!tc::bar_wait(p_full(at), want, &s_quit)) return false;
+      tc::fence_after();
+      if (tc::elected()) {
+#pragma unroll
+        for (int i = S::kKeys / 32; i < S::kKeys / 16; ++i)
+          tc::mma_ta(d, p + i * 8, v + i * 128, o_desc, true);
         tc::commit(bar);
         if (then) tc::commit(then);
       }
       __syncwarp();
+      return true;
     };
     bool go = true;
     for (int round = 0; go && round < rounds; ++round) {
@@ -639,46 +733,50 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
       q_phase ^= 1;
       if (!(go = tc::bar_wait(slot_full(s), phase, &s_quit))) break;
       tc::fence_after();
-      if constexpr (S::kTiles == 2) {
-        for (int t = 0; t < tiles; ++t) {
-          const bool end = t == tiles - 1;
-          logits(t, t, s, end ? slot_free(s) : 0, end && n == 1 ? q_free : 0);
-        }
+      if (S::kTiles == 2 && tiles == 2) {
+        for (int t = 0; t < 2; ++t)
+          logits(t, t, s, t ? slot_free(s) : 0, t && n == 1 ? q_free : 0);
         next_slot();
         for (int j = 0; go && j < n; ++j) {
           const int v_slot = s;
           if (!(go = values_in(x, x.step + j))) break;
           next_slot();
           if (j + 1 < n && !(go = tc::bar_wait(slot_full(s), phase, &s_quit))) break;
-          for (int t = 0; t < tiles; ++t) {
-            const bool end = t == tiles - 1;
-            if (!(go = tc::bar_wait(p_full(t), p_phase[t], &s_quit))) break;
-            p_phase[t] ^= 1;
-            tc::fence_after();
-            outputs(t, t, v_slot, j == 0, end ? slot_free(v_slot) : 0);
-            if (j + 1 < n)
-              logits(t, t, s, end ? slot_free(s) : 0, end && j + 2 == n ? q_free : 0);
+          for (int t = 0; t < 2; ++t) {
+            if (!(go = outputs(t, t, v_slot, j == 0, t ? slot_free(v_slot) : 0))) break;
+            if (j + 1 < n) logits(t, t, s, t ? slot_free(s) : 0, t && j + 2 == n ? q_free : 0);
           }
-          if (!go) break;
-          if (j + 1 < n) next_slot();
+          if (go && j + 1 < n) next_slot();
         }
       } else {
-        logits(0, 0, s, slot_free(s), n == 1 ? q_free : 0);
-        next_slot();
+        // one tile of rows: its steps take the two S in turn, and, where they
+        // fit, two O (whose sums softmax joins)
+        const int ahead = S::kTiles;
+        uint32_t k_phase = phase;
+        int k_slot = s, asked = 0;
+        auto ask = [&]() {
+          logits(0, asked & 1, k_slot, slot_free(k_slot), asked == n - 1 ? q_free : 0);
+          asked++;
+          for (int i = 0; i < 2; ++i)
+            if (++k_slot == S::kSlots) k_slot = 0, k_phase ^= 1;
+        };
+        ask();
         for (int j = 0; go && j < n; ++j) {
-          const int v_slot = s;
-          if (!(go = values_in(x, x.step + j))) break;
           next_slot();
-          if (j + 1 < n) {
-            if (!(go = tc::bar_wait(slot_full(s), phase, &s_quit))) break;
+          // S of the next step, unless its weights are still wanted
+          if (asked < n && asked == j + 1) {
+            if (!(go = tc::bar_wait(slot_full(k_slot), k_phase, &s_quit))) break;
             tc::fence_after();
-            logits(0, (j + 1) & 1, s, slot_free(s), j + 2 == n ? q_free : 0);
-            next_slot();
+            ask();
           }
-          if (!(go = tc::bar_wait(p_full(j & 1), p_phase[j & 1], &s_quit))) break;
-          p_phase[j & 1] ^= 1;
-          tc::fence_after();
-          outputs(0, j & 1, v_slot, j == 0, slot_free(v_slot));
+          if (!(go = values_in(x, x.step + j))) break;
+          if (!(go = outputs(ahead == 2 ? j & 1 : 0, j & 1, s, j < ahead, slot_free(s)))) break;
+          if (ahead == 2 && asked < n) {
+            if (!(go = tc::bar_wait(slot_full(k_slot), k_phase, &s_quit))) break;
+            tc::fence_after();
+            ask();
+          }
+          next_slot();
         }
       }
     }
@@ -692,30 +790,37 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
     // softmax: a thread has a row
     // ------------------------------------------------------------------
     const int tile = wid >> 2, quarter = wid & 3;
-    const int r = tile * 128 + quarter * 32 + lane;
     const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
     const uint32_t o_at = tmem + S::kO + tile * D + lanes;
-    uint32_t full_phase[2] = {0, 0}, sums = 0, join_phase = 0;
+    uint32_t full_phase[2] = {0, 0}, sums = 0, join_phase = 0, twin_phase = 0;
     uint32_t work = 0, steps = 0;
     for (int round = 0; round < rounds; ++round) {
       Piece x;
       if (!piece_at(round, x)) break;
       const int n = x.last - x.step;
-      const bool mine = tile * 128 < x.rows;       // uniform in the four warps
-      const int row = x.row + r;
-      const int pos = x.sp.len - x.sp.tokens + row / c.group;
+      // One tile of rows: both fours have it, and every other step each.
+      const bool twins = S::kTiles == 2 && x.rows <= 128;
+      const int r = (twins ? 0 : tile * 128) + quarter * 32 + lane;
+      const int first = twins ? tile : 0, stride = twins ? 2 : 1;
+      const int own = twins ? (n - tile + 1) >> 1 : tile * 128 < x.rows ? n : 0;   // its steps
+      int group_head;
+      const int token = quotient(x.row + r, c.by_group, group_head);
+      const int pos = x.sp.len - x.sp.tokens + token;
       const int khi = min(pos + 1, x.hi), klo = c.a.window ? max(0, pos + 1 - c.a.window) : 0;
       // logits in powers of two: |scale| (its sign went into q) times log2 e
       float factor = fabsf(c.a.scale) * kLog2e * (c.k_scale ? __ldg(c.k_scale + x.head) : 1.f);
       factor = fmaxf(factor, 1.1754943508222875e-38f);   // 0 times a masked -infinity is NaN
       float m = -INFINITY, l = 0.f;
-      if (mine && n > 0) {
+      if (own > 0) {
         // keys that all of the tile's rows see
-        const int t1 = x.sp.len - x.sp.tokens + (x.row + min(x.rows, tile * 128 + 128) - 1) / c.group;
-        const int t0 = x.sp.len - x.sp.tokens + (x.row + tile * 128) / c.group;
+        const int r0 = twins ? 0 : tile * 128;
+        const int t0 = x.sp.len - x.sp.tokens + quotient(x.row + r0, c.by_group);
+        const int t1 =
+            x.sp.len - x.sp.tokens + quotient(x.row + min(x.rows, r0 + 128) - 1, c.by_group);
         const int clear_lo = c.a.window ? max(0, t1 + 1 - c.a.window) : 0;
         const int clear_hi = min(t0 + 1, x.hi);
-        for (int j = 0; j < n; ++j) {
+        for (int turn = 0; turn < own; ++turn) {
+          const int j = first + turn * stride;
           const int at = S::kTiles == 2 ? tile : j & 1;
           const int k0 = (x.step + j) * S::kKeys;
           if (!tc::bar_wait(s_full(at), full_phase[at], &s_quit)) goto softmax_end;
@@ -728,26 +833,34 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
           tc::ld_wait();
           const uint32_t lost = s_bad[(steps + j) & 7];
           if (k0 < clear_lo || k0 + S::kKeys > clear_hi || lost) {
-            const int a0 = klo - k0, a1 = khi - k0;
+            // a word of 32 keys' bits at a time
 #pragma unroll
-            for (int i = 0; i < S::kKeys; ++i)
-              if (i < a0 || i >= a1 || (lost >> (i >> 4) & 1)) v[i] = 0xff800000u;
+            for (int i = 0; i < S::kKeys; i += 32) {
+              const int a0 = min(max(klo - k0 - i, 0), 32), a1 = min(max(khi - k0 - i, 0), 32);
+              uint32_t see = a1 > a0 ? (0xffffffffu >> (32 - (a1 - a0))) << a0 : 0u;
+              if (lost >> (i >> 4) & 1) see &= 0xffff0000u;
+              if (lost >> (i >> 4) & 2) see &= 0x0000ffffu;
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (!(see >> e & 1)) v[i + e] = 0xff800000u;
+            }
           }
-          float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
           for (int i = 0; i < S::kKeys; i += 4) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) top[e] = fmaxf(top[e], __uint_as_float(v[i + e]));
+            top[0] = max3(top[0], __uint_as_float(v[i]), __uint_as_float(v[i + 1]));
+            top[1] = max3(top[1], __uint_as_float(v[i + 2]), __uint_as_float(v[i + 3]));
           }
-          const float high = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * factor;
+          const float high = fmaxf(top[0], top[1]) * factor;
           const bool moves = high > m + kSlack;
           if (__any_sync(0xffffffffu, moves)) {
             // the reference follows the maximum; what is added up so far with it
             const float f = moves ? exp2_fast(m - high) : 1.f;
             if (moves) m = high;
             l *= f;
-            if (j > 0) {
-              if (S::kTiles == 1 && !tc::bar_wait(o_full(0), (sums + j - 1) & 1, &s_quit))
+            if (turn > 0) {
+              // (two tiles: S is made behind the products before it)
+              if (S::kTiles == 1 && !tc::bar_wait(o_full(0), (sums + turn - 1) & 1, &s_quit))
                 goto softmax_end;
               tc::fence_after();
 #pragma unroll 1
@@ -762,27 +875,38 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
             }
           }
           const float bias = kLift - (m == -INFINITY ? 0.f : m);
-          float add[4] = {0.f, 0.f, 0.f, 0.f};
+          const uint64_t factors = pair(factor, factor), biases = pair(bias, bias);
+          uint64_t add[2] = {0, 0};
 #pragma unroll
           for (int i = 0; i < S::kKeys; i += 32) {
             uint32_t w[16];
 #pragma unroll
             for (int e = 0; e < 32; e += 2) {
-              const float p0 = exp2_fast(fmaf(__uint_as_float(v[i + e]), factor, bias));
-              const float p1 = exp2_fast(fmaf(__uint_as_float(v[i + e + 1]), factor, bias));
-              add[e & 2] += p0;
-              add[(e & 2) + 1] += p1;
-              w[e / 2] = pack2<QT>(p0, p1);
+              float x0, x1;
+              unpair(fma_pair(pair(__uint_as_float(v[i + e]), __uint_as_float(v[i + e + 1])),
+                              factors, biases), x0, x1);
+              x0 = exp2_fast(x0);
+              x1 = exp2_fast(x1);
+              add[e >> 1 & 1] = add_pair(add[e >> 1 & 1], pair(x0, x1));
+              w[e / 2] = pack2<QT>(x0, x1);
             }
             tc::st16(s_at + i / 2, w);
+            if (i + 32 == S::kKeys / 2) {
+              // the first half can be multiplied
+              tc::st_wait();
+              tc::fence_before();
+              tc::bar_arrive(p_half(at));
+            }
           }
-          l += (add[0] + add[1]) + (add[2] + add[3]);
+          float l0, l1;
+          unpair(add_pair(add[0], add[1]), l0, l1);
+          l += l0 + l1;
           tc::st_wait();
           tc::fence_before();
           tc::bar_arrive(p_full(at));
         }
-        sums += n;
-        if (S::kTiles == 1 && n > 1 && !tc::bar_wait(o_full(0), sums & 1, &s_quit)) goto softmax_end;
+        sums += own;
+        if (S::kTiles == 1 && own > 1 && !tc::bar_wait(o_full(0), sums & 1, &s_quit)) goto softmax_end;
         if (!tc::bar_wait(o_full(tile), (sums - 1) & 1, &s_quit)) goto softmax_end;
         tc::fence_after();
       }
@@ -791,10 +915,47 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
       const bool odd = n > 0 && s_odd[work & 3] == work;
       const bool whole = x.count == 1;
       const float v_scale = c.v_scale ? __ldg(c.v_scale + x.head) : 1.f;
+      const bool joined = twins && n > 1;
+      float f0 = 1.f, f1 = 0.f;
+      if (joined) {
+        // the second four's sums go to the first
+        if (tile == 1) {
+          s_twin[0][r] = m;
+          s_twin[1][r] = l;
+          tc::fence_before();
+          tc::bar_arrive(twin);
+          if (!tc::bar_wait(twin_done, twin_phase, &s_quit)) goto softmax_end;
+        } else {
+          if (!tc::bar_wait(twin, twin_phase, &s_quit)) goto softmax_end;
+          tc::fence_after();
+          const float m1 = s_twin[0][r], l1 = s_twin[1][r];
+          const float both = fmaxf(m, m1), ref = both == -INFINITY ? 0.f : both;
+          f0 = exp2_fast(m - ref);
+          f1 = exp2_fast(m1 - ref);
+          l = l * f0 + l1 * f1;
+          m = both;
+        }
+        twin_phase ^= 1;
+      }
+      const bool mine = twins ? tile == 0 : tile * 128 < x.rows;
       if (mine && !odd) {
         const bool in = r < x.rows;
-        const int t = x.sp.first + row / c.group, head = x.head * c.group + row % c.group;
-        const long long line = (long long)t * c.heads + head;
+        const int head = x.head * c.by_group.d + group_head;
+        const long long line = (long long)(x.sp.first + token) * c.heads + head;
+        // 16 columns of the row's sums
+        auto sums16 = [&](int i, float (&o)[16]) {
+          uint32_t u[16];
+          tc::ld16(o_at + i, u);
+          tc::ld_wait();
+#pragma unroll
+          for (int e = 0; e < 16; ++e) o[e] = __uint_as_float(u[e]);
+          if (joined) {
+            tc::ld16(o_at + D + i, u);
+            tc::ld_wait();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[e] = o[e] * f0 + __uint_as_float(u[e]) * f1;
+          }
+        };
         if (whole) {
           const float sink = in && c.a.sinks ? __ldg(c.a.sinks + head) : -INFINITY;
           const Close z = close_row(m, l, sink, kLift);
@@ -803,15 +964,12 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
           uint4* out = reinterpret_cast<uint4*>(static_cast<uint16_t*>(c.a.out) + line * D);
 #pragma unroll 1
           for (int i = 0; i < D; i += 16) {
-            uint32_t o[16];
-            tc::ld16(o_at + i, o);
-            tc::ld_wait();
+            float o[16];
+            sums16(i, o);
             uint32_t w[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-              w[e] = z.scale == 0.f ? 0u
-                                    : pack2<QT>(__uint_as_float(o[2 * e]) * f,
-                                                __uint_as_float(o[2 * e + 1]) * f);
+              w[e] = z.scale == 0.f ? 0u : pack2<QT>(o[2 * e] * f, o[2 * e + 1] * f);
             if (in) {
               out[i / 8] = make_uint4(w[0], w[1], w[2], w[3]);
               out[i / 8 + 1] = make_uint4(w[4], w[5], w[6], w[7]);
@@ -821,14 +979,13 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
           float* part = c.part_o + ((size_t)x.slot * S::kRows + r) * D;
 #pragma unroll 1
           for (int i = 0; i < D; i += 16) {
-            uint32_t o[16];
-            tc::ld16(o_at + i, o);
-            tc::ld_wait();
+            float o[16];
+            sums16(i, o);
             if (in) {
 #pragma unroll
               for (int e = 0; e < 16; e += 4)
-                *reinterpret_cast<uint4*>(part + i + e) =
-                    make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                *reinterpret_cast<float4*>(part + i + e) =
+                    make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
             }
           }
           if (in) {
@@ -841,15 +998,17 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
       } else if (mine) {
         // row by row: the warp's 32 rows
         for (int i = 0; i < 32; ++i) {
-          const int rr = tile * 128 + quarter * 32 + i, one = x.row + rr;
+          const int rr = r - lane + i, one = x.row + rr;
           if (rr >= x.rows) break;
-          const int p = x.sp.len - x.sp.tokens + one / c.group;
+          int g;
+          const int t = quotient(one, c.by_group, g);
+          const int p = x.sp.len - x.sp.tokens + t;
           const int h1 = min(min(p + 1, x.hi), x.last * S::kKeys);
           const int h0 = max(c.a.window ? max(0, p + 1 - c.a.window) : 0, x.step * S::kKeys);
           float o[D / 32], m1, l1;
           plain_row<D, CT, QT>(c, x, one, factor, h0, h1, kLift, o, m1, l1);
-          const int t = x.sp.first + one / c.group, head = x.head * c.group + one % c.group;
-          const long long line = (long long)t * c.heads + head;
+          const int head = x.head * c.by_group.d + g;
+          const long long line = (long long)(x.sp.first + t) * c.heads + head;
           if (whole) {
             const float sink = c.a.sinks ? __ldg(c.a.sinks + head) : -INFINITY;
             const Close z = close_row(m1, l1, sink, kLift);
@@ -870,6 +1029,7 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
           }
         }
       }
+      if (joined && tile == 0) tc::bar_arrive(twin_done);
       if (!whole) {
         // the last piece of an item to arrive adds them up, in order
         __threadfence();
@@ -890,8 +1050,9 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
           constexpr int kPer = D / 32;
           const int first = x.slot - x.index;
           for (int rr = wid; rr < x.rows; rr += 8) {
-            const int one = x.row + rr;
-            const int t = x.sp.first + one / c.group, head = x.head * c.group + one % c.group;
+            int head;
+            const int t = x.sp.first + quotient(x.row + rr, c.by_group, head);
+            head += x.head * c.by_group.d;
             const long long line = (long long)t * c.heads + head;
             float top = -INFINITY, all = 0.f, o[kPer];
             for (int e = 0; e < kPer; ++e) o[e] = 0.f;
@@ -943,7 +1104,8 @@ cudaError_t chunk_as(const moe_reader_kv& kv, const moe_reader_kv_chunk_args& a,
   c.err = kv.err;
   c.heads = kv.cfg.num_q_heads;
   c.kv_heads = kv.cfg.num_kv_heads;
-  c.group = kv.group;
+  c.by_group = divisor(kv.group);
+  c.by_kv = divisor(kv.cfg.num_kv_heads);
   c.shift = kv.page_shift;
   c.pool = kv.cfg.num_pages;
   c.wide = reinterpret_cast<uintptr_t>(a.q) % 16 == 0 && a.q_token_stride % 8 == 0 &&
