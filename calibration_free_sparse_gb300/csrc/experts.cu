@@ -464,13 +464,18 @@ cudaError_t configure_experts(moe_reader_experts& h) {
   const bool bf16 = h.cfg.type == MOE_READER_TYPE_BF16;
   const uint64_t H = h.cfg.hidden, I = h.cfg.inter, E = h.cfg.num_experts;
   cudaError_t e = cudaSuccess;
+  auto map = [&](CUtensorMap* m, const void* w, uint64_t rows, uint64_t cols) {
+    const uint64_t sizes[3] = {cols, rows, E}, strides[2] = {cols, rows * cols};
+    const uint32_t box[3] = {64, 128, 1};
+    return tc::make_map(m, w, bf16, 3, sizes, strides, box);
+  };
   if (h.gate) {
-    e = tc::make_map(&h.gate_map, h.gate, bf16, H, I, E, 0, 128);
-    if (e == cudaSuccess) e = tc::make_map(&h.up_map, h.up, bf16, H, I, E, 0, 128);
+    e = map(&h.gate_map, h.gate, I, H);
+    if (e == cudaSuccess) e = map(&h.up_map, h.up, I, H);
     if (e == cudaSuccess) e = bf16 ? configure_group<true, true>() : configure_group<false, true>();
   }
   if (e == cudaSuccess && h.down) {
-    e = tc::make_map(&h.down_map, h.down, bf16, I, H, E, 0, 128);
+    e = map(&h.down_map, h.down, H, I);
     if (e == cudaSuccess)
       e = bf16 ? configure_group<true, false>() : configure_group<false, false>();
   }

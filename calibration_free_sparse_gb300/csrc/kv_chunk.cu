@@ -81,15 +81,18 @@ __device__ __forceinline__ Span span_of(const moe_reader_kv_chunk_args& a, int r
 constexpr int kChunkThreads = 384;                     // 12 warps: 168 registers a thread
 constexpr int kMaxPieces = kMaxSms;
 
-template <int D> struct ChunkShape {
+template <int D, int CT = kBf16> struct ChunkShape {
   static constexpr int kTiles = D <= 128 ? 2 : 1;        // row tiles
   static constexpr int kRows = 128 * kTiles;
   static constexpr int kKeys = D <= 128 ? 128 : 64;      // keys of a step
   static constexpr int kBlocks = D / 64;                 // 128-byte blocks of a row
   static constexpr int kQBytes = kRows * D * 2;
   static constexpr int kSlotBytes = kKeys * D * 2;       // keys or values of a step
-  static constexpr int kSlots = D == 64 ? 8 : 4;
-  static constexpr size_t kSmem = kQBytes + (size_t)kSlots * kSlotBytes + 1024;
+  // e4m3: two slots' worth of bytes as they come, so one slot of 16-bit values less
+  static constexpr int kSlots = (D == 64 ? 8 : 4) - (CT == kE4m3);
+  static constexpr int kRaw = CT == kE4m3 ? 2 : 0;
+  static constexpr size_t kSmem =
+      kQBytes + (size_t)kSlots * kSlotBytes + kRaw * (kSlotBytes / 2) + 1024;
   // tensor memory: two S, then O
   static constexpr int kO = 2 * kKeys;
 };
@@ -105,9 +108,10 @@ struct ChunkCall {
   uint32_t* arrived;         // [item]
   uint32_t* err;
   int heads, kv_heads, shift, pool;
+  int rows;                  // of an item: whole groups of heads
   Divisor by_group, by_kv;   // query heads per KV head, KV heads
-  int wide;                  // q can be copied 16 bytes at a time
-  CUtensorMap k_map, v_map;  // of 16-bit caches
+  int mapped;                // q_map holds; else q is read value by value
+  CUtensorMap q_map, k_map, v_map;      // k, v: of 16-bit caches
 };
 
 // Part of an item: the rows [row, row + rows) of a request's (token, head of
@@ -144,7 +148,6 @@ struct Work {
 // Item i: block of rows and KV head; the longest rows of a request first.
 template <int D>
 __device__ __forceinline__ Piece item_at(const ChunkCall& c, const Work& w, int i) {
-  using S = ChunkShape<D>;
   Piece x;
   const int b = quotient(i, c.by_kv, x.head);
   int lo = 0, hi = c.a.requests - 1;
@@ -154,8 +157,8 @@ __device__ __forceinline__ Piece item_at(const ChunkCall& c, const Work& w, int 
   }
   x.sp = {w.first[lo], w.tokens[lo], w.len[lo]};
   x.request = lo;
-  x.row = (w.blocks[lo + 1] - 1 - b) * S::kRows;
-  x.rows = min(S::kRows, x.sp.tokens * (int)c.by_group.d - x.row);
+  x.row = (w.blocks[lo + 1] - 1 - b) * c.rows;
+  x.rows = min(c.rows, x.sp.tokens * (int)c.by_group.d - x.row);
   x.item = i;
   x.index = 0;
   x.count = 1;
@@ -285,7 +288,7 @@ __device__ __forceinline__ Close close_row(float m, float l, float sink, float l
 template <int D, int CT, int QT>
 __global__ void __launch_bounds__(kChunkThreads, 1)
 chunk_kernel(const __grid_constant__ ChunkCall c) {
-  using S = ChunkShape<D>;
+  using S = ChunkShape<D, CT>;
   constexpr float kLift = QT == kF16 ? 11.f : 0.f;     // fp16 weights reach down to 2^-35
   constexpr float kSlack = QT == kF16 ? 4.f : 8.f;     // how far a logit may pass the reference
   extern __shared__ char raw[];
@@ -305,6 +308,8 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
   auto slot_free = [&](int s) { return bars + 8 * (S::kSlots + s); };
   auto cleaned = [&](int s) { return bars + 8 * (2 * S::kSlots + s); };
   auto landed = [&](int s) { return bars + 8 * (3 * S::kSlots + s); };
+  auto raw_full = [&](int i) { return bars + 8 * (2 * S::kSlots + i); };   // e4m3: in their place
+  auto raw_free = [&](int i) { return bars + 8 * (2 * S::kSlots + 2 + i); };
   const uint32_t more = bars + 32 * S::kSlots;
   auto s_full = [&](int t) { return more + 8 * t; };          // logits of a tile are there
   auto p_full = [&](int t) { return more + 16 + 8 * t; };     // its weights are
@@ -322,15 +327,21 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
     work_list.tokens[r] = sp.tokens;
     work_list.len[r] = sp.len;
     work_list.blocks[r] =
-        (int)(((long long)sp.tokens * c.by_group.d + S::kRows - 1) / S::kRows);
+        (int)(((long long)sp.tokens * c.by_group.d + c.rows - 1) / c.rows);
   }
   if (bad && blockIdx.x == 0) atomicOr(c.err, bad);
   if (tid == 0) {
     for (int s = 0; s < S::kSlots; ++s) {
       tc::bar_init(slot_full(s), CT == kE4m3 ? 96 : 1);
-      tc::bar_init(cleaned(s), 64);
-      tc::bar_init(landed(s), 1);
       tc::bar_init(slot_free(s), 1);
+      if (CT != kE4m3) {
+        tc::bar_init(cleaned(s), 64);
+        tc::bar_init(landed(s), 1);
+      }
+    }
+    for (int i = 0; i < S::kRaw; ++i) {
+      tc::bar_init(raw_full(i), 1);
+      tc::bar_init(raw_free(i), 96);
     }
     for (int t = 0; t < 2; ++t) {
       tc::bar_init(s_full(t), 1);
@@ -338,7 +349,7 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
       tc::bar_init(p_half(t), 128);
       tc::bar_init(o_full(t), 1);
     }
-    tc::bar_init(q_full, CT == kE4m3 ? 96 : 64);
+    tc::bar_init(q_full, c.mapped ? 1 : CT == kE4m3 ? 96 : 64);
     tc::bar_init(q_free, 1);
     tc::bar_init(join, 256);
     tc::bar_init(drained, 1);
@@ -449,13 +460,28 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
     int s = 0;
     uint32_t phase = 1, q_phase = 1, work = 0, steps = 0, err = 0;
     uint32_t cleared = 0, clear_phase = 0;     // a bit per slot
-    // queries of a piece
+    uint32_t raw_asked = 0;
+    // queries of a piece: blocks of 64 coordinates, each with all rows
     auto queries = [&](const Piece& x) {
+      if (c.mapped) {
+        if (who == 0) {
+          if (!tc::bar_wait(q_free, q_phase, &s_quit)) return false;
+          q_phase ^= 1;
+          const int first = x.sp.first + quotient(x.row, c.by_group);
+          if (tc::elected()) {
+            tc::bar_expect(q_full, S::kBlocks * c.rows * 128);
+            for (int b = 0; b < S::kBlocks; ++b)
+              tc::load_box(q_at + b * S::kRows * 128, &c.q_map, b * 64, x.head * c.by_group.d,
+                           first, q_full);
+          }
+          __syncwarp();
+        }
+        return true;
+      }
       if (!tc::bar_wait(q_free, q_phase, &s_quit)) return false;
       q_phase ^= 1;
       const int piece = lane & 7;
       const uint16_t flip = c.a.scale < 0.f ? 0x8000 : 0;
-#pragma unroll 4
       for (int r = who * 4 + (lane >> 3); r < S::kRows; r += warps * 4) {
         const bool in = r < x.rows;
         int g;
@@ -465,26 +491,18 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
                                       piece * 8
                                 : 0;
         const uint16_t* from = static_cast<const uint16_t*>(c.a.q) + at;
-        const uint32_t to = q_at + (r >> 7) * (S::kBlocks << 14) + tc::swizzled(r & 127, piece);
-        if (c.wide) {
+        const uint32_t to = q_at + tc::swizzled(r, piece);
+        for (int b = 0; b < S::kBlocks; ++b) {
+          uint32_t w[4];
 #pragma unroll
-          for (int b = 0; b < S::kBlocks; ++b)
-            tc::copy16(to + (b << 14), in ? from + b * 64 : from, in);
-        } else {
-          for (int b = 0; b < S::kBlocks; ++b) {
-            uint32_t w[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const uint16_t e0 = in ? __ldg(from + b * 64 + 2 * i) ^ flip : 0;
-              const uint16_t e1 = in ? __ldg(from + b * 64 + 2 * i + 1) ^ flip : 0;
-              w[i] = (uint32_t)e0 | (uint32_t)e1 << 16;
-            }
-            put_smem(to + (b << 14), w[0], w[1], w[2], w[3]);
+          for (int i = 0; i < 4; ++i) {
+            const uint16_t e0 = in ? __ldg(from + b * 64 + 2 * i) ^ flip : 0;
+            const uint16_t e1 = in ? __ldg(from + b * 64 + 2 * i + 1) ^ flip : 0;
+            w[i] = (uint32_t)e0 | (uint32_t)e1 << 16;
           }
+          put_smem(to + b * S::kRows * 128, w[0], w[1], w[2], w[3]);
         }
       }
-      tc::copies_commit();
-      tc::copies_wait<0>();
       tc::publish_smem();
       tc::bar_arrive(q_full);
       return true;
@@ -583,35 +601,54 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
         }
       }
     } else {
-      // 16 values a thread and copy, widened on the way: both 16-bit types hold
-      // them exactly.  A step's values are requested before its keys are
-      // widened, the next step's keys before its values are.
+      // The bytes of a step's keys and values come by bulk copies (a page's
+      // rows of a head lie on end), two slots' worth under way, and the step
+      // after the next's are brought into L2.  Three warps widen them, 16
+      // values a thread at a time; both 16-bit types hold them exactly.
       constexpr int kRow = D / 16, kSub = 32 / kRow;
       constexpr int kN = (S::kKeys / kSub + 2) / 3;
       const int piece = lane % kRow, sub = lane / kRow;
-      auto fetch = [&](const Piece& x, const char* base, int k0, int page, uint4 (&v)[kN]) {
-#pragma unroll
-        for (int i = 0; i < kN; ++i) {
-          const int r = (i * 3 + who) * kSub + sub, key = k0 + r;
-          const int p = __shfl_sync(0xffffffffu, page, (r >> 4) & 31);
-          const bool in = p >= 0 && key >= x.lo && key < x.hi;
-          // (no branch: the loads go out together)
-          const long long at =
-              ((((long long)(in ? p : 0) * c.kv_heads + x.head) << c.shift) +
-               (key & ((1 << c.shift) - 1))) * D + piece * 16;
-          const uint4 w = ldg_stream(reinterpret_cast<const uint4*>(base + at));
-          v[i] = in && r < S::kKeys ? w : make_uint4(0, 0, 0, 0);
-        }
+      const uint32_t raw_at = kv_at + S::kSlots * S::kSlotBytes;
+      const int box = min(1 << c.shift, S::kKeys), boxes = S::kKeys / box;
+      uint32_t& asked = raw_asked;
+      uint32_t taken = 0;                        // by this warp
+      // a page's rows of a step: lane l has box l
+      auto rows_at = [&](const Piece& x, const char* base, int k0, int p) {
+        return base + ((((long long)p * c.kv_heads + x.head) << c.shift) +
+                       (k0 & ((1 << c.shift) - 1))) * D;
       };
-      auto widen = [&](const uint4 (&v)[kN]) {
+      auto box_page = [&](int page) {
+        return __shfl_sync(0xffffffffu, page, (lane * box >> 4) & 31);
+      };
+      auto ask = [&](const Piece& x, int kind, int k0, int page) {      // warp 8
+        const uint32_t at = asked & 1;
+        if (!tc::bar_wait(raw_free(at), (asked >> 1 & 1) ^ 1, &s_quit)) return false;
+        const int p = box_page(page);
+        const bool mine = lane < boxes && p >= 0;
+        const uint32_t n = __popc(__ballot_sync(0xffffffffu, mine));
+        if (lane == 0) tc::bar_expect(raw_full(at), n * box * D);
+        __syncwarp();
+        if (mine)
+          tc::load_bytes(raw_at + at * (S::kSlotBytes / 2) + lane * box * D,
+                         rows_at(x, kind ? c.v : c.k, k0, p), box * D, raw_full(at));
+        asked++;
+        return true;
+      };
+      auto widen = [&](const Piece& x, int k0, int page) {
+        const uint32_t at = taken & 1;
+        if (!tc::bar_wait(raw_full(at), taken >> 1 & 1, &s_quit)) return false;
         if (!tc::bar_wait(slot_free(s), phase, &s_quit)) return false;
+        const uint32_t from = raw_at + at * (S::kSlotBytes / 2) + piece * 16;
         const uint32_t to = kv_at + s * S::kSlotBytes + (piece >> 2) * S::kKeys * 128;
         uint32_t odd = 0;
 #pragma unroll
         for (int i = 0; i < kN; ++i) {
-          const int r = (i * 3 + who) * kSub + sub;
+          const int r = (i * 3 + who) * kSub + sub, key = k0 + r;
           if (r >= S::kKeys) break;
-          const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+          const bool in = __shfl_sync(0xffffffffu, page, r >> 4) >= 0 && key >= x.lo && key < x.hi;
+          uint4 v = get_smem(from + r * D);
+          if (!in) v = make_uint4(0, 0, 0, 0);
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
           uint32_t o[8];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
@@ -623,38 +660,57 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
           put_smem(to + tc::swizzled(r, (piece & 3) * 2 + 1), o[4], o[5], o[6], o[7]);
         }
         if (odd & 0x80808080u) s_odd[work & 3] = work;
+        tc::bar_arrive(raw_free(at));
+        taken++;
         tc::publish_smem();
         tc::bar_arrive(slot_full(s));
         if (++s == S::kSlots) s = 0, phase ^= 1;
         return true;
       };
-      uint4 keys[kN], values[kN];
       for (int round = 0; round < rounds; ++round) {
         Piece x;
         if (!piece_at(round, x)) break;
         if (x.step >= x.last) continue;
         work++;
-        int next = page_of(x, x.step);
-        fetch(x, c.k, x.step * S::kKeys, next, keys);
+        int page = page_of(x, x.step), next = x.step + 1 < x.last ? page_of(x, x.step + 1) : -1;
+        if (wid == 8 && !(ask(x, 0, x.step * S::kKeys, page) && ask(x, 1, x.step * S::kKeys, page)))
+          goto loaders_end;
         if (!queries(x)) goto loaders_end;
         for (int step = x.step; step < x.last; ++step) {
-          const int page = next, k0 = step * S::kKeys;
-          if (step + 1 < x.last) next = page_of(x, step + 1);
+          const int k0 = step * S::kKeys;
+          const int far = step + 2 < x.last ? page_of(x, step + 2) : -1;
           const uint32_t lost = __ballot_sync(0xffffffffu, page == -2);
           if (lost) err |= kErrPage;
           if (tid == 256) s_bad[steps & 7] = lost;
           steps++;
-          fetch(x, c.v, k0, page, values);
-          if (!widen(keys)) goto loaders_end;
-          if (step + 1 < x.last) fetch(x, c.k, k0 + S::kKeys, next, keys);
-          if (!widen(values)) goto loaders_end;
+          if (!widen(x, k0, page)) goto loaders_end;
+          if (wid == 8 && step + 1 < x.last && !ask(x, 0, k0 + S::kKeys, next)) goto loaders_end;
+          if (!widen(x, k0, page)) goto loaders_end;
+          if (wid == 8 && step + 1 < x.last && !ask(x, 1, k0 + S::kKeys, next)) goto loaders_end;
+          if (wid == 8) {
+            const int p = box_page(far);
+            if (lane < boxes && p >= 0) {
+              tc::prefetch_bytes(rows_at(x, c.k, k0 + 2 * S::kKeys, p), box * D);
+              tc::prefetch_bytes(rows_at(x, c.v, k0 + 2 * S::kKeys, p), box * D);
+            }
+          }
+          page = next;
+          next = far;
         }
       }
     }
   loaders_end:
-    tc::copies_wait<0>();
+    // no copy is left under way
+    if (c.mapped && who == 0) {
+      volatile uint32_t ignore = 0;
+      tc::bar_wait(q_full, q_phase, &ignore);
+    }
+    if (!kCopies && wid == 8) {
+      volatile uint32_t ignore = 0;
+      for (uint32_t i = raw_asked < 2 ? 0 : raw_asked - 2; i < raw_asked; ++i)
+        tc::bar_wait(raw_full(i & 1), i >> 1 & 1, &ignore);
+    }
     if (kCopies && wid == 8) {
-      // no copy is left under way
       for (int i = 0; i < (int)min(2 * steps, (uint32_t)S::kSlots); ++i) {
         if (--s < 0) s = S::kSlots - 1, phase ^= 1;
         volatile uint32_t ignore = 0;
@@ -683,13 +739,13 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
     auto next_slot = [&]() { if (++s == S::kSlots) s = 0, phase ^= 1; };
     // S of a row tile; afterwards up to two barriers more
     auto logits = [&](int tile, int at, int slot, uint32_t then, uint32_t then2) {
-      const uint64_t q = tc::desc_k(q_at + tile * (S::kBlocks << 14));
+      const uint64_t q = tc::desc_k(q_at + (tile << 14));
       const uint64_t k = tc::desc_k(kv_at + slot * S::kSlotBytes);
       const uint32_t d = tmem + at * S::kKeys, bar = s_full(at);
       if (tc::elected()) {
 #pragma unroll
         for (int i = 0; i < D / 16; ++i)
-          tc::mma(d, q + ((i >> 2) << 10) + 2 * (i & 3), k + (i >> 2) * S::kKeys * 8 + 2 * (i & 3),
+          tc::mma(d, q + (i >> 2) * S::kRows * 8 + 2 * (i & 3), k + (i >> 2) * S::kKeys * 8 + 2 * (i & 3),
                   s_desc, i > 0);
         tc::commit(bar);
         if (then) tc::commit(then);
@@ -1108,11 +1164,21 @@ cudaError_t chunk_as(const moe_reader_kv& kv, const moe_reader_kv_chunk_args& a,
   c.by_kv = divisor(kv.cfg.num_kv_heads);
   c.shift = kv.page_shift;
   c.pool = kv.cfg.num_pages;
-  c.wide = reinterpret_cast<uintptr_t>(a.q) % 16 == 0 && a.q_token_stride % 8 == 0 &&
-           a.q_head_stride % 8 == 0 && !(a.scale < 0.f);
+  using S = ChunkShape<D>;
+  c.rows = S::kRows / kv.group * kv.group;
+  // a box: all of an item's tokens, one KV head's queries, 64 coordinates
+  c.mapped = reinterpret_cast<uintptr_t>(a.q) % 16 == 0 && a.q_token_stride % 8 == 0 &&
+             a.q_head_stride % 8 == 0 && a.q_token_stride > 0 && a.q_head_stride > 0 &&
+             !(a.scale < 0.f);
+  if (c.mapped) {
+    const uint64_t sizes[3] = {(uint64_t)D, (uint64_t)c.heads, (uint64_t)a.tokens};
+    const uint64_t strides[2] = {(uint64_t)a.q_head_stride, (uint64_t)a.q_token_stride};
+    const uint32_t box[3] = {64, (uint32_t)kv.group, (uint32_t)(c.rows / kv.group)};
+    c.mapped = tc::make_map(&c.q_map, a.q, QT == kBf16, 3, sizes, strides, box) == cudaSuccess;
+  }
   c.k_map = kv.chunk_maps[0];
   c.v_map = kv.chunk_maps[1];
-  chunk_kernel<D, CT, QT><<<kv.sms, kChunkThreads, ChunkShape<D>::kSmem, s>>>(c);
+  chunk_kernel<D, CT, QT><<<kv.sms, kChunkThreads, ChunkShape<D, CT>::kSmem, s>>>(c);
   return cudaGetLastError();
 }
 
@@ -1125,7 +1191,7 @@ cudaError_t chunk_dim(const moe_reader_kv& kv, const moe_reader_kv_chunk_args& a
 
 template <int D, int CT, int QT> cudaError_t configure_as() {
   return cudaFuncSetAttribute(chunk_kernel<D, CT, QT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              (int)ChunkShape<D>::kSmem);
+                              (int)ChunkShape<D, CT>::kSmem);
 }
 template <int D> cudaError_t configure_dim(int type) {
   if (type == kBf16) return configure_as<D, kBf16, kBf16>();
@@ -1142,11 +1208,12 @@ int chunk_rows(const moe_reader_kv_config& c) {
 
 cudaError_t configure_kv_chunk(moe_reader_kv& kv) {
   const moe_reader_kv_config& g = kv.cfg;
-  const uint32_t keys = g.head_dim <= 128 ? 128 : 64;
   for (int i = 0; i < 2 && g.cache_type != kE4m3; ++i) {
-    const cudaError_t e = tc::make_map(
-        &kv.chunk_maps[i], i ? kv.v : kv.k, g.cache_type == kBf16, g.head_dim, g.page_size,
-        g.num_kv_heads, g.num_pages, std::min<uint32_t>(g.page_size, keys));
+    const uint64_t D = g.head_dim, P = g.page_size, H = g.num_kv_heads;
+    const uint64_t sizes[4] = {D, P, H, (uint64_t)g.num_pages}, strides[3] = {D, P * D, H * P * D};
+    const uint32_t box[4] = {64, (uint32_t)std::min(g.page_size, D <= 128 ? 128 : 64), 1, 1};
+    const cudaError_t e = tc::make_map(&kv.chunk_maps[i], i ? kv.v : kv.k, g.cache_type == kBf16, 4,
+                                       sizes, strides, box);
     if (e != cudaSuccess) return e;
   }
   switch (kv.cfg.head_dim) {

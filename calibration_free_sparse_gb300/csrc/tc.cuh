@@ -94,6 +94,16 @@ __device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap* map, i
                :: "r"(dst), "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar) : "memory");
 }
 
+// Bytes on end, multiples of 16.
+__device__ __forceinline__ void load_bytes(uint32_t dst, const void* src, uint32_t bytes,
+                                           uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+               :: "r"(dst), "l"(src), "r"(bytes), "r"(bar) : "memory");
+}
+__device__ __forceinline__ void prefetch_bytes(const void* src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" :: "l"(src), "r"(bytes) : "memory");
+}
+
 // ---- tensor memory ----
 __device__ __forceinline__ void tmem_alloc(uint32_t out, uint32_t columns) {   // one warp
   asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
@@ -190,27 +200,32 @@ __device__ __forceinline__ void st_wait() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
-// A tensor map over a 16-bit array [outer][planes][rows][cols] with boxes of
-// `box_rows` rows of 128 bytes, pieces exchanged as above; what lies outside is 0.
-inline cudaError_t make_map(CUtensorMap* map, const void* base, bool bf16, uint64_t cols,
-                            uint64_t rows, uint64_t planes, uint64_t outer, uint32_t box_rows) {
+// A tensor map over a 16-bit array of up to four dimensions, the innermost
+// (contiguous) first, with strides in elements and boxes whose rows are 128
+// bytes, pieces exchanged as above; what lies outside is 0.
+inline cudaError_t make_map(CUtensorMap* map, const void* base, bool bf16, int dims,
+                            const uint64_t* sizes, const uint64_t* strides, const uint32_t* box) {
   using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
                               const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
                               const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
                               CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-  void* fn = nullptr;
-  cudaDriverEntryPointQueryResult found;
-  cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000,
-                                                   cudaEnableDefault, &found);
-  if (e != cudaSuccess) return e;
-  if (found != cudaDriverEntryPointSuccess || !fn) return cudaErrorNotSupported;
-  const cuuint64_t dims[4] = {cols, rows, planes, outer};
-  const cuuint64_t strides[3] = {cols * 2, rows * cols * 2, planes * rows * cols * 2};
-  const cuuint32_t box[4] = {64, box_rows, 1, 1}, step[4] = {1, 1, 1, 1};
-  const CUresult r = reinterpret_cast<Encode>(fn)(
-      map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
-      outer ? 4 : 3, const_cast<void*>(base), dims, strides, box, step,
-      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+  static Encode encode = nullptr;       // (the same from every thread)
+  if (!encode) {
+    void* fn = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000,
+                                                           cudaEnableDefault, &found);
+    if (e != cudaSuccess) return e;
+    if (found != cudaDriverEntryPointSuccess || !fn) return cudaErrorNotSupported;
+    encode = reinterpret_cast<Encode>(fn);
+  }
+  cuuint64_t bytes[3];
+  for (int i = 0; i + 1 < dims; ++i) bytes[i] = strides[i] * 2;
+  const cuuint32_t step[4] = {1, 1, 1, 1};
+  const CUresult r = encode(
+      map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, dims,
+      const_cast<void*>(base), sizes, bytes, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+      CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
       CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
