@@ -575,21 +575,28 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
               if (!tc::bar_wait(landed(s), clear_phase >> s & 1, &s_quit)) goto loaders_end;
               clear_phase ^= 1u << s;
               bool odd = false;
+              // (a short loop: it runs seldom, and code that is not in the
+              // instruction cache costs more than its latency)
+              const uint32_t at = kv_at + s * S::kSlotBytes;
+#pragma unroll 1
+              for (int r0 = who * 4; r0 < S::kKeys; r0 += 16) {
+                uint4 v[2][S::kBlocks];
 #pragma unroll
-              for (int b = 0; b < S::kBlocks; ++b) {
-                constexpr int kTurns = S::kKeys / 8;
-                uint4 v[kTurns];
-                const uint32_t at = kv_at + s * S::kSlotBytes + b * S::kKeys * 128;
+                for (int h = 0; h < 2; ++h)
 #pragma unroll
-                for (int i = 0; i < kTurns; ++i)
-                  v[i] = get_smem(at + tc::swizzled(i * 8 + who * 4 + (lane >> 3), lane & 7));
+                  for (int b = 0; b < S::kBlocks; ++b)
+                    v[h][b] = get_smem(at + b * S::kKeys * 128 +
+                                       tc::swizzled(r0 + 8 * h + (lane >> 3), lane & 7));
 #pragma unroll
-                for (int i = 0; i < kTurns; ++i) {
-                  const int r = i * 8 + who * 4 + (lane >> 3), key = k0 + r;
-                  const bool in = __shfl_sync(0xffffffffu, page, i >> 1) >= 0 && key >= x.lo &&
+                for (int h = 0; h < 2; ++h) {
+                  const int r = r0 + 8 * h + (lane >> 3), key = k0 + r;
+                  const bool in = __shfl_sync(0xffffffffu, page, r >> 4) >= 0 && key >= x.lo &&
                                   key < x.hi;
-                  if (in) odd |= odd8<QT>(v[i]);
-                  else put_smem(at + tc::swizzled(r, lane & 7), 0, 0, 0, 0);
+#pragma unroll
+                  for (int b = 0; b < S::kBlocks; ++b) {
+                    if (in) odd |= odd8<QT>(v[h][b]);
+                    else put_smem(at + b * S::kKeys * 128 + tc::swizzled(r, lane & 7), 0, 0, 0, 0);
+                  }
                 }
               }
               if (odd) s_odd[work & 3] = work;
@@ -641,14 +648,18 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
         const uint32_t from = raw_at + at * (S::kSlotBytes / 2) + piece * 16;
         const uint32_t to = kv_at + s * S::kSlotBytes + (piece >> 2) * S::kKeys * 128;
         uint32_t odd = 0;
+        uint4 v[kN];
+#pragma unroll
+        for (int i = 0; i < kN; ++i)
+          v[i] = get_smem(from + min((i * 3 + who) * kSub + sub, S::kKeys - 1) * D);
+        tc::bar_arrive(raw_free(at));
 #pragma unroll
         for (int i = 0; i < kN; ++i) {
           const int r = (i * 3 + who) * kSub + sub, key = k0 + r;
           if (r >= S::kKeys) break;
           const bool in = __shfl_sync(0xffffffffu, page, r >> 4) >= 0 && key >= x.lo && key < x.hi;
-          uint4 v = get_smem(from + r * D);
-          if (!in) v = make_uint4(0, 0, 0, 0);
-          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+          if (!in) v[i] = make_uint4(0, 0, 0, 0);
+          const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
           uint32_t o[8];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
@@ -660,7 +671,6 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
           put_smem(to + tc::swizzled(r, (piece & 3) * 2 + 1), o[4], o[5], o[6], o[7]);
         }
         if (odd & 0x80808080u) s_odd[work & 3] = work;
-        tc::bar_arrive(raw_free(at));
         taken++;
         tc::publish_smem();
         tc::bar_arrive(slot_full(s));
@@ -672,13 +682,14 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
         if (!piece_at(round, x)) break;
         if (x.step >= x.last) continue;
         work++;
-        int page = page_of(x, x.step), next = x.step + 1 < x.last ? page_of(x, x.step + 1) : -1;
+        auto ahead = [&](int step) { return step < x.last ? page_of(x, step) : -1; };
+        int page = page_of(x, x.step), next = ahead(x.step + 1), far = ahead(x.step + 2);
         if (wid == 8 && !(ask(x, 0, x.step * S::kKeys, page) && ask(x, 1, x.step * S::kKeys, page)))
           goto loaders_end;
         if (!queries(x)) goto loaders_end;
         for (int step = x.step; step < x.last; ++step) {
           const int k0 = step * S::kKeys;
-          const int far = step + 2 < x.last ? page_of(x, step + 2) : -1;
+          const int farther = ahead(step + 3);
           const uint32_t lost = __ballot_sync(0xffffffffu, page == -2);
           if (lost) err |= kErrPage;
           if (tid == 256) s_bad[steps & 7] = lost;
@@ -696,6 +707,7 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
           }
           page = next;
           next = far;
+          far = farther;
         }
       }
     }
