@@ -78,7 +78,6 @@ __device__ __forceinline__ Span span_of(const moe_reader_kv_chunk_args& a, int r
 // has two buffers).  Four warps a row tile: a thread has a row, so maxima and
 // sums need no exchange.  Three warps bring pages, one issues products.
 // ---------------------------------------------------------------------------
-constexpr int kChunkThreads = 384;                     // 12 warps: 168 registers a thread
 constexpr int kMaxPieces = kMaxSms;
 
 template <int D, int CT = kBf16> struct ChunkShape {
@@ -91,6 +90,13 @@ template <int D, int CT = kBf16> struct ChunkShape {
   // e4m3: two slots' worth of bytes as they come, so one slot of 16-bit values less
   static constexpr int kSlots = (D == 64 ? 8 : 4) - (CT == kE4m3);
   static constexpr int kRaw = CT == kE4m3 ? 2 : 0;
+  // Warps: eight of softmax, the loaders, one that issues products.  Three
+  // loaders leave 168 registers a thread, so that softmax holds a row's logits
+  // of a step; seven (e4m3: one asks, six widen; with three, widening took twice
+  // a step's products) leave 128, and it reads them twice.
+  static constexpr int kLoaders = CT == kE4m3 ? 7 : 3;
+  static constexpr int kThreads = 32 * (9 + kLoaders);
+  static constexpr int kHeld = CT == kE4m3 && kKeys == 128 ? 64 : kKeys;   // logits held
   static constexpr size_t kSmem =
       kQBytes + (size_t)kSlots * kSlotBytes + kRaw * (kSlotBytes / 2) + 1024;
   // tensor memory: two S, then O
@@ -286,7 +292,7 @@ __device__ __forceinline__ Close close_row(float m, float l, float sink, float l
 }
 
 template <int D, int CT, int QT>
-__global__ void __launch_bounds__(kChunkThreads, 1)
+__global__ void __launch_bounds__((ChunkShape<D, CT>::kThreads), 1)
 chunk_kernel(const __grid_constant__ ChunkCall c) {
   using S = ChunkShape<D, CT>;
   constexpr float kLift = QT == kF16 ? 11.f : 0.f;     // fp16 weights reach down to 2^-35
@@ -302,6 +308,7 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
   __shared__ volatile uint32_t s_quit;
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
   const int grid = gridDim.x;
+  constexpr int kWideners = S::kLoaders - 1;
   const uint32_t q_at = (tc::smem_at(raw) + 1023) & ~1023u, kv_at = q_at + S::kQBytes;
   const uint32_t bars = tc::smem_at(s_bar);
   auto slot_full = [&](int s) { return bars + 8 * s; };
@@ -320,7 +327,7 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
 
   // ---- what there is to do: every CTA finds it out for itself ----
   uint32_t bad = 0;
-  for (int r = tid; r < c.a.requests; r += kChunkThreads) {
+  for (int r = tid; r < c.a.requests; r += S::kThreads) {
     const Span sp = span_of(c.a, r, bad);
     if (sp.len > ((long long)c.a.width << c.shift)) bad |= kErrLength;
     work_list.first[r] = sp.first;
@@ -332,7 +339,7 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
   if (bad && blockIdx.x == 0) atomicOr(c.err, bad);
   if (tid == 0) {
     for (int s = 0; s < S::kSlots; ++s) {
-      tc::bar_init(slot_full(s), CT == kE4m3 ? 96 : 1);
+      tc::bar_init(slot_full(s), CT == kE4m3 ? kWideners * 32 : 1);
       tc::bar_init(slot_free(s), 1);
       if (CT != kE4m3) {
         tc::bar_init(cleaned(s), 64);
@@ -341,7 +348,7 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
     }
     for (int i = 0; i < S::kRaw; ++i) {
       tc::bar_init(raw_full(i), 1);
-      tc::bar_init(raw_free(i), 96);
+      tc::bar_init(raw_free(i), kWideners * 32);
     }
     for (int t = 0; t < 2; ++t) {
       tc::bar_init(s_full(t), 1);
@@ -349,7 +356,7 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
       tc::bar_init(p_half(t), 128);
       tc::bar_init(o_full(t), 1);
     }
-    tc::bar_init(q_full, c.mapped ? 1 : CT == kE4m3 ? 96 : 64);
+    tc::bar_init(q_full, c.mapped ? 1 : CT == kE4m3 ? 32 * S::kLoaders : 64);
     tc::bar_init(q_free, 1);
     tc::bar_init(join, 256);
     tc::bar_init(drained, 1);
@@ -359,7 +366,8 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
     s_quit = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (wid == 11) tc::tmem_alloc(tc::smem_at(&s_tmem), 512);
+  constexpr int kProducts = 8 + S::kLoaders;
+  if (wid == kProducts) tc::tmem_alloc(tc::smem_at(&s_tmem), 512);
   __syncthreads();
   if (wid == 0) {
     int sum = 0;
@@ -382,7 +390,7 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
   if (split) {
     // Few items: each is cut into pieces of at most `most` steps, the fewest
     // for which there are no more pieces than CTAs.
-    for (int i = tid; i < items; i += kChunkThreads) {
+    for (int i = tid; i < items; i += S::kThreads) {
       const Piece x = item_at<D>(c, work_list, i);
       work_list.pieces[i] = x.last - x.step;
     }
@@ -448,15 +456,16 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
     return true;
   };
 
-  if (wid >= 8 && wid < 11) {
+  if (wid >= 8 && wid < kProducts) {
     // ------------------------------------------------------------------
     // loaders
     // ------------------------------------------------------------------
     // 16-bit caches: one warp brings pages by tensor copies, two the queries,
     // and these clear values that are in a page but not there (a page ends
-    // inside the step, or is gone).  e4m3: all three bring both.
+    // inside the step, or is gone).  e4m3: one asks for bytes, six widen them.
     constexpr bool kCopies = CT != kE4m3;
-    const int who = wid - (kCopies ? 9 : 8), warps = kCopies ? 2 : 3;
+    const int who = wid - (kCopies ? 9 : 8);
+    constexpr int warps = S::kLoaders - kCopies;
     int s = 0;
     uint32_t phase = 1, q_phase = 1, work = 0, steps = 0, err = 0;
     uint32_t cleared = 0, clear_phase = 0;     // a bit per slot
@@ -610,15 +619,15 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
     } else {
       // The bytes of a step's keys and values come by bulk copies (a page's
       // rows of a head lie on end), two slots' worth under way, and the step
-      // after the next's are brought into L2.  Three warps widen them, 16
+      // after the next's are brought into L2.  Six warps widen them, 16
       // values a thread at a time; both 16-bit types hold them exactly.
       constexpr int kRow = D / 16, kSub = 32 / kRow;
-      constexpr int kN = (S::kKeys / kSub + 2) / 3;
+      constexpr int kN = (S::kKeys / kSub + kWideners - 1) / kWideners;
       const int piece = lane % kRow, sub = lane / kRow;
       const uint32_t raw_at = kv_at + S::kSlots * S::kSlotBytes;
       const int box = min(1 << c.shift, S::kKeys), boxes = S::kKeys / box;
       uint32_t& asked = raw_asked;
-      uint32_t taken = 0;                        // by this warp
+      uint32_t taken = 0;
       // a page's rows of a step: lane l has box l
       auto rows_at = [&](const Piece& x, const char* base, int k0, int p) {
         return base + ((((long long)p * c.kv_heads + x.head) << c.shift) +
@@ -627,7 +636,7 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
       auto box_page = [&](int page) {
         return __shfl_sync(0xffffffffu, page, (lane * box >> 4) & 31);
       };
-      auto ask = [&](const Piece& x, int kind, int k0, int page) {      // warp 8
+      auto ask = [&](const Piece& x, int kind, int k0, int page) {
         const uint32_t at = asked & 1;
         if (!tc::bar_wait(raw_free(at), (asked >> 1 & 1) ^ 1, &s_quit)) return false;
         const int p = box_page(page);
@@ -651,11 +660,11 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
         uint4 v[kN];
 #pragma unroll
         for (int i = 0; i < kN; ++i)
-          v[i] = get_smem(from + min((i * 3 + who) * kSub + sub, S::kKeys - 1) * D);
+          v[i] = get_smem(from + min((i * kWideners + who - 1) * kSub + sub, S::kKeys - 1) * D);
         tc::bar_arrive(raw_free(at));
 #pragma unroll
         for (int i = 0; i < kN; ++i) {
-          const int r = (i * 3 + who) * kSub + sub, key = k0 + r;
+          const int r = (i * kWideners + who - 1) * kSub + sub, key = k0 + r;
           if (r >= S::kKeys) break;
           const bool in = __shfl_sync(0xffffffffu, page, r >> 4) >= 0 && key >= x.lo && key < x.hi;
           if (!in) v[i] = make_uint4(0, 0, 0, 0);
@@ -684,30 +693,33 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
         work++;
         auto ahead = [&](int step) { return step < x.last ? page_of(x, step) : -1; };
         int page = page_of(x, x.step), next = ahead(x.step + 1), far = ahead(x.step + 2);
-        if (wid == 8 && !(ask(x, 0, x.step * S::kKeys, page) && ask(x, 1, x.step * S::kKeys, page)))
-          goto loaders_end;
-        if (!queries(x)) goto loaders_end;
-        for (int step = x.step; step < x.last; ++step) {
-          const int k0 = step * S::kKeys;
-          const int farther = ahead(step + 3);
-          const uint32_t lost = __ballot_sync(0xffffffffu, page == -2);
-          if (lost) err |= kErrPage;
-          if (tid == 256) s_bad[steps & 7] = lost;
-          steps++;
-          if (!widen(x, k0, page)) goto loaders_end;
-          if (wid == 8 && step + 1 < x.last && !ask(x, 0, k0 + S::kKeys, next)) goto loaders_end;
-          if (!widen(x, k0, page)) goto loaders_end;
-          if (wid == 8 && step + 1 < x.last && !ask(x, 1, k0 + S::kKeys, next)) goto loaders_end;
-          if (wid == 8) {
+        if (wid == 8) {
+          for (int step = x.step; step < x.last; ++step) {
+            const int k0 = step * S::kKeys, farther = ahead(step + 3);
+            if (!ask(x, 0, k0, page) || !ask(x, 1, k0, page)) goto loaders_end;
+            if (step == x.step && !queries(x)) goto loaders_end;
             const int p = box_page(far);
             if (lane < boxes && p >= 0) {
               tc::prefetch_bytes(rows_at(x, c.k, k0 + 2 * S::kKeys, p), box * D);
               tc::prefetch_bytes(rows_at(x, c.v, k0 + 2 * S::kKeys, p), box * D);
             }
+            page = next;
+            next = far;
+            far = farther;
           }
-          page = next;
-          next = far;
-          far = farther;
+        } else {
+          if (!queries(x)) goto loaders_end;
+          for (int step = x.step; step < x.last; ++step) {
+            const int k0 = step * S::kKeys, farther = ahead(step + 3);
+            const uint32_t lost = __ballot_sync(0xffffffffu, page == -2);
+            if (lost) err |= kErrPage;
+            if (wid == 9 && lane == 0) s_bad[steps & 7] = lost;
+            steps++;
+            if (!widen(x, k0, page) || !widen(x, k0, page)) goto loaders_end;
+            page = next;
+            next = far;
+            far = farther;
+          }
         }
       }
     }
@@ -730,8 +742,8 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
         if (cleared >> s & 1) tc::bar_wait(landed(s), ~clear_phase >> s & 1, &ignore);
       }
     }
-    if (err && lane == 0 && wid == 8) atomicOr(c.err, err);
-  } else if (wid == 11) {
+    if (err && lane == 0) atomicOr(c.err, err);
+  } else if (wid == kProducts) {
     // ------------------------------------------------------------------
     // products
     // ------------------------------------------------------------------
@@ -895,29 +907,38 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
           full_phase[at] ^= 1;
           tc::fence_after();
           const uint32_t s_at = tmem + at * S::kKeys + lanes;
-          uint32_t v[S::kKeys];
-#pragma unroll
-          for (int i = 0; i < S::kKeys; i += 32) tc::ld32(s_at + i, v + i);
-          tc::ld_wait();
+          constexpr int kHeld = S::kHeld;
+          uint32_t v[kHeld];
           const uint32_t lost = s_bad[(steps + j) & 7];
-          if (k0 < clear_lo || k0 + S::kKeys > clear_hi || lost) {
+          const bool hide = k0 < clear_lo || k0 + S::kKeys > clear_hi || lost;
+          // logits i0.. of the step, those out of sight -infinity
+          auto fetch = [&](int i0) {
+#pragma unroll
+            for (int i = 0; i < kHeld; i += 32) tc::ld32(s_at + i0 + i, v + i);
+            tc::ld_wait();
+            if (!hide) return;
             // a word of 32 keys' bits at a time
 #pragma unroll
-            for (int i = 0; i < S::kKeys; i += 32) {
-              const int a0 = min(max(klo - k0 - i, 0), 32), a1 = min(max(khi - k0 - i, 0), 32);
+            for (int i = 0; i < kHeld; i += 32) {
+              const int at0 = i0 + i;
+              const int a0 = min(max(klo - k0 - at0, 0), 32), a1 = min(max(khi - k0 - at0, 0), 32);
               uint32_t see = a1 > a0 ? (0xffffffffu >> (32 - (a1 - a0))) << a0 : 0u;
-              if (lost >> (i >> 4) & 1) see &= 0xffff0000u;
-              if (lost >> (i >> 4) & 2) see &= 0x0000ffffu;
+              if (lost >> (at0 >> 4) & 1) see &= 0xffff0000u;
+              if (lost >> (at0 >> 4) & 2) see &= 0x0000ffffu;
 #pragma unroll
               for (int e = 0; e < 32; ++e)
                 if (!(see >> e & 1)) v[i + e] = 0xff800000u;
             }
-          }
+          };
           float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-          for (int i = 0; i < S::kKeys; i += 4) {
-            top[0] = max3(top[0], __uint_as_float(v[i]), __uint_as_float(v[i + 1]));
-            top[1] = max3(top[1], __uint_as_float(v[i + 2]), __uint_as_float(v[i + 3]));
+          for (int i0 = 0; i0 < S::kKeys; i0 += kHeld) {
+            fetch(i0);
+#pragma unroll
+            for (int i = 0; i < kHeld; i += 4) {
+              top[0] = max3(top[0], __uint_as_float(v[i]), __uint_as_float(v[i + 1]));
+              top[1] = max3(top[1], __uint_as_float(v[i + 2]), __uint_as_float(v[i + 3]));
+            }
           }
           const float high = fmaxf(top[0], top[1]) * factor;
           const bool moves = high > m + kSlack;
@@ -947,12 +968,14 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
           uint64_t add[2] = {0, 0};
 #pragma unroll
           for (int i = 0; i < S::kKeys; i += 32) {
+            if (kHeld < S::kKeys && i % kHeld == 0) fetch(i);
             uint32_t w[16];
 #pragma unroll
             for (int e = 0; e < 32; e += 2) {
+              const int at0 = i % kHeld + e;
               float x0, x1;
-              unpair(fma_pair(pair(__uint_as_float(v[i + e]), __uint_as_float(v[i + e + 1])),
-                              factors, biases), x0, x1);
+              unpair(fma_pair(pair(__uint_as_float(v[at0]), __uint_as_float(v[at0 + 1])), factors,
+                              biases), x0, x1);
               x0 = exp2_fast(x0);
               x1 = exp2_fast(x1);
               add[e >> 1 & 1] = add_pair(add[e >> 1 & 1], pair(x0, x1));
@@ -1154,7 +1177,7 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
     (void)0;
   }
   __syncthreads();
-  if (wid == 11) tc::tmem_free(tmem, 512);
+  if (wid == kProducts) tc::tmem_free(tmem, 512);
   if (tid == 0 && s_quit) atomicOr(c.err, kErrTimeout);
 }
 
@@ -1190,7 +1213,7 @@ cudaError_t chunk_as(const moe_reader_kv& kv, const moe_reader_kv_chunk_args& a,
   }
   c.k_map = kv.chunk_maps[0];
   c.v_map = kv.chunk_maps[1];
-  chunk_kernel<D, CT, QT><<<kv.sms, kChunkThreads, ChunkShape<D, CT>::kSmem, s>>>(c);
+  chunk_kernel<D, CT, QT><<<kv.sms, ChunkShape<D, CT>::kThreads, ChunkShape<D, CT>::kSmem, s>>>(c);
   return cudaGetLastError();
 }
 
