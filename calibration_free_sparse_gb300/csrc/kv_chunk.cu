@@ -122,11 +122,12 @@ struct ChunkCall {
 
 // Part of an item: the rows [row, row + rows) of a request's (token, head of
 // the group) list, one KV head, the steps [step, last) of its keys.
-struct Piece {
+struct alignas(16) Piece {
   Span sp;
   int request, head, row, rows;
   int p0, p1;                // positions of the first and the last row
   int lo, hi;                // keys that some row sees
+  int base;                  // key of step 0
   int step, last;
   int item, index, count;    // index-th of the item's `count` pieces
   int slot;                  // where its partial result goes
@@ -140,8 +141,10 @@ __device__ __forceinline__ void item_range(const ChunkCall& c, Piece& x) {
   x.p1 = before + quotient(x.row + x.rows - 1, c.by_group);
   x.lo = c.a.window ? max(0, x.p0 + 1 - c.a.window) : 0;
   x.hi = (int)min((long long)x.p1 + 1, (long long)c.a.width << c.shift);
-  x.step = x.lo / S::kKeys;
-  x.last = x.hi > x.lo ? (x.hi + S::kKeys - 1) / S::kKeys : x.step;
+  // steps begin at a page, or inside one at a multiple of theirs
+  x.base = x.lo & -min(1 << c.shift, S::kKeys);
+  x.step = 0;
+  x.last = x.hi > x.lo ? (x.hi - x.base + S::kKeys - 1) / S::kKeys : 0;
 }
 
 // What every role looks its pieces up in.
@@ -299,7 +302,8 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
   constexpr float kSlack = QT == kF16 ? 4.f : 8.f;     // how far a logit may pass the reference
   extern __shared__ char raw[];
   __shared__ Work work_list;
-  __shared__ uint64_t s_bar[4 * S::kSlots + 14];
+  __shared__ Piece s_piece[4];
+  __shared__ uint64_t s_bar[4 * S::kSlots + 22];
   __shared__ float s_twin[2][128];
   // by piece with keys and by step, in turn: loaders are at most two pieces and
   // kSlots / 2 + 2 steps ahead of softmax
@@ -324,19 +328,9 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
   const uint32_t q_full = more + 48, q_free = more + 56, join = more + 64, drained = more + 72;
   auto p_half = [&](int t) { return more + 80 + 8 * t; };     // the first half of its weights
   const uint32_t twin = more + 96, twin_done = more + 104;   // the second four's sums, taken
+  auto piece_full = [&](int i) { return more + 112 + 8 * i; };
+  auto piece_free = [&](int i) { return more + 144 + 8 * i; };
 
-  // ---- what there is to do: every CTA finds it out for itself ----
-  uint32_t bad = 0;
-  for (int r = tid; r < c.a.requests; r += S::kThreads) {
-    const Span sp = span_of(c.a, r, bad);
-    if (sp.len > ((long long)c.a.width << c.shift)) bad |= kErrLength;
-    work_list.first[r] = sp.first;
-    work_list.tokens[r] = sp.tokens;
-    work_list.len[r] = sp.len;
-    work_list.blocks[r] =
-        (int)(((long long)sp.tokens * c.by_group.d + c.rows - 1) / c.rows);
-  }
-  if (bad && blockIdx.x == 0) atomicOr(c.err, bad);
   if (tid == 0) {
     for (int s = 0; s < S::kSlots; ++s) {
       tc::bar_init(slot_full(s), CT == kE4m3 ? kWideners * 32 : 1);
@@ -360,6 +354,10 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
     tc::bar_init(q_free, 1);
     tc::bar_init(join, 256);
     tc::bar_init(drained, 1);
+    for (int i = 0; i < 4; ++i) {
+      tc::bar_init(piece_full(i), 1);
+      tc::bar_init(piece_free(i), 8 + S::kLoaders);      // all warps but the giver
+    }
     tc::bar_init(twin, 128);
     tc::bar_init(twin_done, 128);
     for (int i = 0; i < 4; ++i) s_odd[i] = 0;
@@ -368,6 +366,25 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
   }
   constexpr int kProducts = 8 + S::kLoaders;
   if (wid == kProducts) tc::tmem_alloc(tc::smem_at(&s_tmem), 512);
+  if (tid == 32) {
+    tc::prefetch_map(&c.q_map);
+    if (CT != kE4m3) tc::prefetch_map(&c.k_map), tc::prefetch_map(&c.v_map);
+  }
+  wait_for_earlier_launch();
+  let_next_launch_start();
+
+  // ---- what there is to do: every CTA finds it out for itself ----
+  uint32_t bad = 0;
+  for (int r = tid; r < c.a.requests; r += S::kThreads) {
+    const Span sp = span_of(c.a, r, bad);
+    if (sp.len > ((long long)c.a.width << c.shift)) bad |= kErrLength;
+    work_list.first[r] = sp.first;
+    work_list.tokens[r] = sp.tokens;
+    work_list.len[r] = sp.len;
+    work_list.blocks[r] =
+        (int)(((long long)sp.tokens * c.by_group.d + c.rows - 1) / c.rows);
+  }
+  if (bad && blockIdx.x == 0) atomicOr(c.err, bad);
   __syncthreads();
   if (wid == 0) {
     int sum = 0;
@@ -396,17 +413,20 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
     }
     __syncthreads();
     if (wid == 0) {
-      int low = 4, high = 4;
-      for (int i = lane; i < items; i += 32) high = max(high, work_list.pieces[i]);
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) high = max(high, __shfl_xor_sync(0xffffffffu, high, o));
+      // (with W steps in all and C of them a piece there are at least W / C and
+      // fewer than W / C + items pieces)
+      int all = 0;
+      for (int i = lane; i < items; i += 32) all += work_list.pieces[i];
+      all = warp_sum_i(all);
+      const int most = min(grid, kMaxPieces), spare = most - (int)items;
+      int low = max(4, all / most), high = max(low, spare > 0 ? all / spare + 1 : all);
       while (low < high) {
         const int mid = (low + high) >> 1;
         const Divisor by = divisor(mid);
         int n = 0;
         for (int i = lane; i < items; i += 32)
           n += max(1, quotient(work_list.pieces[i] + mid - 1, by));
-        if (warp_sum_i(n) <= min(grid, kMaxPieces)) high = mid; else low = mid + 1;
+        if (warp_sum_i(n) <= most) high = mid; else low = mid + 1;
       }
       int sum = 0;
       for (int i0 = 0; i0 <= items; i0 += 32) {
@@ -433,14 +453,15 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
 
   // Pieces are dealt to the CTAs in turn, every other round backwards: those
   // of a request get shorter, so that a CTA's long ones meet its short ones.
-  const int rounds = (pieces + grid - 1) / grid;
-  auto piece_at = [&](int round, Piece& x) {
+  // The first loader works them out, one ahead, and hands them to the other
+  // warps in a ring of four (each for itself took a quarter of a short piece's
+  // time).
+  auto piece_at = [&](int round) {
     const int i = round * grid + (round & 1 ? grid - 1 - (int)blockIdx.x : (int)blockIdx.x);
-    if (i >= pieces) return false;
-    if (!split) {
-      x = item_at<D>(c, work_list, i);
-      return true;
-    }
+    Piece x;
+    x.rows = 0;
+    if (i >= pieces) return x;
+    if (!split) return item_at<D>(c, work_list, i);
     int lo = 0, hi = (int)items - 1;
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
@@ -453,7 +474,24 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
     const int n = x.last - x.step, first = x.step;
     x.step = first + (int)((long long)n * x.index / x.count);
     x.last = first + (int)((long long)n * (x.index + 1) / x.count);
+    return x;
+  };
+  auto give = [&](int round) {
+    if (!tc::bar_wait(piece_free(round & 3), (round >> 2 & 1) ^ 1, &s_quit)) return false;
+    if (lane == 0) {
+      s_piece[round & 3] = piece_at(round);
+      tc::bar_arrive(piece_full(round & 3));
+    }
+    __syncwarp();
     return true;
+  };
+  auto take = [&](int round) {
+    return tc::bar_wait(piece_full(round & 3), round >> 2 & 1, &s_quit) &&
+           s_piece[round & 3].rows > 0;
+  };
+  auto leave = [&](int round) {
+    __syncwarp();
+    if (lane == 0) tc::bar_arrive(piece_free(round & 3));
   };
 
   if (wid >= 8 && wid < kProducts) {
@@ -519,7 +557,7 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
     // lane l has the page of keys 16 l.. of a step: -2 not in the pool, -1 out
     // of sight (it may be gone)
     auto page_of = [&](const Piece& x, int step) {
-      const int key = step * S::kKeys + lane * 16;
+      const int key = x.base + step * S::kKeys + lane * 16;
       if (lane < S::kKeys / 16 && key < x.hi && ((key >> c.shift) + 1) << c.shift > x.lo) {
         const int p =
             __ldg(c.a.table + (size_t)x.request * c.a.width + (key >> c.shift));
@@ -530,13 +568,13 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
     if constexpr (kCopies) {
       if (wid == 8) {
         const int rows = min(1 << c.shift, S::kKeys), boxes = S::kKeys / rows;
-        for (int round = 0; round < rounds; ++round) {
-          Piece x;
-          if (!piece_at(round, x)) break;
-          if (x.step >= x.last) continue;
+        if (!give(0)) goto loaders_end;
+        for (int round = 0; s_piece[round & 3].rows > 0; ++round) {
+          if (!give(round + 1)) goto loaders_end;
+          const Piece& x = s_piece[round & 3];
           int next = page_of(x, x.step);
           for (int step = x.step; step < x.last; ++step) {
-            const int page = next, k0 = step * S::kKeys;
+            const int page = next, k0 = x.base + step * S::kKeys;
             if (step + 1 < x.last) next = page_of(x, step + 1);
             const uint32_t lost = __ballot_sync(0xffffffffu, page == -2);
             if (lost) err |= kErrPage;
@@ -570,14 +608,13 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
           }
         }
       } else {
-        for (int round = 0; round < rounds; ++round) {
-          Piece x;
-          if (!piece_at(round, x)) break;
+        for (int round = 0; take(round); leave(round++)) {
+          const Piece& x = s_piece[round & 3];
           if (x.step >= x.last) continue;
           work++;
           if (!queries(x)) goto loaders_end;
           for (int step = x.step; step < x.last; ++step) {
-            const int k0 = step * S::kKeys;
+            const int k0 = x.base + step * S::kKeys;
             s = (s + 1) % S::kSlots;
             if (partial_step<D>(c, x, k0)) {
               const int page = page_of(x, step);
@@ -686,16 +723,17 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
         if (++s == S::kSlots) s = 0, phase ^= 1;
         return true;
       };
-      for (int round = 0; round < rounds; ++round) {
-        Piece x;
-        if (!piece_at(round, x)) break;
-        if (x.step >= x.last) continue;
-        work++;
-        auto ahead = [&](int step) { return step < x.last ? page_of(x, step) : -1; };
-        int page = page_of(x, x.step), next = ahead(x.step + 1), far = ahead(x.step + 2);
-        if (wid == 8) {
+      auto ahead = [&](const Piece& x, int step) {
+        return step < x.last ? page_of(x, step) : -1;
+      };
+      if (wid == 8) {
+        if (!give(0)) goto loaders_end;
+        for (int round = 0; s_piece[round & 3].rows > 0; ++round) {
+          if (!give(round + 1)) goto loaders_end;
+          const Piece& x = s_piece[round & 3];
+          int page = ahead(x, x.step), next = ahead(x, x.step + 1), far = ahead(x, x.step + 2);
           for (int step = x.step; step < x.last; ++step) {
-            const int k0 = step * S::kKeys, farther = ahead(step + 3);
+            const int k0 = x.base + step * S::kKeys, farther = ahead(x, step + 3);
             if (!ask(x, 0, k0, page) || !ask(x, 1, k0, page)) goto loaders_end;
             if (step == x.step && !queries(x)) goto loaders_end;
             const int p = box_page(far);
@@ -707,10 +745,16 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
             next = far;
             far = farther;
           }
-        } else {
+        }
+      } else {
+        for (int round = 0; take(round); leave(round++)) {
+          const Piece& x = s_piece[round & 3];
+          if (x.step >= x.last) continue;
+          work++;
           if (!queries(x)) goto loaders_end;
+          int page = ahead(x, x.step), next = ahead(x, x.step + 1);
           for (int step = x.step; step < x.last; ++step) {
-            const int k0 = step * S::kKeys, farther = ahead(step + 3);
+            const int k0 = x.base + step * S::kKeys, far = ahead(x, step + 2);
             const uint32_t lost = __ballot_sync(0xffffffffu, page == -2);
             if (lost) err |= kErrPage;
             if (wid == 9 && lane == 0) s_bad[steps & 7] = lost;
@@ -718,7 +762,6 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
             if (!widen(x, k0, page) || !widen(x, k0, page)) goto loaders_end;
             page = next;
             next = far;
-            far = farther;
           }
         }
       }
@@ -754,7 +797,7 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
     uint32_t clean_phase = 0;                    // a bit per slot
     // a step's values: there, and cleared where they have to be
     auto values_in = [&](const Piece& x, int step) {
-      if (CT == kE4m3 || !partial_step<D>(c, x, step * S::kKeys))
+      if (CT == kE4m3 || !partial_step<D>(c, x, x.base + step * S::kKeys))
         return tc::bar_wait(slot_full(s), phase, &s_quit);
       const uint32_t want = clean_phase >> s & 1;
       clean_phase ^= 1u << s;
@@ -804,9 +847,8 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
       return true;
     };
     bool go = true;
-    for (int round = 0; go && round < rounds; ++round) {
-      Piece x;
-      if (!piece_at(round, x)) break;
+    for (int round = 0; go && take(round); leave(round++)) {
+      const Piece& x = s_piece[round & 3];
       if (x.step >= x.last) continue;
       const int tiles = x.rows > 128 ? 2 : 1, n = x.last - x.step;
       if (!(go = tc::bar_wait(q_full, q_phase, &s_quit))) break;
@@ -872,11 +914,10 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
     const int tile = wid >> 2, quarter = wid & 3;
     const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
     const uint32_t o_at = tmem + S::kO + tile * D + lanes;
-    uint32_t full_phase[2] = {0, 0}, sums = 0, join_phase = 0, twin_phase = 0;
+    uint32_t full_phase[2] = {0, 0}, added = 0, join_phase = 0, twin_phase = 0;
     uint32_t work = 0, steps = 0;
-    for (int round = 0; round < rounds; ++round) {
-      Piece x;
-      if (!piece_at(round, x)) break;
+    for (int round = 0; take(round); leave(round++)) {
+      const Piece& x = s_piece[round & 3];
       const int n = x.last - x.step;
       // One tile of rows: both fours have it, and every other step each.
       const bool twins = S::kTiles == 2 && x.rows <= 128;
@@ -902,7 +943,7 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
         for (int turn = 0; turn < own; ++turn) {
           const int j = first + turn * stride;
           const int at = S::kTiles == 2 ? tile : j & 1;
-          const int k0 = (x.step + j) * S::kKeys;
+          const int k0 = x.base + (x.step + j) * S::kKeys;
           if (!tc::bar_wait(s_full(at), full_phase[at], &s_quit)) goto softmax_end;
           full_phase[at] ^= 1;
           tc::fence_after();
@@ -949,7 +990,7 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
             l *= f;
             if (turn > 0) {
               // (two tiles: S is made behind the products before it)
-              if (S::kTiles == 1 && !tc::bar_wait(o_full(0), (sums + turn - 1) & 1, &s_quit))
+              if (S::kTiles == 1 && !tc::bar_wait(o_full(0), (added + turn - 1) & 1, &s_quit))
                 goto softmax_end;
               tc::fence_after();
 #pragma unroll 1
@@ -996,9 +1037,9 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
           tc::fence_before();
           tc::bar_arrive(p_full(at));
         }
-        sums += own;
-        if (S::kTiles == 1 && own > 1 && !tc::bar_wait(o_full(0), sums & 1, &s_quit)) goto softmax_end;
-        if (!tc::bar_wait(o_full(tile), (sums - 1) & 1, &s_quit)) goto softmax_end;
+        added += own;
+        if (S::kTiles == 1 && own > 1 && !tc::bar_wait(o_full(0), added & 1, &s_quit)) goto softmax_end;
+        if (!tc::bar_wait(o_full(tile), (added - 1) & 1, &s_quit)) goto softmax_end;
         tc::fence_after();
       }
       steps += n;
@@ -1033,18 +1074,18 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
         const bool in = r < x.rows;
         const int head = x.head * c.by_group.d + group_head;
         const long long line = (long long)(x.sp.first + token) * c.heads + head;
-        // 16 columns of the row's sums
-        auto sums16 = [&](int i, float (&o)[16]) {
-          uint32_t u[16];
-          tc::ld16(o_at + i, u);
+        // 32 columns of the row's sums
+        auto sums = [&](int i, float (&o)[32]) {
+          uint32_t u[32];
+          tc::ld32(o_at + i, u);
           tc::ld_wait();
 #pragma unroll
-          for (int e = 0; e < 16; ++e) o[e] = __uint_as_float(u[e]);
+          for (int e = 0; e < 32; ++e) o[e] = __uint_as_float(u[e]);
           if (joined) {
-            tc::ld16(o_at + D + i, u);
+            tc::ld32(o_at + D + i, u);
             tc::ld_wait();
 #pragma unroll
-            for (int e = 0; e < 16; ++e) o[e] = o[e] * f0 + __uint_as_float(u[e]) * f1;
+            for (int e = 0; e < 32; ++e) o[e] = o[e] * f0 + __uint_as_float(u[e]) * f1;
           }
         };
         if (whole) {
@@ -1054,27 +1095,28 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
           if (in && c.a.lse) c.a.lse[line] = z.lse;
           uint4* out = reinterpret_cast<uint4*>(static_cast<uint16_t*>(c.a.out) + line * D);
 #pragma unroll 1
-          for (int i = 0; i < D; i += 16) {
-            float o[16];
-            sums16(i, o);
-            uint32_t w[8];
+          for (int i = 0; i < D; i += 32) {
+            float o[32];
+            sums(i, o);
+            uint32_t w[16];
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
+            for (int e = 0; e < 16; ++e)
               w[e] = z.scale == 0.f ? 0u : pack2<QT>(o[2 * e] * f, o[2 * e + 1] * f);
             if (in) {
-              out[i / 8] = make_uint4(w[0], w[1], w[2], w[3]);
-              out[i / 8 + 1] = make_uint4(w[4], w[5], w[6], w[7]);
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                out[i / 8 + e] = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
             }
           }
         } else {
           float* part = c.part_o + ((size_t)x.slot * S::kRows + r) * D;
 #pragma unroll 1
-          for (int i = 0; i < D; i += 16) {
-            float o[16];
-            sums16(i, o);
+          for (int i = 0; i < D; i += 32) {
+            float o[32];
+            sums(i, o);
             if (in) {
 #pragma unroll
-              for (int e = 0; e < 16; e += 4)
+              for (int e = 0; e < 32; e += 4)
                 *reinterpret_cast<float4*>(part + i + e) =
                     make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
             }
@@ -1094,8 +1136,9 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
           int g;
           const int t = quotient(one, c.by_group, g);
           const int p = x.sp.len - x.sp.tokens + t;
-          const int h1 = min(min(p + 1, x.hi), x.last * S::kKeys);
-          const int h0 = max(c.a.window ? max(0, p + 1 - c.a.window) : 0, x.step * S::kKeys);
+          const int h1 = min(min(p + 1, x.hi), x.base + x.last * S::kKeys);
+          const int h0 = max(c.a.window ? max(0, p + 1 - c.a.window) : 0,
+                             x.base + x.step * S::kKeys);
           float o[D / 32], m1, l1;
           plain_row<D, CT, QT>(c, x, one, factor, h0, h1, kLift, o, m1, l1);
           const int head = x.head * c.by_group.d + g;
@@ -1138,37 +1181,62 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
         join_phase ^= 1;
         if (s_last) {
           __threadfence();
-          constexpr int kPer = D / 32;
+          // a warp has four rows at a time, a lane D / 32 of their coordinates
+          constexpr int kPer = D / 32, kAtOnce = 4;
           const int first = x.slot - x.index;
-          for (int rr = wid; rr < x.rows; rr += 8) {
-            int head;
-            const int t = x.sp.first + quotient(x.row + rr, c.by_group, head);
-            head += x.head * c.by_group.d;
-            const long long line = (long long)t * c.heads + head;
-            float top = -INFINITY, all = 0.f, o[kPer];
-            for (int e = 0; e < kPer; ++e) o[e] = 0.f;
-            for (int i = 0; i < x.count; ++i)
-              top = fmaxf(top, __ldcg(c.part_ml + (size_t)(first + i) * 2 * S::kRows + rr));
-            const float ref = top == -INFINITY ? 0.f : top;
-            for (int i = 0; i < x.count; ++i) {
-              const float* ml = c.part_ml + (size_t)(first + i) * 2 * S::kRows + rr;
-              const float f = exp2_fast(__ldcg(ml) - ref);
-              const float li = __ldcg(ml + S::kRows);
-              all += li * f;
-              const float* part = c.part_o + ((size_t)(first + i) * S::kRows + rr) * D + lane * kPer;
-              if (f == 0.f && li == li) continue;
+          for (int r0 = wid * kAtOnce; r0 < x.rows; r0 += 8 * kAtOnce) {
+            float top[kAtOnce], all[kAtOnce], o[kAtOnce][kPer];
 #pragma unroll
-              for (int e = 0; e < kPer; ++e) o[e] += __ldcg(part + e) * f;
+            for (int h = 0; h < kAtOnce; ++h) {
+              top[h] = -INFINITY;
+              all[h] = 0.f;
+#pragma unroll
+              for (int e = 0; e < kPer; ++e) o[h][e] = 0.f;
             }
-            const float sink = c.a.sinks ? __ldg(c.a.sinks + head) : -INFINITY;
-            const Close z = close_row(top, all, sink, kLift);
-            if (lane == 0 && c.a.lse) c.a.lse[line] = z.lse;
-            uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(c.a.out) + line * D +
-                                                        lane * kPer);
-            const float f = z.scale * v_scale;
+#pragma unroll 2
+            for (int i = 0; i < x.count; ++i) {
+              float mi[kAtOnce], li[kAtOnce], part[kAtOnce][kPer];
 #pragma unroll
-            for (int e = 0; e < kPer; e += 2)
-              out[e / 2] = z.scale == 0.f ? 0u : pack2<QT>(o[e] * f, o[e + 1] * f);
+              for (int h = 0; h < kAtOnce; ++h) {
+                const int rr = min(r0 + h, x.rows - 1);
+                const float* ml = c.part_ml + (size_t)(first + i) * 2 * S::kRows + rr;
+                mi[h] = __ldcg(ml);
+                li[h] = __ldcg(ml + S::kRows);
+                const float* from = c.part_o + ((size_t)(first + i) * S::kRows + rr) * D + lane * kPer;
+#pragma unroll
+                for (int e = 0; e < kPer; e += 2) {
+                  const float2 t = __ldcg(reinterpret_cast<const float2*>(from + e));
+                  part[h][e] = t.x;
+                  part[h][e + 1] = t.y;
+                }
+              }
+#pragma unroll
+              for (int h = 0; h < kAtOnce; ++h) {
+                const float both = fmaxf(top[h], mi[h]), ref = both == -INFINITY ? 0.f : both;
+                const float was = exp2_fast(top[h] - ref), is = exp2_fast(mi[h] - ref);
+                top[h] = both;
+                all[h] = all[h] * was + li[h] * is;
+#pragma unroll
+                for (int e = 0; e < kPer; ++e) o[h][e] = o[h][e] * was + part[h][e] * is;
+              }
+            }
+#pragma unroll
+            for (int h = 0; h < kAtOnce; ++h) {
+              if (r0 + h >= x.rows) break;
+              int head;
+              const int t = x.sp.first + quotient(x.row + r0 + h, c.by_group, head);
+              head += x.head * c.by_group.d;
+              const long long line = (long long)t * c.heads + head;
+              const float sink = c.a.sinks ? __ldg(c.a.sinks + head) : -INFINITY;
+              const Close z = close_row(top[h], all[h], sink, kLift);
+              if (lane == 0 && c.a.lse) c.a.lse[line] = z.lse;
+              uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(c.a.out) +
+                                                          line * D + lane * kPer);
+              const float f = z.scale * v_scale;
+#pragma unroll
+              for (int e = 0; e < kPer; e += 2)
+                out[e / 2] = z.scale == 0.f ? 0u : pack2<QT>(o[h][e] * f, o[h][e + 1] * f);
+            }
           }
         }
       }
@@ -1213,8 +1281,8 @@ cudaError_t chunk_as(const moe_reader_kv& kv, const moe_reader_kv_chunk_args& a,
   }
   c.k_map = kv.chunk_maps[0];
   c.v_map = kv.chunk_maps[1];
-  chunk_kernel<D, CT, QT><<<kv.sms, ChunkShape<D, CT>::kThreads, ChunkShape<D, CT>::kSmem, s>>>(c);
-  return cudaGetLastError();
+  using T = ChunkShape<D, CT>;
+  return launch_early(chunk_kernel<D, CT, QT>, dim3(kv.sms), T::kThreads, T::kSmem, s, c);
 }
 
 template <int D>

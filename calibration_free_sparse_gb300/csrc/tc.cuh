@@ -94,6 +94,9 @@ __device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap* map, i
                :: "r"(dst), "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar) : "memory");
 }
 
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];" :: "l"(map) : "memory");
+}
 // Bytes on end, multiples of 16.
 __device__ __forceinline__ void load_bytes(uint32_t dst, const void* src, uint32_t bytes,
                                            uint32_t bar) {
