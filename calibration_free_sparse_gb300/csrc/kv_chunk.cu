@@ -280,6 +280,29 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return r;
 }
 
+// Of four lanes with a row each, four pieces long: lane i gets piece i of every
+// row (in order), so that the four store a row's 64 bytes together.
+__device__ __forceinline__ void exchange4(uint4 (&v)[4]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 1; o <= 2; o <<= 1) {
+    const bool up = lane & o;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (i & o) continue;
+      // pieces i (kept by the lower lane) and i + o
+      uint4 &a = v[i], &b = v[i + o];
+      const uint4 give = up ? a : b;
+      uint4 got;
+      got.x = __shfl_xor_sync(0xffffffffu, give.x, o);
+      got.y = __shfl_xor_sync(0xffffffffu, give.y, o);
+      got.z = __shfl_xor_sync(0xffffffffu, give.z, o);
+      got.w = __shfl_xor_sync(0xffffffffu, give.w, o);
+      if (up) a = got; else b = got;
+    }
+  }
+}
+
 // What a row adds up to with its sink: the factor of its sums, lse.
 struct Close {
   float scale, lse;
@@ -966,9 +989,11 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
               uint32_t see = a1 > a0 ? (0xffffffffu >> (32 - (a1 - a0))) << a0 : 0u;
               if (lost >> (at0 >> 4) & 1) see &= 0xffff0000u;
               if (lost >> (at0 >> 4) & 2) see &= 0x0000ffffu;
+              if (!__all_sync(0xffffffffu, see == 0xffffffffu)) {
 #pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if (!(see >> e & 1)) v[i + e] = 0xff800000u;
+                for (int e = 0; e < 32; ++e)
+                  if (!(see >> e & 1)) v[i + e] = 0xff800000u;
+              }
             }
           };
           float top[2] = {-INFINITY, -INFINITY};
@@ -1093,23 +1118,36 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
           const Close z = close_row(m, l, sink, kLift);
           const float f = z.scale * v_scale;
           if (in && c.a.lse) c.a.lse[line] = z.lse;
-          uint4* out = reinterpret_cast<uint4*>(static_cast<uint16_t*>(c.a.out) + line * D);
+          // four lanes store four rows, one after the other, 64 bytes at a time
+          // (a lane for itself would touch 32 lines a store)
+          const long long mine_at = in ? line * D : -1;
+          long long at[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            at[e] = __shfl_sync(0xffffffffu, mine_at, (lane & ~3) + e);
 #pragma unroll 1
           for (int i = 0; i < D; i += 32) {
             float o[32];
             sums(i, o);
-            uint32_t w[16];
+            uint4 w[4];
 #pragma unroll
-            for (int e = 0; e < 16; ++e)
-              w[e] = z.scale == 0.f ? 0u : pack2<QT>(o[2 * e] * f, o[2 * e + 1] * f);
-            if (in) {
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                out[i / 8 + e] = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
+            for (int e = 0; e < 4; ++e) {
+              w[e].x = pack2<QT>(o[8 * e] * f, o[8 * e + 1] * f);
+              w[e].y = pack2<QT>(o[8 * e + 2] * f, o[8 * e + 3] * f);
+              w[e].z = pack2<QT>(o[8 * e + 4] * f, o[8 * e + 5] * f);
+              w[e].w = pack2<QT>(o[8 * e + 6] * f, o[8 * e + 7] * f);
+              if (z.scale == 0.f) w[e] = make_uint4(0, 0, 0, 0);
             }
+            exchange4(w);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (at[e] >= 0)
+                *reinterpret_cast<uint4*>(static_cast<uint16_t*>(c.a.out) + at[e] + i +
+                                          (lane & 3) * 8) = w[e];
           }
         } else {
-          float* part = c.part_o + ((size_t)x.slot * S::kRows + r) * D;
+          // four columns of all rows lie together
+          float4* part = reinterpret_cast<float4*>(c.part_o) + (size_t)x.slot * S::kRows * D / 4 + r;
 #pragma unroll 1
           for (int i = 0; i < D; i += 32) {
             float o[32];
@@ -1117,8 +1155,7 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
             if (in) {
 #pragma unroll
               for (int e = 0; e < 32; e += 4)
-                *reinterpret_cast<float4*>(part + i + e) =
-                    make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                part[(i + e) / 4 * S::kRows] = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
             }
           }
           if (in) {
@@ -1154,7 +1191,8 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
             }
           } else {
             for (int e = 0; e < D / 32; ++e)
-              c.part_o[((size_t)x.slot * S::kRows + rr) * D + lane + 32 * e] = o[e];
+              c.part_o[(((size_t)x.slot * D / 4 + (lane + 32 * e) / 4) * S::kRows + rr) * 4 +
+                       (lane & 3)] = o[e];
             if (lane == 0) {
               float* ml = c.part_ml + (size_t)x.slot * 2 * S::kRows + rr;
               ml[0] = m1;
@@ -1181,61 +1219,55 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
         join_phase ^= 1;
         if (s_last) {
           __threadfence();
-          // a warp has four rows at a time, a lane D / 32 of their coordinates
-          constexpr int kPer = D / 32, kAtOnce = 4;
-          const int first = x.slot - x.index;
-          for (int r0 = wid * kAtOnce; r0 < x.rows; r0 += 8 * kAtOnce) {
-            float top[kAtOnce], all[kAtOnce], o[kAtOnce][kPer];
+          // a lane has a row, a warp some columns of 32 rows
+          constexpr int kCols = D / 8;
+          const int from = x.slot - x.index, col = wid * kCols;
+          for (int r0 = 0; r0 < x.rows; r0 += 32) {
+            const bool in = r0 + lane < x.rows;
+            const int rr = min(r0 + lane, x.rows - 1);
+            float top = -INFINITY, all = 0.f, o[kCols];
 #pragma unroll
-            for (int h = 0; h < kAtOnce; ++h) {
-              top[h] = -INFINITY;
-              all[h] = 0.f;
-#pragma unroll
-              for (int e = 0; e < kPer; ++e) o[h][e] = 0.f;
-            }
+            for (int e = 0; e < kCols; ++e) o[e] = 0.f;
 #pragma unroll 2
             for (int i = 0; i < x.count; ++i) {
-              float mi[kAtOnce], li[kAtOnce], part[kAtOnce][kPer];
+              const float* ml = c.part_ml + (size_t)(from + i) * 2 * S::kRows + rr;
+              const float mi = __ldcg(ml), li = __ldcg(ml + S::kRows);
+              const float4* part = reinterpret_cast<const float4*>(c.part_o) +
+                                   ((size_t)(from + i) * D + col) / 4 * S::kRows + rr;
+              float4 p[kCols / 4];
 #pragma unroll
-              for (int h = 0; h < kAtOnce; ++h) {
-                const int rr = min(r0 + h, x.rows - 1);
-                const float* ml = c.part_ml + (size_t)(first + i) * 2 * S::kRows + rr;
-                mi[h] = __ldcg(ml);
-                li[h] = __ldcg(ml + S::kRows);
-                const float* from = c.part_o + ((size_t)(first + i) * S::kRows + rr) * D + lane * kPer;
+              for (int e = 0; e < kCols / 4; ++e) p[e] = __ldcg(part + e * S::kRows);
+              const float both = fmaxf(top, mi), ref = both == -INFINITY ? 0.f : both;
+              const float was = exp2_fast(top - ref), is = exp2_fast(mi - ref);
+              top = both;
+              all = all * was + li * is;
 #pragma unroll
-                for (int e = 0; e < kPer; e += 2) {
-                  const float2 t = __ldcg(reinterpret_cast<const float2*>(from + e));
-                  part[h][e] = t.x;
-                  part[h][e + 1] = t.y;
-                }
-              }
-#pragma unroll
-              for (int h = 0; h < kAtOnce; ++h) {
-                const float both = fmaxf(top[h], mi[h]), ref = both == -INFINITY ? 0.f : both;
-                const float was = exp2_fast(top[h] - ref), is = exp2_fast(mi[h] - ref);
-                top[h] = both;
-                all[h] = all[h] * was + li[h] * is;
-#pragma unroll
-                for (int e = 0; e < kPer; ++e) o[h][e] = o[h][e] * was + part[h][e] * is;
+              for (int e = 0; e < kCols / 4; ++e) {
+                o[4 * e] = o[4 * e] * was + p[e].x * is;
+                o[4 * e + 1] = o[4 * e + 1] * was + p[e].y * is;
+                o[4 * e + 2] = o[4 * e + 2] * was + p[e].z * is;
+                o[4 * e + 3] = o[4 * e + 3] * was + p[e].w * is;
               }
             }
+            int head;
+            const int t = x.sp.first + quotient(x.row + rr, c.by_group, head);
+            head += x.head * c.by_group.d;
+            const long long line = (long long)t * c.heads + head;
+            const float sink = c.a.sinks ? __ldg(c.a.sinks + head) : -INFINITY;
+            const Close z = close_row(top, all, sink, kLift);
+            if (in && wid == 0 && c.a.lse) c.a.lse[line] = z.lse;
+            uint4* out =
+                reinterpret_cast<uint4*>(static_cast<uint16_t*>(c.a.out) + line * D + col);
+            const float f = z.scale * v_scale;
+            if (in) {
 #pragma unroll
-            for (int h = 0; h < kAtOnce; ++h) {
-              if (r0 + h >= x.rows) break;
-              int head;
-              const int t = x.sp.first + quotient(x.row + r0 + h, c.by_group, head);
-              head += x.head * c.by_group.d;
-              const long long line = (long long)t * c.heads + head;
-              const float sink = c.a.sinks ? __ldg(c.a.sinks + head) : -INFINITY;
-              const Close z = close_row(top[h], all[h], sink, kLift);
-              if (lane == 0 && c.a.lse) c.a.lse[line] = z.lse;
-              uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(c.a.out) +
-                                                          line * D + lane * kPer);
-              const float f = z.scale * v_scale;
-#pragma unroll
-              for (int e = 0; e < kPer; e += 2)
-                out[e / 2] = z.scale == 0.f ? 0u : pack2<QT>(o[h][e] * f, o[h][e + 1] * f);
+              for (int e = 0; e < kCols; e += 8)
+                out[e / 8] = z.scale == 0.f
+                                 ? make_uint4(0, 0, 0, 0)
+                                 : make_uint4(pack2<QT>(o[e] * f, o[e + 1] * f),
+                                              pack2<QT>(o[e + 2] * f, o[e + 3] * f),
+                                              pack2<QT>(o[e + 4] * f, o[e + 5] * f),
+                                              pack2<QT>(o[e + 6] * f, o[e + 7] * f));
             }
           }
         }
