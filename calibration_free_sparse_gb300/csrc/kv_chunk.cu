@@ -116,7 +116,8 @@ struct ChunkCall {
   int heads, kv_heads, shift, pool;
   int rows;                  // of an item: whole groups of heads
   Divisor by_group, by_kv;   // query heads per KV head, KV heads
-  int mapped;                // q_map holds; else q is read value by value
+  int wide;                  // q can be read 16 bytes at a time
+  int mapped;                // q_map holds; else threads read q
   CUtensorMap q_map, k_map, v_map;      // k, v: of 16-bit caches
 };
 
@@ -131,6 +132,7 @@ struct alignas(16) Piece {
   int step, last;
   int item, index, count;    // index-th of the item's `count` pieces
   int slot;                  // where its partial result goes
+  int turn;                  // of the CTA's pieces that have keys
 };
 
 template <int D>
@@ -238,21 +240,11 @@ template <int QT> __device__ __forceinline__ bool odd8(uint4 v) {
   return odd;
 }
 
-// Two e4m3 values in the high bytes of the halves, widened: their bits moved to
-// where the type has exponent and mantissa are the value times 2^-120 (bf16) or
-// 2^-8 (fp16), subnormal ones too, and a product with a power of two is exact.
-// (The conversion instructions took four times as long.)  NaN becomes 480: a
-// step that holds one goes row by row.
-template <int QT> __device__ __forceinline__ uint32_t widen2(uint32_t v) {
-  uint32_t r;
-  if constexpr (QT == kBf16) {
-    const uint32_t t = (v >> 4 & 0x07f007f0u) | (v & 0x80008000u);
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(t), "r"(0x7b807b80u));
-  } else {
-    const uint32_t t = (v >> 1 & 0x3f803f80u) | (v & 0x80008000u);
-    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(t), "r"(0x5c005c00u));
-  }
-  return r;
+// Two e4m3 values in fp16, which holds them all.
+__device__ __forceinline__ uint32_t widen2(uint32_t two) {
+  const __half2_raw h =
+      __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(two & 0xffff), __NV_E4M3);
+  return (uint32_t)h.x | (uint32_t)h.y << 16;
 }
 
 // Pairs of fp32 in one instruction.
@@ -321,13 +313,21 @@ template <int D, int CT, int QT>
 __global__ void __launch_bounds__((ChunkShape<D, CT>::kThreads), 1)
 chunk_kernel(const __grid_constant__ ChunkCall c) {
   using S = ChunkShape<D, CT>;
-  constexpr float kLift = QT == kF16 ? 11.f : 0.f;     // fp16 weights reach down to 2^-35
-  constexpr float kSlack = QT == kF16 ? 4.f : 8.f;     // how far a logit may pass the reference
+  // The products' type: the cache's, fp16 for e4m3 (the one conversion that
+  // there is an instruction for; widening to bf16 took twice the issue slots and
+  // left the weights three bits less).  Queries in bf16 are brought to fp16 by
+  // a power of two per row that puts the largest near 2^15: exact down to 2^-32
+  // of it.
+  constexpr int MT = CT == kE4m3 ? kF16 : QT;
+  constexpr bool kScaled = CT == kE4m3 && QT == kBf16;
+  constexpr float kLift = MT == kF16 ? 11.f : 0.f;     // fp16 weights reach down to 2^-35
+  constexpr float kSlack = MT == kF16 ? 4.f : 8.f;     // how far a logit may pass the reference
   extern __shared__ char raw[];
   __shared__ Work work_list;
   __shared__ Piece s_piece[4];
   __shared__ uint64_t s_bar[4 * S::kSlots + 22];
   __shared__ float s_twin[2][128];
+  __shared__ float s_q_scale[2][kScaled ? S::kRows : 1];    // by piece with keys, in turn
   // by piece with keys and by step, in turn: loaders are at most two pieces and
   // kSlots / 2 + 2 steps ahead of softmax
   __shared__ volatile uint32_t s_odd[4], s_bad[8];
@@ -499,10 +499,14 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
     x.last = first + (int)((long long)n * (x.index + 1) / x.count);
     return x;
   };
+  int turns = 0;                          // the giver's
   auto give = [&](int round) {
     if (!tc::bar_wait(piece_free(round & 3), (round >> 2 & 1) ^ 1, &s_quit)) return false;
     if (lane == 0) {
-      s_piece[round & 3] = piece_at(round);
+      Piece x = piece_at(round);
+      x.turn = turns;
+      turns += x.rows > 0 && x.step < x.last;
+      s_piece[round & 3] = x;
       tc::bar_arrive(piece_full(round & 3));
     }
     __syncwarp();
@@ -552,6 +556,57 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
       q_phase ^= 1;
       const int piece = lane & 7;
       const uint16_t flip = c.a.scale < 0.f ? 0x8000 : 0;
+      if constexpr (kScaled) {
+        const int turn = x.turn & 1;
+#pragma unroll 1
+        for (int r = who * 4 + (lane >> 3); r < S::kRows; r += warps * 4) {
+          const bool in = r < x.rows;
+          int g;
+          const int t = x.sp.first + quotient(x.row + r, c.by_group, g);
+          const long long at = in ? t * c.a.q_token_stride +
+                                        (int)(x.head * c.by_group.d + g) * c.a.q_head_stride +
+                                        piece * 8
+                                  : 0;
+          const uint16_t* from = static_cast<const uint16_t*>(c.a.q) + at;
+          uint4 v[S::kBlocks];
+          float top = 0.f;
+#pragma unroll
+          for (int b = 0; b < S::kBlocks; ++b) {
+            v[b] = make_uint4(0, 0, 0, 0);
+            if (in && c.wide) {
+              v[b] = __ldg(reinterpret_cast<const uint4*>(from + b * 64));
+            } else if (in) {
+              uint32_t w[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                w[i] = (uint32_t)__ldg(from + b * 64 + 2 * i) |
+                       (uint32_t)__ldg(from + b * 64 + 2 * i + 1) << 16;
+              v[b] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+            const uint32_t w[4] = {v[b].x, v[b].y, v[b].z, v[b].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              top = fmaxf(top, fmaxf(fabsf(bf16_lo(w[i])), fabsf(bf16_hi(w[i]))));
+          }
+#pragma unroll
+          for (int o = 1; o < 8; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+          const int e = floor_log2_held(top) - 14;
+          const float by = two_to(-e) * (flip ? -1.f : 1.f);
+          if (piece == 0) s_q_scale[turn][r] = two_to(e);
+#pragma unroll
+          for (int b = 0; b < S::kBlocks; ++b) {
+            const uint32_t w[4] = {v[b].x, v[b].y, v[b].z, v[b].w};
+            uint32_t o[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              o[i] = pack2<kF16>(bf16_lo(w[i]) * by, bf16_hi(w[i]) * by);
+            put_smem(q_at + b * S::kRows * 128 + tc::swizzled(r, piece), o[0], o[1], o[2], o[3]);
+          }
+        }
+        tc::publish_smem();
+        tc::bar_arrive(q_full);
+        return true;
+      }
       for (int r = who * 4 + (lane >> 3); r < S::kRows; r += warps * 4) {
         const bool in = r < x.rows;
         int g;
@@ -663,7 +718,7 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
                                   key < x.hi;
 #pragma unroll
                   for (int b = 0; b < S::kBlocks; ++b) {
-                    if (in) odd |= odd8<QT>(v[h][b]);
+                    if (in) odd |= odd8<MT>(v[h][b]);
                     else put_smem(at + b * S::kKeys * 128 + tc::swizzled(r, lane & 7), 0, 0, 0, 0);
                   }
                 }
@@ -680,7 +735,7 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
       // The bytes of a step's keys and values come by bulk copies (a page's
       // rows of a head lie on end), two slots' worth under way, and the step
       // after the next's are brought into L2.  Six warps widen them, 16
-      // values a thread at a time; both 16-bit types hold them exactly.
+      // values a thread at a time, to fp16, which holds them exactly.
       constexpr int kRow = D / 16, kSub = 32 / kRow;
       constexpr int kN = (S::kKeys / kSub + kWideners - 1) / kWideners;
       const int piece = lane % kRow, sub = lane / kRow;
@@ -710,7 +765,7 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
         asked++;
         return true;
       };
-      auto widen = [&](const Piece& x, int k0, int page) {
+      auto widen = [&](const Piece& x, int k0, int page, bool watch) {
         const uint32_t at = taken & 1;
         if (!tc::bar_wait(raw_full(at), taken >> 1 & 1, &s_quit)) return false;
         if (!tc::bar_wait(slot_free(s), phase, &s_quit)) return false;
@@ -732,9 +787,9 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
           uint32_t o[8];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            odd |= (w[j] & 0x7f7f7f7fu) + 0x01010101u;
-            o[2 * j] = widen2<QT>(__byte_perm(w[j], 0, 0x1404));
-            o[2 * j + 1] = widen2<QT>(__byte_perm(w[j], 0, 0x3424));
+            if (watch) odd |= (w[j] & 0x7f7f7f7fu) + 0x01010101u;
+            o[2 * j] = widen2(w[j]);
+            o[2 * j + 1] = widen2(w[j] >> 16);
           }
           put_smem(to + tc::swizzled(r, (piece & 3) * 2), o[0], o[1], o[2], o[3]);
           put_smem(to + tc::swizzled(r, (piece & 3) * 2 + 1), o[4], o[5], o[6], o[7]);
@@ -782,7 +837,9 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
             if (lost) err |= kErrPage;
             if (wid == 9 && lane == 0) s_bad[steps & 7] = lost;
             steps++;
-            if (!widen(x, k0, page) || !widen(x, k0, page)) goto loaders_end;
+            // (0 times NaN is not 0: keys' NaN reach the rows that see them)
+            if (!widen(x, k0, page, false) || !widen(x, k0, page, partial_step<D>(c, x, k0)))
+              goto loaders_end;
             page = next;
             next = far;
           }
@@ -813,8 +870,8 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
     // ------------------------------------------------------------------
     // products
     // ------------------------------------------------------------------
-    constexpr uint32_t s_desc = tc::instr<QT == kBf16>(S::kKeys);
-    constexpr uint32_t o_desc = tc::instr<QT == kBf16>(D, true);
+    constexpr uint32_t s_desc = tc::instr<MT == kBf16>(S::kKeys);
+    constexpr uint32_t o_desc = tc::instr<MT == kBf16>(D, true);
     int s = 0;
     uint32_t phase = 0, q_phase = 0, p_phase[2] = {0, 0};
     uint32_t clean_phase = 0;                    // a bit per slot
@@ -955,6 +1012,7 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
       float factor = fabsf(c.a.scale) * kLog2e * (c.k_scale ? __ldg(c.k_scale + x.head) : 1.f);
       factor = fmaxf(factor, 1.1754943508222875e-38f);   // 0 times a masked -infinity is NaN
       float m = -INFINITY, l = 0.f;
+      float by = factor;
       if (own > 0) {
         // keys that all of the tile's rows see
         const int r0 = twins ? 0 : tile * 128;
@@ -970,6 +1028,8 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
           if (!tc::bar_wait(s_full(at), full_phase[at], &s_quit)) goto softmax_end;
           full_phase[at] ^= 1;
           tc::fence_after();
+          if (kScaled && turn == 0)
+            by = fmaxf(factor * s_q_scale[x.turn & 1][r], 1.1754943508222875e-38f);
           const uint32_t s_at = tmem + at * S::kKeys + lanes;
           constexpr int kHeld = S::kHeld;
           uint32_t v[kHeld];
@@ -1006,7 +1066,7 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
               top[1] = max3(top[1], __uint_as_float(v[i + 2]), __uint_as_float(v[i + 3]));
             }
           }
-          const float high = fmaxf(top[0], top[1]) * factor;
+          const float high = fmaxf(top[0], top[1]) * by;
           const bool moves = high > m + kSlack;
           if (__any_sync(0xffffffffu, moves)) {
             // the reference follows the maximum; what is added up so far with it
@@ -1030,7 +1090,7 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
             }
           }
           const float bias = kLift - (m == -INFINITY ? 0.f : m);
-          const uint64_t factors = pair(factor, factor), biases = pair(bias, bias);
+          const uint64_t factors = pair(by, by), biases = pair(bias, bias);
           uint64_t add[2] = {0, 0};
 #pragma unroll
           for (int i = 0; i < S::kKeys; i += 32) {
@@ -1045,7 +1105,7 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
               x0 = exp2_fast(x0);
               x1 = exp2_fast(x1);
               add[e >> 1 & 1] = add_pair(add[e >> 1 & 1], pair(x0, x1));
-              w[e / 2] = pack2<QT>(x0, x1);
+              w[e / 2] = pack2<MT>(x0, x1);
             }
             tc::st16(s_at + i / 2, w);
             if (i + 32 == S::kKeys / 2) {
@@ -1302,9 +1362,10 @@ cudaError_t chunk_as(const moe_reader_kv& kv, const moe_reader_kv_chunk_args& a,
   using S = ChunkShape<D>;
   c.rows = S::kRows / kv.group * kv.group;
   // a box: all of an item's tokens, one KV head's queries, 64 coordinates
-  c.mapped = reinterpret_cast<uintptr_t>(a.q) % 16 == 0 && a.q_token_stride % 8 == 0 &&
-             a.q_head_stride % 8 == 0 && a.q_token_stride > 0 && a.q_head_stride > 0 &&
-             !(a.scale < 0.f);
+  c.wide = reinterpret_cast<uintptr_t>(a.q) % 16 == 0 && a.q_token_stride % 8 == 0 &&
+           a.q_head_stride % 8 == 0;
+  c.mapped = c.wide && a.q_token_stride > 0 && a.q_head_stride > 0 && !(a.scale < 0.f) &&
+             !(CT == kE4m3 && QT == kBf16);
   if (c.mapped) {
     const uint64_t sizes[3] = {(uint64_t)D, (uint64_t)c.heads, (uint64_t)a.tokens};
     const uint64_t strides[2] = {(uint64_t)a.q_head_stride, (uint64_t)a.q_token_stride};
