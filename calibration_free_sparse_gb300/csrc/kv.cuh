@@ -28,10 +28,10 @@ struct moe_reader_kv {
   float* part_ml;             // [sms][2][2][16]  their references and sums of weights
   uint32_t* arrived;          // [rows]           pieces written; zero between launches
   size_t arrived_bytes;
-  float* chunk_o;             // [sms][chunk_rows][D]  unnormalised outputs of a chunk's pieces
-  float* chunk_ml;            // [sms][2][chunk_rows]  their references and sums of weights
+  float* chunk_o;             // [sms][2][D / 4][chunk_rows][4]  unnormalised outputs of pieces
+  float* chunk_ml;            // [sms][2][2][chunk_rows]  their references and sums of weights
   CUtensorMap chunk_maps[2];  // of keys and values, 16-bit caches
-  uint32_t* chunk_arrived;    // [kMaxSms]        pieces written, behind `arrived`
+  uint32_t* chunk_arrived;    // [kChunkItems]    pieces written, behind `arrived`
   uint32_t* err;              // [1]              device error word
 };
 
@@ -41,6 +41,7 @@ constexpr int kMaxGroup = 64;
 constexpr int kMaxRequests = 1024;
 constexpr int kMaxSelectPages = 49152;
 constexpr int kMaxSms = 256;          // CTAs of attend at most
+constexpr int kChunkItems = 512;      // of kv_chunk that are cut at most
 
 constexpr uint32_t kErrLength = MOE_READER_ERR_LENGTH;
 constexpr uint32_t kErrPage = MOE_READER_ERR_PAGE;

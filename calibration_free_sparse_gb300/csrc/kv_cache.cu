@@ -775,11 +775,11 @@ int moe_reader_kv_create(const moe_reader_kv_config* cfg, void* k, void* v, int8
   const size_t ml_bytes = (size_t)mr::kMaxSms * 2 * 2 * 16 * sizeof(float);
   const size_t items = (size_t)cfg->max_requests * cfg->num_kv_heads * mr::attend_row_tiles(*cfg);
   const size_t item_bytes = (items * 4 + 255) & ~(size_t)255;
-  const size_t c_bytes = item_bytes + mr::kMaxSms * 4;
+  const size_t c_bytes = item_bytes + mr::kChunkItems * 4;
   const cudaError_t counted =
       cudaDeviceGetAttribute(&kv->sms, cudaDevAttrMultiProcessorCount, kv->device);
   kv->sms = std::min(kv->sms, mr::kMaxSms);
-  const size_t chunk_rows = (size_t)kv->sms * mr::chunk_rows(*cfg);
+  const size_t chunk_rows = 2 * (size_t)kv->sms * mr::chunk_rows(*cfg);
   const size_t zeroed = o_bytes + ml_bytes + c_bytes + 256;
   const size_t bytes = zeroed + chunk_rows * (cfg->head_dim + 2) * sizeof(float);
   cudaError_t ce = mr::device_alloc(&kv->base, bytes);

@@ -78,7 +78,8 @@ __device__ __forceinline__ Span span_of(const moe_reader_kv_chunk_args& a, int r
 // has two buffers).  Four warps a row tile: a thread has a row, so maxima and
 // sums need no exchange.  Three warps bring pages, one issues products.
 // ---------------------------------------------------------------------------
-constexpr int kMaxPieces = kMaxSms;
+constexpr int kMaxItems = kChunkItems;   // that are dealt by steps
+constexpr int kItemCost = 2;          // of an item beside its steps, in steps
 
 template <int D, int CT = kBf16> struct ChunkShape {
   static constexpr int kTiles = D <= 128 ? 2 : 1;        // row tiles
@@ -131,7 +132,7 @@ struct alignas(16) Piece {
   int base;                  // key of step 0
   int step, last;
   int item, index, count;    // index-th of the item's `count` pieces
-  int slot;                  // where its partial result goes
+  int owner;                 // the CTA of its first piece
   int turn;                  // of the CTA's pieces that have keys
 };
 
@@ -153,7 +154,7 @@ __device__ __forceinline__ void item_range(const ChunkCall& c, Piece& x) {
 struct Work {
   int blocks[kMaxRequests + 1];       // a request's first block of rows
   int first[kMaxRequests], tokens[kMaxRequests], len[kMaxRequests];
-  int pieces[kMaxPieces + 1];         // an item's first piece, where items are cut
+  long long at[kMaxItems + 1];        // steps and costs before an item, where they are dealt
 };
 
 // Item i: block of rows and KV head; the longest rows of a request first.
@@ -173,7 +174,7 @@ __device__ __forceinline__ Piece item_at(const ChunkCall& c, const Work& w, int 
   x.item = i;
   x.index = 0;
   x.count = 1;
-  x.slot = 0;
+  x.owner = 0;
   item_range<D>(c, x);
   return x;
 }
@@ -425,78 +426,86 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
   }
   __syncthreads();
   const long long items = (long long)work_list.blocks[c.a.requests] * c.kv_heads;
-  const bool split = items <= min(grid, kMaxPieces);
-  int pieces = (int)items;
-  if (split) {
-    // Few items: each is cut into pieces of at most `most` steps, the fewest
-    // for which there are no more pieces than CTAs.
+  // Few items: their steps, one item's after the other's, are dealt to the CTAs
+  // in equal shares (a whole item a CTA left a quarter of them idle in the last
+  // round), and what a share cuts is added up.  Many: whole.
+  const bool dealt = items <= min(3 * grid, kMaxItems);
+  long long all = 0;
+  if (dealt) {
     for (int i = tid; i < items; i += S::kThreads) {
       const Piece x = item_at<D>(c, work_list, i);
-      work_list.pieces[i] = x.last - x.step;
+      work_list.at[i] = x.last - x.step + kItemCost;
     }
     __syncthreads();
     if (wid == 0) {
-      // (with W steps in all and C of them a piece there are at least W / C and
-      // fewer than W / C + items pieces)
-      int all = 0;
-      for (int i = lane; i < items; i += 32) all += work_list.pieces[i];
-      all = warp_sum_i(all);
-      const int most = min(grid, kMaxPieces), spare = most - (int)items;
-      int low = max(4, all / most), high = max(low, spare > 0 ? all / spare + 1 : all);
-      while (low < high) {
-        const int mid = (low + high) >> 1;
-        const Divisor by = divisor(mid);
-        int n = 0;
-        for (int i = lane; i < items; i += 32)
-          n += max(1, quotient(work_list.pieces[i] + mid - 1, by));
-        if (warp_sum_i(n) <= most) high = mid; else low = mid + 1;
-      }
-      int sum = 0;
+      long long sum = 0;
       for (int i0 = 0; i0 <= items; i0 += 32) {
         const int i = i0 + lane;
-        const int n = i < items ? max(1, (work_list.pieces[i] + high - 1) / high) : 0;
-        int at = n;
+        const long long n = i < items ? work_list.at[i] : 0;
+        long long at = n;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-          const int u = __shfl_up_sync(0xffffffffu, at, o);
+          const long long u = __shfl_up_sync(0xffffffffu, at, o);
           if (lane >= o) at += u;
         }
         __syncwarp();
-        if (i <= items) work_list.pieces[i] = sum + at - n;
+        if (i <= items) work_list.at[i] = sum + at - n;
         sum += __shfl_sync(0xffffffffu, at, 31);
       }
     }
     __syncthreads();
-    pieces = work_list.pieces[items];
+    all = work_list.at[items];
   }
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
   const uint32_t tmem = s_tmem;
 
-  // Pieces are dealt to the CTAs in turn, every other round backwards: those
-  // of a request get shorter, so that a CTA's long ones meet its short ones.
-  // The first loader works them out, one ahead, and hands them to the other
-  // warps in a ring of four (each for itself took a quarter of a short piece's
-  // time).
-  auto piece_at = [&](int round) {
-    const int i = round * grid + (round & 1 ? grid - 1 - (int)blockIdx.x : (int)blockIdx.x);
-    Piece x;
-    x.rows = 0;
-    if (i >= pieces) return x;
-    if (!split) return item_at<D>(c, work_list, i);
+  // The first loader works a CTA's pieces out, one ahead, and hands them to the
+  // other warps in a ring of four (each for itself took a quarter of a short
+  // piece's time).
+  const long long sharers = min((long long)grid, all / 4 + 1);     // four steps at least
+  auto owner_of = [&](long long at) { return (int)(((at + 1) * sharers - 1) / all); };
+  long long share_lo = 0, share_hi = 0;
+  int next_item = 0;
+  if (dealt && wid == 8 && blockIdx.x < sharers) {
+    share_lo = blockIdx.x * all / sharers;
+    share_hi = (blockIdx.x + 1) * all / sharers;
     int lo = 0, hi = (int)items - 1;
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
-      if (work_list.pieces[mid] <= i) lo = mid; else hi = mid - 1;
+      if (work_list.at[mid] <= share_lo) lo = mid; else hi = mid - 1;
     }
-    x = item_at<D>(c, work_list, lo);
-    x.index = i - work_list.pieces[lo];
-    x.count = work_list.pieces[lo + 1] - work_list.pieces[lo];
-    x.slot = i;
-    const int n = x.last - x.step, first = x.step;
-    x.step = first + (int)((long long)n * x.index / x.count);
-    x.last = first + (int)((long long)n * (x.index + 1) / x.count);
+    next_item = lo;
+  }
+  auto piece_at = [&](int round) {
+    Piece x;
+    x.rows = 0;
+    if (!dealt) {
+      // in turn, every other round backwards: a request's items get shorter, so
+      // that a CTA's long ones meet its short ones
+      const long long i =
+          (long long)round * grid + (round & 1 ? grid - 1 - (int)blockIdx.x : (int)blockIdx.x);
+      return i < items ? item_at<D>(c, work_list, (int)i) : x;
+    }
+    while (next_item < items && work_list.at[next_item] < share_hi) {
+      const int i = next_item++;
+      const long long at = work_list.at[i];
+      const int n = (int)(work_list.at[i + 1] - at) - kItemCost;
+      const int from = (int)min(max(share_lo - at, 0LL), (long long)n);
+      const int to = (int)min(share_hi - at, (long long)n);
+      // (an item without keys is its first owner's)
+      if (n > 0 ? from >= to : at < share_lo) continue;
+      x = item_at<D>(c, work_list, i);
+      if (n > 0) {
+        x.owner = owner_of(at);
+        x.index = (int)blockIdx.x - x.owner;
+        x.count = owner_of(at + n - 1) - x.owner + 1;
+        x.last = x.step + to;
+        x.step += from;
+      }
+      break;
+    }
     return x;
   };
   int turns = 0;                          // the giver's
@@ -1129,6 +1138,8 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
       }
       steps += n;
       work += n > 0;
+      // partial results: a share begins and ends inside an item at most
+      const int part_slot = 2 * (int)blockIdx.x + (x.index == 0);
       const bool odd = n > 0 && s_odd[work & 3] == work;
       const bool whole = x.count == 1;
       const float v_scale = c.v_scale ? __ldg(c.v_scale + x.head) : 1.f;
@@ -1207,7 +1218,7 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
           }
         } else {
           // four columns of all rows lie together
-          float4* part = reinterpret_cast<float4*>(c.part_o) + (size_t)x.slot * S::kRows * D / 4 + r;
+          float4* part = reinterpret_cast<float4*>(c.part_o) + (size_t)part_slot * S::kRows * D / 4 + r;
 #pragma unroll 1
           for (int i = 0; i < D; i += 32) {
             float o[32];
@@ -1219,7 +1230,7 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
             }
           }
           if (in) {
-            float* ml = c.part_ml + (size_t)x.slot * 2 * S::kRows + r;
+            float* ml = c.part_ml + (size_t)part_slot * 2 * S::kRows + r;
             ml[0] = m;
             ml[S::kRows] = l;
           }
@@ -1251,10 +1262,10 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
             }
           } else {
             for (int e = 0; e < D / 32; ++e)
-              c.part_o[(((size_t)x.slot * D / 4 + (lane + 32 * e) / 4) * S::kRows + rr) * 4 +
+              c.part_o[(((size_t)part_slot * D / 4 + (lane + 32 * e) / 4) * S::kRows + rr) * 4 +
                        (lane & 3)] = o[e];
             if (lane == 0) {
-              float* ml = c.part_ml + (size_t)x.slot * 2 * S::kRows + rr;
+              float* ml = c.part_ml + (size_t)part_slot * 2 * S::kRows + rr;
               ml[0] = m1;
               ml[S::kRows] = l1;
             }
@@ -1281,7 +1292,7 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
           __threadfence();
           // a lane has a row, a warp some columns of 32 rows
           constexpr int kCols = D / 8;
-          const int from = x.slot - x.index, col = wid * kCols;
+          const int col = wid * kCols;
           for (int r0 = 0; r0 < x.rows; r0 += 32) {
             const bool in = r0 + lane < x.rows;
             const int rr = min(r0 + lane, x.rows - 1);
@@ -1290,10 +1301,11 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
             for (int e = 0; e < kCols; ++e) o[e] = 0.f;
 #pragma unroll 2
             for (int i = 0; i < x.count; ++i) {
-              const float* ml = c.part_ml + (size_t)(from + i) * 2 * S::kRows + rr;
+              const size_t slot = 2 * (x.owner + i) + (i == 0);
+              const float* ml = c.part_ml + slot * 2 * S::kRows + rr;
               const float mi = __ldcg(ml), li = __ldcg(ml + S::kRows);
               const float4* part = reinterpret_cast<const float4*>(c.part_o) +
-                                   ((size_t)(from + i) * D + col) / 4 * S::kRows + rr;
+                                   (slot * D + col) / 4 * S::kRows + rr;
               float4 p[kCols / 4];
 #pragma unroll
               for (int e = 0; e < kCols / 4; ++e) p[e] = __ldcg(part + e * S::kRows);
