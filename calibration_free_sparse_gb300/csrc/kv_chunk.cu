@@ -774,7 +774,7 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
         asked++;
         return true;
       };
-      auto widen = [&](const Piece& x, int k0, int page, bool watch) {
+      auto widen = [&](const Piece& x, int k0, int page, bool hide, bool watch) {
         const uint32_t at = taken & 1;
         if (!tc::bar_wait(raw_full(at), taken >> 1 & 1, &s_quit)) return false;
         if (!tc::bar_wait(slot_free(s), phase, &s_quit)) return false;
@@ -786,24 +786,34 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
         for (int i = 0; i < kN; ++i)
           v[i] = get_smem(from + min((i * kWideners + who - 1) * kSub + sub, S::kKeys - 1) * D);
         tc::bar_arrive(raw_free(at));
+        if (hide) {
+          // rows out of sight, or of pages that are not there
+#pragma unroll
+          for (int i = 0; i < kN; ++i) {
+            const int r = (i * kWideners + who - 1) * kSub + sub, key = k0 + r;
+            const bool in = __shfl_sync(0xffffffffu, page, r >> 4 & 31) >= 0 && key >= x.lo &&
+                            key < x.hi;
+            if (!in) v[i] = make_uint4(0, 0, 0, 0);
+            const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) odd |= (w[j] & 0x7f7f7f7fu) + 0x01010101u;
+          }
+        }
+        // lanes of odd blocks store their second half first: those of a block lie
+        // in the same banks as the other's
+        const bool swap = piece >> 2 & 1;
+        const int first = (piece & 3) * 2 + swap;
 #pragma unroll
         for (int i = 0; i < kN; ++i) {
-          const int r = (i * kWideners + who - 1) * kSub + sub, key = k0 + r;
+          const int r = (i * kWideners + who - 1) * kSub + sub;
           if (r >= S::kKeys) break;
-          const bool in = __shfl_sync(0xffffffffu, page, r >> 4) >= 0 && key >= x.lo && key < x.hi;
-          if (!in) v[i] = make_uint4(0, 0, 0, 0);
-          const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-          uint32_t o[8];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            if (watch) odd |= (w[j] & 0x7f7f7f7fu) + 0x01010101u;
-            o[2 * j] = widen2(w[j]);
-            o[2 * j + 1] = widen2(w[j] >> 16);
-          }
-          put_smem(to + tc::swizzled(r, (piece & 3) * 2), o[0], o[1], o[2], o[3]);
-          put_smem(to + tc::swizzled(r, (piece & 3) * 2 + 1), o[4], o[5], o[6], o[7]);
+          const uint32_t a0 = swap ? v[i].z : v[i].x, a1 = swap ? v[i].w : v[i].y;
+          const uint32_t b0 = swap ? v[i].x : v[i].z, b1 = swap ? v[i].y : v[i].w;
+          const uint32_t at0 = to + tc::swizzled(r, first), at1 = to + tc::swizzled(r, first ^ 1);
+          put_smem(at0, widen2(a0), widen2(a0 >> 16), widen2(a1), widen2(a1 >> 16));
+          put_smem(at1, widen2(b0), widen2(b0 >> 16), widen2(b1), widen2(b1 >> 16));
         }
-        if (odd & 0x80808080u) s_odd[work & 3] = work;
+        if (watch && odd & 0x80808080u) s_odd[work & 3] = work;
         taken++;
         tc::publish_smem();
         tc::bar_arrive(slot_full(s));
@@ -847,7 +857,8 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
             if (wid == 9 && lane == 0) s_bad[steps & 7] = lost;
             steps++;
             // (0 times NaN is not 0: keys' NaN reach the rows that see them)
-            if (!widen(x, k0, page, false) || !widen(x, k0, page, partial_step<D>(c, x, k0)))
+            const bool hide = lost || partial_step<D>(c, x, k0);
+            if (!widen(x, k0, page, hide, false) || !widen(x, k0, page, hide, true))
               goto loaders_end;
             page = next;
             next = far;
