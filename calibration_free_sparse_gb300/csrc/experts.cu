@@ -100,24 +100,24 @@ experts_plan_kernel(moe_reader_experts_plan_args a) {
 // of rows cost few columns of nothing, and an expert with three tokens is read
 // at the speed of its weights.  A tile is 2 x 128 weight rows (gate and up of
 // 128 channels; 256 channels of down) by up to N plan rows; a persistent CTA per SM
-// takes tiles in turn.  One warp brings weights by tensor copies, four gather
-// the plan rows' inputs by 16-byte copies (a token's row stands wherever the
-// caller has it), one issues the products, eight write a finished tile out while
-// the next one is summed (two sets of accumulators where they fit).
-constexpr int kGroupThreads = 512;
+// takes tiles in turn.  One warp brings weights by tensor copies, one the
+// activations or eight the tokens, one issues the products, eight write a
+// finished tile out while the next one is summed (two sets of accumulators where
+// they fit).
 constexpr int kBoxBytes = 128 * 128;          // 128 weight rows of 64 values
 
 template <int N> struct GroupShape {
   static constexpr int kStageBytes = 2 * kBoxBytes + N * 128;
   static constexpr int kStages = N >= 256 ? 3 : N >= 128 ? 4 : N >= 64 ? 5 : 6;
-  static constexpr int kLag = kStages > 3 ? 2 : 1;     // copies under way behind the newest
+  static constexpr int kLag = kStages - 2;             // copies under way behind the newest
+  static constexpr int kRowBox = N < 64 ? N : 64;      // plan rows of a tensor copy
   static constexpr int kSets = N <= 128 ? 2 : 1;       // sets of accumulators
   static constexpr size_t kSmem = (size_t)kStages * kStageBytes + 1024;
 };
 
 struct GroupArgs {
-  const char* in;            // rows of the right operand
-  long long in_stride;       // bytes
+  const void* in;            // rows of the right operand
+  long long in_stride;       // elements
   const int32_t* order;      // the pair of each row (in = token rows), or null (in = plan rows)
   const int32_t* offsets;
   void* out;                 // act, or slots
@@ -125,10 +125,13 @@ struct GroupArgs {
   int pairs, topk;
 };
 
+// Warps: weights, products, activations, none; eight write out; eight bring tokens.
+template <bool kAct> constexpr int group_threads() { return kAct ? 640 : 384; }
+
 template <int N, bool kBf16, bool kAct>
-__global__ void __launch_bounds__(kGroupThreads, 1)
+__global__ void __launch_bounds__(group_threads<kAct>(), 1)
 group_kernel(const __grid_constant__ CUtensorMap map0, const __grid_constant__ CUtensorMap map1,
-             GroupArgs a, uint32_t* err) {
+             const __grid_constant__ CUtensorMap in_map, GroupArgs a, uint32_t* err) {
   using S = GroupShape<N>;
   extern __shared__ char raw[];
   __shared__ int s_first[kMaxExperts + 1], s_tiles[kMaxExperts + 1];
@@ -146,12 +149,12 @@ group_kernel(const __grid_constant__ CUtensorMap map0, const __grid_constant__ C
   const uint32_t drained = bars + 8 * (3 * S::kStages + 2 * S::kSets);
 
   // the experts' first rows and tiles
-  for (int e = tid; e <= a.experts; e += kGroupThreads)
+  for (int e = tid; e <= a.experts; e += group_threads<kAct>())
     s_first[e] = min(max(__ldg(a.offsets + e), 0), a.pairs);
   if (tid == 0) {
     for (int s = 0; s < S::kStages; ++s) {
       tc::bar_init(weights_in(s), 1);
-      tc::bar_init(rows_in(s), 128);
+      tc::bar_init(rows_in(s), kAct ? 256 : 1);
       tc::bar_init(stage_free(s), 1);
     }
     for (int s = 0; s < S::kSets; ++s) {
@@ -198,9 +201,11 @@ group_kernel(const __grid_constant__ CUtensorMap map0, const __grid_constant__ C
       const int mid = (lo + hi + 1) >> 1;
       if (s_tiles[mid] <= t) lo = mid; else hi = mid - 1;
     }
+    // an expert's rows in tiles of about one size
     const int all = s_first[lo + 1] - s_first[lo], n_tiles = (all + N - 1) / N;
-    const int at = t - s_tiles[lo], n = at % n_tiles;
-    return Tile{lo, at / n_tiles, s_first[lo] + n * N, min(N, all - n * N)};
+    const int at = t - s_tiles[lo], m = at / n_tiles, n = at - m * n_tiles;
+    const int size = ((all + n_tiles - 1) / n_tiles + 15) & ~15, from = min(n * size, all);
+    return Tile{lo, m, s_first[lo] + from, min(size, all - from)};
   };
 
   if (wid == 0) {
@@ -267,41 +272,66 @@ group_kernel(const __grid_constant__ CUtensorMap map0, const __grid_constant__ C
     __syncwarp();
     volatile uint32_t ignore = 0;
     tc::bar_wait(drained, 0, &ignore);
-  } else if (wid >= 4 && wid < 8) {
-    // the plan rows' inputs: eight threads a row of 128 bytes, 16 rows at once
-    const int id = tid - 128, piece = id & 7, sub = id >> 3;
+  } else if (wid == 2 && !kAct) {
+    // activations: the plan's rows on end, by tensor copies too (what they bring
+    // of the next expert's is not multiplied)
+    int s = 0, used = 0;
+    uint32_t phase = 1;
+    for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
+      const Tile x = tile_at(t);
+      const int boxes = (x.rows + S::kRowBox - 1) / S::kRowBox;
+      for (int k = 0; k < k_steps; ++k) {
+        if (!tc::bar_wait(stage_free(s), phase, &s_quit)) goto rows_end;
+        if (tc::elected()) {
+          tc::bar_expect(rows_in(s), boxes * S::kRowBox * 128);
+          for (int i = 0; i < boxes; ++i)
+            tc::load_box(stage_at(s) + 2 * kBoxBytes + i * S::kRowBox * 128, &in_map, k * 64,
+                         x.first + i * S::kRowBox, 0, rows_in(s));
+        }
+        __syncwarp();
+        used++;
+        if (++s == S::kStages) s = 0, phase ^= 1;
+      }
+    }
+  rows_end:
+    // no copy is left under way
+    for (int i = 0; i < min(used, S::kStages); ++i) {
+      if (--s < 0) s = S::kStages - 1, phase ^= 1;
+      volatile uint32_t ignore = 0;
+      tc::bar_wait(rows_in(s), phase ^ 1, &ignore);
+    }
+  } else if (wid >= 12) {
+    // Tokens, wherever they stand: eight lanes copy a row's 128 bytes, 32 rows at
+    // once.  (Tensor copies of four rows take about 50 cycles each, one after the
+    // other: 64 of them took three times a stage's products.)
+    const int id = tid - 384, piece = id & 7, sub = id >> 3;
     int s = 0, late = 0, behind = 0;       // `late`: oldest stage not yet handed over
     uint32_t phase = 1;
     for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
       const Tile x = tile_at(t);
       const int n16 = (x.rows + 15) & ~15;
-      const char* from[N / 16];
+      constexpr int kTurns = (N + 31) / 32;
+      const char* from[kTurns];
       uint32_t in = 0;
 #pragma unroll
-      for (int i = 0; i < N / 16; ++i) {
-        const int r = i * 16 + sub;
+      for (int i = 0; i < kTurns; ++i) {
+        const int r = i * 32 + sub;
         long long at = 0;
         if (r < x.rows) {
-          int row = x.first + r;
-          if (kAct) {
-            row = __ldg(a.order + row);
-            if ((unsigned)row < (unsigned)a.pairs) in |= 1u << i, at = row / a.topk;
-          } else {
-            in |= 1u << i;
-            at = row;
-          }
+          const int pair = __ldg(a.order + x.first + r);
+          if ((unsigned)pair < (unsigned)a.pairs) in |= 1u << i, at = pair / a.topk;
         }
-        from[i] = a.in + at * a.in_stride + piece * 16;
+        from[i] = static_cast<const char*>(a.in) + at * a.in_stride * 2 + piece * 16;
       }
       for (int k = 0; k < k_steps; ++k) {
-        if (!tc::bar_wait(stage_free(s), phase, &s_quit)) goto rows_end;
+        if (!tc::bar_wait(stage_free(s), phase, &s_quit)) goto tokens_end;
         const uint32_t to = stage_at(s) + 2 * kBoxBytes + tc::swizzled(sub, piece);
         const bool k_in = k * 64 + piece * 8 < a.k;
 #pragma unroll
-        for (int i = 0; i < N / 16; ++i)
-          if (i * 16 < n16) {
+        for (int i = 0; i < kTurns; ++i)
+          if (i * 32 + sub < n16) {
             const bool there = k_in && (in >> i & 1);
-            tc::copy16(to + i * 2048, there ? from[i] + k * 128 : a.in, there);
+            tc::copy16(to + i * 4096, there ? from[i] + k * 128 : from[i] - piece * 16, there);
           }
         tc::copies_commit();
         if (behind == S::kLag) {
@@ -315,16 +345,16 @@ group_kernel(const __grid_constant__ CUtensorMap map0, const __grid_constant__ C
         if (++s == S::kStages) s = 0, phase ^= 1;
       }
     }
-  rows_end:
+  tokens_end:
     tc::copies_wait<0>();
     tc::publish_smem();
     for (; behind > 0; --behind) {
       tc::bar_arrive(rows_in(late));
       if (++late == S::kStages) late = 0;
     }
-  } else if (wid >= 8) {
+  } else if (wid >= 4) {
     // a finished tile: a thread has one channel (row) and half of the columns
-    const int quarter = wid & 3, half = (wid - 8) >> 2;
+    const int quarter = wid & 3, half = (wid - 4) >> 2;
     int set = 0;
     uint32_t set_phase = 0;
     for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
@@ -339,25 +369,28 @@ group_kernel(const __grid_constant__ CUtensorMap map0, const __grid_constant__ C
         tc::ld16(at + c * 16, u);
         tc::ld16(at + N + c * 16, v);
         tc::ld_wait();
+        const int left = x.rows - c * 16;
+        const long long row = x.first + c * 16;
+        if constexpr (kAct) {
+          // silu(gate) * up in fp32, rounded once
+          uint16_t* out = static_cast<uint16_t*>(a.out) + row * a.channels + ch;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int col = c * 16 + i;
-          if (col >= x.rows) break;
-          const long long row = x.first + col;
-          const float f = __uint_as_float(u[i]), g = __uint_as_float(v[i]);
-          if constexpr (kAct) {
-            // silu(gate) * up in fp32, rounded once
-            const float y = f / (1.f + __expf(-f)) * g;
-            if (ch < a.channels) {
-              if constexpr (kBf16)
-                static_cast<__nv_bfloat16*>(a.out)[row * a.channels + ch] = __float2bfloat16_rn(y);
-              else
-                static_cast<__half*>(a.out)[row * a.channels + ch] = __float2half_rn(y);
-            }
-          } else {
-            float* out = static_cast<float*>(a.out) + row * a.channels + ch;
-            if (ch < a.channels) out[0] = f;
-            if (ch + 128 < a.channels) out[128] = g;
+          for (int i = 0; i < 16; ++i) {
+            const float f = __uint_as_float(u[i]), g = __uint_as_float(v[i]);
+            const float y = __fdividef(f, 1.f + __expf(-f)) * g;
+            uint16_t bits;
+            if constexpr (kBf16) bits = __bfloat16_as_ushort(__float2bfloat16_rn(y));
+            else bits = __half_as_ushort(__float2half_rn(y));
+            if (i < left && ch < a.channels) *out = bits;
+            out += a.channels;
+          }
+        } else {
+          float* out = static_cast<float*>(a.out) + row * a.channels + ch;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            if (i < left && ch < a.channels) out[0] = __uint_as_float(u[i]);
+            if (i < left && ch + 128 < a.channels) out[128] = __uint_as_float(v[i]);
+            out += a.channels;
           }
         }
       }
@@ -406,7 +439,16 @@ template <int N, bool kBf16, bool kAct>
 cudaError_t group_as(const moe_reader_experts& h, const GroupArgs& a, cudaStream_t s) {
   const CUtensorMap& m0 = kAct ? h.gate_map : h.down_map;
   const CUtensorMap& m1 = kAct ? h.up_map : h.down_map;
-  group_kernel<N, kBf16, kAct><<<h.sms, kGroupThreads, GroupShape<N>::kSmem, s>>>(m0, m1, a, h.err);
+  CUtensorMap in = {};
+  if (!kAct) {
+    const uint64_t sizes[3] = {(uint64_t)a.k, (uint64_t)a.pairs, 1};
+    const uint64_t strides[2] = {(uint64_t)a.k, (uint64_t)a.k * a.pairs};
+    const uint32_t box[3] = {64, (uint32_t)GroupShape<N>::kRowBox, 1};
+    const cudaError_t e = tc::make_map(&in, a.in, kBf16, 3, sizes, strides, box);
+    if (e != cudaSuccess) return e;
+  }
+  group_kernel<N, kBf16, kAct><<<h.sms, group_threads<kAct>(), GroupShape<N>::kSmem, s>>>(
+      m0, m1, in, a, h.err);
   return cudaGetLastError();
 }
 
@@ -418,13 +460,14 @@ cudaError_t group(const moe_reader_experts& h, const GroupArgs& a, cudaStream_t 
   const int mean = a.pairs / a.experts;
   if (mean <= 32) return group_as<32, kBf16, kAct>(h, a, s);
   if (mean <= 64) return group_as<64, kBf16, kAct>(h, a, s);
-  return group_as<128, kBf16, kAct>(h, a, s);
+  if (mean <= 112) return group_as<128, kBf16, kAct>(h, a, s);
+  return group_as<256, kBf16, kAct>(h, a, s);
 }
 
 template <bool kBf16>
 cudaError_t activate_as(const moe_reader_experts& h, const moe_reader_experts_activate_args& a,
                         cudaStream_t s) {
-  const GroupArgs g = {static_cast<const char*>(a.x), 2 * a.x_stride, a.order, a.offsets, a.act,
+  const GroupArgs g = {a.x, a.x_stride, a.order, a.offsets, a.act,
                        h.cfg.num_experts, h.cfg.hidden, h.cfg.inter,
                        a.tokens * a.experts_per_token, a.experts_per_token};
   return group<kBf16, true>(h, g, s);
@@ -434,7 +477,7 @@ template <bool kBf16>
 cudaError_t combine_as(const moe_reader_experts& h, const moe_reader_experts_combine_args& a,
                        cudaStream_t s) {
   const int H = h.cfg.hidden, topk = a.experts_per_token;
-  const GroupArgs g = {static_cast<const char*>(a.act), 2LL * h.cfg.inter, nullptr, a.offsets,
+  const GroupArgs g = {a.act, h.cfg.inter, nullptr, a.offsets,
                        a.slots, h.cfg.num_experts, h.cfg.inter, H, a.tokens * topk, topk};
   const cudaError_t e = group<kBf16, false>(h, g, s);
   if (e != cudaSuccess) return e;
@@ -458,6 +501,7 @@ cudaError_t configure_group() {
   cudaError_t e = configure_one<32, kBf16, kAct>();
   if (e == cudaSuccess) e = configure_one<64, kBf16, kAct>();
   if (e == cudaSuccess) e = configure_one<128, kBf16, kAct>();
+  if (e == cudaSuccess) e = configure_one<256, kBf16, kAct>();
   return e;
 }
 cudaError_t configure_experts(moe_reader_experts& h) {
