@@ -17,7 +17,9 @@ constexpr uint32_t kErrRow = MOE_READER_ERR_ROW;
 // ---------------------------------------------------------------------------
 constexpr int kPoolCtas = 16;         // one cluster
 constexpr int kPoolThreads = 1024;
-constexpr int kPoolWarps = kPoolCtas * kPoolThreads / 32;
+// Pools and tables up to these sizes take one CTA, which counts in its shared
+// memory.
+constexpr int kSmallPool = 16384, kSmallTable = 8192;
 
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
@@ -56,41 +58,52 @@ __device__ __forceinline__ int held_pages(int len, int width, int shift, uint32_
 // Counts references, ranks the pages in use and the free ones by ballots, and
 // (compact) pairs the k-th page in use behind the first `used` with the k-th
 // free one among them.  Each phase needs all of the one before, so the grid is
-// one cluster and its hardware barrier separates them: one launch, no counters
-// that live between calls.  Warp w of the cluster owns a run of the pool; ranks
+// one cluster and its hardware barrier separates them, or one CTA where the pool
+// is small (a barrier of the cluster and the trips to L2 between two took the
+// most time: 2660 pages of 16 rows 10.8 us, 6.2 with one CTA; 10 thousand of 512
+// rows 10.4 and 14.5): one launch, no counters
+// that live between calls.  Warp w of the grid owns a run of the pool; ranks
 // before a run are sums over the warps' totals, gathered in the first CTA.
 // Between the phases free_pages holds the sources' ranks.
-template <bool kCompact>
+template <bool kCompact, int kCtas>
 __global__ void __launch_bounds__(kPoolThreads)
 pool_kernel(moe_reader_kv_pages_args a, int shift, int pool, uint32_t* err) {
+  constexpr int kPoolWarps = kCtas * kPoolThreads / 32;
+  extern __shared__ int s_refs[];       // one CTA: the references
+  int* const refs = kCtas == 1 ? s_refs : a.refs;
+  auto refs_of = [&](long long p) { return kCtas == 1 ? s_refs[p] : __ldcg(a.refs + p); };
+  auto sync = [&]() {
+    if (kCtas == 1) __syncthreads(); else cluster_sync();
+  };
   __shared__ int s_total[kPoolWarps];   // the first CTA's: pages in use per warp's run
   __shared__ int s_front;               // the first CTA's: pages in use among the first `used`
   __shared__ int s_before[kPoolThreads / 32], s_used;
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
-  const int cta = (int)cluster_rank(), warp = cta * (kPoolThreads / 32) + wid;
+  const int cta = kCtas == 1 ? 0 : (int)cluster_rank(), warp = cta * (kPoolThreads / 32) + wid;
   const long long first = (long long)cta * kPoolThreads + threadIdx.x;
-  constexpr long long kAll = (long long)kPoolCtas * kPoolThreads;
+  constexpr long long kAll = (long long)kCtas * kPoolThreads;
   uint32_t bad = 0;
+  wait_for_earlier_launch();
 
-  for (long long p = first; p < pool; p += kAll) a.refs[p] = 0;
-  cluster_sync();
+  for (long long p = first; p < pool; p += kAll) refs[p] = 0;
+  sync();
   for (int r = warp; r < a.requests; r += kPoolWarps) {
     const int held = held_pages(__ldg(a.lens + r), a.width, shift, bad);
     for (int c = lane; c < held; c += 32) {
       const int p = a.table[(size_t)r * a.width + c];
-      if ((unsigned)p < (unsigned)pool) atomicAdd(a.refs + p, 1);
+      if ((unsigned)p < (unsigned)pool) atomicAdd(refs + p, 1);
       else bad |= kErrPage;
     }
   }
-  cluster_sync();
+  sync();
 
   const int per = (int)(((long long)pool + kPoolWarps * 32 - 1) / (kPoolWarps * 32)) * 32;
   const long long lo = (long long)warp * per, hi = min(lo + per, (long long)pool);
   int mine = 0;
   for (long long p = lo; p < hi; p += 32)
-    mine += __popc(__ballot_sync(0xffffffffu, p + lane < hi && __ldcg(a.refs + p + lane) > 0));
+    mine += __popc(__ballot_sync(0xffffffffu, p + lane < hi && refs_of(p + lane) > 0));
   if (lane == 0) put_cluster(in_first_cta(s_total + warp), mine);
-  cluster_sync();
+  sync();
   // pages in use before this CTA's warps, and in all
   if (wid == 0) {
     int before = 0, all = 0;
@@ -119,17 +132,17 @@ pool_kernel(moe_reader_kv_pages_args a, int shift, int pool, uint32_t* err) {
     if (used >= lo && used < hi) {
       int n = before;
       for (long long p = lo; p < used; p += 32)
-        n += __popc(__ballot_sync(0xffffffffu, p + lane < used && __ldcg(a.refs + p + lane) > 0));
+        n += __popc(__ballot_sync(0xffffffffu, p + lane < used && refs_of(p + lane) > 0));
       if (lane == 0) put_cluster(in_first_cta(&s_front), n);
     } else if (warp == 0 && used == pool && lane == 0) {
       put_cluster(in_first_cta(&s_front), used);
     }
-    cluster_sync();
+    sync();
     const int front = get_cluster(in_first_cta(&s_front)), moves = used - front;
     int n = before;
     for (long long p = lo; p < hi; p += 32) {
       const bool in = p + lane < hi;
-      const bool use = in && __ldcg(a.refs + p + lane) > 0;
+      const bool use = in && refs_of(p + lane) > 0;
       const uint32_t uses = __ballot_sync(0xffffffffu, use);
       const int id = (int)p + lane, rank = n + __popc(uses & ((1u << lane) - 1));
       if (in && use && id >= used) {
@@ -144,7 +157,7 @@ pool_kernel(moe_reader_kv_pages_args a, int shift, int pool, uint32_t* err) {
       a.moves[0] = moves;
       a.count[0] = pool - used;
     }
-    cluster_sync();
+    sync();
     for (int r = warp; r < a.requests; r += kPoolWarps) {
       uint32_t known = 0;
       const int held = held_pages(__ldg(a.lens + r), a.width, shift, known);
@@ -156,17 +169,17 @@ pool_kernel(moe_reader_kv_pages_args a, int shift, int pool, uint32_t* err) {
     }
     for (long long k = first; k < moves; k += kAll) {
       const int s = __ldcg(a.src + k);
-      a.refs[__ldcg(a.dst + k)] = __ldcg(a.refs + s);
-      a.refs[s] = 0;
+      refs[__ldcg(a.dst + k)] = refs_of(s);
+      refs[s] = 0;
     }
-    cluster_sync();
+    sync();
     for (long long i = first; i < pool; i += kAll)
       a.free_pages[i] = i < pool - used ? (int)(used + i) : -1;
   } else {
     int n = before;
     for (long long p = lo; p < hi; p += 32) {
       const bool in = p + lane < hi;
-      const bool use = in && __ldcg(a.refs + p + lane) > 0;
+      const bool use = in && refs_of(p + lane) > 0;
       const uint32_t uses = __ballot_sync(0xffffffffu, use);
       const int id = (int)p + lane, rank = n + __popc(uses & ((1u << lane) - 1));
       if (in && !use) a.free_pages[id - rank] = id;
@@ -174,7 +187,11 @@ pool_kernel(moe_reader_kv_pages_args a, int shift, int pool, uint32_t* err) {
     }
     for (long long i = pool - used + first; i < pool; i += kAll) a.free_pages[i] = -1;
     if (first == 0) a.count[0] = pool - used;
-    cluster_sync();       // no CTA ends while others read the first one's memory
+    sync();       // no CTA ends while others read the first one's memory
+  }
+  if (kCtas == 1) {
+    __syncthreads();
+    for (long long p = first; p < pool; p += kAll) a.refs[p] = s_refs[p];
   }
   if (bad) atomicOr(err, bad);
 }
@@ -182,6 +199,10 @@ pool_kernel(moe_reader_kv_pages_args a, int shift, int pool, uint32_t* err) {
 template <bool kCompact>
 cudaError_t launch_pool(const moe_reader_kv& kv, const moe_reader_kv_pages_args& a,
                         cudaStream_t s) {
+  const int pool = kv.cfg.num_pages;
+  if (pool <= kSmallPool && (long long)a.requests * a.width <= kSmallTable)
+    return launch_early(pool_kernel<kCompact, 1>, dim3(1), kPoolThreads, pool * sizeof(int), s, a,
+                        kv.page_shift, pool, kv.err);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(kPoolCtas);
   cfg.blockDim = dim3(kPoolThreads);
@@ -192,8 +213,7 @@ cudaError_t launch_pool(const moe_reader_kv& kv, const moe_reader_kv_pages_args&
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, pool_kernel<kCompact>, a, kv.page_shift, kv.cfg.num_pages,
-                            kv.err);
+  return cudaLaunchKernelEx(&cfg, pool_kernel<kCompact, kPoolCtas>, a, kv.page_shift, pool, kv.err);
 }
 
 // ---------------------------------------------------------------------------
@@ -210,6 +230,7 @@ fork_kernel(moe_reader_kv_fork_args a, int shift, int pool, uint32_t* err) {
   __shared__ uint8_t s_parent[kMaxRequests];  // a row is some fork's parent
   __shared__ int s_before, s_all;
   const int tid = threadIdx.x, mine = blockIdx.x, ps = 1 << shift;
+  wait_for_earlier_launch();
   for (int r = tid; r < a.rows; r += kForkThreads) s_first[r] = a.forks, s_parent[r] = 0;
   if (tid == 0) s_before = s_all = 0;
   __syncthreads();
@@ -290,6 +311,7 @@ struct CopyShape {
 __global__ void __launch_bounds__(kCopyThreads)
 copy_kernel(moe_reader_kv_copy_args a, CopyShape c, char* k, char* v, char* codes, float* steps,
             int pool, uint32_t* err) {
+  wait_for_earlier_launch();
   long long n = a.count ? min(max(__ldg(a.count), 0), a.pages) : a.pages;
   const long long each = 2 * c.units + (codes != nullptr);
   for (long long u = blockIdx.x; u < n * each; u += gridDim.x) {
@@ -331,10 +353,19 @@ copy_kernel(moe_reader_kv_copy_args a, CopyShape c, char* k, char* v, char* code
 }  // namespace
 
 cudaError_t configure_kv_pages() {
-  cudaError_t e = cudaFuncSetAttribute(pool_kernel<false>,
+  const int bytes = kSmallPool * (int)sizeof(int);
+  cudaError_t e = cudaFuncSetAttribute(pool_kernel<false, kPoolCtas>,
                                        cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-  if (e != cudaSuccess) return e;
-  return cudaFuncSetAttribute(pool_kernel<true>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(pool_kernel<true, kPoolCtas>,
+                             cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(pool_kernel<false, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             bytes);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(pool_kernel<true, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             bytes);
+  return e;
 }
 
 cudaError_t launch_kv_collect(const moe_reader_kv& kv, const moe_reader_kv_pages_args& a,
@@ -348,9 +379,8 @@ cudaError_t launch_kv_compact(const moe_reader_kv& kv, const moe_reader_kv_pages
 
 cudaError_t launch_kv_fork(const moe_reader_kv& kv, const moe_reader_kv_fork_args& a,
                            cudaStream_t s) {
-  fork_kernel<<<std::max(a.forks, 1), kForkThreads, 0, s>>>(a, kv.page_shift, kv.cfg.num_pages,
-                                                            kv.err);
-  return cudaGetLastError();
+  return launch_early(fork_kernel, dim3(std::max(a.forks, 1)), kForkThreads, 0, s, a, kv.page_shift,
+                      kv.cfg.num_pages, kv.err);
 }
 
 cudaError_t launch_kv_copy(const moe_reader_kv& kv, const moe_reader_kv_copy_args& a,
@@ -364,11 +394,9 @@ cudaError_t launch_kv_copy(const moe_reader_kv& kv, const moe_reader_kv_copy_arg
   c.units = (int)((c.page_bytes + kCopyUnit - 1) / kCopyUnit);
   const long long units = a.pages * (2LL * c.units + (kv.codes != nullptr));
   const int grid = (int)std::min<long long>(units, 8LL * kv.sms);
-  copy_kernel<<<grid, kCopyThreads, 0, s>>>(a, c, static_cast<char*>(kv.k),
-                                            static_cast<char*>(kv.v),
-                                            reinterpret_cast<char*>(kv.codes), kv.steps,
-                                            g.num_pages, kv.err);
-  return cudaGetLastError();
+  return launch_early(copy_kernel, dim3(grid), kCopyThreads, 0, s, a, c, static_cast<char*>(kv.k),
+                      static_cast<char*>(kv.v), reinterpret_cast<char*>(kv.codes), kv.steps,
+                      g.num_pages, kv.err);
 }
 
 }  // namespace mr
