@@ -16,6 +16,7 @@ namespace {
 std::atomic<int> g_fail_next_alloc{0};
 std::atomic<int> g_stall_next_prepare{0};
 std::atomic<int> g_stall_next_attend{0};
+std::atomic<int> g_stall_next_prompt{0};
 
 using mr::Dims;
 
@@ -178,6 +179,9 @@ cudaError_t device_alloc(void** p, size_t bytes) {
 bool take_prepare_stall() { return g_stall_next_prepare.exchange(0) != 0; }
 bool take_attend_stall() {
   return g_stall_next_attend.load(std::memory_order_relaxed) && g_stall_next_attend.exchange(0) != 0;
+}
+bool take_prompt_stall() {
+  return g_stall_next_prompt.load(std::memory_order_relaxed) && g_stall_next_prompt.exchange(0) != 0;
 }
 
 }  // namespace mr
@@ -551,7 +555,7 @@ int moe_reader_set_wait_limit(moe_reader_t* h, uint64_t ns) {
 int moe_reader_inject_fault(moe_reader_t* h, uint32_t what) {
   const uint32_t handle_bits = MOE_READER_INJECT_DECODE_STALL;
   const uint32_t global_bits = MOE_READER_INJECT_PREPARE_STALL | MOE_READER_INJECT_ALLOC_FAIL |
-                               MOE_READER_INJECT_ATTEND_STALL;
+                               MOE_READER_INJECT_ATTEND_STALL | MOE_READER_INJECT_PROMPT_STALL;
   if (what == 0 || (what & ~(handle_bits | global_bits))) return MOE_READER_EINVAL;
   if (h ? (what & global_bits) != 0 : (what & handle_bits) != 0) return MOE_READER_EINVAL;
   if (h) {
@@ -561,6 +565,7 @@ int moe_reader_inject_fault(moe_reader_t* h, uint32_t what) {
   if (what & MOE_READER_INJECT_PREPARE_STALL) g_stall_next_prepare.store(1);
   if (what & MOE_READER_INJECT_ALLOC_FAIL) g_fail_next_alloc.store(1);
   if (what & MOE_READER_INJECT_ATTEND_STALL) g_stall_next_attend.store(1);
+  if (what & MOE_READER_INJECT_PROMPT_STALL) g_stall_next_prompt.store(1);
   return MOE_READER_OK;
 }
 

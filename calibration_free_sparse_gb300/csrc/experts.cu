@@ -141,6 +141,7 @@ struct GroupArgs {
   void* out;                 // act, or slots
   int experts, k, channels;  // channels: I, or H
   int pairs, topk;
+  int stall;                 // wait for a product that was never issued
 };
 
 // Warps: weights, products, activations, none; eight write out; eight bring tokens.
@@ -259,7 +260,7 @@ group_kernel(const __grid_constant__ CUtensorMap map0, const __grid_constant__ C
     // products
     int s = 0, set = 0;
     uint32_t phase = 0, set_phase = 1;
-    bool go = true;
+    bool go = !a.stall || tc::bar_wait(drained, 0, &s_quit);
     for (int t = blockIdx.x; go && t < tiles; t += gridDim.x) {
       const Tile x = tile_at(t);
       const uint32_t idesc = tc::instr<kBf16>((x.rows + 15) & ~15);
@@ -490,7 +491,7 @@ cudaError_t activate_as(const moe_reader_experts& h, const moe_reader_experts_ac
                         cudaStream_t s) {
   const GroupArgs g = {a.x, a.x_stride, a.order, a.offsets, a.act,
                        h.cfg.num_experts, h.cfg.hidden, h.cfg.inter,
-                       a.tokens * a.experts_per_token, a.experts_per_token};
+                       a.tokens * a.experts_per_token, a.experts_per_token, take_prompt_stall()};
   return group<kBf16, true>(h, g, s);
 }
 
@@ -499,7 +500,8 @@ cudaError_t combine_as(const moe_reader_experts& h, const moe_reader_experts_com
                        cudaStream_t s) {
   const int H = h.cfg.hidden, topk = a.experts_per_token;
   const GroupArgs g = {a.act, h.cfg.inter, nullptr, a.offsets,
-                       a.slots, h.cfg.num_experts, h.cfg.inter, H, a.tokens * topk, topk};
+                       a.slots, h.cfg.num_experts, h.cfg.inter, H, a.tokens * topk, topk,
+                       take_prompt_stall()};
   const cudaError_t e = group<kBf16, false>(h, g, s);
   if (e != cudaSuccess) return e;
   const dim3 grid((unsigned)a.tokens, (unsigned)((H + 1023) / 1024));

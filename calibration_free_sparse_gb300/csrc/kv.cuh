@@ -56,6 +56,9 @@ cudaError_t launch_kv_attend(const moe_reader_kv& kv, const moe_reader_kv_attend
 cudaError_t configure_kv_attend(const moe_reader_kv& kv);
 // One-shot injection of a turn that never comes in the next attend.
 bool take_attend_stall();
+// The same of a product that was never issued, in the next kv_chunk or product
+// of the experts.
+bool take_prompt_stall();
 // Items of attend: (request, KV head, tile of the group's query heads).
 int attend_row_tiles(const moe_reader_kv_config& c);
 cudaError_t launch_kv_select(const moe_reader_kv& kv, const moe_reader_kv_select_args& a,

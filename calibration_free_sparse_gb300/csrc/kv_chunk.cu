@@ -118,6 +118,7 @@ struct ChunkCall {
   int rows;                  // of an item: whole groups of heads
   Divisor by_group, by_kv;   // query heads per KV head, KV heads
   int wide;                  // q can be read 16 bytes at a time
+  int stall;                 // wait for a product that was never issued
   int mapped;                // q_map holds; else threads read q
   CUtensorMap q_map, k_map, v_map;      // k, v: of 16-bit caches
 };
@@ -317,7 +318,7 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
   // The products' type: the cache's, fp16 for e4m3 (the one conversion that
   // there is an instruction for; widening to bf16 took twice the issue slots and
   // left the weights three bits less).  Queries in bf16 are brought to fp16 by
-  // a power of two per row that puts the largest near 2^15: exact down to 2^-32
+  // a power of two per row that puts the largest near 2^15: exact down to 2^-30
   // of it.
   constexpr int MT = CT == kE4m3 ? kF16 : QT;
   constexpr bool kScaled = CT == kE4m3 && QT == kBf16;
@@ -391,7 +392,7 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
   constexpr int kProducts = 8 + S::kLoaders;
   if (wid == kProducts) tc::tmem_alloc(tc::smem_at(&s_tmem), 512);
   if (tid == 32) {
-    tc::prefetch_map(&c.q_map);
+    if (c.mapped) tc::prefetch_map(&c.q_map);
     if (CT != kE4m3) tc::prefetch_map(&c.k_map), tc::prefetch_map(&c.v_map);
   }
   wait_for_earlier_launch();
@@ -544,6 +545,7 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
     uint32_t phase = 1, q_phase = 1, work = 0, steps = 0, err = 0;
     uint32_t cleared = 0, clear_phase = 0;     // a bit per slot
     uint32_t raw_asked = 0;
+    int issued = 0;
     // queries of a piece: blocks of 64 coordinates, each with all rows
     auto queries = [&](const Piece& x) {
       if (c.mapped) {
@@ -599,18 +601,31 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
           }
 #pragma unroll
           for (int o = 1; o < 8; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-          const int e = floor_log2_held(top) - 14;
+          // (the powers and their inverses are normal numbers)
+          const int e = min(max((int)(__float_as_uint(top) >> 23) - 127, -100), 127) - 14;
           const float by = two_to(-e) * (flip ? -1.f : 1.f);
+          int cut = 0, large = 0;
           if (piece == 0) s_q_scale[turn][r] = two_to(e);
 #pragma unroll
           for (int b = 0; b < S::kBlocks; ++b) {
             const uint32_t w[4] = {v[b].x, v[b].y, v[b].z, v[b].w};
             uint32_t o[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              o[i] = pack2<kF16>(bf16_lo(w[i]) * by, bf16_hi(w[i]) * by);
+            for (int i = 0; i < 4; ++i) {
+              const float lo = bf16_lo(w[i]) * by, hi = bf16_hi(w[i]) * by;
+              o[i] = pack2<kF16>(lo, hi);
+              const float2 is = __half22float2(*reinterpret_cast<const __half2*>(&o[i]));
+              cut |= (is.x != lo && lo == lo) | (is.y != hi && hi == hi);
+              large += (fabsf(lo) >= 0.00390625f) + (fabsf(hi) >= 0.00390625f);
+            }
             put_smem(q_at + b * S::kRows * 128 + tc::swizzled(r, piece), o[0], o[1], o[2], o[3]);
           }
+          // bits lost far below the largest coordinate count where hardly any
+          // other is near it: such pieces go row by row
+          large += cut << 16;
+#pragma unroll
+          for (int o = 1; o < 8; o <<= 1) large += __shfl_xor_sync(0xffffffffu, large, o);
+          if (large >> 16 && (large & 0xffff) < D / 8) s_odd[(x.turn + 1) & 3] = x.turn + 1;
         }
         tc::publish_smem();
         tc::bar_arrive(q_full);
@@ -682,6 +697,7 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
                 if (clear) tc::bar_arrive(slot_full(s));
               }
               if (clear) cleared |= 1u << s, clear_phase ^= 1u << s;
+              issued++;
               __syncwarp();
               if (lane < boxes) {
                 const uint32_t to = kv_at + s * S::kSlotBytes + lane * rows * 128;
@@ -878,7 +894,7 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
         tc::bar_wait(raw_full(i & 1), i >> 1 & 1, &ignore);
     }
     if (kCopies && wid == 8) {
-      for (int i = 0; i < (int)min(2 * steps, (uint32_t)S::kSlots); ++i) {
+      for (int i = 0; i < min(issued, S::kSlots); ++i) {
         if (--s < 0) s = S::kSlots - 1, phase ^= 1;
         volatile uint32_t ignore = 0;
         tc::bar_wait(slot_full(s), phase ^ 1, &ignore);
@@ -946,7 +962,7 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
       __syncwarp();
       return true;
     };
-    bool go = true;
+    bool go = !c.stall || tc::bar_wait(drained, 0, &s_quit);
     for (int round = 0; go && take(round); leave(round++)) {
       const Piece& x = s_piece[round & 3];
       if (x.step >= x.last) continue;
@@ -1089,9 +1105,11 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
           const float high = fmaxf(top[0], top[1]) * by;
           const bool moves = high > m + kSlack;
           if (__any_sync(0xffffffffu, moves)) {
-            // the reference follows the maximum; what is added up so far with it
-            const float f = moves ? exp2_fast(m - high) : 1.f;
-            if (moves) m = high;
+            // the reference follows the maximum, in whole powers of two, so that
+            // rescaling and the exponents below round nothing; what is added up
+            // so far follows it
+            const float to = ceilf(high), f = moves ? exp2_fast(m - to) : 1.f;
+            if (moves) m = to;
             l *= f;
             if (turn > 0) {
               // (two tiles: S is made behind the products before it)
@@ -1366,7 +1384,7 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
 
 template <int D, int CT, int QT>
 cudaError_t chunk_as(const moe_reader_kv& kv, const moe_reader_kv_chunk_args& a, cudaStream_t s) {
-  ChunkCall c;
+  ChunkCall c = {};
   c.a = a;
   c.k = static_cast<const char*>(kv.k);
   c.v = static_cast<const char*>(kv.v);
@@ -1384,6 +1402,7 @@ cudaError_t chunk_as(const moe_reader_kv& kv, const moe_reader_kv_chunk_args& a,
   c.pool = kv.cfg.num_pages;
   using S = ChunkShape<D>;
   c.rows = S::kRows / kv.group * kv.group;
+  c.stall = take_prompt_stall();
   // a box: all of an item's tokens, one KV head's queries, 64 coordinates
   c.wide = reinterpret_cast<uintptr_t>(a.q) % 16 == 0 && a.q_token_stride % 8 == 0 &&
            a.q_head_stride % 8 == 0;
@@ -1427,7 +1446,8 @@ int chunk_rows(const moe_reader_kv_config& c) {
 
 cudaError_t configure_kv_chunk(moe_reader_kv& kv) {
   const moe_reader_kv_config& g = kv.cfg;
-  for (int i = 0; i < 2 && g.cache_type != kE4m3; ++i) {
+  // (an e4m3 cache's pages come by bulk copies: its maps are not used)
+  for (int i = 0; i < 2; ++i) {
     const uint64_t D = g.head_dim, P = g.page_size, H = g.num_kv_heads;
     const uint64_t sizes[4] = {D, P, H, (uint64_t)g.num_pages}, strides[3] = {D, P * D, H * P * D};
     const uint32_t box[4] = {64, (uint32_t)std::min(g.page_size, D <= 128 ? 128 : 64), 1, 1};

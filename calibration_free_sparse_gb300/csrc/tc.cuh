@@ -7,6 +7,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 namespace mr {
 namespace tc {
 
@@ -212,7 +214,8 @@ inline cudaError_t make_map(CUtensorMap* map, const void* base, bool bf16, int d
                               const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
                               const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
                               CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-  static Encode encode = nullptr;       // (the same from every thread)
+  static std::atomic<Encode> found_before{nullptr};
+  Encode encode = found_before.load(std::memory_order_relaxed);
   if (!encode) {
     void* fn = nullptr;
     cudaDriverEntryPointQueryResult found;
@@ -221,6 +224,7 @@ inline cudaError_t make_map(CUtensorMap* map, const void* base, bool bf16, int d
     if (e != cudaSuccess) return e;
     if (found != cudaDriverEntryPointSuccess || !fn) return cudaErrorNotSupported;
     encode = reinterpret_cast<Encode>(fn);
+    found_before.store(encode, std::memory_order_relaxed);
   }
   cuuint64_t bytes[3];
   for (int i = 0; i + 1 < dims; ++i) bytes[i] = strides[i] * 2;

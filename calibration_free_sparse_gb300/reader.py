@@ -21,7 +21,7 @@ FLAG_TRIT5 = 0x2      # sketch codes stored five trits per byte
 ERR_EXPERT_RANGE, ERR_EXPERT_DUP, ERR_WEIGHT, ERR_X_NONFINITE, ERR_TIMEOUT = 1, 2, 4, 8, 16
 # one-shot fault injections for tests of failure detection (moe_reader_inject_fault)
 INJECT_DECODE_STALL, INJECT_PREPARE_STALL, INJECT_ALLOC_FAIL = 0x1, 0x2, 0x4
-INJECT_ATTEND_STALL = 0x10
+INJECT_ATTEND_STALL, INJECT_PROMPT_STALL = 0x10, 0x20
 ARRAYS = ("codes", "scales", "dnorm", "G", "V", "Dt", "b", "U")
 
 EXPORT = {

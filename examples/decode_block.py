@@ -12,6 +12,12 @@ Per layer and step, with h the residual stream of a batch of requests:
     h       += y = routed experts by the channel reader    MoeReader.decode,
                                                            residual_norm
 
+A prompt, or a chunk of one, goes the same way with many tokens a request:
+``PagedCache.attend_chunk`` in place of ``attend``, and its routed experts whole
+(``Experts.activate``, ``Experts.combine``).  ``Decoder.fork`` continues a request
+in several ways on shared pages, ``Decoder.free_requests`` gives pages back and
+moves the others together.
+
 The page plan (``PagePlan.update``) is made once a step for all layers, from
 the requests' lengths, on the GPU.  Weights are random: there is no text here,
 only the step.  Run it with ``python examples/decode_block.py``.
@@ -25,7 +31,7 @@ import torch
 
 sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 
-from calibration_free_sparse_gb300 import block  # noqa: E402
+from calibration_free_sparse_gb300 import block, experts  # noqa: E402
 from calibration_free_sparse_gb300 import synthetic as S  # noqa: E402
 from calibration_free_sparse_gb300.reader import MoeReader  # noqa: E402
 
@@ -56,6 +62,7 @@ class Layer:
         weights = S.weights_device(seed, w.E, w.I, w.H, "cuda")
         self.reader = MoeReader(w.H, w.E, w.topk, w.I, *weights, S.signs(seed, w.Hp),
                                 screen_coords=w.c, rank=w.r, max_batch=max_requests)
+        self.experts = experts.Experts(*weights)
 
 
 class Decoder:
@@ -72,6 +79,7 @@ class Decoder:
         self.free = torch.arange(pages, **i32)
         self.lens = torch.zeros(max_requests, **i32)
         self.plan = self.layers[0].cache.plan(self.table, max_requests)
+        self.pool = self.layers[0].cache.pool(max_requests)
         f32 = dict(device="cuda")
         self.x = torch.empty((max_requests, workload.H), **f32)
         self.y = torch.empty((max_requests, workload.H), **f32)
@@ -108,10 +116,60 @@ class Decoder:
         self.free = torch.roll(self.free, -int(plan.taken))
         return h
 
+    def prompt(self, h, new):
+        """Take a chunk of prompts: h [tokens][H] float32, the new tokens of all
+        requests in order (updated in place), new int32 [requests]: how many
+        each has."""
+        w, T = self.w, h.shape[0]
+        f32, bf = dict(device="cuda"), dict(dtype=torch.bfloat16, device="cuda")
+        plan = self.layers[0].cache.plan(self.table, T).update(self.lens, new, self.free)
+        routed = experts.ExpertPlan(w.E, w.topk, T, hidden=w.H)
+        x, y = torch.empty((T, w.H), **f32), torch.empty((T, w.H), **f32)
+        act = torch.empty((T * w.topk, w.I), **bf)
+        for layer in self.layers:
+            heads, kv, dim = layer.q_heads, layer.kv_heads, layer.head_dim
+            block.residual_norm(h, x, pre_weight=layer.norm1)
+            qkv = (x.to(torch.bfloat16) @ layer.qkv).view(T, heads + 2 * kv, dim)
+            layer.cache.append(qkv[:, heads:heads + kv], qkv[:, heads + kv:], plan.slots)
+            attended = torch.empty((T, heads, dim), **bf)
+            layer.cache.attend_chunk(qkv[:, :heads], self.table, plan.lens, plan.starts, attended)
+            block.residual_norm(h, x, y=attended.view(T, -1) @ layer.out, scale=self.scale,
+                                pre_weight=layer.norm2, h_out=h)
+            xb = x.to(torch.bfloat16)
+            top = torch.topk(xb.float() @ layer.router.float(), w.topk)
+            routed.update(top.indices.to(torch.int32).contiguous())
+            layer.experts.activate(xb, routed, act)
+            layer.experts.combine(act, routed, top.values.softmax(-1).contiguous(), y)
+            block.residual_norm(h, y=y, scale=self.scale, h_out=h)
+        self.lens.copy_(plan.lens)
+        self._collect()
+        return h
+
+    def _collect(self):
+        self.pool.collect(self.table, self.lens)
+        self.free = self.pool.free[:int(self.pool.count)].clone()
+
+    def fork(self, parents, children):
+        """Requests `children` (rows that hold nothing) go on from `parents`."""
+        rows = [torch.tensor(r, dtype=torch.int32, device="cuda") for r in (parents, children)]
+        self.pool.fork(*rows, self.table, self.lens, self.free)
+        for layer in self.layers:
+            layer.cache.copy_pages(self.pool.src, self.pool.dst)
+        self._collect()
+
+    def free_requests(self, rows):
+        """End requests, and move the pages of the others to the front."""
+        self.lens[rows] = 0
+        self.pool.compact(self.table, self.lens)
+        for layer in self.layers:
+            layer.cache.copy_pages(self.pool.src, self.pool.dst, count=self.pool.moves)
+        self.free = self.pool.free[:int(self.pool.count)].clone()
+
     def status(self):
         """Raise if a device-side check failed."""
         for layer in self.layers:
-            for code, bits in (layer.cache.status(), layer.reader.status()):
+            for code, bits in (layer.cache.status(), layer.reader.status(),
+                               layer.experts.status()):
                 if code:
                     raise RuntimeError(f"device error bits {bits:#x} ({code})")
 
@@ -134,6 +192,15 @@ def main(steps=200, keep=4):
         decoder.status()
         print(f"{name}: {decoder.requests} requests of {int(decoder.lens[0])} tokens, "
               f"{len(decoder.layers)} layers, {ms:.2f} ms a step, |h| {float(h.norm()):.3f}")
+    decoder.free_requests(list(range(decoder.requests)))
+    new = torch.tensor([100, 60, 0, 0], dtype=torch.int32, device="cuda")
+    h = decoder.prompt(torch.randn((160, decoder.w.H), generator=g, device="cuda"), new)
+    decoder.fork([0, 0], [2, 3])
+    one = torch.ones(decoder.requests, dtype=torch.int32, device="cuda")
+    decoder.step(torch.randn((decoder.requests, decoder.w.H), generator=g, device="cuda"), one)
+    decoder.status()
+    print(f"two prompts, |h| {float(h.norm()):.3f}; the first one continued in three ways: "
+          f"{decoder.lens.tolist()} tokens, {decoder.free.shape[0]} pages free")
 
 
 if __name__ == "__main__":

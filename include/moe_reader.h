@@ -296,12 +296,18 @@ int moe_reader_set_wait_limit(moe_reader_t* h, uint64_t ns);
  *       waits, where a row ends inside a CTA's share of keys, for a turn that
  *       does not come; the wait runs out after about a millisecond, the CTA
  *       adds up no more rows and the call ends with MOE_READER_ERR_TIMEOUT.
+ *   MOE_READER_INJECT_PROMPT_STALL   (h = NULL) the next moe_reader_kv_chunk,
+ *       moe_reader_experts_activate or _combine waits, before its first product,
+ *       for one that was never issued; the wait runs out after a second, the
+ *       CTAs' other waits end with it, copies under way are awaited, tensor
+ *       memory is freed and the call ends with MOE_READER_ERR_TIMEOUT.
  * Each injection fires once.  EINVAL for an unknown bit or a wrong h.
  */
 #define MOE_READER_INJECT_DECODE_STALL  0x1u
 #define MOE_READER_INJECT_PREPARE_STALL 0x2u
 #define MOE_READER_INJECT_ALLOC_FAIL    0x4u
 #define MOE_READER_INJECT_ATTEND_STALL  0x10u
+#define MOE_READER_INJECT_PROMPT_STALL  0x20u
 int moe_reader_inject_fault(moe_reader_t* h, uint32_t what);
 
 /* moe_reader_status -- synchronize the device (a captured decode runs on
