@@ -31,6 +31,13 @@ template <int QT> __device__ __forceinline__ uint32_t pack2(float lo, float hi) 
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
+// Two weights' upper 16 bits, and what that cuts off: both parts above zero for
+// a weight above zero, so that infinite values stay infinite.
+__device__ __forceinline__ uint32_t cut2(float x, float y, uint32_t& rest) {
+  const uint32_t a = max(__float_as_uint(x), 1u) - 1, b = max(__float_as_uint(y), 1u) - 1;
+  rest = pack2<kBf16>(x - __uint_as_float(a & 0xffff0000u), y - __uint_as_float(b & 0xffff0000u));
+  return __byte_perm(a, b, 0x7632);
+}
 __device__ __forceinline__ float exp2_fast(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -322,6 +329,12 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
   // of it.
   constexpr int MT = CT == kE4m3 ? kF16 : QT;
   constexpr bool kScaled = CT == kE4m3 && QT == kBf16;
+  // bf16 weights of items of few rows, whose products wait for their keys anyway,
+  // go in two parts: what the first cut off, in a second product of the same
+  // type (16 bits of a weight instead of 8: the output's error is its own
+  // rounding).  Where products bound the time they would take half as long again.
+  constexpr bool kFine = CT == kBf16;
+  constexpr int kFineRows = S::kTiles == 2 ? 128 : 64;
   constexpr float kLift = MT == kF16 ? 11.f : 0.f;     // fp16 weights reach down to 2^-35
   constexpr float kSlack = MT == kF16 ? 4.f : 8.f;     // how far a logit may pass the reference
   extern __shared__ char raw[];
@@ -937,7 +950,7 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
       __syncwarp();
     };
     // O += P V, the first half of the keys as soon as its weights are there
-    auto outputs = [&](int tile, int at, int slot, bool first, uint32_t then) {
+    auto outputs = [&](int tile, int at, int slot, bool first, bool fine, uint32_t then) {
       const uint32_t want = p_phase[at];
       p_phase[at] ^= 1;
       if (!tc::bar_wait(p_half(at), want, &s_quit)) return false;
@@ -948,6 +961,11 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
 #pragma unroll
         for (int i = 0; i < S::kKeys / 32; ++i)
           tc::mma_ta(d, p + i * 8, v + i * 128, o_desc, !first || i > 0);
+        if (kFine && fine) {
+#pragma unroll
+          for (int i = 0; i < S::kKeys / 32; ++i)
+            tc::mma_ta(d, p + S::kKeys / 2 + i * 8, v + i * 128, o_desc, true);
+        }
       }
       __syncwarp();
       if (!tc::bar_wait(p_full(at), want, &s_quit)) return false;
@@ -956,6 +974,11 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
 #pragma unroll
         for (int i = S::kKeys / 32; i < S::kKeys / 16; ++i)
           tc::mma_ta(d, p + i * 8, v + i * 128, o_desc, true);
+        if (kFine && fine) {
+#pragma unroll
+          for (int i = S::kKeys / 32; i < S::kKeys / 16; ++i)
+            tc::mma_ta(d, p + S::kKeys / 2 + i * 8, v + i * 128, o_desc, true);
+        }
         tc::commit(bar);
         if (then) tc::commit(then);
       }
@@ -981,7 +1004,7 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
           next_slot();
           if (j + 1 < n && !(go = tc::bar_wait(slot_full(s), phase, &s_quit))) break;
           for (int t = 0; t < 2; ++t) {
-            if (!(go = outputs(t, t, v_slot, j == 0, t ? slot_free(v_slot) : 0))) break;
+            if (!(go = outputs(t, t, v_slot, j == 0, false, t ? slot_free(v_slot) : 0))) break;
             if (j + 1 < n) logits(t, t, s, t ? slot_free(s) : 0, t && j + 2 == n ? q_free : 0);
           }
           if (go && j + 1 < n) next_slot();
@@ -1008,7 +1031,8 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
             ask();
           }
           if (!(go = values_in(x, x.step + j))) break;
-          if (!(go = outputs(ahead == 2 ? j & 1 : 0, j & 1, s, j < ahead, slot_free(s)))) break;
+          if (!(go = outputs(ahead == 2 ? j & 1 : 0, j & 1, s, j < ahead, x.rows <= kFineRows,
+                              slot_free(s)))) break;
           if (ahead == 2 && asked < n) {
             if (!(go = tc::bar_wait(slot_full(k_slot), k_phase, &s_quit))) break;
             tc::fence_after();
@@ -1039,6 +1063,7 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
       const bool twins = S::kTiles == 2 && x.rows <= 128;
       const int r = (twins ? 0 : tile * 128) + quarter * 32 + lane;
       const int first = twins ? tile : 0, stride = twins ? 2 : 1;
+      const bool fine = kFine && x.rows <= kFineRows;
       const int own = twins ? (n - tile + 1) >> 1 : tile * 128 < x.rows ? n : 0;   // its steps
       int group_head;
       const int token = quotient(x.row + r, c.by_group, group_head);
@@ -1105,11 +1130,11 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
           const float high = fmaxf(top[0], top[1]) * by;
           const bool moves = high > m + kSlack;
           if (__any_sync(0xffffffffu, moves)) {
-            // the reference follows the maximum, in whole powers of two, so that
-            // rescaling and the exponents below round nothing; what is added up
-            // so far follows it
-            const float to = ceilf(high), f = moves ? exp2_fast(m - to) : 1.f;
-            if (moves) m = to;
+            // the reference follows the maximum (itself: the weight of a lone key
+            // is a power of two, and its value comes out as it is); what is
+            // added up so far follows it
+            const float f = moves ? exp2_fast(m - high) : 1.f;
+            if (moves) m = high;
             l *= f;
             if (turn > 0) {
               // (two tiles: S is made behind the products before it)
@@ -1133,7 +1158,7 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
 #pragma unroll
           for (int i = 0; i < S::kKeys; i += 32) {
             if (kHeld < S::kKeys && i % kHeld == 0) fetch(i);
-            uint32_t w[16];
+            uint32_t w[16], rest[kFine ? 16 : 1];
 #pragma unroll
             for (int e = 0; e < 32; e += 2) {
               const int at0 = i % kHeld + e;
@@ -1143,9 +1168,13 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
               x0 = exp2_fast(x0);
               x1 = exp2_fast(x1);
               add[e >> 1 & 1] = add_pair(add[e >> 1 & 1], pair(x0, x1));
-              w[e / 2] = pack2<MT>(x0, x1);
+              if (kFine && fine) w[e / 2] = cut2(x0, x1, rest[kFine ? e / 2 : 0]);
+              else w[e / 2] = pack2<MT>(x0, x1);
             }
             tc::st16(s_at + i / 2, w);
+            if constexpr (kFine) {
+              if (fine) tc::st16(s_at + S::kKeys / 2 + i / 2, rest);
+            }
             if (i + 32 == S::kKeys / 2) {
               // the first half can be multiplied
               tc::st_wait();
