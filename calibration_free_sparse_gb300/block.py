@@ -1,10 +1,12 @@
-"""The rest of a decode step around the MoE reader: a paged key/value cache
-and the norm that joins it to the reader.
+"""The rest of a decode step around the MoE reader, and a prompt's attention: a
+paged key/value cache and the norm that joins it to the reader.
 
 ``PagedCache`` wraps one layer's cache arrays: ``plan`` (page tables and slot
 maps from request lengths), ``append`` (new rows into their slots),
-``attend`` (one new token per request) and ``select`` (pages by a cheap score,
-for ``attend(pages=...)``).  ``residual_norm`` is post-norm, gate, scaled
+``attend`` (one new token per request), ``attend_chunk`` (several: a prompt, a
+chunk of one, drafted tokens) and ``select`` (pages by a cheap score, for
+``attend(pages=...)``).  ``PagePool`` keeps track of a table's pages: free ones,
+rows forked from others, the pool compacted (``copy_pages`` copies what moves).  ``residual_norm`` is post-norm, gate, scaled
 residual and pre-norm in one pass.  Definitions, types and errors stand in
 ``include/moe_reader.h``; this module checks the tensors and marshals the
 arguments.  Every call is asynchronous on the current stream (or ``stream``),

@@ -13,7 +13,7 @@
 struct moe_reader_kv {
   moe_reader_kv_config cfg;
   int device;
-  int sms;                    // CTAs of attend: one per SM
+  int sms;                    // CTAs of attend and of chunk: one per SM
   int page_shift;             // log2(page_size)
   int group;                  // query heads per KV head
   void* k;                    // caller-owned [num_pages][Hkv][page_size][D]

@@ -462,7 +462,8 @@ typedef struct {
  *             by (finite, > 0); required for E4M3, NULL otherwise.
  *
  * All of them are the caller's and must outlive the handle, which owns only
- * its workspace (partial results and counters of attend).  Calls on one
+ * its workspace (partial results and counters of attend and of kv_chunk: 20 MB
+ * with heads of 64, 40 with longer ones).  Calls on one
  * handle must not overlap on the GPU, and the calling thread's current device
  * has to be the handle's (EINVAL).  Errors: EINVAL, ENOMEM, ECUDA.
  */
@@ -621,8 +622,11 @@ int moe_reader_kv_attend(moe_reader_kv_t* kv, const moe_reader_kv_attend_args* a
  * logit of NaN makes the head's row and its lse NaN.  What a row does not see
  * (later tokens, rows behind the last one) does not touch it, whatever it
  * holds.  Logits, references and sums are fp32; the weights enter the product
- * with V as values of q_type.  A V of infinity makes its coordinate infinite,
- * unless the key's weight is 0.
+ * with V as values of the cache's type (for E4M3 in fp16, where the queries too
+ * are brought to fp16, by a power of two per row; a row whose bits that would
+ * lose goes without it), and in bf16 where there are few rows with what that cut
+ * off.  A V of infinity makes its coordinate infinite, unless the key's weight
+ * is 0.  Rows that two requests claim (starts that do not ascend) are either's.
  * A negative length counts as 0, starts are cut to [0, tokens], a request with
  * fewer tokens than new ones has rows of nothing in front, and keys beyond the
  * table do not exist (all ERR_LENGTH); a page that is not in the pool is skipped
