@@ -1,5 +1,6 @@
 // Attention of several new tokens per request over the paged cache.
 #include <algorithm>
+#include <type_traits>
 
 #include "device_util.cuh"
 #include "internal.cuh"
@@ -1169,33 +1170,36 @@ chunk_kernel(const __grid_constant__ ChunkCall c) {
           const float bias = kLift - (m == -INFINITY ? 0.f : m);
           const uint64_t factors = pair(by, by), biases = pair(bias, bias);
           uint64_t add[2] = {0, 0};
+          auto weigh = [&](auto parts) {
+            constexpr bool kParts = decltype(parts)::value;
 #pragma unroll
-          for (int i = 0; i < S::kKeys; i += 32) {
-            if (kHeld < S::kKeys && i % kHeld == 0) fetch(i);
-            uint32_t w[16], rest[kFine ? 16 : 1];
+            for (int i = 0; i < S::kKeys; i += 32) {
+              if (kHeld < S::kKeys && i % kHeld == 0) fetch(i);
+              uint32_t w[16], rest[kParts ? 16 : 1];
 #pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-              const int at0 = i % kHeld + e;
-              float x0, x1;
-              unpair(fma_pair(pair(__uint_as_float(v[at0]), __uint_as_float(v[at0 + 1])), factors,
-                              biases), x0, x1);
-              x0 = exp2_fast(x0);
-              x1 = exp2_fast(x1);
-              add[e >> 1 & 1] = add_pair(add[e >> 1 & 1], pair(x0, x1));
-              if (kFine && fine) w[e / 2] = cut2(x0, x1, rest[kFine ? e / 2 : 0]);
-              else w[e / 2] = pack2<MT>(x0, x1);
+              for (int e = 0; e < 32; e += 2) {
+                const int at0 = i % kHeld + e;
+                float x0, x1;
+                unpair(fma_pair(pair(__uint_as_float(v[at0]), __uint_as_float(v[at0 + 1])), factors,
+                                biases), x0, x1);
+                x0 = exp2_fast(x0);
+                x1 = exp2_fast(x1);
+                add[e >> 1 & 1] = add_pair(add[e >> 1 & 1], pair(x0, x1));
+                if constexpr (kParts) w[e / 2] = cut2(x0, x1, rest[e / 2]);
+                else w[e / 2] = pack2<MT>(x0, x1);
+              }
+              tc::st16(s_at + i / 2, w);
+              if constexpr (kParts) tc::st16(s_at + S::kKeys / 2 + i / 2, rest);
+              if (i + 32 == S::kKeys / 2) {
+                // the first half can be multiplied
+                tc::st_wait();
+                tc::fence_before();
+                tc::bar_arrive(p_half(at));
+              }
             }
-            tc::st16(s_at + i / 2, w);
-            if constexpr (kFine) {
-              if (fine) tc::st16(s_at + S::kKeys / 2 + i / 2, rest);
-            }
-            if (i + 32 == S::kKeys / 2) {
-              // the first half can be multiplied
-              tc::st_wait();
-              tc::fence_before();
-              tc::bar_arrive(p_half(at));
-            }
-          }
+          };
+          if (kFine && fine) weigh(std::bool_constant<kFine>());
+          else weigh(std::false_type());
           float l0, l1;
           unpair(add_pair(add[0], add[1]), l0, l1);
           l += l0 + l1;
