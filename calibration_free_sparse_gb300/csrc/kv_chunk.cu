@@ -95,8 +95,8 @@ __device__ __forceinline__ Span span_of(const moe_reader_kv_chunk_args& a, int r
 //  - the same with pages by 16-byte copies of three warps 715, with products
 //    issued by a lane of a divergent warp (operands moved to uniform registers
 //    one by one) 490, without packed pairs and handing weights over in halves 420.
-//  - 500 tokens over 32768 of an e4m3 cache, 32/8 heads: 293 us (widening).
-//  - 5 tokens of 16 requests, 32/4 heads, up to 4096 tokens: 33 us, 73 MB; 4 of
+//  - 500 tokens over 32768 of an e4m3 cache, 32/8 heads: 291 us (widening).
+//  - 5 tokens of 16 requests, 32/4 heads, up to 4096 tokens: 35 us, 73 MB; 4 of
 //    them are found out by every CTA, 5 the first pages' way, 14 streaming, 6 the
 //    joining of rows.
 // ---------------------------------------------------------------------------
